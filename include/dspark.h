@@ -65,6 +65,7 @@ extern "C" {
 /* storage types */
 #define DSPARK_F32 0
 #define DSPARK_BF16 1
+#define DSPARK_F16 2   /* logits and their gradients of the calls on rows of logits */
 
 /* scheduler modes */
 #define DSPARK_SCHED_FIXED 0   /* no truncation: l_r = gamma */
@@ -413,6 +414,98 @@ int dspark_round_ex(const float* U, const float* T, const void* W1, const void* 
                     int32_t* ell_out, int32_t* nstar_out, double* theta_out,
                     int32_t* n_out, int32_t* tok_out,
                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Rows of logits: log probabilities and distillation.  No counterpart on the
+ * pages' hot path; a serving engine returns the first to its clients, and a
+ * draft is trained on the second ([blog] section 9 names the losses of the
+ * draft and a cache of the target's outputs, without their code).
+ *
+ * Conventions of these calls.  logits holds N rows of V entries (dtype
+ * DSPARK_F32, DSPARK_BF16 or DSPARK_F16), row i starting row_stride entries
+ * after row i - 1 (row_stride >= V; any element alignment; 1 <= V <= 2^21,
+ * N <= 2^24, N = 0 does nothing).  Rows come in groups of R (N % R == 0); with lens [N / R] i32
+ * only the first lens[g] rows of group g count and the others' outputs are
+ * zeros (alternatives -1 / -inf), with lens NULL every row counts.  Sums are
+ * kept in fp32.  An entry of -inf has probability 0; a row of nothing else has
+ * lse -inf, entropy 0, loss 0 and gradient 0.  A NaN or +inf in a row makes its
+ * outputs NaN (these calls have no workspace to report it in).  They need no
+ * workspace, and may run concurrently with any other call.
+ *
+ * dspark_token_logprobs: for row i and its token t = tokens[i]
+ *   lse = log sum_v exp x_v, logp = x_t - lse, entropy = -sum_v p_v log p_v,
+ *   and the top_k (0..128, <= V) largest entries, largest first and equal ones
+ *   by index: top_idx [N, top_k] i32, top_logp [N, top_k] f32 (x - lse).  Entries
+ *   of -inf are no alternatives: -1 and -inf stand in their places.
+ *   A token of -1 is none (logp 0); another one outside [0, V) gives NaN.
+ * Out: logp, entropy, lse [N] f32; top_idx_out, top_logp_out (NULL with top_k 0).
+ */
+int dspark_token_logprobs(const void* logits, int dtype, int64_t row_stride, const int32_t* tokens,
+                          const int32_t* lens, int N, int R, int V, int top_k,
+                          float* logp_out, float* entropy_out, float* lse_out,
+                          int32_t* top_idx_out, float* top_logp_out, void* stream);
+
+/*
+ * dspark_token_logprobs of the tokens a round emitted: T [B, gamma+1, V]
+ * (dtype), x [B, gamma], n and tok [B] as dspark_verify takes and gives them.
+ * Row j of request b scores x[b, j] for j < n[b] and tok[b] for j = n[b]; the
+ * rows after it do not count (n[b] < 0: none do; n[b] is held at gamma).
+ * Outputs [B, gamma+1] (and [B, gamma+1, top_k]).  B <= 65535, gamma <= 32.
+ */
+int dspark_emitted_logprobs(const void* T, int dtype, const int32_t* x, const int32_t* n, const int32_t* tok,
+                            int B, int gamma, int V, int top_k,
+                            float* logp_out, float* entropy_out, float* lse_out,
+                            int32_t* top_idx_out, float* top_logp_out, void* stream);
+
+/*
+ * The gradient of dspark_token_logprobs' logp and entropy:
+ *   dx_v = g_logp (1[v = t] - p_v) - g_entropy p_v (log p_v + entropy)
+ * from its lse and entropy outputs.  g_logp, g_entropy [N] f32 (either may be
+ * NULL: 0; entropy is needed with g_entropy).  A row that does not count gets
+ * zeros; a token of -1 has no g_logp part.
+ * Out: dlogits_out [N, V] dense, of the logits' type; it may be the logits
+ * themselves when those are dense, and may not overlap them otherwise.
+ */
+int dspark_token_logprobs_backward(const void* logits, int dtype, int64_t row_stride, const int32_t* tokens,
+                                   const float* lse, const float* entropy, const float* g_logp,
+                                   const float* g_entropy, const int32_t* lens, int N, int R, int V,
+                                   void* dlogits_out, void* stream);
+
+/*
+ * Kullback-Leibler loss of a student's logits against a teacher's K kept logits
+ * (1 <= K <= 128) at a temperature tau > 0.  With z = logits / tau, q =
+ * softmax(z), entries (i_k, t_k) = (top_idx, top_val) [N, K] (index -1: absent):
+ *  - teacher_lse NULL: p = softmax(t / tau) over the kept entries and
+ *      loss = sum_k p_k (log p_k - log q_{i_k});
+ *  - teacher_lse [N] f32, the log-sum-exp of the teacher's whole row of t / tau:
+ *      p_k = exp(t_k / tau - teacher_lse), p_r = max(0, 1 - sum_k p_k) and
+ *      loss = sum_k p_k (log p_k - log q_{i_k}) + p_r (log p_r - log q_r), q_r
+ *      the student's mass outside the kept entries.
+ * dspark_token_logprobs' top_idx, top_logp and teacher_lse = 0 are such entries
+ * at tau = 1.  An index may repeat (each entry is a term of its own); one
+ * outside [-1, V) makes the row's outputs NaN.  A row none of whose entries has
+ * mass does not count.
+ * Out: loss_out [N] f32; stats_out [N, 2] f32, the lse of z and that of its
+ * entries outside the kept ones (the lse again with teacher_lse NULL).
+ * dlogits_out (may be NULL) [N, V] dense, type gdtype (the logits' type, or
+ * DSPARK_BF16 for fp32 logits): weight[i] * d loss_i / d logits, weight [N] f32
+ * or NULL (1); zeros in rows that do not count.  It may be the logits
+ * themselves when those are dense and of its type, and may not overlap them
+ * otherwise.
+ */
+int dspark_distill_loss(const void* logits, int dtype, int64_t row_stride, const int32_t* top_idx,
+                        const float* top_val, const float* teacher_lse, const float* weight,
+                        const int32_t* lens, int N, int R, int V, int K, float temperature,
+                        float* loss_out, float* stats_out, void* dlogits_out, int gdtype, void* stream);
+
+/*
+ * The gradient of dspark_distill_loss alone, from its stats output and an
+ * upstream gradient g [N] f32 (in the place of weight).
+ */
+int dspark_distill_loss_backward(const void* logits, int dtype, int64_t row_stride, const int32_t* top_idx,
+                                 const float* top_val, const float* stats, const float* g,
+                                 const float* teacher_lse, const int32_t* lens, int N, int R, int V, int K,
+                                 float temperature, void* dlogits_out, int gdtype, void* stream);
 
 /*
  * The Markov draft without a caller workspace.  The method has no counterpart:

@@ -10,9 +10,12 @@ Entry points (same names as the C ABI in include/dspark.h; the optional
 arguments of markov_draft, schedule, verify and round map to the C ABI's _ex
 forms):
   markov_draft, confidence, schedule, verify, round, read_status,
-  acceptance_label, sts_fit
+  acceptance_label, sts_fit, token_logprobs, emitted_logprobs,
+  token_logprobs_backward, distill_loss, distill_loss_backward
 """
+import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -21,7 +24,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libdspark.so")
 
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_WORKSPACE, ERR_NONFINITE = range(7)
-F32, BF16 = 0, 1
+F32, BF16, F16 = 0, 1, 2
 SCHED_FIXED, SCHED_GREEDY, SCHED_TOPK = 0, 1, 2
 EARLY_TARGET_STATS, ADVANCE_ROUND, TARGET_STATS_FROM_VERIFY, SCRATCH_FROM_DRAFT, GATED_STATES = 1, 2, 4, 8, 16
 ALL_ROW_STATS = 32
@@ -92,6 +95,18 @@ def _load():
                                            i32, i32, vp, u64, u64, vp, ctypes.c_uint, vp, vp, vp, vp, vp, vp, vp,
                                            vp, sz, vp]
     L.dspark_draft_schedule_ex.restype = i32
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    L.dspark_token_logprobs.argtypes = [vp, i32, i64, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
+    L.dspark_token_logprobs.restype = i32
+    L.dspark_emitted_logprobs.argtypes = [vp, i32, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
+    L.dspark_emitted_logprobs.restype = i32
+    L.dspark_token_logprobs_backward.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, vp]
+    L.dspark_token_logprobs_backward.restype = i32
+    L.dspark_distill_loss.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, vp, vp, vp, i32, vp]
+    L.dspark_distill_loss.restype = i32
+    L.dspark_distill_loss_backward.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, vp,
+                                               i32, vp]
+    L.dspark_distill_loss_backward.restype = i32
     L.dspark_read_status.argtypes = [vp, ctypes.POINTER(i32), vp]
     L.dspark_read_status.restype = i32
     L.dspark_selftest_wait_timeout.argtypes = [i32, vp, sz, vp]
@@ -362,6 +377,200 @@ def sts_fit(z, ell, acc, grid):
     _check(L.dspark_sts_fit(_ptr(z), _ptr(ell), _ptr(acc), N, G, _ptr(grid), grid.numel(), _ptr(T), _ptr(e), _ptr(ws),
                             ws.numel(), _stream(dev)), "sts_fit")
     return T, e
+
+
+_ROW_DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+
+
+def _on(dev):
+    """The context that makes dev the current device (the library launches on it)."""
+    return torch.cuda.device(dev) if torch.cuda.current_device() != dev.index else contextlib.nullcontext()
+
+
+def _row_args(logits, rows, what="logits"):
+    """device, leading shape, N, R, V, row stride and dtype code of rows of logits."""
+    if logits is None or not logits.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if logits.dtype not in _ROW_DTYPES:
+        raise TypeError(f"{what} must be float32, bfloat16 or float16, got {logits.dtype}")
+    if logits.dim() < 1 or logits.shape[-1] < 1:
+        raise ValueError(f"{what} must be [..., V] with V >= 1, got {list(logits.shape)}")
+    lead, V = tuple(logits.shape[:-1]), logits.shape[-1]
+    N = math.prod(lead)
+    if V > 1 and N > 0 and logits.stride(-1) != 1:
+        raise ValueError(f"{what} must have entries of a row next to each other")
+    stride = V
+    if N > 1:
+        try:
+            stride = logits.view(N, V).stride(0)
+        except RuntimeError:
+            raise ValueError(f"{what} must have rows a fixed distance apart (strides {logits.stride()})") from None
+        if stride < V:
+            raise ValueError(f"{what} must not have overlapping rows (strides {logits.stride()})")
+    R = 1
+    if rows is not None:
+        if len(lead) != 2:
+            raise ValueError(f"rows needs {what} [B, R, V], got {list(logits.shape)}")
+        _need(rows, "rows", torch.int32, logits.device)
+        _sized(rows, "rows", lead[:1])
+        R = max(lead[1], 1)
+    return logits.device, lead, N, R, V, stride, _ROW_DTYPES[logits.dtype]
+
+
+def _row_vector(t, what, lead, dev, dtype=torch.float32):
+    if t is not None:
+        _need(t, what, dtype, dev)
+        _sized(t, what, lead)
+    return _ptr(t)
+
+
+def _gradient_out(out, logits, dtype):
+    """A dense gradient of these logits, checked or allocated.  It may be the
+    logits themselves, and may not overlap them in another way."""
+    if out is None:
+        return torch.empty(logits.shape, dtype=dtype, device=logits.device)
+    _need(out, "out", dtype, logits.device)
+    _sized(out, "out", logits.shape)
+    if out.numel() > 0:
+        a0, b0 = out.data_ptr(), logits.data_ptr()
+        last = sum((n - 1) * s for n, s in zip(logits.shape, logits.stride()))
+        a1, b1 = a0 + out.numel() * out.element_size(), b0 + (last + 1) * logits.element_size()
+        same = a0 == b0 and logits.dtype == dtype and logits.is_contiguous()
+        if a0 < b1 and b0 < a1 and not same:
+            raise ValueError("out overlaps the logits; it may only be the same dense tensor")
+    return out
+
+
+def _logprob_outputs(lead, top_k, dev):
+    logp, entropy, lse = (torch.empty(lead, dtype=torch.float32, device=dev) for _ in range(3))
+    if not top_k:
+        return logp, entropy, lse, None, None
+    return (logp, entropy, lse, torch.empty((*lead, top_k), dtype=torch.int32, device=dev),
+            torch.empty((*lead, top_k), dtype=torch.float32, device=dev))
+
+
+def token_logprobs(logits, tokens, top_k=0, rows=None):
+    """logp, entropy, lse [...] f32 of logits [..., V] (f32, bf16 or f16, rows a
+    fixed distance apart) at tokens [...] i32 (-1: none), and the top_k <= 128
+    most probable entries of each row, largest first and equal ones by index:
+    top_idx i32, top_logp f32 [..., top_k] (None with top_k = 0).
+    rows [B] i32, with logits [B, R, V]: only the first rows[b] rows of b count
+    (the others' outputs are 0, -1 and -inf)."""
+    L = _load()
+    dev, lead, N, R, V, stride, dt = _row_args(logits, rows)
+    _row_vector(_need(tokens, "tokens"), "tokens", lead, dev, torch.int32)
+    out = _logprob_outputs(lead, _top_k(top_k, V), dev)
+    with _on(dev):
+        _check(L.dspark_token_logprobs(_ptr(logits), dt, stride, _ptr(tokens), _ptr(rows), N, R, V, top_k,
+                                       *map(_ptr, out), _stream(dev)), "token_logprobs")
+    return out
+
+
+def _top_k(top_k, V):
+    if not 0 <= top_k <= V:
+        raise ValueError(f"top_k must be in [0, V = {V}], got {top_k}")
+    return top_k
+
+
+def emitted_logprobs(T, x, n, tok, top_k=0):
+    """token_logprobs of the tokens a round emitted, from its target logits T
+    [B, G+1, V] and its outputs x [B, G], n and tok [B]: row j < n[b] scores
+    x[b, j], row n[b] scores tok[b], and the rows after it do not count."""
+    L = _load()
+    dev, lead, N, _, V, stride, dt = _row_args(T, None, "T")
+    if len(lead) != 2 or lead[1] < 2 or not T.is_contiguous():
+        raise ValueError(f"T must be [B, gamma+1, V] and contiguous, got {list(T.shape)}")
+    B, G = lead[0], lead[1] - 1
+    for t, name, shape in [(x, "x", (B, G)), (n, "n", (B,)), (tok, "tok", (B,))]:
+        _row_vector(_need(t, name), name, shape, dev, torch.int32)
+    out = _logprob_outputs(lead, _top_k(top_k, V), dev)
+    with _on(dev):
+        _check(L.dspark_emitted_logprobs(_ptr(T), dt, _ptr(x), _ptr(n), _ptr(tok), B, G, V, top_k, *map(_ptr, out),
+                                         _stream(dev)), "emitted_logprobs")
+    return out
+
+
+def token_logprobs_backward(logits, tokens, lse, entropy=None, g_logp=None, g_entropy=None, rows=None, out=None):
+    """The gradient of the logits, of their type and dense, from the upstream
+    gradients g_logp and g_entropy [...] f32 (None: 0) of token_logprobs' logp
+    and entropy; lse and entropy are that call's outputs.  out: a dense tensor
+    to write, which may be the logits themselves."""
+    L = _load()
+    dev, lead, N, R, V, stride, dt = _row_args(logits, rows)
+    _row_vector(_need(tokens, "tokens"), "tokens", lead, dev, torch.int32)
+    _row_vector(_need(lse, "lse"), "lse", lead, dev)
+    if g_entropy is not None:
+        _need(entropy, "entropy")
+    for t, name in [(entropy, "entropy"), (g_logp, "g_logp"), (g_entropy, "g_entropy")]:
+        _row_vector(t, name, lead, dev)
+    out = _gradient_out(out, logits, logits.dtype)
+    with _on(dev):
+        _check(L.dspark_token_logprobs_backward(_ptr(logits), dt, stride, _ptr(tokens), _ptr(lse), _ptr(entropy),
+                                                _ptr(g_logp), _ptr(g_entropy), _ptr(rows), N, R, V, _ptr(out),
+                                                _stream(dev)), "token_logprobs_backward")
+    return out
+
+
+def _distill_args(logits, top_idx, top_val, teacher_lse, rows, temperature):
+    dev, lead, N, R, V, stride, dt = _row_args(logits, rows)
+    _need(top_idx, "top_idx", torch.int32, dev); _need(top_val, "top_val", torch.float32, dev)
+    if top_idx.dim() != len(lead) + 1 or top_idx.shape[-1] < 1:
+        raise ValueError(f"top_idx must be {list(lead)} + [K], got {list(top_idx.shape)}")
+    K = top_idx.shape[-1]
+    _sized(top_idx, "top_idx", (*lead, K)); _sized(top_val, "top_val", (*lead, K))
+    _row_vector(teacher_lse, "teacher_lse", lead, dev)
+    if not 0.0 < temperature < math.inf:
+        raise ValueError(f"temperature must be positive and finite, got {temperature}")
+    return dev, lead, N, R, V, stride, dt, K
+
+
+def distill_loss(logits, top_idx, top_val, temperature=1.0, teacher_lse=None, weight=None, rows=None, grad=False,
+                 grad_dtype=None, out=None):
+    """Kullback-Leibler loss of a student's logits [..., V] against a teacher's K
+    kept logits top_val [..., K] f32 at top_idx [..., K] i32 (-1: absent; K <= 128):
+    loss [...] f32, stats [..., 2] f32 (for distill_loss_backward) and, with
+    grad, weight * d loss / d logits of type grad_dtype (the logits' own, or
+    bfloat16 for float32 logits), else None, in one call.
+    teacher_lse [...] f32, the log-sum-exp of the teacher's whole row of
+    top_val / temperature: the teacher's remaining mass is matched, as one
+    bucket, with the student's; None: the kept entries are renormalised.
+    weight [...] f32 (None: 1) scales the gradient, not the loss.
+    rows as in token_logprobs; out as in token_logprobs_backward."""
+    L = _load()
+    dev, lead, N, R, V, stride, dt, K = _distill_args(logits, top_idx, top_val, teacher_lse, rows, temperature)
+    _row_vector(weight, "weight", lead, dev)
+    if not grad and (out is not None or grad_dtype is not None):
+        raise ValueError("out and grad_dtype need grad")
+    gdt = logits.dtype if grad_dtype is None else grad_dtype
+    if gdt not in _ROW_DTYPES:
+        raise TypeError(f"grad_dtype must be float32, bfloat16 or float16, got {gdt}")
+    dlogits = _gradient_out(out, logits, gdt) if grad else None
+    loss = torch.empty(lead, dtype=torch.float32, device=dev)
+    stats = torch.empty((*lead, 2), dtype=torch.float32, device=dev)
+    with _on(dev):
+        _check(L.dspark_distill_loss(_ptr(logits), dt, stride, _ptr(top_idx), _ptr(top_val), _ptr(teacher_lse),
+                                     _ptr(weight), _ptr(rows), N, R, V, K, temperature, _ptr(loss), _ptr(stats),
+                                     _ptr(dlogits), _ROW_DTYPES[gdt], _stream(dev)), "distill_loss")
+    return loss, stats, dlogits
+
+
+def distill_loss_backward(logits, top_idx, top_val, stats, g, temperature=1.0, teacher_lse=None, rows=None,
+                          grad_dtype=None, out=None):
+    """g * d loss / d logits of distill_loss from its stats and an upstream
+    gradient g [...] f32; the other arguments as for that call."""
+    L = _load()
+    dev, lead, N, R, V, stride, dt, K = _distill_args(logits, top_idx, top_val, teacher_lse, rows, temperature)
+    _row_vector(_need(stats, "stats"), "stats", (*lead, 2), dev)
+    _row_vector(_need(g, "g"), "g", lead, dev)
+    gdt = logits.dtype if grad_dtype is None else grad_dtype
+    if gdt not in _ROW_DTYPES:
+        raise TypeError(f"grad_dtype must be float32, bfloat16 or float16, got {gdt}")
+    out = _gradient_out(out, logits, gdt)
+    with _on(dev):
+        _check(L.dspark_distill_loss_backward(_ptr(logits), dt, stride, _ptr(top_idx), _ptr(top_val), _ptr(stats),
+                                              _ptr(g), _ptr(teacher_lse), _ptr(rows), N, R, V, K, temperature,
+                                              _ptr(out), _ROW_DTYPES[gdt], _stream(dev)), "distill_loss_backward")
+    return out
 
 
 class RoundOutputs:

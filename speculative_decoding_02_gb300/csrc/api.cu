@@ -1,6 +1,7 @@
 // The C ABI of libdspark: host-side argument checks, workspace checks and the
 // enqueueing of the per-round kernels.  Every entry point validates its sizes
 // and pointers before it enqueues anything and never synchronises the stream.
+#include <math.h>
 #include <stdint.h>
 
 #include "kernels.h"
@@ -69,6 +70,40 @@ int verify_checks(const float* T, const float* U, const void* W1, const void* W2
     return DSPARK_ERR_INVALID;
   if (!aligned(T, 16) || !aligned(U, 16)) return DSPARK_ERR_INVALID;
   return check_ws(ws, ws_bytes, B, gamma, V);
+}
+
+// The checks of a call on N rows of logits.
+int rows_checks(const void* logits, int dtype, int64_t row_stride, int N, int R, int V) {
+  if (dtype != DSPARK_F32 && dtype != DSPARK_BF16 && dtype != DSPARK_F16) return DSPARK_ERR_INVALID;
+  if (N < 0 || R <= 0 || V <= 0) return DSPARK_ERR_INVALID;
+  if (N > kMaxRows || V > kMaxRowV) return DSPARK_ERR_UNSUPPORTED;
+  if (N % R != 0 || (N > 1 && row_stride < V)) return DSPARK_ERR_INVALID;
+  if (N > 0 && (!logits || !aligned(logits, dtype == DSPARK_F32 ? 4 : 2))) return DSPARK_ERR_INVALID;
+  return DSPARK_OK;
+}
+
+int top_checks(int N, int V, int top_k, const float* logp_out, const float* entropy_out, const float* lse_out,
+               const int32_t* top_idx_out, const float* top_logp_out) {
+  if (top_k < 0 || top_k > V) return DSPARK_ERR_INVALID;
+  if (top_k > kMaxTop) return DSPARK_ERR_UNSUPPORTED;
+  if (N > 0 && (!logp_out || !entropy_out || !lse_out || (top_k > 0 && (!top_idx_out || !top_logp_out))))
+    return DSPARK_ERR_INVALID;
+  return DSPARK_OK;
+}
+
+int distill_checks(const void* logits, int dtype, int64_t row_stride, const int32_t* top_idx, const float* top_val,
+                   int N, int R, int V, int K, float temperature, const void* dlogits, int gdtype) {
+  DSPARK_TRY(rows_checks(logits, dtype, row_stride, N, R, V));
+  // (a temperature whose reciprocal overflows is none)
+  if (K <= 0 || !(temperature > 0.f) || !(temperature < INFINITY) || !(1.f / temperature < INFINITY))
+    return DSPARK_ERR_INVALID;
+  if (K > kMaxTop) return DSPARK_ERR_UNSUPPORTED;
+  if (N > 0 && (!top_idx || !top_val)) return DSPARK_ERR_INVALID;
+  if (dlogits) {
+    if (gdtype != dtype && !(dtype == DSPARK_F32 && gdtype == DSPARK_BF16)) return DSPARK_ERR_UNSUPPORTED;
+    if (!aligned(dlogits, gdtype == DSPARK_F32 ? 4 : 2)) return DSPARK_ERR_INVALID;
+  }
+  return DSPARK_OK;
 }
 
 }  // namespace
@@ -319,6 +354,72 @@ int dspark_round(const float* U, const float* T, const void* W1, const void* W2,
   return dspark_round_ex(U, T, W1, W2, wdtype, h, hdtype, w, sts_T, anchor, B, gamma, V, r, H, sps, n_sps, mode,
                          khist, seed, round, nullptr, 0u, x_out, p_out, lse_out, c_out, ell_out, nstar_out,
                          theta_out, n_out, tok_out, workspace, workspace_bytes, stream);
+}
+
+int dspark_token_logprobs(const void* logits, int dtype, int64_t row_stride, const int32_t* tokens,
+                          const int32_t* lens, int N, int R, int V, int top_k, float* logp_out, float* entropy_out,
+                          float* lse_out, int32_t* top_idx_out, float* top_logp_out, void* stream) {
+  DSPARK_TRY(rows_checks(logits, dtype, row_stride, N, R, V));
+  DSPARK_TRY(top_checks(N, V, top_k, logp_out, entropy_out, lse_out, top_idx_out, top_logp_out));
+  if (N == 0) return DSPARK_OK;
+  if (!tokens) return DSPARK_ERR_INVALID;
+  LogprobArgs a{logits, dtype, row_stride, tokens, nullptr, nullptr, nullptr, lens, N, R, V, top_k, logp_out,
+                entropy_out, lse_out, top_idx_out, top_logp_out};
+  return cuda_status(launch_token_logprobs(a, (cudaStream_t)stream));
+}
+
+int dspark_emitted_logprobs(const void* T, int dtype, const int32_t* x, const int32_t* n, const int32_t* tok, int B,
+                            int gamma, int V, int top_k, float* logp_out, float* entropy_out, float* lse_out,
+                            int32_t* top_idx_out, float* top_logp_out, void* stream) {
+  if (B < 0 || gamma <= 0) return DSPARK_ERR_INVALID;
+  if (B > 65535 || gamma > kMaxGamma) return DSPARK_ERR_UNSUPPORTED;
+  const int N = B * (gamma + 1);
+  DSPARK_TRY(rows_checks(T, dtype, V, N, gamma + 1, V));
+  DSPARK_TRY(top_checks(N, V, top_k, logp_out, entropy_out, lse_out, top_idx_out, top_logp_out));
+  if (N == 0) return DSPARK_OK;
+  if (!x || !n || !tok) return DSPARK_ERR_INVALID;
+  LogprobArgs a{T, dtype, V, nullptr, x, n, tok, nullptr, N, gamma + 1, V, top_k, logp_out,
+                entropy_out, lse_out, top_idx_out, top_logp_out};
+  return cuda_status(launch_token_logprobs(a, (cudaStream_t)stream));
+}
+
+int dspark_token_logprobs_backward(const void* logits, int dtype, int64_t row_stride, const int32_t* tokens,
+                                   const float* lse, const float* entropy, const float* g_logp,
+                                   const float* g_entropy, const int32_t* lens, int N, int R, int V, void* dlogits_out,
+                                   void* stream) {
+  DSPARK_TRY(rows_checks(logits, dtype, row_stride, N, R, V));
+  if (N == 0) return DSPARK_OK;
+  if (!tokens || !lse || !dlogits_out || (g_entropy && !entropy)) return DSPARK_ERR_INVALID;
+  if (!aligned(dlogits_out, dtype == DSPARK_F32 ? 4 : 2)) return DSPARK_ERR_INVALID;
+  LogprobBackwardArgs a{logits, dtype, row_stride, tokens, lse, entropy, g_logp, g_entropy, lens, N, R, V,
+                        dlogits_out};
+  return cuda_status(launch_token_logprobs_backward(a, (cudaStream_t)stream));
+}
+
+int dspark_distill_loss(const void* logits, int dtype, int64_t row_stride, const int32_t* top_idx,
+                        const float* top_val, const float* teacher_lse, const float* weight, const int32_t* lens,
+                        int N, int R, int V, int K, float temperature, float* loss_out, float* stats_out,
+                        void* dlogits_out, int gdtype, void* stream) {
+  DSPARK_TRY(distill_checks(logits, dtype, row_stride, top_idx, top_val, N, R, V, K, temperature, dlogits_out,
+                            gdtype));
+  if (N == 0) return DSPARK_OK;
+  if (!loss_out || !stats_out) return DSPARK_ERR_INVALID;
+  DistillArgs a{logits, dtype, row_stride, top_idx, top_val, teacher_lse, weight, lens, N, R, V, K, temperature,
+                1.f / temperature, loss_out, stats_out, nullptr, dlogits_out, dlogits_out ? gdtype : dtype};
+  return cuda_status(launch_distill(a, (cudaStream_t)stream));
+}
+
+int dspark_distill_loss_backward(const void* logits, int dtype, int64_t row_stride, const int32_t* top_idx,
+                                 const float* top_val, const float* stats, const float* g, const float* teacher_lse,
+                                 const int32_t* lens, int N, int R, int V, int K, float temperature,
+                                 void* dlogits_out, int gdtype, void* stream) {
+  DSPARK_TRY(distill_checks(logits, dtype, row_stride, top_idx, top_val, N, R, V, K, temperature, dlogits_out,
+                            gdtype));
+  if (N == 0) return DSPARK_OK;
+  if (!stats || !g || !dlogits_out) return DSPARK_ERR_INVALID;
+  DistillArgs a{logits, dtype, row_stride, top_idx, top_val, teacher_lse, g, lens, N, R, V, K, temperature,
+                1.f / temperature, nullptr, nullptr, stats, dlogits_out, gdtype};
+  return cuda_status(launch_distill(a, (cudaStream_t)stream));
 }
 
 int dspark_selftest_wait_timeout(int mode, void* workspace, size_t workspace_bytes, void* stream) {

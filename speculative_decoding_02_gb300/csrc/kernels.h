@@ -205,4 +205,65 @@ cudaError_t launch_schedule(const float* c, int B, int gamma, const float* sps, 
 
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream);
 
+// Rows of logits (log probabilities, distillation): N rows of V entries, row i
+// `row_stride` entries after row i - 1; rows come in groups of R, of which the
+// first lens[g] count (all of them when lens is null).
+constexpr int kMaxTop = 128;          // alternatives, or a teacher's kept entries, per row
+constexpr int kMaxRowV = 1 << 21;     // entries of a row
+constexpr int kMaxRows = 1 << 24;
+
+struct LogprobArgs {
+  const void* logits;
+  int dtype;
+  long long row_stride;
+  const int32_t* tokens;   // [N]: -1 none
+  // a round's emitted tokens instead (n not null): row j of request b scores
+  // x[b][j] for j < n[b] and tok[b] for j = n[b]; R - 1 drafted positions
+  const int32_t* x;
+  const int32_t* n;
+  const int32_t* tok;
+  const int32_t* lens;
+  int N, R, V, K;
+  float* logp;
+  float* entropy;
+  float* lse;
+  int32_t* top_idx;        // [N][K]
+  float* top_logp;
+};
+cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t stream);
+
+struct LogprobBackwardArgs {
+  const void* logits;
+  int dtype;
+  long long row_stride;
+  const int32_t* tokens;
+  const float* lse;
+  const float* entropy;    // read where g_entropy is not 0
+  const float* g_logp;     // null: 0
+  const float* g_entropy;  // null: 0
+  const int32_t* lens;
+  int N, R, V;
+  void* dlogits;           // [N][V] dense, may be the logits
+};
+cudaError_t launch_token_logprobs_backward(const LogprobBackwardArgs& a, cudaStream_t stream);
+
+struct DistillArgs {
+  const void* logits;
+  int dtype;
+  long long row_stride;
+  const int32_t* top_idx;     // [N][K], -1: absent
+  const float* top_val;       // [N][K]
+  const float* teacher_lse;   // [N], or null
+  const float* weight;        // [N], or null (1)
+  const int32_t* lens;
+  int N, R, V, K;
+  float tau, inv_tau;
+  float* loss;                // [N]
+  float* stats;               // [N][2]
+  const float* stats_in;      // [N][2]: the backward pass alone (no loss, no stats)
+  void* dlogits;              // [N][V] dense or null; may be the logits
+  int gdtype;
+};
+cudaError_t launch_distill(const DistillArgs& a, cudaStream_t stream);
+
 }  // namespace dspark
