@@ -508,6 +508,38 @@ int dspark_distill_loss_backward(const void* logits, int dtype, int64_t row_stri
                                  float temperature, void* dlogits_out, int gdtype, void* stream);
 
 /*
+ * The Markov head outside the draft, for training it ([blog] section 4): the
+ * logits that the draft samples from, at given tokens,
+ *   l[b, k-1, v] = U[b, k-1, v] + sum_i W1[x_{k-1}, i] * W2[v, i]   (x_0 = anchor),
+ * as a tensor [B, gamma, V] of type ldtype (DSPARK_F32 or DSPARK_BF16, rounded
+ * once).  l_out may be U itself when ldtype is DSPARK_F32.  A previous token
+ * outside [0, V) adds nothing and records DSPARK_ERR_INVALID.  Tensor-core path
+ * only (bf16 weights, r = 256, V >= 192; U, W1, W2, l_out 16-byte aligned),
+ * else DSPARK_ERR_UNSUPPORTED.  Workspace: its status word (256 bytes).
+ */
+int dspark_markov_logits(const float* U, const void* W1, const void* W2, int wdtype,
+                         const int32_t* anchor, const int32_t* x, int B, int gamma, int V, int r,
+                         void* l_out, int ldtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The gradients of both weights from the gradient of those logits, dlogits
+ * [B, gamma, V] bf16 (as dspark_distill_loss and dspark_token_logprobs_backward
+ * give it; the gradient of U is dlogits itself):
+ *   dW2[v, i] = sum_{b,k} dlogits[b, k-1, v] * W1[x_{k-1}, i]
+ *   dW1[t, i] = sum_{(b,k): x_{k-1} = t} sum_v dlogits[b, k-1, v] * W2[v, i]
+ * Out: dW1_out, dW2_out [V, r] f32, wholly written; sums in fp32, in an order
+ * that depends on the sizes alone.  A previous token outside [0, V) takes no
+ * part and records DSPARK_ERR_INVALID.  Same limits as dspark_markov_logits.
+ * Workspace: dspark_head_workspace_size bytes (0 when a size is not positive or
+ * out of range), 256-byte aligned; the call clears its status word.
+ */
+size_t dspark_head_workspace_size(int B, int gamma, int V);
+int dspark_markov_head_backward(const void* dlogits, const void* W1, const void* W2, int wdtype,
+                                const int32_t* anchor, const int32_t* x, int B, int gamma, int V, int r,
+                                float* dW1_out, float* dW2_out, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
  * The Markov draft without a caller workspace.  The method has no counterpart:
  * this entry serves callers that cannot allocate device memory at the time of
  * the call (an engine whose pool owns all of HBM, a plugin given no allocator,

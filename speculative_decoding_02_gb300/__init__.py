@@ -11,7 +11,8 @@ arguments of markov_draft, schedule, verify and round map to the C ABI's _ex
 forms):
   markov_draft, confidence, schedule, verify, round, read_status,
   acceptance_label, sts_fit, token_logprobs, emitted_logprobs,
-  token_logprobs_backward, distill_loss, distill_loss_backward
+  token_logprobs_backward, distill_loss, distill_loss_backward,
+  markov_logits, markov_head_backward
 """
 import contextlib
 import ctypes
@@ -102,6 +103,12 @@ def _load():
     L.dspark_emitted_logprobs.restype = i32
     L.dspark_token_logprobs_backward.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, vp]
     L.dspark_token_logprobs_backward.restype = i32
+    L.dspark_head_workspace_size.argtypes = [i32, i32, i32]
+    L.dspark_head_workspace_size.restype = sz
+    L.dspark_markov_logits.argtypes = [vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, vp, i32, vp, sz, vp]
+    L.dspark_markov_logits.restype = i32
+    L.dspark_markov_head_backward.argtypes = [vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp, sz, vp]
+    L.dspark_markov_head_backward.restype = i32
     L.dspark_distill_loss.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, vp, vp, vp, i32, vp]
     L.dspark_distill_loss.restype = i32
     L.dspark_distill_loss_backward.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, vp,
@@ -571,6 +578,59 @@ def distill_loss_backward(logits, top_idx, top_val, stats, g, temperature=1.0, t
                                               _ptr(g), _ptr(teacher_lse), _ptr(rows), N, R, V, K, temperature,
                                               _ptr(out), _ROW_DTYPES[gdt], _stream(dev)), "distill_loss_backward")
     return out
+
+
+def _head_args(logits, what, dtype, W1, W2, anchor, x):
+    _need(logits, what, dtype)
+    dev = logits.device
+    if logits.dim() != 3:
+        raise ValueError(f"{what} must be [B, gamma, V], got {list(logits.shape)}")
+    B, G, V = logits.shape
+    _need(W1, "W1", device=dev); _need(W2, "W2", W1.dtype, dev)
+    _need(anchor, "anchor", torch.int32, dev); _need(x, "x", torch.int32, dev)
+    r = W1.shape[-1]
+    _sized(W1, "W1", (V, r)); _sized(W2, "W2", (V, r)); _sized(anchor, "anchor", (B,)); _sized(x, "x", (B, G))
+    return dev, B, G, V, r
+
+
+def markov_logits(U, W1, W2, anchor, x, dtype=torch.float32, ws=None, out=None):
+    """l [B, G, V] = U + W1[x_{k-1}] W2^T (x_0 = anchor), the logits the draft
+    samples from at tokens x [B, G], as float32 or bfloat16.  out: a tensor to
+    write, which may be U itself (float32).  Tensor-core path only (bf16
+    weights, r = 256)."""
+    L = _load()
+    dev, B, G, V, r = _head_args(U, "U", torch.float32, W1, W2, anchor, x)
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+    out = _gradient_out(out, U, dtype)
+    ws = workspace(B, G, V, dev) if ws is None else ws
+    with _on(dev):
+        _check(L.dspark_markov_logits(_ptr(U), _ptr(W1), _ptr(W2), _dt(W1, "W1"), _ptr(anchor), _ptr(x), B, G, V, r,
+                                      _ptr(out), _ROW_DTYPES[dtype], _ptr(ws), ws.numel(), _stream(dev)),
+               "markov_logits")
+    return out
+
+
+def head_workspace(B, gamma, V, device):
+    """A workspace of markov_head_backward for these sizes."""
+    n = int(_load().dspark_head_workspace_size(B, gamma, V))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def markov_head_backward(dlogits, W1, W2, anchor, x, ws=None):
+    """dW1, dW2 [V, r] f32 from the gradient dlogits [B, G, V] bf16 of
+    markov_logits.  ws: a head_workspace to keep (and read_status of); by
+    default one is allocated for the call."""
+    L = _load()
+    dev, B, G, V, r = _head_args(dlogits, "dlogits", torch.bfloat16, W1, W2, anchor, x)
+    dW1 = torch.empty((V, r), dtype=torch.float32, device=dev)
+    dW2 = torch.empty((V, r), dtype=torch.float32, device=dev)
+    ws = head_workspace(B, G, V, dev) if ws is None else ws
+    with _on(dev):
+        _check(L.dspark_markov_head_backward(_ptr(dlogits), _ptr(W1), _ptr(W2), _dt(W1, "W1"), _ptr(anchor), _ptr(x),
+                                             B, G, V, r, _ptr(dW1), _ptr(dW2), _ptr(ws), ws.numel(), _stream(dev)),
+               "markov_head_backward")
+    return dW1, dW2
 
 
 class RoundOutputs:

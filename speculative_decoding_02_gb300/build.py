@@ -16,7 +16,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libdspark.so")
 SOURCES = ["api.cu", "draft.cu", "draft_tc.cu", "label_tc.cu", "sched.cu", "verify.cu", "noalloc.cu", "sts.cu",
-           "logprobs.cu", "distill.cu"]
+           "logprobs.cu", "distill.cu", "head_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

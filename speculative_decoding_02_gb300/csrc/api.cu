@@ -396,6 +396,41 @@ int dspark_token_logprobs_backward(const void* logits, int dtype, int64_t row_st
   return cuda_status(launch_token_logprobs_backward(a, (cudaStream_t)stream));
 }
 
+size_t dspark_head_workspace_size(int B, int gamma, int V) {
+  if (B <= 0 || gamma <= 0 || V <= 0 || B > 65535 || gamma > kMaxGamma) return 0;
+  return head_workspace_bytes(B * gamma, V);
+}
+
+int dspark_markov_logits(const float* U, const void* W1, const void* W2, int wdtype, const int32_t* anchor,
+                         const int32_t* x, int B, int gamma, int V, int r, void* l_out, int ldtype, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  DSPARK_TRY(check_shapes(B, gamma, V, r));
+  DSPARK_TRY(check_dtype(wdtype));
+  DSPARK_TRY(check_dtype(ldtype));
+  if (!U || !W1 || !W2 || !anchor || !x || !l_out) return DSPARK_ERR_INVALID;
+  if (!aligned(U, 16) || !aligned(W1, 16) || !aligned(W2, 16) || !aligned(l_out, 16)) return DSPARK_ERR_INVALID;
+  if (!draft_tc_supported(wdtype, r, V)) return DSPARK_ERR_UNSUPPORTED;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < 256) return DSPARK_ERR_WORKSPACE;
+  MarkovLogitArgs a{U, W1, W2, anchor, x, B, gamma, V, l_out, ldtype, ws_ptr<int>(workspace, 0)};
+  return cuda_status(launch_markov_logits(a, (cudaStream_t)stream));
+}
+
+int dspark_markov_head_backward(const void* dlogits, const void* W1, const void* W2, int wdtype,
+                                const int32_t* anchor, const int32_t* x, int B, int gamma, int V, int r,
+                                float* dW1_out, float* dW2_out, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  DSPARK_TRY(check_shapes(B, gamma, V, r));
+  DSPARK_TRY(check_dtype(wdtype));
+  if (!dlogits || !W1 || !W2 || !anchor || !x || !dW1_out || !dW2_out) return DSPARK_ERR_INVALID;
+  if (!aligned(dlogits, 16) || !aligned(W1, 16) || !aligned(W2, 16) || !aligned(dW1_out, 16) || !aligned(dW2_out, 16))
+    return DSPARK_ERR_INVALID;
+  if (!draft_tc_supported(wdtype, r, V)) return DSPARK_ERR_UNSUPPORTED;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < head_workspace_bytes(B * gamma, V))
+    return DSPARK_ERR_WORKSPACE;
+  HeadBackwardArgs a{dlogits, W1, W2, anchor, x, B, gamma, V, dW1_out, dW2_out, workspace};
+  return cuda_status(launch_markov_head_backward(a, (cudaStream_t)stream));
+}
+
 int dspark_distill_loss(const void* logits, int dtype, int64_t row_stride, const int32_t* top_idx,
                         const float* top_val, const float* teacher_lse, const float* weight, const int32_t* lens,
                         int N, int R, int V, int K, float temperature, float* loss_out, float* stats_out,

@@ -1,0 +1,683 @@
+// The Markov head outside the sampling kernel, for training it ("[DeepSeek-6]
+// DSpark" blog, section 4): its logits for given tokens, and the gradients of
+// its two weights.  bf16 weights of rank 256, on the tensor cores.  Rows n =
+// b * G + k - 1 are the positions of all requests, E[n] = W1[x_{k-1}] (x_0 the
+// anchor), N = B * G of them:
+//
+//   markov_logits:  l = U + E W2^T                       [N, V]
+//   head backward:  dW2 = D^T E                          [V, 256]
+//                   dE = D W2,  dW1[t] = sum over n with x_{k-1} = t of dE[n]
+//
+// with D [N, V] bf16 the gradient of l.  All products are exact in fp32 and
+// summed in fp32 in tensor memory.  Both are bound by HBM when N is large: the
+// logits by one read of U and one write of l (W2 stays in L2), the gradients by
+// two reads of D.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "kernels.h"
+#include "tc_common.cuh"
+
+namespace dspark {
+namespace {
+
+using namespace tc;
+
+constexpr int HM = 128;            // rows of a tile (TMEM lanes)
+constexpr int HK = 256;            // Markov rank
+constexpr int kMaxSmem = 232448;   // dynamic shared memory one CTA may use
+
+// E[m, 64a .. 64a+63] = W1[tok] into this warp's TMEM lanes (zeros without a token).
+__device__ __forceinline__ void gather_e(const __nv_bfloat16* W1, int tok, int a, uint32_t taddr) {
+  const uint4* wrow = reinterpret_cast<const uint4*>(W1 + (size_t)max(tok, 0) * HK);
+  uint32_t ev[32];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint4 val = tok >= 0 ? __ldg(wrow + a * 8 + c) : make_uint4(0, 0, 0, 0);
+    ev[4 * c] = val.x; ev[4 * c + 1] = val.y; ev[4 * c + 2] = val.z; ev[4 * c + 3] = val.w;
+  }
+  tmem_store_32cols(taddr, ev);
+}
+
+// The token before row n's position; -1 (and DSPARK_ERR_INVALID recorded) when
+// it is outside [0, V).
+__device__ __forceinline__ int previous_token(const int32_t* anchor, const int32_t* x, long long n, int G, int V,
+                                              int* status) {
+  const long long b = n / G;
+  const int k = (int)(n - b * G);
+  const int t = k == 0 ? anchor[b] : x[n - 1];
+  if (t >= 0 && t < V) return t;
+  record_status(status, DSPARK_ERR_INVALID);
+  return -1;
+}
+
+// ---------------------------------------------------------------------------
+// Logits.  Persistent CTAs, each a contiguous range of tiles of 128 rows x 64
+// columns, row tile by row tile:
+//   warp 0     TMA producer: the W2 rows of a tile (evict_last: every row tile
+//              reads them again from L2) and its U box (256 contiguous bytes a row);
+//   warp 1     MMA issuer: E (tensor memory) times the W2 rows into one of two
+//              accumulators;
+//   warps 2-9  a thread owns a row and 32 columns: adds the accumulator to U in
+//              place and one of them stores the tile by TMA; at a row tile's end
+//              they gather the next E.
+// ---------------------------------------------------------------------------
+constexpr int GN = 64;             // columns of a tile
+constexpr int GUStages = 4, GWStages = 2;
+constexpr int GEpiWarps = 8;
+constexpr int GThreads = 64 + 32 * GEpiWarps;
+constexpr int GUBytes = HM * GN * 4;     // 32768
+constexpr int GWBytes = GN * HK * 2;     // 32768
+constexpr uint32_t GTmemCols = 256;      // two accumulators, then E
+constexpr uint32_t GTmemE = 2 * GN;
+constexpr int GSmemBytes = 1024 + GUStages * GUBytes + GWStages * GWBytes + 512;
+static_assert(GSmemBytes <= kMaxSmem, "shared memory");
+
+struct __align__(8) GBars {
+  uint64_t full_u[GUStages], empty_u[GUStages];
+  uint64_t full_w[GWStages], empty_w[GWStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t e_full, drain;
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(GBars) <= 512, "barrier block");
+
+struct LogitParams {
+  const __nv_bfloat16* W1;
+  const int32_t* anchor;
+  const int32_t* x;
+  int* status;
+  int N, G, V;
+  int ntiles;        // column tiles
+  int tail_tile;     // the column tile that comes and goes as [rows x 32] boxes (V % 32 != 0), else -1
+  long long units;
+};
+
+__device__ __forceinline__ void tma_s2g_2d(const CUtensorMap* map, const void* src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1)
+               : "memory");
+}
+__device__ __forceinline__ void tma_s2g_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+__device__ __forceinline__ void tma_s2g_4d(const CUtensorMap* map, const void* src, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// All bulk stores of this thread but the newest kLeft have read their shared memory.
+template <int kLeft>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
+}
+
+// kOut: DSPARK_F32 or DSPARK_BF16 logits.
+template <int kOut>
+__global__ void __launch_bounds__(GThreads, 1)
+markov_logits_tc(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap u_map,
+                 const __grid_constant__ CUtensorMap u4_map, const __grid_constant__ CUtensorMap o_map,
+                 const __grid_constant__ CUtensorMap o4_map, const LogitParams p) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  unsigned char* U_s = smem;
+  unsigned char* W_s = U_s + GUStages * GUBytes;
+  GBars* bars = reinterpret_cast<GBars*>(W_s + GWStages * GWBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long u0 = p.units * blockIdx.x / gridDim.x, u1 = p.units * (blockIdx.x + 1) / gridDim.x;
+  volatile int* abort = &bars->abort;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < GUStages; ++s) { mbar_init(&bars->full_u[s], 1); mbar_init(&bars->empty_u[s], 1); }
+    for (int s = 0; s < GWStages; ++s) { mbar_init(&bars->full_w[s], 1); mbar_init(&bars->empty_w[s], 1); }
+    for (int s = 0; s < 2; ++s) { mbar_init(&bars->acc_full[s], 1); mbar_init(&bars->acc_empty[s], GEpiWarps); }
+    mbar_init(&bars->e_full, GEpiWarps);
+    mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&w_map);
+    prefetch_tensormap(&u_map);
+    prefetch_tensormap(&u4_map);
+    prefetch_tensormap(&o_map);
+    prefetch_tensormap(&o4_map);
+  }
+  if (warp == 1) tmem_alloc(&bars->tmem_base, GTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      const uint64_t pol_w = policy_evict_last(), pol_u = policy_evict_first();
+      uint32_t i = 0;
+      bool ok = true;
+      for (long long u = u0; u < u1; ++u, ++i) {
+        const int m0 = (int)(u / p.ntiles) * HM, t = (int)(u % p.ntiles), v0 = t * GN;
+        const int sw = i % GWStages, su = i % GUStages;
+        ok = mbar_wait(&bars->empty_w[sw], ((i / GWStages) & 1) ^ 1, abort, p.status);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&bars->full_w[sw], GWBytes);
+        for (int a = 0; a < HK / 64; ++a)
+          tma_g2s_2d(W_s + sw * GWBytes + a * GN * 128, &w_map, a * 64, v0, &bars->full_w[sw], pol_w);
+        ok = mbar_wait(&bars->empty_u[su], ((i / GUStages) & 1) ^ 1, abort, p.status);
+        if (!ok) break;
+        unsigned char* dst = U_s + su * GUBytes;
+        mbar_arrive_expect_tx(&bars->full_u[su], GUBytes);
+        if (t != p.tail_tile) {
+          tma_g2s_4d(dst, &u4_map, 0, v0 / 32, 0, m0, &bars->full_u[su], pol_u);
+        } else {
+          tma_g2s_3d(dst, &u_map, v0, 0, m0, &bars->full_u[su], pol_u);
+          tma_g2s_3d(dst + HM * 128, &u_map, v0 + 32, 0, m0, &bars->full_u[su], pol_u);
+        }
+      }
+      if (*abort) {
+        // what was issued lands before the CTA leaves (a wait for a phase
+        // that is over returns at once)
+        for (int s = 0; s < GWStages; ++s) {
+          const uint32_t n = (i + GWStages - 1 - s) / GWStages + (i % GWStages == (uint32_t)s && !ok ? 1 : 0);
+          if (n > 0) mbar_drain(&bars->full_w[s], (n - 1) & 1);
+        }
+        for (int s = 0; s < GUStages; ++s) {
+          const uint32_t n = (i + GUStages - 1 - s) / GUStages;
+          if (n > 0) mbar_drain(&bars->full_u[s], (n - 1) & 1);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(HM, GN);
+      uint32_t i = 0, em = 0;
+      int m = -1;
+      bool ok = true;
+      for (long long u = u0; u < u1 && ok; ++u, ++i) {
+        if ((int)(u / p.ntiles) != m) {
+          m = (int)(u / p.ntiles);
+          if (!(ok = mbar_wait(&bars->e_full, em++ & 1, abort, p.status))) break;
+        }
+        const int acc = i & 1, sw = i % GWStages;
+        if (!(ok = mbar_wait(&bars->acc_empty[acc], ((i >> 1) & 1) ^ 1, abort, p.status))) break;
+        if (!(ok = mbar_wait(&bars->full_w[sw], (i / GWStages) & 1, abort, p.status))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int a = 0; a < HK / 64; ++a) {
+          const uint64_t bd = sw128_kmajor_desc(smem_u32(W_s + sw * GWBytes + a * GN * 128));
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16_tmem_a(tmem + acc * GN, tmem + GTmemE + a * 32 + kk * 8, bd + (uint64_t)(kk * 2), idesc,
+                             (a | kk) != 0);
+        }
+        umma_commit(&bars->empty_w[sw]);
+        umma_commit(&bars->acc_full[acc]);
+      }
+      umma_commit(&bars->drain);
+      mbar_drain(&bars->drain, 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3, h = (warp - 2) >> 2;
+    const int r = q * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+    uint32_t i = 0;
+    int m = -1;
+    bool ok = true;
+    // (a warp whose wait gave up goes on through the tiles' barriers, which the
+    // others may be at, and does nothing else)
+    for (long long u = u0; u < u1; ++u, ++i) {
+      const int t = (int)(u % p.ntiles);
+      const int acc = i & 1, su = i % GUStages;
+      unsigned char* tile = U_s + su * GUBytes;
+      const int line = t != p.tail_tile ? 2 * r + h : h * HM + r;
+      float v[32];
+      if (ok && (int)(u / p.ntiles) != m) {
+        // (this warp has seen the last accumulator of the row tile before
+        // complete, so no MMA reads the old E)
+        m = (int)(u / p.ntiles);
+        const long long n = (long long)m * HM + r;
+        const int tok = n < p.N ? previous_token(p.anchor, p.x, n, p.G, p.V, p.status) : -1;
+        gather_e(p.W1, tok, 2 * h, lanes + GTmemE + 2 * h * 32);
+        gather_e(p.W1, tok, 2 * h + 1, lanes + GTmemE + (2 * h + 1) * 32);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->e_full);
+      }
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->acc_full[acc], (i >> 1) & 1, abort, p.status));
+      if (ok) {
+        tc_fence_after();
+        tmem_load_cols<32>(lanes + acc * GN + h * 32, v);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->acc_empty[acc]);
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->full_u[su], (i / GUStages) & 1, abort, p.status));
+      }
+      if (ok) {
+        // this thread's 32 columns of U: the 128-byte line 2r + h of a tile box
+        // (h * 128 + r of a tail tile's two boxes), its 16-byte chunk j at j ^ (line & 7)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float4* c = reinterpret_cast<float4*>(tile + line * 128 + ((j ^ (line & 7)) << 4));
+          float4 f = *c;
+          f.x += v[4 * j]; f.y += v[4 * j + 1]; f.z += v[4 * j + 2]; f.w += v[4 * j + 3];
+          if (kOut == DSPARK_F32) *c = f;
+          else { v[4 * j] = f.x; v[4 * j + 1] = f.y; v[4 * j + 2] = f.z; v[4 * j + 3] = f.w; }
+        }
+      }
+      if (kOut == DSPARK_BF16) {
+        // the tile's first half becomes [128 rows][64 columns] bf16, once
+        // every thread has read its U
+        named_bar_sync(1, GEpiWarps * 32);
+        if (ok) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            __nv_bfloat162 o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = __floats2bfloat162_rn(v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
+            *reinterpret_cast<uint4*>(tile + r * 128 + (((4 * h + j) ^ (r & 7)) << 4)) = *reinterpret_cast<uint4*>(o);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      named_bar_sync(1, GEpiWarps * 32);
+      if (ok && warp == 2 && lane == 0) {
+        const int v0 = t * GN, m0 = m * HM;
+        if (kOut == DSPARK_BF16) {
+          tma_s2g_2d(&o_map, tile, v0, m0);
+        } else if (t != p.tail_tile) {
+          tma_s2g_4d(&o4_map, tile, 0, v0 / 32, 0, m0);
+        } else {
+          tma_s2g_3d(&o_map, tile, v0, 0, m0);
+          if (v0 + 32 < p.V) tma_s2g_3d(&o_map, tile + HM * 128, v0 + 32, 0, m0);
+        }
+        bulk_commit();
+        // the tile before is out of its stage
+        bulk_wait_read<1>();
+        if (i > 0) mbar_arrive(&bars->empty_u[(i - 1) % GUStages]);
+      }
+    }
+    if (warp == 2 && lane == 0) bulk_wait_read<0>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, GTmemCols);
+}
+
+// ---------------------------------------------------------------------------
+// Weight gradients.  One kernel for both products, each an accumulation over K
+// in stages of 64 into kHalves accumulators of 128 x 256:
+//   kW2:  dW2 tile [128 kHalves v, 256] over K = rows n:  A = D^T (the stage
+//         holds [64 n][64 v] boxes, M-major), B = E [64 n][256] (N-major)
+//   else: part of dE [128 kHalves n, 256] over a range of K = v:  A = D ([128 n]
+//         [64 v] boxes, K-major), B = W2 [64 v][256] (N-major)
+// ---------------------------------------------------------------------------
+constexpr int BThreads = 64 + 128;
+
+template <int kHalves>
+struct BShape {
+  static constexpr int kABytes = kHalves * HM * 64 * 2;
+  static constexpr int kBBytes = HK * 64 * 2;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = kHalves == 2 ? 3 : 4;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + 256;
+  static_assert(kSmem <= kMaxSmem, "shared memory");
+};
+
+struct __align__(8) BBars {
+  uint64_t full[4], empty[4];
+  uint64_t acc_full, acc_empty, drain;
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(BBars) <= 256, "barrier block");
+
+struct GradParams {
+  float* out;        // kW2: dW2 [V][256]; else partials [splits][rows][256]
+  int* status;
+  int rows;          // kW2: V; else the rows of this chunk of D
+  int row0;          // else: the chunk's first row of D
+  int ksteps;        // 64-wide steps of K
+  int tiles;         // kW2: tiles of 128 kHalves v; else row groups
+  int splits;        // else: parts of K (tiles * splits CTAs)
+};
+
+// A matrix in 128-byte swizzled boxes of [K rows][64 of M or N]: 8 rows of K
+// make a 1024-byte group, boxes of 64 are `box_bytes` apart.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t box_bytes) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(box_bytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+constexpr uint32_t kAMajorM = 1u << 15, kBMajorN = 1u << 16;   // instruction descriptor: not K-major
+
+template <bool kW2, int kHalves>
+__global__ void __launch_bounds__(BThreads, 1)
+head_grad_tc(const __grid_constant__ CUtensorMap d_map, const __grid_constant__ CUtensorMap b_map, const GradParams p) {
+  using S = BShape<kHalves>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  BBars* bars = reinterpret_cast<BBars*>(smem + S::kStages * S::kStageBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort = &bars->abort;
+  constexpr uint32_t kCols = kHalves * 256;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) { mbar_init(&bars->full[s], 1); mbar_init(&bars->empty[s], 1); }
+    mbar_init(&bars->acc_full, 1);
+    mbar_init(&bars->acc_empty, 4);
+    mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&d_map);
+    prefetch_tensormap(&b_map);
+  }
+  if (warp == 1) tmem_alloc(&bars->tmem_base, kCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  // this CTA's tiles and, of each, its steps of K
+  const int tile0 = kW2 ? blockIdx.x : blockIdx.x / p.splits;
+  const int tile_step = kW2 ? gridDim.x : p.tiles;
+  const int split = kW2 ? 0 : blockIdx.x % p.splits;
+  const int k0 = kW2 ? 0 : (int)((long long)p.ksteps * split / p.splits);
+  const int k1 = kW2 ? p.ksteps : (int)((long long)p.ksteps * (split + 1) / p.splits);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol_d = policy_evict_first(), pol_b = policy_evict_last();
+      uint32_t i = 0;
+      bool ok = true;
+      for (int tile = tile0; tile < p.tiles && ok; tile += tile_step) {
+        for (int k = k0; k < k1; ++k, ++i) {
+          const int s = i % S::kStages;
+          ok = mbar_wait(&bars->empty[s], ((i / S::kStages) & 1) ^ 1, abort, p.status);
+          if (!ok) break;
+          unsigned char* a = smem + s * S::kStageBytes;
+          unsigned char* b = a + S::kABytes;
+          mbar_arrive_expect_tx(&bars->full[s], S::kStageBytes);
+          if (kW2) {
+            for (int j = 0; j < 2 * kHalves; ++j)
+              tma_g2s_2d(a + j * 8192, &d_map, tile * HM * kHalves + j * 64, k * 64, &bars->full[s], pol_d);
+          } else {
+            for (int j = 0; j < kHalves; ++j)
+              tma_g2s_2d(a + j * 16384, &d_map, k * 64, p.row0 + (tile * kHalves + j) * HM, &bars->full[s], pol_d);
+          }
+          for (int j = 0; j < HK / 64; ++j) tma_g2s_2d(b + j * 8192, &b_map, j * 64, k * 64, &bars->full[s], pol_b);
+        }
+      }
+      if (*abort) {
+        for (int s = 0; s < S::kStages; ++s) {
+          const uint32_t n = (i + S::kStages - 1 - s) / S::kStages;
+          if (n > 0) mbar_drain(&bars->full[s], (n - 1) & 1);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(HM, HK) | kBMajorN | (kW2 ? kAMajorM : 0u);
+      uint32_t i = 0, done = 0;
+      bool ok = true;
+      for (int tile = tile0; tile < p.tiles && ok; tile += tile_step, ++done) {
+        if (!(ok = mbar_wait(&bars->acc_empty, (done & 1) ^ 1, abort, p.status))) break;
+        tc_fence_after();
+        for (int k = k0; k < k1; ++k, ++i) {
+          const int s = i % S::kStages;
+          if (!(ok = mbar_wait(&bars->full[s], (i / S::kStages) & 1, abort, p.status))) break;
+          tc_fence_after();
+          const uint32_t a = smem_u32(smem + s * S::kStageBytes);
+          const uint64_t bd = sw128_mnmajor_desc(a + S::kABytes, 8192);
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) {
+            const uint64_t ad = kW2 ? sw128_mnmajor_desc(a + h * 16384, 8192) : sw128_kmajor_desc(a + h * 16384);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)   // 16 of K: two 1024-byte groups, or 32 bytes of a K-major row
+              umma_bf16(tmem + h * 256, ad + (uint64_t)(kk * (kW2 ? 128 : 2)), bd + (uint64_t)(kk * 128), idesc,
+                        k != k0 || kk != 0);
+          }
+          umma_commit(&bars->empty[s]);
+        }
+        if (ok) umma_commit(&bars->acc_full);
+      }
+      umma_commit(&bars->drain);
+      mbar_drain(&bars->drain, 0);
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3;
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+    uint32_t done = 0;
+    for (int tile = tile0; tile < p.tiles; tile += tile_step, ++done) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->acc_full, done & 1, abort, p.status))) break;
+      tc_fence_after();
+      for (int h = 0; h < kHalves; ++h) {
+        const int row = (tile * kHalves + h) * HM + q * 32 + lane;
+        float4* o = reinterpret_cast<float4*>(p.out + ((size_t)split * (kW2 ? 0 : p.rows) + row) * HK);
+        for (int c = 0; c < HK / 32; ++c) {
+          float v[32];
+          tmem_load_cols<32>(lanes + h * 256 + c * 32, v);
+          if (row < p.rows) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              o[c * 8 + j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->acc_empty);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kCols);
+}
+
+// E [N][256] and the previous tokens [N] (-1: none), a warp per row.
+__global__ void __launch_bounds__(256) gather_rows(const __nv_bfloat16* __restrict__ W1, const int32_t* __restrict__ anchor,
+                                                   const int32_t* __restrict__ x, int N, int G, int V,
+                                                   uint4* __restrict__ E, int32_t* __restrict__ prev, int* status) {
+  const int n = (int)((blockIdx.x * (long long)blockDim.x + threadIdx.x) >> 5), lane = threadIdx.x & 31;
+  if (n >= N) return;
+  const int tok = previous_token(anchor, x, n, G, V, status);
+  E[(size_t)n * 32 + lane] =
+      tok >= 0 ? __ldg(reinterpret_cast<const uint4*>(W1 + (size_t)tok * HK) + lane) : make_uint4(0, 0, 0, 0);
+  if (lane == 0) prev[n] = tok;
+}
+
+// dW1 of a chunk of rows: the block of a token's first row in the chunk adds
+// the K parts of every row of that token, in order of the rows, to dW1[token].
+__global__ void __launch_bounds__(HK) scatter_rows(const float* __restrict__ part, const int32_t* __restrict__ prev,
+                                                   int rows, int splits, float* __restrict__ dW1) {
+  const int n = blockIdx.x, tok = prev[n];
+  if (tok < 0) return;
+  __shared__ int later[HK];
+  bool earlier = false;
+  for (int j = threadIdx.x; j < n; j += HK) earlier = earlier || prev[j] == tok;
+  if (__syncthreads_or(earlier)) return;
+  float acc = 0.f;
+  for (int j0 = n; j0 < rows; j0 += HK) {
+    const int j = j0 + threadIdx.x;
+    const bool same = j < rows && prev[j] == tok;
+    if (!__syncthreads_or(same)) continue;
+    later[threadIdx.x] = same;
+    __syncthreads();
+    for (int i = 0; i < HK && j0 + i < rows; ++i) {
+      if (!later[i]) continue;
+#pragma unroll 8
+      for (int s = 0; s < splits; ++s) acc += part[((size_t)s * rows + j0 + i) * HK + threadIdx.x];
+    }
+    __syncthreads();
+  }
+  dW1[(size_t)tok * HK + threadIdx.x] += acc;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// A [rows, cols] bf16 matrix in boxes of `box_rows` x 64, 128-byte swizzled.
+cudaError_t make_bf16_map(const void* base, int rows, int cols, int box_rows, CUtensorMap* map) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  return sms;
+}
+
+template <bool kW2, int kHalves>
+cudaError_t launch_grad(int grid, const CUtensorMap& d, const CUtensorMap& b, const GradParams& p, cudaStream_t stream) {
+  auto kern = head_grad_tc<kW2, kHalves>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, BShape<kHalves>::kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, BThreads, BShape<kHalves>::kSmem, stream>>>(d, b, p);
+  return cudaGetLastError();
+}
+
+// Rows of D whose dE parts the workspace holds at a time, and parts of K for
+// them: one CTA an SM.
+constexpr int kChunkRows = 4096;
+constexpr int kMaxCtas = 160;
+struct GradPlan {
+  int halves, groups, splits;
+};
+GradPlan plan_chunk(int rows, int V, int sms) {
+  GradPlan g;
+  g.halves = rows > HM ? 2 : 1;
+  g.groups = div_up(rows, g.halves * HM);
+  g.splits = std::max(1, std::min(std::min(sms, kMaxCtas) / g.groups, div_up(V, 64)));
+  return g;
+}
+
+}  // namespace
+
+// Workspace: status word, previous tokens, E, the dE parts of a chunk.
+size_t head_workspace_bytes(int N, int V) {
+  // rows * splits of a chunk (plan_chunk): at most 256 rows for each CTA, and
+  // at most kMaxCtas or V / 64 parts of the rows there are
+  const size_t splits = std::min(kMaxCtas, div_up(V, 64));
+  const size_t parts = std::min<size_t>((size_t)kMaxCtas * 2 * HM, splits * std::min(N, kChunkRows));
+  return 256 + align256(4ull * N) + align256(512ull * N) + align256(1024ull * parts);
+}
+
+cudaError_t launch_markov_logits(const MarkovLogitArgs& a, cudaStream_t stream) {
+  const int N = a.B * a.G;
+  CUtensorMap w, u, u4, o, o4;
+  cudaError_t e;
+  if ((e = make_w2_tensor_map(a.W2, a.V, &w, GN)) != cudaSuccess) return e;
+  if ((e = make_u_tensor_map(a.U, N, 1, a.V, HM, &u)) != cudaSuccess) return e;
+  if ((e = make_u_tile_map(a.U, N, 1, a.V, HM, &u4)) != cudaSuccess) return e;
+  if (a.odtype == DSPARK_F32) {
+    if ((e = make_u_tensor_map(static_cast<const float*>(a.out), N, 1, a.V, HM, &o)) != cudaSuccess) return e;
+    if ((e = make_u_tile_map(static_cast<const float*>(a.out), N, 1, a.V, HM, &o4)) != cudaSuccess) return e;
+  } else {
+    if ((e = make_bf16_map(a.out, N, a.V, HM, &o)) != cudaSuccess) return e;
+    o4 = o;
+  }
+  LogitParams p{};
+  p.W1 = static_cast<const __nv_bfloat16*>(a.W1);
+  p.anchor = a.anchor;
+  p.x = a.x;
+  p.status = a.status;
+  p.N = N; p.G = a.G; p.V = a.V;
+  p.ntiles = div_up(a.V, GN);
+  p.tail_tile = a.V % 32 != 0 ? p.ntiles - 1 : -1;
+  p.units = (long long)div_up(N, HM) * p.ntiles;
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorUnknown;
+  const int grid = (int)std::min<long long>(p.units, sms);
+  auto kern = a.odtype == DSPARK_F32 ? markov_logits_tc<DSPARK_F32> : markov_logits_tc<DSPARK_BF16>;
+  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GSmemBytes)) != cudaSuccess) return e;
+  kern<<<grid, GThreads, GSmemBytes, stream>>>(w, u, u4, o, o4, p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_markov_head_backward(const HeadBackwardArgs& a, cudaStream_t stream) {
+  const int N = a.B * a.G;
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorUnknown;
+  char* ws = static_cast<char*>(a.ws);
+  int* status = reinterpret_cast<int*>(ws);
+  int32_t* prev = reinterpret_cast<int32_t*>(ws + 256);
+  char* E = ws + 256 + align256(4ull * N);
+  float* part = reinterpret_cast<float*>(E + align256(512ull * N));
+  cudaError_t e;
+  if ((e = cudaMemsetAsync(status, 0, sizeof(int), stream)) != cudaSuccess) return e;
+  if ((e = cudaMemsetAsync(a.dW1, 0, sizeof(float) * HK * (size_t)a.V, stream)) != cudaSuccess) return e;
+  gather_rows<<<(unsigned)div_up(N, 8), 256, 0, stream>>>(static_cast<const __nv_bfloat16*>(a.W1), a.anchor, a.x, N,
+                                                         a.G, a.V, reinterpret_cast<uint4*>(E), prev, status);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+
+  // dW2: one tile of 256 (or, while those leave SMs idle, 128) v per CTA at a time
+  CUtensorMap dm, bm;
+  if ((e = make_bf16_map(a.dlogits, N, a.V, 64, &dm)) != cudaSuccess) return e;
+  if ((e = make_bf16_map(E, N, HK, 64, &bm)) != cudaSuccess) return e;
+  GradParams p{};
+  p.out = a.dW2;
+  p.status = status;
+  p.rows = a.V;
+  p.ksteps = div_up(N, 64);
+  const int halves = div_up(a.V, 2 * HM) >= sms ? 2 : 1;
+  p.tiles = div_up(a.V, halves * HM);
+  p.splits = 1;
+  const int grid = std::min(p.tiles, sms);
+  e = halves == 2 ? launch_grad<true, 2>(grid, dm, bm, p, stream) : launch_grad<true, 1>(grid, dm, bm, p, stream);
+  if (e != cudaSuccess) return e;
+
+  // dE and dW1, a chunk of rows at a time
+  if ((e = make_bf16_map(a.dlogits, N, a.V, HM, &dm)) != cudaSuccess) return e;
+  if ((e = make_bf16_map(a.W2, a.V, HK, 64, &bm)) != cudaSuccess) return e;
+  for (int r0 = 0; r0 < N; r0 += kChunkRows) {
+    const int rows = std::min(N - r0, kChunkRows);
+    const GradPlan g = plan_chunk(rows, a.V, sms);
+    p.out = part;
+    p.rows = rows;
+    p.row0 = r0;
+    p.ksteps = div_up(a.V, 64);
+    p.tiles = g.groups;
+    p.splits = g.splits;
+    e = g.halves == 2 ? launch_grad<false, 2>(g.groups * g.splits, dm, bm, p, stream)
+                      : launch_grad<false, 1>(g.groups * g.splits, dm, bm, p, stream);
+    if (e != cudaSuccess) return e;
+    scatter_rows<<<rows, HK, 0, stream>>>(part, prev + r0, rows, g.splits, a.dW1);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace dspark

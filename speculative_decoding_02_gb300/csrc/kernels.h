@@ -247,6 +247,34 @@ struct LogprobBackwardArgs {
 };
 cudaError_t launch_token_logprobs_backward(const LogprobBackwardArgs& a, cudaStream_t stream);
 
+// The Markov head's logits and weight gradients (draft_tc_supported weights).
+struct MarkovLogitArgs {
+  const float* U;          // [B][G][V]
+  const void* W1;
+  const void* W2;
+  const int32_t* anchor;
+  const int32_t* x;        // [B][G]
+  int B, G, V;
+  void* out;               // [B][G][V]
+  int odtype;
+  int* status;
+};
+cudaError_t launch_markov_logits(const MarkovLogitArgs& a, cudaStream_t stream);
+
+struct HeadBackwardArgs {
+  const void* dlogits;     // [B][G][V] bf16
+  const void* W1;
+  const void* W2;
+  const int32_t* anchor;
+  const int32_t* x;
+  int B, G, V;
+  float* dW1;              // [V][256]
+  float* dW2;
+  void* ws;                // head_workspace_bytes(B * G, V)
+};
+size_t head_workspace_bytes(int N, int V);
+cudaError_t launch_markov_head_backward(const HeadBackwardArgs& a, cudaStream_t stream);
+
 struct DistillArgs {
   const void* logits;
   int dtype;
