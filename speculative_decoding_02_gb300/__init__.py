@@ -14,7 +14,6 @@ forms):
   token_logprobs_backward, distill_loss, distill_loss_backward,
   markov_logits, markov_head_backward
 """
-import contextlib
 import ctypes
 import math
 import os
@@ -109,10 +108,13 @@ def _load():
     L.dspark_markov_logits.restype = i32
     L.dspark_markov_head_backward.argtypes = [vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp, sz, vp]
     L.dspark_markov_head_backward.restype = i32
-    L.dspark_distill_loss.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, vp, vp, vp, i32, vp]
+    L.dspark_distill_loss.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, vp, vp, vp, i32,
+                                      vp, sz, vp]
+    L.dspark_distill_workspace_size.argtypes = [i32, i32, i32]
+    L.dspark_distill_workspace_size.restype = sz
     L.dspark_distill_loss.restype = i32
     L.dspark_distill_loss_backward.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, vp,
-                                               i32, vp]
+                                               i32, vp, sz, vp]
     L.dspark_distill_loss_backward.restype = i32
     L.dspark_read_status.argtypes = [vp, ctypes.POINTER(i32), vp]
     L.dspark_read_status.restype = i32
@@ -389,9 +391,27 @@ def sts_fit(z, ell, acc, grid):
 _ROW_DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 
-def _on(dev):
-    """The context that makes dev the current device (the library launches on it)."""
-    return torch.cuda.device(dev) if torch.cuda.current_device() != dev.index else contextlib.nullcontext()
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(fn, where, dev, *args):
+    """fn(*args, stream) on the current stream of dev, with dev current (the
+    library launches on the current device).  These calls take ten
+    microseconds on the GPU for a few rows, so the host's share is kept small:
+    plain addresses, and the stream's handle without a stream object."""
+    if torch.cuda.current_device() == dev.index:
+        code = fn(*args, _stream_handle(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, _stream_handle(dev.index))
+    if code != OK:
+        raise DSparkError(code, where)
+
+
+# (a private name of torch, with the public way where a version lacks it)
+_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _row_args(logits, rows, what="logits"):
@@ -467,9 +487,8 @@ def token_logprobs(logits, tokens, top_k=0, rows=None):
     dev, lead, N, R, V, stride, dt = _row_args(logits, rows)
     _row_vector(_need(tokens, "tokens"), "tokens", lead, dev, torch.int32)
     out = _logprob_outputs(lead, _top_k(top_k, V), dev)
-    with _on(dev):
-        _check(L.dspark_token_logprobs(_ptr(logits), dt, stride, _ptr(tokens), _ptr(rows), N, R, V, top_k,
-                                       *map(_ptr, out), _stream(dev)), "token_logprobs")
+    _launch(L.dspark_token_logprobs, "token_logprobs", dev, logits.data_ptr(), dt, stride, tokens.data_ptr(),
+            _address(rows), N, R, V, top_k, *map(_address, out))
     return out
 
 
@@ -491,9 +510,8 @@ def emitted_logprobs(T, x, n, tok, top_k=0):
     for t, name, shape in [(x, "x", (B, G)), (n, "n", (B,)), (tok, "tok", (B,))]:
         _row_vector(_need(t, name), name, shape, dev, torch.int32)
     out = _logprob_outputs(lead, _top_k(top_k, V), dev)
-    with _on(dev):
-        _check(L.dspark_emitted_logprobs(_ptr(T), dt, _ptr(x), _ptr(n), _ptr(tok), B, G, V, top_k, *map(_ptr, out),
-                                         _stream(dev)), "emitted_logprobs")
+    _launch(L.dspark_emitted_logprobs, "emitted_logprobs", dev, T.data_ptr(), dt, x.data_ptr(), n.data_ptr(),
+            tok.data_ptr(), B, G, V, top_k, *map(_address, out))
     return out
 
 
@@ -511,10 +529,9 @@ def token_logprobs_backward(logits, tokens, lse, entropy=None, g_logp=None, g_en
     for t, name in [(entropy, "entropy"), (g_logp, "g_logp"), (g_entropy, "g_entropy")]:
         _row_vector(t, name, lead, dev)
     out = _gradient_out(out, logits, logits.dtype)
-    with _on(dev):
-        _check(L.dspark_token_logprobs_backward(_ptr(logits), dt, stride, _ptr(tokens), _ptr(lse), _ptr(entropy),
-                                                _ptr(g_logp), _ptr(g_entropy), _ptr(rows), N, R, V, _ptr(out),
-                                                _stream(dev)), "token_logprobs_backward")
+    _launch(L.dspark_token_logprobs_backward, "token_logprobs_backward", dev, logits.data_ptr(), dt, stride,
+            tokens.data_ptr(), lse.data_ptr(), _address(entropy), _address(g_logp), _address(g_entropy),
+            _address(rows), N, R, V, out.data_ptr())
     return out
 
 
@@ -531,8 +548,14 @@ def _distill_args(logits, top_idx, top_val, teacher_lse, rows, temperature):
     return dev, lead, N, R, V, stride, dt, K
 
 
+def distill_workspace(N, V, K, device):
+    """A workspace of distill_loss and distill_loss_backward for N rows."""
+    n = int(_load().dspark_distill_workspace_size(N, V, K))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
 def distill_loss(logits, top_idx, top_val, temperature=1.0, teacher_lse=None, weight=None, rows=None, grad=False,
-                 grad_dtype=None, out=None):
+                 grad_dtype=None, out=None, ws=None):
     """Kullback-Leibler loss of a student's logits [..., V] against a teacher's K
     kept logits top_val [..., K] f32 at top_idx [..., K] i32 (-1: absent; K <= 128):
     loss [...] f32, stats [..., 2] f32 (for distill_loss_backward) and, with
@@ -542,7 +565,9 @@ def distill_loss(logits, top_idx, top_val, temperature=1.0, teacher_lse=None, we
     top_val / temperature: the teacher's remaining mass is matched, as one
     bucket, with the student's; None: the kept entries are renormalised.
     weight [...] f32 (None: 1) scales the gradient, not the loss.
-    rows as in token_logprobs; out as in token_logprobs_backward."""
+    rows as in token_logprobs; out as in token_logprobs_backward.  ws (with
+    grad): a distill_workspace to keep; by default one is allocated for the
+    call."""
     L = _load()
     dev, lead, N, R, V, stride, dt, K = _distill_args(logits, top_idx, top_val, teacher_lse, rows, temperature)
     _row_vector(weight, "weight", lead, dev)
@@ -552,17 +577,19 @@ def distill_loss(logits, top_idx, top_val, temperature=1.0, teacher_lse=None, we
     if gdt not in _ROW_DTYPES:
         raise TypeError(f"grad_dtype must be float32, bfloat16 or float16, got {gdt}")
     dlogits = _gradient_out(out, logits, gdt) if grad else None
+    if grad and ws is None:
+        ws = distill_workspace(N, V, K, dev)
     loss = torch.empty(lead, dtype=torch.float32, device=dev)
     stats = torch.empty((*lead, 2), dtype=torch.float32, device=dev)
-    with _on(dev):
-        _check(L.dspark_distill_loss(_ptr(logits), dt, stride, _ptr(top_idx), _ptr(top_val), _ptr(teacher_lse),
-                                     _ptr(weight), _ptr(rows), N, R, V, K, temperature, _ptr(loss), _ptr(stats),
-                                     _ptr(dlogits), _ROW_DTYPES[gdt], _stream(dev)), "distill_loss")
+    _launch(L.dspark_distill_loss, "distill_loss", dev, logits.data_ptr(), dt, stride, top_idx.data_ptr(),
+            top_val.data_ptr(), _address(teacher_lse), _address(weight), _address(rows), N, R, V, K, temperature,
+            loss.data_ptr(), stats.data_ptr(), _address(dlogits), _ROW_DTYPES[gdt], _address(ws),
+            0 if ws is None else ws.numel())
     return loss, stats, dlogits
 
 
 def distill_loss_backward(logits, top_idx, top_val, stats, g, temperature=1.0, teacher_lse=None, rows=None,
-                          grad_dtype=None, out=None):
+                          grad_dtype=None, out=None, ws=None):
     """g * d loss / d logits of distill_loss from its stats and an upstream
     gradient g [...] f32; the other arguments as for that call."""
     L = _load()
@@ -573,10 +600,10 @@ def distill_loss_backward(logits, top_idx, top_val, stats, g, temperature=1.0, t
     if gdt not in _ROW_DTYPES:
         raise TypeError(f"grad_dtype must be float32, bfloat16 or float16, got {gdt}")
     out = _gradient_out(out, logits, gdt)
-    with _on(dev):
-        _check(L.dspark_distill_loss_backward(_ptr(logits), dt, stride, _ptr(top_idx), _ptr(top_val), _ptr(stats),
-                                              _ptr(g), _ptr(teacher_lse), _ptr(rows), N, R, V, K, temperature,
-                                              _ptr(out), _ROW_DTYPES[gdt], _stream(dev)), "distill_loss_backward")
+    ws = distill_workspace(N, V, K, dev) if ws is None else ws
+    _launch(L.dspark_distill_loss_backward, "distill_loss_backward", dev, logits.data_ptr(), dt, stride,
+            top_idx.data_ptr(), top_val.data_ptr(), stats.data_ptr(), g.data_ptr(), _address(teacher_lse),
+            _address(rows), N, R, V, K, temperature, out.data_ptr(), _ROW_DTYPES[gdt], ws.data_ptr(), ws.numel())
     return out
 
 
@@ -604,10 +631,8 @@ def markov_logits(U, W1, W2, anchor, x, dtype=torch.float32, ws=None, out=None):
         raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
     out = _gradient_out(out, U, dtype)
     ws = workspace(B, G, V, dev) if ws is None else ws
-    with _on(dev):
-        _check(L.dspark_markov_logits(_ptr(U), _ptr(W1), _ptr(W2), _dt(W1, "W1"), _ptr(anchor), _ptr(x), B, G, V, r,
-                                      _ptr(out), _ROW_DTYPES[dtype], _ptr(ws), ws.numel(), _stream(dev)),
-               "markov_logits")
+    _launch(L.dspark_markov_logits, "markov_logits", dev, U.data_ptr(), W1.data_ptr(), W2.data_ptr(), _dt(W1, "W1"),
+            anchor.data_ptr(), x.data_ptr(), B, G, V, r, out.data_ptr(), _ROW_DTYPES[dtype], ws.data_ptr(), ws.numel())
     return out
 
 
@@ -626,10 +651,9 @@ def markov_head_backward(dlogits, W1, W2, anchor, x, ws=None):
     dW1 = torch.empty((V, r), dtype=torch.float32, device=dev)
     dW2 = torch.empty((V, r), dtype=torch.float32, device=dev)
     ws = head_workspace(B, G, V, dev) if ws is None else ws
-    with _on(dev):
-        _check(L.dspark_markov_head_backward(_ptr(dlogits), _ptr(W1), _ptr(W2), _dt(W1, "W1"), _ptr(anchor), _ptr(x),
-                                             B, G, V, r, _ptr(dW1), _ptr(dW2), _ptr(ws), ws.numel(), _stream(dev)),
-               "markov_head_backward")
+    _launch(L.dspark_markov_head_backward, "markov_head_backward", dev, dlogits.data_ptr(), W1.data_ptr(),
+            W2.data_ptr(), _dt(W1, "W1"), anchor.data_ptr(), x.data_ptr(), B, G, V, r, dW1.data_ptr(), dW2.data_ptr(),
+            ws.data_ptr(), ws.numel())
     return dW1, dW2
 
 

@@ -8,18 +8,18 @@
 //     bucket, matched with the student's mass q_r outside the kept entries:
 //     L = (the sum above) + p_r (log p_r - log q_r),
 //     dL/dS_v = (q_v - p(v)) / tau on a kept entry,
-//               q_v (1 - p_r / q_r) / tau elsewhere
-//   where p(v) is the sum of p_k over the k with i_k = v.
+//               q_v (1 - p_r / q_r) / tau = r_v (q_r - p_r) / tau elsewhere
+//   where p(v) is the sum of p_k over the k with i_k = v and r = q / q_r.
 //
 // q_r is not taken as 1 - sum q (which loses it when the kept entries hold
-// almost everything): the pass sums the entries outside the kept ones, which a
-// bitmap of the row in shared memory marks and a flag per block makes cheap,
-// and adds the kept entries' exponentials afterwards.
+// almost everything): the kept entries, which a bitmap of the segment in shared
+// memory marks, leave the row's sum, and their exponentials are added afterwards.
 //
-// A cluster of CTAs takes a row (logits_row.cuh).  The loss needs one pass; its
-// gradient a second one over the same row, which then comes from L2 when the
-// rows in flight fit there, so that HBM sees one read and one write.  The
-// gradient of the kept entries is stored after the others', behind a barrier.
+// Two kernels, each bound by HBM.  The first sums a row by a cluster of 1 to 16
+// CTAs (logits_row.cuh), whose CTA 0 finishes the row: its loss and, into the
+// workspace, the coefficients of its gradient and the gradients of its kept
+// entries.  The second streams the gradient; it starts while the first one
+// ends (programmatic dependent launch), with its first loads under way.
 #include <algorithm>
 
 #include "logits_row.cuh"
@@ -29,274 +29,326 @@ namespace {
 
 using namespace lrow;
 
+constexpr int kMarkedPlaces = 262144;   // of a CTA's part of a row: a bitmap of 32 KB
+
+// What the first kernel leaves for the second.
+struct WsView {
+  float4* coef;      // [N] ref, cw, whether the row has a gradient
+  int* kept_at;      // [N][K] entry whose gradient is kept_g (-1: none)
+  float* kept_g;
+  size_t total;
+};
+__host__ __device__ inline WsView ws_view(void* ws, int N, int K) {
+  WsView v;
+  v.coef = ws_ptr<float4>(ws, 0);
+  size_t off = align256(16ull * N);
+  v.kept_at = ws_ptr<int>(ws, off);       off = align256(off + 4ull * N * K);
+  v.kept_g = ws_ptr<float>(ws, off);      off = align256(off + 4ull * N * K);
+  v.total = off;
+  return v;
+}
+
+__device__ __forceinline__ bool scored(const DistillArgs& p, int row) {
+  if (p.lens == nullptr) return true;
+  const int g = row / p.R;
+  return row - g * p.R < p.lens[g];
+}
+
 struct Shared {
   Stat part[kWarps];
   Stat cta;               // of this CTA's part, outside the kept entries with a tail
-  float z[kMaxTop];       // the student's kept logits, unscaled
-  float p[kMaxTop];       // the teacher's probability of entry k
-  float psum[kMaxTop];    // p(i_k); -1 where entry k is absent or an earlier one has its index
-  int idx[kMaxTop];       // -1: absent
-  double logp[kMaxTop];   // log p_k
-  float p_rest;
-  int bad, any;           // an index outside [-1, V); an entry with mass
+  int idx[kMaxTop];       // the row's kept entries, -1: absent
+  float p[kMaxTop];       // the teacher's probability
+  float red[3][kWarps];
 };
 
-// The teacher's side of one row and the student's logits there, in shared
-// memory (each CTA of a cluster for itself).  Entries of the row outside the
-// places [lo, hi) are not read from the student.
-template <typename T, bool kTail>
-__device__ void load_teacher(Shared& sh, const DistillArgs& p, int row, const T* rp, int lo, int hi) {
-  const int tid = threadIdx.x;
-  if (tid == 0) sh.bad = 0;
-  __syncthreads();
-  if (tid < kMaxTop) {
-    int i = tid < p.K ? p.top_idx[(size_t)row * p.K + tid] : -1;
-    if (i < -1 || i >= p.V) {
-      sh.bad = 1;
-      i = -1;
-    }
-    sh.idx[tid] = i;
-    sh.z[tid] = i >= lo && i < hi ? Elem<T>::to_float(rp[i]) : 0.f;
-    sh.logp[tid] = i >= 0 ? (double)p.top_val[(size_t)row * p.K + tid] * (double)p.inv_tau : -INFINITY;
-  }
-  __syncthreads();
-  if (tid < 32) {
-    constexpr int PER = kMaxTop / 32;
-    double base;
-    if (kTail) {
-      base = (double)p.teacher_lse[row];
-    } else {
-      double m = -INFINITY, s = 0.0;
+// Sums over the CTA (every thread gets them): slot `which` of sh.red.
+__device__ __forceinline__ float cta_add(Shared& sh, int which, float v) {
 #pragma unroll
-      for (int j = 0; j < PER; ++j) m = fmax(m, sh.logp[tid + 32 * j]);
-      for (int off = 16; off > 0; off >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, off));
-#pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        const double t = sh.logp[tid + 32 * j];
-        if (t != -INFINITY) s += (double)expf((float)(t - m));
-      }
-      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      base = m + (double)logf((float)s);
-    }
-    double total = 0.0;
-    bool any = false;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int k = tid + 32 * j;
-      double lp = sh.logp[k];
-      float pk = 0.f;
-      if (lp != -INFINITY) {   // (-inf: no mass)
-        lp -= base;
-        pk = expf((float)lp);
-        sh.logp[k] = lp;
-        any = true;
-      }
-      sh.p[k] = pk;
-      total += (double)pk;
-    }
-    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-    any = __any_sync(0xffffffffu, any);
-    if (tid == 0) {
-      sh.p_rest = kTail ? (total <= 1.0 ? (float)(1.0 - total) : (total > 1.0 ? 0.f : (float)total)) : 0.f;
-      sh.any = any;
-    }
-  }
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  if ((threadIdx.x & 31) == 0) sh.red[which][threadIdx.x >> 5] = v;
   __syncthreads();
-  if (tid < p.K) {
-    const int i = sh.idx[tid];
-    float s = i < 0 ? -1.f : 0.f;
-    for (int k = 0; i >= 0 && k < p.K; ++k) {
-      if (sh.idx[k] != i) continue;
-      if (k < tid) {
-        s = -1.f;
-        break;
-      }
-      s += sh.p[k];
-    }
-    sh.psum[tid] = s;
-  }
+  float s = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) s += sh.red[which][w];
+  return s;
+}
+__device__ __forceinline__ float cta_max(Shared& sh, int which, float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, off));
+  if ((threadIdx.x & 31) == 0) sh.red[which][threadIdx.x >> 5] = v;
   __syncthreads();
+  float s = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) s = max_nan(s, sh.red[which][w]);
+  return s;
 }
 
-// kTail: the teacher's lse is given.  With p.stats_in the backward pass alone.
-template <typename T, typename G, bool kTail>
-__global__ void __launch_bounds__(kThreads, 2) distill_kernel(const DistillArgs p) {
+// A row's loss and statistics and its gradient's coefficients, by one whole
+// CTA, from the row's state (`pass`; outside the kept entries with a tail) or
+// from the statistics of the forward call.
+template <typename T, bool kTail>
+__device__ void finish_row(Shared& sh, const DistillArgs& p, int row, bool pass, const Stat rest, float lse_in,
+                           float lse_rest_in) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const T* rp = static_cast<const T*>(p.logits) + (size_t)row * p.row_stride;
+  const float nan = __int_as_float(0x7FC00000);
+  // entry k of the teacher, a thread each
+  int idx = -1;
+  float val = -INFINITY, z = 0.f;
+  bool bad = false;
+  if (tid < p.K) {
+    idx = p.top_idx[(size_t)row * p.K + tid];
+    val = p.top_val[(size_t)row * p.K + tid];
+    bad = idx < -1 || idx >= p.V;
+    if (idx < 0 || bad) {
+      idx = -1;
+      val = -INFINITY;
+    } else {
+      z = Elem<T>::to_float(rp[idx]);
+    }
+  }
+  if (tid < kMaxTop) sh.idx[tid] = idx;
+  const bool any = __syncthreads_or(val != -INFINITY);
+  bad = __syncthreads_or(bad);
+
+  // log p_k and p_k (products and differences rounded once)
+  float t = -INFINITY, base = 0.f;
+  if (kTail) {
+    if (val != -INFINITY) t = fmaf(val, p.inv_tau, -p.teacher_lse[row]);
+  } else {
+    const float m = cta_max(sh, 0, val);
+    if (val != -INFINITY) t = (val - m) * p.inv_tau;
+    base = logf(cta_add(sh, 1, t == -INFINITY ? 0.f : expf(t)));
+  }
+  const float logp = t == -INFINITY ? -INFINITY : t - base;
+  const float pk = t == -INFINITY ? 0.f : expf(logp);
+  if (tid < kMaxTop) sh.p[tid] = pk;
+  const float total = cta_add(sh, 2, pk);
+  const float p_rest = kTail ? (total > 1.f ? 0.f : 1.f - total) : 0.f;   // (a NaN total stays one)
+  // p(v): equal indices add up in the first of them
+  float pv = 0.f;
+  bool first = idx >= 0;
+  if (first) {
+    for (int k = 0; k < p.K; ++k) {
+      if (sh.idx[k] != idx) continue;
+      if (k < tid) {
+        first = false;
+        break;
+      }
+      pv += sh.p[k];
+    }
+  }
+
+  // the student's side
+  bool none = false;
+  float ref = 0.f, coef = 0.f, q_ref = 0.f, q_scale = 0.f, ls = 0.f, lse = 0.f, lse_rest = 0.f;
+  if (pass) {
+    Stat all = rest;
+    if (kTail) {
+      const float m = cta_max(sh, 0, first ? z : -INFINITY);
+      const float s = cta_add(sh, 1, first && m != -INFINITY ? expf((z - m) * p.inv_tau) : 0.f);
+      all = stat_reduce<2>(lane & 1 ? Stat{m, s, 0.f} : rest, p.inv_tau);
+    }
+    none = all.m == -INFINITY;
+    ls = none ? 0.f : logf(all.s);
+    lse = fmaf(all.m, p.inv_tau, ls);
+    lse_rest = rest.m == -INFINITY ? -INFINITY : fmaf(rest.m, p.inv_tau, logf(rest.s));
+    q_ref = all.m;
+    q_scale = 1.f / all.s;
+    ref = all.m;
+    coef = q_scale;
+    if (kTail) {
+      ref = rest.m == -INFINITY ? 0.f : rest.m;
+      const float q_rest = rest.m == -INFINITY ? 0.f : expf((rest.m - all.m) * p.inv_tau) * rest.s / all.s;
+      coef = rest.m == -INFINITY ? 0.f : (q_rest - p_rest) / rest.s;
+    }
+    if (any && stat_bad(all)) {
+      bad = true;
+      lse = lse_rest = nan;
+    }
+  } else {
+    none = lse_in == -INFINITY;
+    // the references in units of the logits, with what their rounding lost
+    q_ref = none ? 0.f : lse_in * p.tau;
+    q_scale = expf(-fmaf(lse_in, p.tau, -q_ref) * p.inv_tau);
+    ref = q_ref;
+    coef = q_scale;
+    if (kTail) {
+      ref = lse_rest_in == -INFINITY ? 0.f : lse_rest_in * p.tau;
+      coef = lse_rest_in == -INFINITY
+                 ? 0.f
+                 : (expf(lse_rest_in - lse_in) - p_rest) * expf(-fmaf(lse_rest_in, p.tau, -ref) * p.inv_tau);
+    }
+  }
+  const bool on = (any || bad) && !none;
+  if (p.stats_in == nullptr) {
+    float L = !(pk == 0.f) ? pk * (logp - ((z - q_ref) * p.inv_tau - ls)) : 0.f;
+    L = cta_add(sh, 0, L);
+    if (kTail && !(p_rest == 0.f)) L += p_rest * (logf(p_rest) - (lse_rest - lse));
+    if (tid == 0) {
+      const bool counts = any || bad;
+      p.loss[row] = bad ? nan : (on ? L : 0.f);
+      p.stats[2 * (size_t)row] = bad ? nan : (counts ? lse : 0.f);
+      p.stats[2 * (size_t)row + 1] = bad ? nan : (counts ? (kTail ? lse_rest : lse) : 0.f);
+    }
+  }
+  if (bad) coef = q_scale = nan;
+  if (p.dlogits != nullptr) {
+    const WsView ws = ws_view(p.ws, p.N, p.K);
+    const float w = (p.weight != nullptr ? p.weight[row] : 1.f) * p.inv_tau;
+    if (tid == 0) ws.coef[row] = make_float4(ref, coef * w, on ? 1.f : 0.f, 0.f);
+    if (tid < p.K) {
+      ws.kept_at[(size_t)row * p.K + tid] = on && first ? idx : -1;
+      ws.kept_g[(size_t)row * p.K + tid] = w * (q_scale * ex2((z - q_ref) * p.inv_tau * kLog2e) - pv);
+    }
+  }
+}
+
+// The first kernel.  kTail: the teacher's lse is given.  With p.stats_in (the
+// backward pass alone) only rows whose lse is too large to be used are summed.
+template <typename T, bool kTail>
+__global__ void __launch_bounds__(kThreads, 4) distill_sum_kernel(const DistillArgs p) {
   constexpr int VEC = Elem<T>::VEC;
   constexpr int kBlockPlaces = kBlockVecs * VEC;
   __shared__ Shared sh;
-  extern __shared__ __align__(16) uint32_t bits[];   // kTail: one bit per place of this CTA's part, then a byte per block
+  extern __shared__ uint32_t marked[];   // kTail: one bit per place of the part, then a byte per block
   cg::cluster_group cluster = cg::this_cluster();
   const int c = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int row = (int)(blockIdx.x / c);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  pdl_trigger();
   const bool backward = p.stats_in != nullptr;
-  const bool grad = p.dlogits != nullptr;
-  const T* rp = static_cast<const T*>(p.logits) + (size_t)row * p.row_stride;
-  const Row<T> R(rp, p.V);
-  const BlockRange br = block_range(R.nvec, rank, c);
-  const int lo = max(br.begin * kBlockPlaces - R.shift, 0), hi = min(br.end * kBlockPlaces - R.shift, p.V);
-  const int b0 = row / p.R;
-  bool on = p.lens == nullptr || row - b0 * p.R < p.lens[b0];
+  if (!scored(p, row)) {
+    if (rank == 0 && tid == 0) {
+      if (!backward) p.loss[row] = p.stats[2 * (size_t)row] = p.stats[2 * (size_t)row + 1] = 0.f;
+      if (p.dlogits != nullptr) ws_view(p.ws, p.N, p.K).coef[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    return;
+  }
   float lse_in = 0.f, lse_rest_in = 0.f;
-  if (backward && on) {
+  if (backward) {
     lse_in = p.stats_in[2 * (size_t)row];
     lse_rest_in = p.stats_in[2 * (size_t)row + 1];
   }
   const bool pass = !backward || (lse_in != -INFINITY && fabsf(lse_in) > kLargeLse);
-  if (on) {
-    // (a pass over the row reads every kept logit; a backward pass, whose CTAs
-    // do not wait for each other and may overwrite the logits, only its own part's)
-    load_teacher<T, kTail>(sh, p, row, rp, pass ? 0 : lo, pass ? p.V : hi);
-    on = sh.any != 0 || sh.bad != 0;
+  if (!pass) {
+    if (rank == 0) finish_row<T, kTail>(sh, p, row, false, stat_empty(), lse_in, lse_rest_in);
+    return;
   }
-
-  // q_v outside the kept entries is coef0 * exp((x - ref) / tau), the gradient
-  // coef * that; a kept entry's is q_scale * exp((x - q_ref) / tau) - p(v), times w
-  float ref = 0.f, coef = 0.f, q_ref = 0.f, q_scale = 0.f;
-  float w = 0.f;
-  if (grad && on) w = (p.weight != nullptr ? p.weight[row] : 1.f) * p.inv_tau;
-  const float nan = __int_as_float(0x7FC00000);
-  const float scale = p.inv_tau * kLog2e;
-
-  if (on && pass) {
-    if (kTail) {
-      const int nblk = br.end - br.begin;
-      const int words = nblk * (kBlockPlaces / 32);
-      unsigned char* flag = reinterpret_cast<unsigned char*>(bits + words);
-      for (int i = tid; i < words; i += kThreads) bits[i] = 0;
-      for (int i = tid; i < nblk; i += kThreads) flag[i] = 0;
+  const Row<T> R(static_cast<const T*>(p.logits) + (size_t)row * p.row_stride, p.V);
+  const BlockRange br = block_range(R.nvec, rank, c);
+  const int place0 = br.begin * kBlockPlaces - R.shift;   // entry at the part's first place
+  const int nblk = br.end - br.begin, words = nblk * (kBlockPlaces / 32);
+  unsigned char* block_marked = reinterpret_cast<unsigned char*>(marked + words);
+  auto mark = [&]() {
+    if constexpr (kTail) {
+      const int i = tid < p.K ? p.top_idx[(size_t)row * p.K + tid] : -1;
+      for (int k = tid; k < words; k += kThreads) marked[k] = 0;
+      for (int k = tid; k < nblk; k += kThreads) block_marked[k] = 0;
       __syncthreads();
-      if (tid < p.K && sh.idx[tid] >= lo && sh.idx[tid] < hi) {
-        const int place = sh.idx[tid] + R.shift - br.begin * kBlockPlaces;
-        atomicOr(&bits[place >> 5], 1u << (place & 31));
-        flag[place / kBlockPlaces] = 1;
+      const int place = i - place0;
+      if (i >= 0 && i < p.V && place >= 0 && place < nblk * kBlockPlaces) {
+        atomicOr(&marked[place >> 5], 1u << (place & 31));
+        block_marked[place / kBlockPlaces] = 1;
       }
       __syncthreads();
     }
-    const unsigned char* flag = reinterpret_cast<const unsigned char*>(bits + (br.end - br.begin) * (kBlockPlaces / 32));
-    stat_row<T, false>(
-        R, br, scale, p.inv_tau, sh.part, &sh.cta,
-        [&](int b, uint4(&cur)[kVecPerLane]) {
-          if constexpr (kTail) {
-            if (!flag[b - br.begin]) return;
-            // kept entries leave the sum of the rest
-#pragma unroll
-            for (int j = 0; j < kVecPerLane; ++j) {
-              const int place = ((b - br.begin) * kBlockVecs + j * 32 + lane) * VEC;
-              const uint32_t m = (bits[place >> 5] >> (place & 31)) & ((1u << VEC) - 1u);
-              if (m == 0) continue;
-              T* e = reinterpret_cast<T*>(&cur[j]);
-#pragma unroll
-              for (int i = 0; i < VEC; ++i)
-                if (m >> i & 1u) e[i] = Elem<T>::from_float(-INFINITY);
-            }
-          }
-        },
-        [](int, float, float) {});
-    cluster.sync();
-    // every CTA: the states of all parts, then the kept entries' with a tail
-    const Stat rest = stat_cluster(cluster, &sh.cta, c, p.inv_tau);
-    Stat all = rest;
-    if (kTail) {
-      Stat kept = stat_empty();
-#pragma unroll
-      for (int j = 0; j < kMaxTop / 32; ++j) {
-        const int k = lane + 32 * j;
-        if (k < p.K && sh.psum[k] != -1.f) kept = stat_merge(kept, Stat{sh.z[k], 1.f, 0.f}, p.inv_tau);
-      }
-      all = stat_merge(stat_reduce<32>(kept, p.inv_tau), rest, p.inv_tau);
-    }
-    const bool bad = stat_bad(all) || sh.bad != 0;
-    const bool none = all.m == -INFINITY;
-    const float ls = none ? 0.f : logf(all.s);
-    const float lse = fmaf(all.m, p.inv_tau, ls);
-    const float lse_rest = rest.m == -INFINITY ? -INFINITY : fmaf(rest.m, p.inv_tau, logf(rest.s));
-    // the student's mass outside the kept entries
-    const float q_rest = kTail && rest.m != -INFINITY ? expf((rest.m - all.m) * p.inv_tau) * rest.s / all.s : 0.f;
-    if (!backward && rank == 0 && warp == 0) {
-      float L = 0.f;
-#pragma unroll
-      for (int j = 0; j < kMaxTop / 32; ++j) {
-        const int k = lane + 32 * j;
-        if (sh.p[k] > 0.f || sh.p[k] != sh.p[k])
-          L += sh.p[k] * (float)(sh.logp[k] - (((double)sh.z[k] - all.m) * p.inv_tau - ls));
-      }
-      for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-      if (kTail && !(sh.p_rest == 0.f)) L += sh.p_rest * (logf(sh.p_rest) - (lse_rest - lse));
-      if (lane == 0) {
-        p.loss[row] = bad ? nan : (none ? 0.f : L);
-        p.stats[2 * (size_t)row] = bad ? nan : lse;
-        p.stats[2 * (size_t)row + 1] = bad ? nan : (kTail ? lse_rest : lse);
-      }
-    }
-    if (bad) {
-      coef = q_scale = nan;
-    } else if (none) {
-      w = 0.f;
-    } else {
-      q_ref = all.m;
-      q_scale = 1.f / all.s;
-      ref = kTail ? (rest.m == -INFINITY ? 0.f : rest.m) : q_ref;
-      coef = kTail ? (rest.m == -INFINITY ? 0.f : (q_rest - sh.p_rest) / rest.s) : q_scale;
-    }
-    on = on && !none;
-  } else if (on) {
-    const float lse = lse_in, lse_rest = lse_rest_in;
-    if (lse == -INFINITY) {
-      on = false;
-    } else {
-      // the references in units of the logits, with what their rounding lost
-      q_ref = lse * p.tau;
-      q_scale = expf(-fmaf(lse, p.tau, -q_ref) * p.inv_tau);
-      ref = q_ref;
-      coef = q_scale;
-      if (kTail) {
-        ref = lse_rest == -INFINITY ? 0.f : lse_rest * p.tau;
-        coef = lse_rest == -INFINITY ? 0.f
-                                     : (expf(lse_rest - lse) - sh.p_rest) * expf(-fmaf(lse_rest, p.tau, -ref) * p.inv_tau);
-      }
-      if (sh.bad) coef = q_scale = nan;
-    }
-  } else if (!backward && rank == 0 && tid == 0) {
-    p.loss[row] = p.stats[2 * (size_t)row] = p.stats[2 * (size_t)row + 1] = 0.f;
-  }
-
-  if (grad) {
-    G* out = static_cast<G*>(p.dlogits) + (size_t)row * p.V;
-    const bool aligned = ((reinterpret_cast<uintptr_t>(out) - R.shift * sizeof(G)) & (VEC * sizeof(G) - 1)) == 0;
-    const float cw = coef * w;
-    for (int b = br.begin + warp; b < br.end; b += kWarps) {
-      uint4 r[kVecPerLane];
-      if (on) {
-#pragma unroll
-        for (int j = 0; j < kVecPerLane; ++j) r[j] = R.load(b * kBlockVecs + j * 32 + lane);
-      }
+  };
+  auto leave_out = [&](int b, uint4(&cur)[kVecPerLane]) {
+    if constexpr (kTail) {
+      if (!block_marked[b - br.begin]) return;
 #pragma unroll
       for (int j = 0; j < kVecPerLane; ++j) {
-        const int i = b * kBlockVecs + j * 32 + lane, e0 = R.first_entry(i);
-        alignas(16) G g[VEC];
-        float x[VEC];
-        if (on) Elem<T>::unpack(r[j], x);
+        const int place = ((b - br.begin) * kBlockVecs + j * 32 + lane) * VEC;
+        const uint32_t m = (marked[place >> 5] >> (place & 31)) & ((1u << VEC) - 1u);
+        if (m == 0) continue;
+        T* e = reinterpret_cast<T*>(&cur[j]);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) g[e] = Elem<G>::from_float(on ? ex2((x[e] - ref) * scale) * cw : 0.f);
-        if (aligned && R.whole(i)) {
-          if constexpr (sizeof(G) * VEC == 16) __stcs(reinterpret_cast<uint4*>(out + e0), *reinterpret_cast<const uint4*>(g));
-          else __stcs(reinterpret_cast<uint2*>(out + e0), *reinterpret_cast<const uint2*>(g));
-        } else {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e)
-            if (e0 + e >= 0 && e0 + e < p.V) out[e0 + e] = g[e];
-        }
+        for (int i = 0; i < VEC; ++i)
+          if (m >> i & 1u) e[i] = Elem<T>::from_float(-INFINITY);
       }
     }
-    if (on) {
-      __syncthreads();   // the kept entries' gradients replace what the loop stored there
-      if (tid < p.K && sh.idx[tid] >= lo && sh.idx[tid] < hi && sh.psum[tid] != -1.f)
-        out[sh.idx[tid]] =
-            Elem<G>::from_float(w * (q_scale * ex2((sh.z[tid] - q_ref) * scale) - sh.psum[tid]));
-    }
+  };
+  stat_row<T, false>(R, br, p.inv_tau * kLog2e, p.inv_tau, sh.part, &sh.cta, mark, leave_out, Nothing());
+  cluster.sync();
+  Stat v = stat_empty();
+  if (rank == 0) v = stat_cluster(cluster, &sh.cta, c, p.inv_tau);
+  cluster.sync();   // the other CTAs' shared memory is read until here
+  if (rank == 0) finish_row<T, kTail>(sh, p, row, true, v, 0.f, 0.f);
+}
+
+// The second kernel: c CTAs a row, one warp a block at a time.
+template <typename T, typename G>
+__global__ void __launch_bounds__(kThreads, 4) distill_gradient_kernel(const DistillArgs p, int c) {
+  constexpr int VEC = Elem<T>::VEC;
+  constexpr int kBlockPlaces = kBlockVecs * VEC;
+  const int row = (int)(blockIdx.x / c), rank = (int)(blockIdx.x % c);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const WsView ws = ws_view(p.ws, p.N, p.K);
+  const Row<T> R(static_cast<const T*>(p.logits) + (size_t)row * p.row_stride, p.V);
+  const BlockRange br = block_range(R.nvec, rank, c);
+  const int lo = max(br.begin * kBlockPlaces - R.shift, 0), hi = min(br.end * kBlockPlaces - R.shift, p.V);
+  const float scale = p.inv_tau * kLog2e;
+  const bool on = scored(p, row);
+  uint4 cur[kVecPerLane], nxt[kVecPerLane];
+  int b = br.begin + warp;
+  if (on && b < br.end) R.load_block(b, lane, cur);
+  pdl_wait();
+  const float4 k = __ldcg(ws.coef + row);
+  const bool live = k.z != 0.f;
+  const float ref = k.x, cw = k.y;
+  int kept = -1;
+  float kept_g = 0.f;
+  if (live && tid < p.K) {
+    kept = __ldcg(ws.kept_at + (size_t)row * p.K + tid);
+    kept_g = __ldcg(ws.kept_g + (size_t)row * p.K + tid);
   }
-  if (pass) cluster.sync();   // a neighbour's shared memory is read until here
+  G* out = static_cast<G*>(p.dlogits) + (size_t)row * p.V;
+  // an output row whose vectors start where the logits' do is stored by vectors
+  const bool aligned = ((reinterpret_cast<uintptr_t>(out) - R.shift * sizeof(G)) & (VEC * sizeof(G) - 1)) == 0;
+  for (; b < br.end; b += kWarps) {
+    if (live && b + kWarps < br.end) R.load_block(b + kWarps, lane, nxt);
+    const bool inside = aligned && R.inside(b);
+#pragma unroll
+    for (int j = 0; j < kVecPerLane; ++j) {
+      const int i = b * kBlockVecs + j * 32 + lane, e0 = R.first_entry(i);
+      alignas(16) G g[VEC];
+      float x[VEC];
+      if (live) Elem<T>::unpack(cur[j], x);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) g[e] = Elem<G>::from_float(live ? ex2((x[e] - ref) * scale) * cw : 0.f);
+      if (inside || (aligned && R.whole(i))) {
+        if constexpr (sizeof(G) * VEC == 16) __stcs(reinterpret_cast<uint4*>(out + e0), *reinterpret_cast<const uint4*>(g));
+        else __stcs(reinterpret_cast<uint2*>(out + e0), *reinterpret_cast<const uint2*>(g));
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (e0 + e >= 0 && e0 + e < p.V) out[e0 + e] = g[e];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kVecPerLane; ++j) cur[j] = nxt[j];
+  }
+  if (live) {
+    __syncthreads();   // the kept entries' gradients replace what the loop stored there
+    if (kept >= lo && kept < hi) out[kept] = Elem<G>::from_float(kept_g);
+  }
+}
+
+template <typename T>
+cudaError_t launch_sum(const DistillArgs& a, int sms, cudaStream_t stream) {
+  constexpr int kBlockPlaces = kBlockVecs * Elem<T>::VEC;
+  const int nblk = div_up(a.V, kBlockPlaces) + 1;
+  // (a backward pass seldom sums a row)
+  const int least = div_up(nblk, kMarkedPlaces / kBlockPlaces);
+  int c = 1;
+  if (a.stats_in == nullptr) c = cluster_for(a.N, nblk, least, sms);
+  else while (c < least) c *= 2;
+  const bool tail = a.teacher_lse != nullptr;
+  const int smem = tail ? div_up(nblk, c) * (kBlockPlaces / 8 + 1) : 0;
+  auto kern = tail ? distill_sum_kernel<T, true> : distill_sum_kernel<T, false>;
+  return launch_rows(kern, a.N, c, smem, stream, a);
 }
 
 template <typename T, typename G>
@@ -304,31 +356,19 @@ cudaError_t launch(const DistillArgs& a, cudaStream_t stream) {
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  constexpr int kBlockPlaces = kBlockVecs * Elem<T>::VEC;
-  const int nblk = div_up(a.V, kBlockPlaces) + 1;
-  const bool backward = a.stats_in != nullptr;
-  const bool tail = a.teacher_lse != nullptr;
-  int c;
-  if (backward) {
-    c = 1;
-    while (c < kMaxCluster && nblk > 2 * kWarps * c) c *= 2;   // about two blocks a warp
-  } else {
-    int least = div_up(nblk * (kBlockPlaces / 1024), 256);   // 256 K places: a bitmap of 32 KB
-    if (a.dlogits != nullptr) {
-      // the second pass finds the row in L2 while the rows in flight stay under 48 MB
-      const long long row_bytes = (long long)a.V * (long long)sizeof(T);
-      least = std::max(least, (int)std::min<long long>(row_bytes * 2 * sms / (48ll << 20) + 1, kMaxCluster));
-    }
-    c = cluster_for(a.N, least, sms);
-  }
-  const size_t smem = tail ? (size_t)div_up(nblk, c) * (kBlockPlaces / 8 + 1) + 16 : 0;
-  auto kern = tail ? distill_kernel<T, G, true> : distill_kernel<T, G, false>;
-  if (smem > 0 && (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
-    return e;
-  return launch_rows(kern, a.N, c, smem, stream, a);
+  if ((e = launch_sum<T>(a, sms, stream)) != cudaSuccess || a.dlogits == nullptr) return e;
+  const int nblk = div_up(a.V, kBlockVecs * Elem<T>::VEC) + 1;
+  const int c = div_up(nblk, 8 * kWarps);   // at most eight blocks a warp
+  if ((long long)a.N * c > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  return launch_pdl(distill_gradient_kernel<T, G>, dim3((unsigned)a.N * c), dim3(kThreads), 0, stream, a, c);
 }
 
 }  // namespace
+
+size_t distill_workspace_bytes(int N, int V, int K) {
+  (void)V;
+  return ws_view(nullptr, N, K).total;
+}
 
 cudaError_t launch_distill(const DistillArgs& a, cudaStream_t stream) {
   if (a.dtype == DSPARK_F32)

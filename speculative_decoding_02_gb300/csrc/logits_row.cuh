@@ -10,7 +10,12 @@
 // The softmax of a row is taken in one pass: each warp keeps a maximum m that
 // is the same on its 32 lanes, and per lane s = sum exp(x - m) and
 // t = sum exp(x - m) (m - x) over what it has read (from which the entropy is
-// log s + t / s); a block whose maximum is above m rescales both first.
+// log s + t / s); a block whose maximum is above m rescales both first.  Two
+// entries share each packed fp32 addition, product and fused product.
+//
+// CTAs of 256 threads, four or five to an SM, rather than two of 512: a row's
+// barriers and short serial phases (merging states, choosing alternatives, the
+// teacher's side) then overlap with the other rows' streams.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -24,11 +29,11 @@ namespace lrow {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kVecPerLane = 4;
 constexpr int kBlockVecs = 32 * kVecPerLane;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <typename T>
@@ -76,6 +81,15 @@ struct Elem<__half> {
   }
 };
 
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 // A row as its vectors: `base` is the row's address rounded down to 16 bytes.
 template <typename T>
 struct Row {
@@ -96,17 +110,7 @@ struct Row {
     return e0 >= 0 && e0 + Elem<T>::VEC <= V;
   }
   // Vector i with -inf in the places outside the row (i >= nvec: all of them).
-  __device__ __forceinline__ uint4 load(int i) const {
-    if (whole(i)) {
-      uint4 v;
-      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                   : "l"(base + i)
-                   : "memory");
-      return v;
-    }
-    return load_edge(i);
-  }
+  __device__ __forceinline__ uint4 load(int i) const { return whole(i) ? ld_stream(base + i) : load_edge(i); }
   __device__ __noinline__ uint4 load_edge(int i) const {
     uint4 v = make_uint4(Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf);
     T* p = reinterpret_cast<T*>(&v);
@@ -114,6 +118,21 @@ struct Row {
     for (int e = 0; e < Elem<T>::VEC; ++e)
       if (e0 + e >= 0 && e0 + e < V) p[e] = row[e0 + e];
     return v;
+  }
+  // Every vector of block b is whole.
+  __device__ __forceinline__ bool inside(int b) const {
+    return first_entry(b * kBlockVecs) >= 0 && first_entry((b + 1) * kBlockVecs) <= V;
+  }
+  // This lane's vectors of block b.
+  __device__ __forceinline__ void load_block(int b, int lane, uint4 (&r)[kVecPerLane]) const {
+    const int i0 = b * kBlockVecs + lane;
+    if (inside(b)) {
+#pragma unroll
+      for (int j = 0; j < kVecPerLane; ++j) r[j] = ld_stream(base + i0 + j * 32);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVecPerLane; ++j) r[j] = load(i0 + j * 32);
+    }
   }
 };
 
@@ -182,85 +201,138 @@ struct Stat {
 };
 __device__ __forceinline__ Stat stat_empty() { return Stat{-INFINITY, 0.f, 0.f}; }
 
-// Two states of one row whose exponents are scaled by `inv` (t: for inv = 1).
-__device__ __forceinline__ Stat stat_merge(const Stat& a, const Stat& b, float inv = 1.f) {
-  // (a NaN maximum or sum stays one: such a row is reported by NaN outputs)
-  if (b.m == -INFINITY) return a;
-  if (a.m == -INFINITY) return b;
-  const float M = max_nan(a.m, b.m);
-  const float fa = expf((a.m - M) * inv), fb = expf((b.m - M) * inv);
-  // a state so far below M that its factor is 0 adds nothing (M - m may be inf)
-  const float ta = fa > 0.f ? fa * fmaf(a.s, M - a.m, a.t) : fa;
-  const float tb = fb > 0.f ? fb * fmaf(b.s, M - b.m, b.t) : fb;
-  return Stat{M, a.s * fa + b.s * fb, ta + tb};
-}
+// The states of W lanes of one row (exponents scaled by `inv`; t: for inv = 1)
+// as one, on each of the W.  A NaN or +inf maximum gives a NaN sum.
 template <int W>
-__device__ __forceinline__ Stat stat_reduce(Stat v, float inv = 1.f) {
+__device__ __forceinline__ Stat stat_reduce(const Stat& v, float inv = 1.f) {
+  float M = v.m;
+#pragma unroll
+  for (int off = W / 2; off > 0; off >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, off));
+  // (a state so far below M that its factor is 0 adds nothing: M - m may be inf)
+  const float f = v.m == -INFINITY && M == M ? 0.f : expf((v.m - M) * inv);
+  float s = v.s * f;
+  float t = f > 0.f ? f * fmaf(v.s, M - v.m, v.t) : f;
 #pragma unroll
   for (int off = W / 2; off > 0; off >>= 1) {
-    Stat o;
-    o.m = __shfl_xor_sync(0xffffffffu, v.m, off);
-    o.s = __shfl_xor_sync(0xffffffffu, v.s, off);
-    o.t = __shfl_xor_sync(0xffffffffu, v.t, off);
-    v = stat_merge(v, o, inv);
+    s += __shfl_xor_sync(0xffffffffu, s, off);
+    t += __shfl_xor_sync(0xffffffffu, t, off);
   }
-  return v;
+  return Stat{M, s, t};
 }
 
+// Packed fp32 arithmetic on the pairs of a 64-bit register.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// A lane's running state: the warp's maximum, and the sums of its even and odd
+// entries (t with the opposite sign).
+struct LaneStat {
+  float m;
+  uint64_t s, t;
+};
+__device__ __forceinline__ LaneStat lane_stat_empty() { return LaneStat{-INFINITY, 0, 0}; }
+
 // Takes a lane's vectors of one block into its state; bmax is the block's
-// maximum (the same on every lane), the state's maximum is too.
-// d = x - m is held at -1000 / scale and above so that an entry of -inf adds 0
-// to t (0 * -1000) and not NaN.
+// maximum (the same on every lane, as the state's is).
+// With kEntropy d = x - m is held at -1000 and above so that an entry of -inf
+// adds 0 to t (0 * -1000) and not NaN.
 template <typename T, bool kEntropy>
-__device__ __forceinline__ void stat_block(Stat& st, const uint4 (&r)[kVecPerLane], float bmax, float scale) {
+__device__ __forceinline__ void stat_block(LaneStat& st, const uint4 (&r)[kVecPerLane], float bmax, float scale) {
   if (!(bmax <= st.m)) {
-    const float m = bmax;
-    if (st.m == -INFINITY) {
-      st.m = m;
-    } else {
-      const float f = ex2((st.m - m) * scale);
-      if (kEntropy) st.t = f > 0.f ? f * fmaf(st.s, m - st.m, st.t) : f;
-      st.s *= f;
-      st.m = m;
+    if (st.m != -INFINITY) {
+      const float up = bmax - st.m, f = ex2(-up * scale);
+      const uint64_t f2 = pack2(f, f);
+      if (kEntropy) st.t = f > 0.f ? mul2(f2, fma2(st.s, pack2(-up, -up), st.t)) : f2;
+      st.s = mul2(st.s, f2);
     }
+    st.m = bmax;
   }
   const float m = st.m == -INFINITY ? 0.f : st.m;
+  const uint64_t nm = pack2(-m, -m), sc = pack2(scale, scale);
 #pragma unroll
   for (int j = 0; j < kVecPerLane; ++j) {
     float f[Elem<T>::VEC];
     Elem<T>::unpack(r[j], f);
 #pragma unroll
-    for (int e = 0; e < Elem<T>::VEC; ++e) {
-      float d = f[e] - m;
-      if (kEntropy) d = fmaxf(d, -1000.f);
-      const float p = ex2(d * scale);
-      st.s += p;
-      if (kEntropy) st.t = fmaf(-p, d, st.t);
+    for (int e = 0; e < Elem<T>::VEC; e += 2) {
+      uint64_t d = add2(pack2(f[e], f[e + 1]), nm);
+      float a, b;
+      if (kEntropy) {
+        unpack2(d, a, b);
+        d = pack2(fmaxf(a, -1000.f), fmaxf(b, -1000.f));
+      }
+      unpack2(mul2(d, sc), a, b);
+      const uint64_t p = pack2(ex2(a), ex2(b));
+      st.s = add2(st.s, p);
+      if (kEntropy) st.t = fma2(p, d, st.t);
     }
   }
 }
 
-// The state of this CTA's blocks of a row, the same on warp 0's lanes (left in
-// *out, which the caller reads behind a barrier).  `each(b, cur)` may change a
-// block's vectors before they are taken in; `seen(b, lane maximum, block
-// maximum)` sees what a block holds.  The next block's loads are in flight
-// while one is taken in.
-template <typename T, bool kEntropy, typename Each, typename Seen>
-__device__ __forceinline__ void stat_row(const Row<T>& R, const BlockRange& br, float scale, float inv, Stat* part,
-                                         Stat* out, Each each, Seen seen) {
+// The warp's state from its lanes'.
+__device__ __forceinline__ Stat lanes_sum(const LaneStat& v) {
+  float s, s1, t, t1;
+  unpack2(v.s, s, s1);
+  unpack2(v.t, t, t1);
+  s += s1;
+  t += t1;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, off);
+    t += __shfl_xor_sync(0xffffffffu, t, off);
+  }
+  return Stat{v.m, s, -t};
+}
+
+// The states of the CTA's warps as one in *out, which is read behind a barrier.
+__device__ __forceinline__ void cta_stat(const LaneStat& st, float inv, Stat* part, Stat* out) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Stat st = stat_empty();
+  const Stat v = lanes_sum(st);
+  if (lane == 0) part[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    const Stat w = stat_reduce<kWarps>(lane < kWarps ? part[lane] : stat_empty(), inv);
+    if (lane == 0) *out = w;
+  }
+}
+
+// The state of this CTA's blocks of a row, read from global memory, in *out
+// (behind a barrier).  before() runs once the first loads are in flight;
+// each(b, vectors) may change a block's vectors before they are taken in, and
+// seen(b, lane maximum, block maximum) sees what the block holds.  The next
+// block's loads are in flight while one is taken in.
+template <typename T, bool kEntropy, typename Before, typename Each, typename Seen>
+__device__ __forceinline__ void stat_row(const Row<T>& R, const BlockRange& br, float scale, float inv, Stat* part,
+                                         Stat* out, Before before, Each each, Seen seen) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  LaneStat st = lane_stat_empty();
   uint4 cur[kVecPerLane], nxt[kVecPerLane];
   int b = br.begin + warp;
-  if (b < br.end) {
-#pragma unroll
-    for (int j = 0; j < kVecPerLane; ++j) cur[j] = R.load(b * kBlockVecs + j * 32 + lane);
-  }
+  if (b < br.end) R.load_block(b, lane, cur);
+  before();
   for (; b < br.end; b += kWarps) {
-    if (b + kWarps < br.end) {
-#pragma unroll
-      for (int j = 0; j < kVecPerLane; ++j) nxt[j] = R.load((b + kWarps) * kBlockVecs + j * 32 + lane);
-    }
+    if (b + kWarps < br.end) R.load_block(b + kWarps, lane, nxt);
     each(b, cur);
     const float lm = lane_max(cur, (const T*)nullptr);
     const float bm = warp_max_nan(lm);
@@ -269,13 +341,7 @@ __device__ __forceinline__ void stat_row(const Row<T>& R, const BlockRange& br, 
 #pragma unroll
     for (int j = 0; j < kVecPerLane; ++j) cur[j] = nxt[j];
   }
-  st = stat_reduce<32>(st, inv);
-  if (lane == 0) part[warp] = st;
-  __syncthreads();
-  if (warp == 0) {
-    st = stat_reduce<kWarps>(lane < kWarps ? part[lane] : stat_empty(), inv);
-    if (lane == 0) *out = st;
-  }
+  cta_stat(st, inv, part, out);
 }
 
 // The state of a whole row from the `cta` of each of the cluster's c CTAs, the
@@ -283,13 +349,19 @@ __device__ __forceinline__ void stat_row(const Row<T>& R, const BlockRange& br, 
 // before a CTA leaves.
 __device__ __forceinline__ Stat stat_cluster(cg::cluster_group& cluster, Stat* cta, int c, float inv) {
   const int lane = threadIdx.x & 31;
-  Stat v = lane < c ? *cluster.map_shared_rank(cta, lane) : stat_empty();
-  v = stat_reduce<kMaxCluster>(v, inv);
+  Stat v = stat_reduce<kMaxCluster>(lane < c ? *cluster.map_shared_rank(cta, lane) : stat_empty(), inv);
   v.m = __shfl_sync(0xffffffffu, v.m, 0);
   v.s = __shfl_sync(0xffffffffu, v.s, 0);
   v.t = __shfl_sync(0xffffffffu, v.t, 0);
   return v;
 }
+
+// A hook of stat_row that does nothing.
+struct Nothing {
+  __device__ __forceinline__ void operator()() const {}
+  __device__ __forceinline__ void operator()(int, uint4 (&)[kVecPerLane]) const {}
+  __device__ __forceinline__ void operator()(int, float, float) const {}
+};
 
 // A NaN or +inf was in the row.
 __device__ __forceinline__ bool stat_bad(const Stat& v) { return !(v.m < INFINITY) || !(v.s >= 0.f); }
@@ -300,11 +372,11 @@ __device__ __forceinline__ bool stat_bad(const Stat& v) { return !(v.m < INFINIT
 // lost beside it) they take the row's state anew.
 constexpr float kLargeLse = 1024.f;
 
-// c CTAs a row so that a call with few rows still fills the card (about two
-// CTAs on each SM); `least` from what one CTA can hold.
-inline int cluster_for(int rows, int least, int sms) {
+// CTAs a row (a power of two): at least `least`, and for few rows as many more
+// as give each SM about two while every warp keeps a block.
+inline int cluster_for(int rows, int nblk, int least, int sms) {
   int c = 1;
-  while (c < kMaxCluster && (c < least || (long long)rows * c * 2 <= 2ll * sms)) c *= 2;
+  while (c < kMaxCluster && (c < least || ((long long)rows * c <= sms && nblk > kWarps * c))) c *= 2;
   return c;
 }
 
@@ -312,6 +384,11 @@ inline int cluster_for(int rows, int least, int sms) {
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_rows(void (*kern)(KArgs...), int rows, int c, size_t smem, cudaStream_t stream,
                                Args&&... args) {
+  if (c > 8) {
+    // (8 is the largest size that needs no opt-in)
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)rows * c);
   cfg.blockDim = dim3(kThreads);

@@ -8,10 +8,10 @@
 // of 1 to 8 CTAs takes a row; their states and top lists meet in CTA 0 through
 // distributed shared memory.  The top entries cost the pass one maximum per
 // lane and one stored maximum per block:
-//   1. the K-th largest of the 512 lane maxima is a lower bound of the row
+//   1. the K-th largest of the CTA's 256 lane maxima is a lower bound of the row
 //      part's K-th largest entry (K distinct entries are at least that large);
 //   2. only the blocks whose maximum reaches it are read again (from L2), and
-//      their entries that reach it become candidates, about K (1 + K / 1024)
+//      their entries that reach it become candidates, about K (1 + K / 512)
 //      of them in a row of no particular order;
 //   3. a candidate's rank is the number of larger ones (64-bit keys of value,
 //      then lower index, so no two are equal and ties go to the lowest index).
@@ -87,24 +87,34 @@ __device__ __forceinline__ void append(Shared& sh, unsigned long long key) {
   if (i < kMaxTop) sh.list[i] = key;
 }
 
-// Calls f(key) for every entry of this warp's blocks whose maximum reaches t0
-// and that itself does.
+__device__ __forceinline__ float order_value(uint32_t o) { return argmax_key_value((unsigned long long)o << 32); }
+
+// Calls f(key) for every entry that reaches the order t0, block by block of
+// this warp's.
 template <typename T, typename F>
 __device__ __forceinline__ void for_candidates(const Row<T>& R, const BlockRange& br, const float* bmax, uint32_t t0,
                                                int warp, int lane, F f) {
-  for (int b = br.begin + warp; b < br.end; b += kWarps) {
-    if (order32(bmax[b - br.begin]) < t0) continue;
-    uint4 r[kVecPerLane];
+  const float least = order_value(t0);
+  const int mine = br.begin + warp;   // this warp's blocks: mine, mine + kWarps, ...
+  for (int b0 = mine; b0 < br.end; b0 += 32 * kWarps) {
+    const int bl = b0 + lane * kWarps;
+    unsigned hit = __ballot_sync(0xffffffffu, bl < br.end && !(bmax[bl < br.end ? bl - br.begin : 0] < least));
+    for (; hit != 0; hit &= hit - 1) {
+      const int b = b0 + (__ffs(hit) - 1) * kWarps;
+      uint4 r[kVecPerLane];
+      R.load_block(b, lane, r);
+      if (lane_max(r, (const T*)nullptr) < least) continue;
 #pragma unroll
-    for (int j = 0; j < kVecPerLane; ++j) r[j] = R.load(b * kBlockVecs + j * 32 + lane);
+      for (int j = 0; j < kVecPerLane; ++j) {
+        float v[Elem<T>::VEC];
+        Elem<T>::unpack(r[j], v);
+        const int e0 = R.first_entry(b * kBlockVecs + j * 32 + lane);
 #pragma unroll
-    for (int j = 0; j < kVecPerLane; ++j) {
-      float v[Elem<T>::VEC];
-      Elem<T>::unpack(r[j], v);
-#pragma unroll
-      for (int e = 0; e < Elem<T>::VEC; ++e)
-        if (order32(v[e]) >= t0) f(entry_key(v[e], R.first_entry(b * kBlockVecs + j * 32 + lane) + e));
+        for (int e = 0; e < Elem<T>::VEC; ++e)
+          if (v[e] >= least) f(entry_key(v[e], e0 + e));
+      }
     }
+    __syncwarp();
   }
 }
 
@@ -117,7 +127,9 @@ __device__ void cta_top(Shared& sh, const Row<T>& R, const BlockRange& br, float
   uint32_t t0 = 0;
   for (int bit = 31; bit >= 0; --bit) {
     const uint32_t c = t0 | (1u << bit);
-    if (__syncthreads_count(mine >= c) >= K) t0 = c;
+    const int n = __syncthreads_count(mine >= c);
+    if (n >= K) t0 = c;
+    if (n >= K && n <= K + K / 8) break;   // (any lower bound will do)
   }
   t0 = max(t0, kNegInfOrder + 1);
   if (tid == 0) sh.ncand = sh.nlist = 0;
@@ -164,7 +176,7 @@ __device__ void cta_top(Shared& sh, const Row<T>& R, const BlockRange& br, float
 static_assert(kRankDirect >= kMaxTop, "the bisection needs at least K candidates");
 
 template <typename T, bool kTop>
-__global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobArgs p) {
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs p) {
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int c = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -189,14 +201,12 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobArgs
   const BlockRange br = block_range(R.nvec, rank, c);
 
   float tmax = -INFINITY;
-  stat_row<T, true>(
-      R, br, kLog2e, 1.f, sh.part, &sh.cta, [](int, uint4(&)[kVecPerLane]) {},
-      [&](int b, float lm, float bm) {
-        if (kTop) {
-          tmax = fmaxf(tmax, lm);
-          if (lane == 0) sh.bmax[b - br.begin] = bm;
-        }
-      });
+  stat_row<T, true>(R, br, kLog2e, 1.f, sh.part, &sh.cta, Nothing(), Nothing(), [&](int b, float lm, float bm) {
+    if (kTop) {
+      tmax = fmaxf(tmax, lm);
+      if (lane == 0) sh.bmax[b - br.begin] = bm;
+    }
+  });
   if (kTop) cta_top<T>(sh, R, br, tmax, p.K, warp, lane);
 
   cluster.sync();
@@ -251,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobArgs
 // write).  An output row whose vectors start where the logits' do is stored by
 // vectors, any other entry by entry.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) logprobs_backward_kernel(const LogprobBackwardArgs p) {
+__global__ void __launch_bounds__(kThreads, 4) logprobs_backward_kernel(const LogprobBackwardArgs p) {
   constexpr int VEC = Elem<T>::VEC;
   __shared__ Stat part[kWarps], cta;
   cg::cluster_group cluster = cg::this_cluster();
@@ -272,8 +282,7 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_backward_kernel(const Lo
   float ref = on ? p.lse[row] : -INFINITY, ls = 0.f;
   if (ref != ref) gl = nan;
   if (fabsf(ref) > kLargeLse && ref != -INFINITY) {
-    stat_row<T, false>(
-        R, br, kLog2e, 1.f, part, &cta, [](int, uint4(&)[kVecPerLane]) {}, [](int, float, float) {});
+    stat_row<T, false>(R, br, kLog2e, 1.f, part, &cta, Nothing(), Nothing(), Nothing());
     cluster.sync();
     const Stat v = stat_cluster(cluster, &cta, c, 1.f);
     cluster.sync();
@@ -286,10 +295,7 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_backward_kernel(const Lo
   const bool aligned = ((reinterpret_cast<uintptr_t>(out) - R.shift * sizeof(T)) & 15) == 0;
   for (int b = br.begin + warp; b < br.end; b += kWarps) {
     uint4 r[kVecPerLane];
-    if (!zero) {
-#pragma unroll
-      for (int j = 0; j < kVecPerLane; ++j) r[j] = R.load(b * kBlockVecs + j * 32 + lane);
-    }
+    if (!zero) R.load_block(b, lane, r);
 #pragma unroll
     for (int j = 0; j < kVecPerLane; ++j) {
       const int i = b * kBlockVecs + j * 32 + lane, e0 = R.first_entry(i);
@@ -330,7 +336,7 @@ template <typename T>
 cudaError_t backward(const LogprobBackwardArgs& a, cudaStream_t stream) {
   const int nblk = div_up(div_up(a.V, Elem<T>::VEC) + 1, kBlockVecs);
   int c = 1;
-  while (c < kMaxCluster && nblk > 2 * kWarps * c) c *= 2;   // about two blocks a warp
+  while (c < 8 && nblk > 2 * kWarps * c) c *= 2;   // two blocks a warp and more
   return launch_rows(logprobs_backward_kernel<T>, a.N, c, 0, stream, a);
 }
 
@@ -341,7 +347,8 @@ cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t stream) {
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
   const int per_block = kBlockVecs * (a.dtype == DSPARK_F32 ? 4 : 8);
-  const int c = cluster_for(a.N, div_up(div_up(a.V, per_block) + 1, kMaxBlocks), sms);
+  const int nblk = div_up(a.V, per_block) + 1;
+  const int c = cluster_for(a.N, nblk, div_up(nblk, kMaxBlocks), sms);
   if (a.dtype == DSPARK_F32) return forward<float>(a, c, stream);
   if (a.dtype == DSPARK_BF16) return forward<__nv_bfloat16>(a, c, stream);
   return forward<__half>(a, c, stream);
