@@ -429,7 +429,8 @@ int dspark_round_ex(const float* U, const float* T, const void* W1, const void* 
  * zeros (alternatives -1 / -inf), with lens NULL every row counts.  Sums are
  * kept in fp32.  An entry of -inf has probability 0; a row of nothing else has
  * lse -inf, entropy 0, loss 0 and gradient 0.  A NaN or +inf in a row makes its
- * outputs NaN, which is how these calls report it (they have no status word).
+ * outputs NaN, which is how these calls report it: they take no workspace, and
+ * may run concurrently with any other call.
  *
  * dspark_token_logprobs: for row i and its token t = tokens[i]
  *   lse = log sum_v exp x_v, logp = x_t - lse, entropy = -sum_v p_v log p_v,
@@ -491,15 +492,11 @@ int dspark_token_logprobs_backward(const void* logits, int dtype, int64_t row_st
  * or NULL (1); zeros in rows that do not count.  It may be the logits
  * themselves when those are dense and of its type, and may not overlap them
  * otherwise.
- * Workspace (only with dlogits_out): dspark_distill_workspace_size bytes (0
- * when a size is out of range), 256-byte aligned; it holds nothing between calls.
  */
 int dspark_distill_loss(const void* logits, int dtype, int64_t row_stride, const int32_t* top_idx,
                         const float* top_val, const float* teacher_lse, const float* weight,
                         const int32_t* lens, int N, int R, int V, int K, float temperature,
-                        float* loss_out, float* stats_out, void* dlogits_out, int gdtype,
-                        void* workspace, size_t workspace_bytes, void* stream);
-size_t dspark_distill_workspace_size(int N, int V, int K);
+                        float* loss_out, float* stats_out, void* dlogits_out, int gdtype, void* stream);
 
 /*
  * The gradient of dspark_distill_loss alone, from its stats output and an
@@ -508,8 +505,7 @@ size_t dspark_distill_workspace_size(int N, int V, int K);
 int dspark_distill_loss_backward(const void* logits, int dtype, int64_t row_stride, const int32_t* top_idx,
                                  const float* top_val, const float* stats, const float* g,
                                  const float* teacher_lse, const int32_t* lens, int N, int R, int V, int K,
-                                 float temperature, void* dlogits_out, int gdtype,
-                                 void* workspace, size_t workspace_bytes, void* stream);
+                                 float temperature, void* dlogits_out, int gdtype, void* stream);
 
 /*
  * The Markov head outside the draft, for training it ([blog] section 4): the

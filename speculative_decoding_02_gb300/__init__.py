@@ -108,13 +108,10 @@ def _load():
     L.dspark_markov_logits.restype = i32
     L.dspark_markov_head_backward.argtypes = [vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp, sz, vp]
     L.dspark_markov_head_backward.restype = i32
-    L.dspark_distill_loss.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, vp, vp, vp, i32,
-                                      vp, sz, vp]
-    L.dspark_distill_workspace_size.argtypes = [i32, i32, i32]
-    L.dspark_distill_workspace_size.restype = sz
+    L.dspark_distill_loss.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, vp, vp, vp, i32, vp]
     L.dspark_distill_loss.restype = i32
     L.dspark_distill_loss_backward.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, vp,
-                                               i32, vp, sz, vp]
+                                               i32, vp]
     L.dspark_distill_loss_backward.restype = i32
     L.dspark_read_status.argtypes = [vp, ctypes.POINTER(i32), vp]
     L.dspark_read_status.restype = i32
@@ -548,14 +545,8 @@ def _distill_args(logits, top_idx, top_val, teacher_lse, rows, temperature):
     return dev, lead, N, R, V, stride, dt, K
 
 
-def distill_workspace(N, V, K, device):
-    """A workspace of distill_loss and distill_loss_backward for N rows."""
-    n = int(_load().dspark_distill_workspace_size(N, V, K))
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
-
-
 def distill_loss(logits, top_idx, top_val, temperature=1.0, teacher_lse=None, weight=None, rows=None, grad=False,
-                 grad_dtype=None, out=None, ws=None):
+                 grad_dtype=None, out=None):
     """Kullback-Leibler loss of a student's logits [..., V] against a teacher's K
     kept logits top_val [..., K] f32 at top_idx [..., K] i32 (-1: absent; K <= 128):
     loss [...] f32, stats [..., 2] f32 (for distill_loss_backward) and, with
@@ -565,9 +556,7 @@ def distill_loss(logits, top_idx, top_val, temperature=1.0, teacher_lse=None, we
     top_val / temperature: the teacher's remaining mass is matched, as one
     bucket, with the student's; None: the kept entries are renormalised.
     weight [...] f32 (None: 1) scales the gradient, not the loss.
-    rows as in token_logprobs; out as in token_logprobs_backward.  ws (with
-    grad): a distill_workspace to keep; by default one is allocated for the
-    call."""
+    rows as in token_logprobs; out as in token_logprobs_backward."""
     L = _load()
     dev, lead, N, R, V, stride, dt, K = _distill_args(logits, top_idx, top_val, teacher_lse, rows, temperature)
     _row_vector(weight, "weight", lead, dev)
@@ -577,19 +566,16 @@ def distill_loss(logits, top_idx, top_val, temperature=1.0, teacher_lse=None, we
     if gdt not in _ROW_DTYPES:
         raise TypeError(f"grad_dtype must be float32, bfloat16 or float16, got {gdt}")
     dlogits = _gradient_out(out, logits, gdt) if grad else None
-    if grad and ws is None:
-        ws = distill_workspace(N, V, K, dev)
     loss = torch.empty(lead, dtype=torch.float32, device=dev)
     stats = torch.empty((*lead, 2), dtype=torch.float32, device=dev)
     _launch(L.dspark_distill_loss, "distill_loss", dev, logits.data_ptr(), dt, stride, top_idx.data_ptr(),
             top_val.data_ptr(), _address(teacher_lse), _address(weight), _address(rows), N, R, V, K, temperature,
-            loss.data_ptr(), stats.data_ptr(), _address(dlogits), _ROW_DTYPES[gdt], _address(ws),
-            0 if ws is None else ws.numel())
+            loss.data_ptr(), stats.data_ptr(), _address(dlogits), _ROW_DTYPES[gdt])
     return loss, stats, dlogits
 
 
 def distill_loss_backward(logits, top_idx, top_val, stats, g, temperature=1.0, teacher_lse=None, rows=None,
-                          grad_dtype=None, out=None, ws=None):
+                          grad_dtype=None, out=None):
     """g * d loss / d logits of distill_loss from its stats and an upstream
     gradient g [...] f32; the other arguments as for that call."""
     L = _load()
@@ -600,10 +586,9 @@ def distill_loss_backward(logits, top_idx, top_val, stats, g, temperature=1.0, t
     if gdt not in _ROW_DTYPES:
         raise TypeError(f"grad_dtype must be float32, bfloat16 or float16, got {gdt}")
     out = _gradient_out(out, logits, gdt)
-    ws = distill_workspace(N, V, K, dev) if ws is None else ws
     _launch(L.dspark_distill_loss_backward, "distill_loss_backward", dev, logits.data_ptr(), dt, stride,
             top_idx.data_ptr(), top_val.data_ptr(), stats.data_ptr(), g.data_ptr(), _address(teacher_lse),
-            _address(rows), N, R, V, K, temperature, out.data_ptr(), _ROW_DTYPES[gdt], ws.data_ptr(), ws.numel())
+            _address(rows), N, R, V, K, temperature, out.data_ptr(), _ROW_DTYPES[gdt])
     return out
 
 

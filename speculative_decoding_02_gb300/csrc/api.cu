@@ -106,10 +106,6 @@ int distill_checks(const void* logits, int dtype, int64_t row_stride, const int3
   return DSPARK_OK;
 }
 
-int check_distill_ws(const void* ws, size_t ws_bytes, int N, int V, int K) {
-  return ws && aligned(ws, 256) && ws_bytes >= distill_workspace_bytes(N, V, K) ? DSPARK_OK : DSPARK_ERR_WORKSPACE;
-}
-
 }  // namespace
 
 extern "C" {
@@ -435,37 +431,29 @@ int dspark_markov_head_backward(const void* dlogits, const void* W1, const void*
   return cuda_status(launch_markov_head_backward(a, (cudaStream_t)stream));
 }
 
-size_t dspark_distill_workspace_size(int N, int V, int K) {
-  if (N <= 0 || V <= 0 || K <= 0 || N > kMaxRows || V > kMaxRowV || K > kMaxTop) return 0;
-  return distill_workspace_bytes(N, V, K);
-}
-
 int dspark_distill_loss(const void* logits, int dtype, int64_t row_stride, const int32_t* top_idx,
                         const float* top_val, const float* teacher_lse, const float* weight, const int32_t* lens,
                         int N, int R, int V, int K, float temperature, float* loss_out, float* stats_out,
-                        void* dlogits_out, int gdtype, void* workspace, size_t workspace_bytes, void* stream) {
+                        void* dlogits_out, int gdtype, void* stream) {
   DSPARK_TRY(distill_checks(logits, dtype, row_stride, top_idx, top_val, N, R, V, K, temperature, dlogits_out,
                             gdtype));
   if (N == 0) return DSPARK_OK;
   if (!loss_out || !stats_out) return DSPARK_ERR_INVALID;
-  if (dlogits_out) DSPARK_TRY(check_distill_ws(workspace, workspace_bytes, N, V, K));
   DistillArgs a{logits, dtype, row_stride, top_idx, top_val, teacher_lse, weight, lens, N, R, V, K, temperature,
-                1.f / temperature, loss_out, stats_out, nullptr, dlogits_out, dlogits_out ? gdtype : dtype,
-                workspace};
+                1.f / temperature, loss_out, stats_out, nullptr, dlogits_out, dlogits_out ? gdtype : dtype};
   return cuda_status(launch_distill(a, (cudaStream_t)stream));
 }
 
 int dspark_distill_loss_backward(const void* logits, int dtype, int64_t row_stride, const int32_t* top_idx,
                                  const float* top_val, const float* stats, const float* g, const float* teacher_lse,
                                  const int32_t* lens, int N, int R, int V, int K, float temperature,
-                                 void* dlogits_out, int gdtype, void* workspace, size_t workspace_bytes, void* stream) {
+                                 void* dlogits_out, int gdtype, void* stream) {
   DSPARK_TRY(distill_checks(logits, dtype, row_stride, top_idx, top_val, N, R, V, K, temperature, dlogits_out,
                             gdtype));
   if (N == 0) return DSPARK_OK;
   if (!stats || !g || !dlogits_out) return DSPARK_ERR_INVALID;
-  DSPARK_TRY(check_distill_ws(workspace, workspace_bytes, N, V, K));
   DistillArgs a{logits, dtype, row_stride, top_idx, top_val, teacher_lse, g, lens, N, R, V, K, temperature,
-                1.f / temperature, nullptr, nullptr, stats, dlogits_out, gdtype, workspace};
+                1.f / temperature, nullptr, nullptr, stats, dlogits_out, gdtype};
   return cuda_status(launch_distill(a, (cudaStream_t)stream));
 }
 

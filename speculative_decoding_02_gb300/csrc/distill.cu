@@ -15,11 +15,11 @@
 // almost everything): the kept entries, which a bitmap of the segment in shared
 // memory marks, leave the row's sum, and their exponentials are added afterwards.
 //
-// Two kernels, each bound by HBM.  The first sums a row by a cluster of 1 to 16
-// CTAs (logits_row.cuh), whose CTA 0 finishes the row: its loss and, into the
-// workspace, the coefficients of its gradient and the gradients of its kept
-// entries.  The second streams the gradient; it starts while the first one
-// ends (programmatic dependent launch), with its first loads under way.
+// A cluster of 1 to 16 CTAs takes a row (logits_row.cuh) and HBM bounds it.  The
+// loss needs one pass; the gradient a second one over the same part by the same
+// CTA, backwards, which L2 still holds when the rows in flight fit there, so
+// that HBM sees about one read and one write.  What depends on the teacher
+// alone is worked out while the first block's loads are under way.
 #include <algorithm>
 
 #include "logits_row.cuh"
@@ -29,37 +29,20 @@ namespace {
 
 using namespace lrow;
 
-constexpr int kMarkedPlaces = 262144;   // of a CTA's part of a row: a bitmap of 32 KB
-
-// What the first kernel leaves for the second.
-struct WsView {
-  float4* coef;      // [N] ref, cw, whether the row has a gradient
-  int* kept_at;      // [N][K] entry whose gradient is kept_g (-1: none)
-  float* kept_g;
-  size_t total;
-};
-__host__ __device__ inline WsView ws_view(void* ws, int N, int K) {
-  WsView v;
-  v.coef = ws_ptr<float4>(ws, 0);
-  size_t off = align256(16ull * N);
-  v.kept_at = ws_ptr<int>(ws, off);       off = align256(off + 4ull * N * K);
-  v.kept_g = ws_ptr<float>(ws, off);      off = align256(off + 4ull * N * K);
-  v.total = off;
-  return v;
-}
-
-__device__ __forceinline__ bool scored(const DistillArgs& p, int row) {
-  if (p.lens == nullptr) return true;
-  const int g = row / p.R;
-  return row - g * p.R < p.lens[g];
-}
+constexpr int kCtasPerSm = 4;
+constexpr int kMarkedPlaces = 262144;           // of a CTA's part of a row: a bitmap of 32 KB
+constexpr long long kFlightBytes = 96ll << 20;  // of the rows in flight with a gradient
 
 struct Shared {
   Stat part[kWarps];
   Stat cta;               // of this CTA's part, outside the kept entries with a tail
-  int idx[kMaxTop];       // the row's kept entries, -1: absent
+  // the row's kept entries
+  int idx[kMaxTop];       // -1: absent
   float p[kMaxTop];       // the teacher's probability
-  float red[3][kWarps];
+  float logp[kMaxTop];
+  float pv[kMaxTop];      // p(v) at the first entry of its index, -1 elsewhere
+  float z[kMaxTop];       // the student's logit
+  float red[4][kWarps];
 };
 
 // Sums over the CTA (every thread gets them): slot `which` of sh.red.
@@ -84,16 +67,17 @@ __device__ __forceinline__ float cta_max(Shared& sh, int which, float v) {
   return s;
 }
 
-// A row's loss and statistics and its gradient's coefficients, by one whole
-// CTA, from the row's state (`pass`; outside the kept entries with a tail) or
-// from the statistics of the forward call.
+// The teacher's side of a row and the student's logits there, by the CTA, into
+// sh; returns the state of the kept entries (with a tail), the rest's mass,
+// whether an index is out of range and whether an entry has mass.
+struct Kept {
+  Stat stat;
+  float p_rest;
+  bool bad, any;
+};
 template <typename T, bool kTail>
-__device__ void finish_row(Shared& sh, const DistillArgs& p, int row, bool pass, const Stat rest, float lse_in,
-                           float lse_rest_in) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  const T* rp = static_cast<const T*>(p.logits) + (size_t)row * p.row_stride;
-  const float nan = __int_as_float(0x7FC00000);
-  // entry k of the teacher, a thread each
+__device__ __forceinline__ Kept load_kept(Shared& sh, const DistillArgs& p, int row, const T* rp) {
+  const int tid = threadIdx.x;
   int idx = -1;
   float val = -INFINITY, z = 0.f;
   bool bad = false;
@@ -109,9 +93,7 @@ __device__ void finish_row(Shared& sh, const DistillArgs& p, int row, bool pass,
     }
   }
   if (tid < kMaxTop) sh.idx[tid] = idx;
-  const bool any = __syncthreads_or(val != -INFINITY);
-  bad = __syncthreads_or(bad);
-
+  Kept r;
   // log p_k and p_k (products and differences rounded once)
   float t = -INFINITY, base = 0.f;
   if (kTail) {
@@ -123,92 +105,36 @@ __device__ void finish_row(Shared& sh, const DistillArgs& p, int row, bool pass,
   }
   const float logp = t == -INFINITY ? -INFINITY : t - base;
   const float pk = t == -INFINITY ? 0.f : expf(logp);
-  if (tid < kMaxTop) sh.p[tid] = pk;
+  if (tid < kMaxTop) {
+    sh.p[tid] = pk;
+    sh.logp[tid] = logp;
+    sh.z[tid] = z;
+  }
   const float total = cta_add(sh, 2, pk);
-  const float p_rest = kTail ? (total > 1.f ? 0.f : 1.f - total) : 0.f;   // (a NaN total stays one)
+  r.p_rest = kTail ? (total > 1.f ? 0.f : 1.f - total) : 0.f;   // (a NaN total stays one)
   // p(v): equal indices add up in the first of them
   float pv = 0.f;
   bool first = idx >= 0;
-  if (first) {
-    for (int k = 0; k < p.K; ++k) {
-      if (sh.idx[k] != idx) continue;
-      if (k < tid) {
-        first = false;
-        break;
-      }
-      pv += sh.p[k];
-    }
+  for (int k = 0; first && k < p.K; ++k) {
+    if (sh.idx[k] != idx) continue;
+    first = k >= tid;
+    pv += sh.p[k];
   }
-
-  // the student's side
-  bool none = false;
-  float ref = 0.f, coef = 0.f, q_ref = 0.f, q_scale = 0.f, ls = 0.f, lse = 0.f, lse_rest = 0.f;
-  if (pass) {
-    Stat all = rest;
-    if (kTail) {
-      const float m = cta_max(sh, 0, first ? z : -INFINITY);
-      const float s = cta_add(sh, 1, first && m != -INFINITY ? expf((z - m) * p.inv_tau) : 0.f);
-      all = stat_reduce<2>(lane & 1 ? Stat{m, s, 0.f} : rest, p.inv_tau);
-    }
-    none = all.m == -INFINITY;
-    ls = none ? 0.f : logf(all.s);
-    lse = fmaf(all.m, p.inv_tau, ls);
-    lse_rest = rest.m == -INFINITY ? -INFINITY : fmaf(rest.m, p.inv_tau, logf(rest.s));
-    q_ref = all.m;
-    q_scale = 1.f / all.s;
-    ref = all.m;
-    coef = q_scale;
-    if (kTail) {
-      ref = rest.m == -INFINITY ? 0.f : rest.m;
-      const float q_rest = rest.m == -INFINITY ? 0.f : expf((rest.m - all.m) * p.inv_tau) * rest.s / all.s;
-      coef = rest.m == -INFINITY ? 0.f : (q_rest - p_rest) / rest.s;
-    }
-    if (any && stat_bad(all)) {
-      bad = true;
-      lse = lse_rest = nan;
-    }
-  } else {
-    none = lse_in == -INFINITY;
-    // the references in units of the logits, with what their rounding lost
-    q_ref = none ? 0.f : lse_in * p.tau;
-    q_scale = expf(-fmaf(lse_in, p.tau, -q_ref) * p.inv_tau);
-    ref = q_ref;
-    coef = q_scale;
-    if (kTail) {
-      ref = lse_rest_in == -INFINITY ? 0.f : lse_rest_in * p.tau;
-      coef = lse_rest_in == -INFINITY
-                 ? 0.f
-                 : (expf(lse_rest_in - lse_in) - p_rest) * expf(-fmaf(lse_rest_in, p.tau, -ref) * p.inv_tau);
-    }
+  if (tid < kMaxTop) sh.pv[tid] = first ? pv : -1.f;
+  r.stat = stat_empty();
+  if (kTail) {
+    r.stat.m = cta_max(sh, 3, first ? z : -INFINITY);
+    r.stat.s = cta_add(sh, 0, first && r.stat.m != -INFINITY ? expf((z - r.stat.m) * p.inv_tau) : 0.f);
   }
-  const bool on = (any || bad) && !none;
-  if (p.stats_in == nullptr) {
-    float L = !(pk == 0.f) ? pk * (logp - ((z - q_ref) * p.inv_tau - ls)) : 0.f;
-    L = cta_add(sh, 0, L);
-    if (kTail && !(p_rest == 0.f)) L += p_rest * (logf(p_rest) - (lse_rest - lse));
-    if (tid == 0) {
-      const bool counts = any || bad;
-      p.loss[row] = bad ? nan : (on ? L : 0.f);
-      p.stats[2 * (size_t)row] = bad ? nan : (counts ? lse : 0.f);
-      p.stats[2 * (size_t)row + 1] = bad ? nan : (counts ? (kTail ? lse_rest : lse) : 0.f);
-    }
-  }
-  if (bad) coef = q_scale = nan;
-  if (p.dlogits != nullptr) {
-    const WsView ws = ws_view(p.ws, p.N, p.K);
-    const float w = (p.weight != nullptr ? p.weight[row] : 1.f) * p.inv_tau;
-    if (tid == 0) ws.coef[row] = make_float4(ref, coef * w, on ? 1.f : 0.f, 0.f);
-    if (tid < p.K) {
-      ws.kept_at[(size_t)row * p.K + tid] = on && first ? idx : -1;
-      ws.kept_g[(size_t)row * p.K + tid] = w * (q_scale * ex2((z - q_ref) * p.inv_tau * kLog2e) - pv);
-    }
-  }
+  r.any = __syncthreads_or(val != -INFINITY);
+  r.bad = __syncthreads_or(bad);
+  return r;
 }
 
-// The first kernel.  kTail: the teacher's lse is given.  With p.stats_in (the
-// backward pass alone) only rows whose lse is too large to be used are summed.
-template <typename T, bool kTail>
-__global__ void __launch_bounds__(kThreads, 4) distill_sum_kernel(const DistillArgs p) {
+// kTail: the teacher's lse is given.  With p.stats_in the backward pass alone,
+// which takes the row's state anew only where its lse is too large to be used.
+template <typename T, typename G, bool kTail>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const DistillArgs p) {
   constexpr int VEC = Elem<T>::VEC;
   constexpr int kBlockPlaces = kBlockVecs * VEC;
   __shared__ Shared sh;
@@ -216,159 +142,186 @@ __global__ void __launch_bounds__(kThreads, 4) distill_sum_kernel(const DistillA
   cg::cluster_group cluster = cg::this_cluster();
   const int c = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int row = (int)(blockIdx.x / c);
-  const int tid = threadIdx.x, lane = tid & 31;
-  pdl_trigger();
-  const bool backward = p.stats_in != nullptr;
-  if (!scored(p, row)) {
-    if (rank == 0 && tid == 0) {
-      if (!backward) p.loss[row] = p.stats[2 * (size_t)row] = p.stats[2 * (size_t)row + 1] = 0.f;
-      if (p.dlogits != nullptr) ws_view(p.ws, p.N, p.K).coef[row] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    return;
-  }
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool backward = p.stats_in != nullptr, grad = p.dlogits != nullptr;
+  const float nan = __int_as_float(0x7FC00000);
+  const float scale = p.inv_tau * kLog2e;
+  const T* rp = static_cast<const T*>(p.logits) + (size_t)row * p.row_stride;
+  const Row<T> R(rp, p.V);
+  const BlockRange br = block_range(R.nvec, rank, c);
+  const int place0 = br.begin * kBlockPlaces - R.shift;   // entry at the part's first place
+  const int nblk = br.end - br.begin;
+  const int group = row / p.R;
+  bool on = p.lens == nullptr || row - group * p.R < p.lens[group];
   float lse_in = 0.f, lse_rest_in = 0.f;
-  if (backward) {
+  if (backward && on) {
     lse_in = p.stats_in[2 * (size_t)row];
     lse_rest_in = p.stats_in[2 * (size_t)row + 1];
   }
-  const bool pass = !backward || (lse_in != -INFINITY && fabsf(lse_in) > kLargeLse);
-  if (!pass) {
-    if (rank == 0) finish_row<T, kTail>(sh, p, row, false, stat_empty(), lse_in, lse_rest_in);
-    return;
-  }
-  const Row<T> R(static_cast<const T*>(p.logits) + (size_t)row * p.row_stride, p.V);
-  const BlockRange br = block_range(R.nvec, rank, c);
-  const int place0 = br.begin * kBlockPlaces - R.shift;   // entry at the part's first place
-  const int nblk = br.end - br.begin, words = nblk * (kBlockPlaces / 32);
-  unsigned char* block_marked = reinterpret_cast<unsigned char*>(marked + words);
-  auto mark = [&]() {
-    if constexpr (kTail) {
-      const int i = tid < p.K ? p.top_idx[(size_t)row * p.K + tid] : -1;
-      for (int k = tid; k < words; k += kThreads) marked[k] = 0;
-      for (int k = tid; k < nblk; k += kThreads) block_marked[k] = 0;
-      __syncthreads();
-      const int place = i - place0;
-      if (i >= 0 && i < p.V && place >= 0 && place < nblk * kBlockPlaces) {
-        atomicOr(&marked[place >> 5], 1u << (place & 31));
-        block_marked[place / kBlockPlaces] = 1;
-      }
-      __syncthreads();
-    }
+  const bool pass = on && (!backward || (lse_in != -INFINITY && fabsf(lse_in) > kLargeLse));
+
+  Kept kept;
+  kept.any = kept.bad = false;
+  // outside the kept entries the gradient is cw exp((x - ref) / tau), on one
+  // w (q_scale exp((x - q_ref) / tau) - p(v))
+  float ref = 0.f, cw = 0.f, q_ref = 0.f, q_scale = 0.f;
+  const float w = grad && on ? (p.weight != nullptr ? p.weight[row] : 1.f) * p.inv_tau : 0.f;
+
+  // The gradient goes through the part backwards: what was read last is surest
+  // to be in L2.  Its first block is under way while the CTAs meet.
+  uint4 cur[kVecPerLane], nxt[kVecPerLane];
+  int b = nblk > warp ? br.begin + warp + (nblk - 1 - warp) / kWarps * kWarps : -1;
+  auto first_block = [&]() {
+    if (grad && b >= 0) R.template load_block<Hold::kShort>(b, lane, cur);
   };
-  auto leave_out = [&](int b, uint4(&cur)[kVecPerLane]) {
-    if constexpr (kTail) {
-      if (!block_marked[b - br.begin]) return;
+
+  if (pass) {
+    const int words = nblk * (kBlockPlaces / 32);
+    unsigned char* block_marked = reinterpret_cast<unsigned char*>(marked + words);
+    auto before = [&]() {
+      if constexpr (kTail) {
+        for (int k = tid; k < words; k += kThreads) marked[k] = 0;
+        for (int k = tid; k < nblk; k += kThreads) block_marked[k] = 0;
+      }
+      kept = load_kept<T, kTail>(sh, p, row, rp);
+      if constexpr (kTail) {
+        const int place = tid < p.K && sh.idx[tid] >= 0 ? sh.idx[tid] - place0 : -1;
+        if (place >= 0 && place < nblk * kBlockPlaces) {
+          atomicOr(&marked[place >> 5], 1u << (place & 31));
+          block_marked[place / kBlockPlaces] = 1;
+        }
+        __syncthreads();
+      }
+    };
+    auto leave_out = [&](int b, uint4(&cur)[kVecPerLane]) {
+      if constexpr (kTail) {
+        if (!block_marked[b - br.begin]) return;
+#pragma unroll
+        for (int j = 0; j < kVecPerLane; ++j) {
+          const int place = ((b - br.begin) * kBlockVecs + j * 32 + lane) * VEC;
+          const uint32_t m = (marked[place >> 5] >> (place & 31)) & ((1u << VEC) - 1u);
+          if (m == 0) continue;
+          T* e = reinterpret_cast<T*>(&cur[j]);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i)
+            if (m >> i & 1u) e[i] = Elem<T>::from_float(-INFINITY);
+        }
+      }
+    };
+    stat_row<T, false, Hold::kLong>(R, br, scale, p.inv_tau, sh.part, &sh.cta, before, leave_out, Nothing());
+    cluster_arrive();
+    first_block();
+    cluster_wait();
+    const Stat rest = stat_cluster(cluster, &sh.cta, c, p.inv_tau);
+    cluster_arrive();   // (this CTA has read the others' shared memory)
+    const Stat all = kTail ? stat_reduce<2>(lane & 1 ? kept.stat : rest, p.inv_tau) : rest;
+    const bool bad = kept.bad || (kept.any && stat_bad(all));
+    const bool none = all.m == -INFINITY;
+    const float ls = none ? 0.f : logf(all.s);
+    q_ref = none ? 0.f : all.m;
+    q_scale = 1.f / all.s;
+    ref = q_ref;
+    cw = w * q_scale;
+    if (kTail) {
+      ref = rest.m == -INFINITY ? 0.f : rest.m;
+      const float q_rest = expf((rest.m - all.m) * p.inv_tau) * rest.s / all.s;
+      cw = rest.m == -INFINITY ? 0.f : w * ((q_rest - kept.p_rest) / rest.s);
+    }
+    on = (kept.any || bad) && !none;
+    if (bad) cw = q_scale = nan;
+    if (!backward && rank == 0) {
+      const float pk = tid < p.K ? sh.p[tid] : 0.f;
+      float L = cta_add(sh, 1, !(pk == 0.f) ? pk * (sh.logp[tid] - ((sh.z[tid] - q_ref) * p.inv_tau - ls)) : 0.f);
+      const float lse = fmaf(all.m, p.inv_tau, ls);
+      const float lse_rest = rest.m == -INFINITY ? -INFINITY : fmaf(rest.m, p.inv_tau, logf(rest.s));
+      if (kTail && !(kept.p_rest == 0.f)) L += kept.p_rest * (logf(kept.p_rest) - (lse_rest - lse));
+      if (tid == 0) {
+        const bool counts = kept.any || bad;
+        p.loss[row] = bad ? nan : (on ? L : 0.f);
+        p.stats[2 * (size_t)row] = bad ? nan : (counts ? lse : 0.f);
+        p.stats[2 * (size_t)row + 1] = bad ? nan : (counts ? (kTail ? lse_rest : lse) : 0.f);
+      }
+    }
+  } else if (on) {
+    first_block();
+    kept = load_kept<T, kTail>(sh, p, row, rp);
+    // the references in units of the logits, with what their rounding lost
+    on = (kept.any || kept.bad) && lse_in != -INFINITY;
+    q_ref = on ? lse_in * p.tau : 0.f;
+    q_scale = expf(-fmaf(lse_in, p.tau, -q_ref) * p.inv_tau);
+    ref = q_ref;
+    cw = w * q_scale;
+    if (kTail) {
+      ref = lse_rest_in == -INFINITY ? 0.f : lse_rest_in * p.tau;
+      cw = lse_rest_in == -INFINITY ? 0.f
+                                    : w * ((expf(lse_rest_in - lse_in) - kept.p_rest) *
+                                           expf(-fmaf(lse_rest_in, p.tau, -ref) * p.inv_tau));
+    }
+    if (kept.bad) cw = q_scale = nan;
+  } else if (!backward && rank == 0 && tid == 0) {
+    p.loss[row] = p.stats[2 * (size_t)row] = p.stats[2 * (size_t)row + 1] = 0.f;
+  }
+
+  if (grad) {
+    G* out = static_cast<G*>(p.dlogits) + (size_t)row * p.V;
+    // an output row whose vectors start where the logits' do is stored by vectors
+    const bool aligned = ((reinterpret_cast<uintptr_t>(out) - R.shift * sizeof(G)) & (VEC * sizeof(G) - 1)) == 0;
+    for (; b >= br.begin + warp; b -= kWarps) {
+      if (on && b - kWarps >= br.begin + warp) R.template load_block<Hold::kShort>(b - kWarps, lane, nxt);
+      const bool inside = aligned && R.inside(b);
 #pragma unroll
       for (int j = 0; j < kVecPerLane; ++j) {
-        const int place = ((b - br.begin) * kBlockVecs + j * 32 + lane) * VEC;
-        const uint32_t m = (marked[place >> 5] >> (place & 31)) & ((1u << VEC) - 1u);
-        if (m == 0) continue;
-        T* e = reinterpret_cast<T*>(&cur[j]);
+        const int i = b * kBlockVecs + j * 32 + lane, e0 = R.first_entry(i);
+        alignas(16) G g[VEC];
+        float x[VEC];
+        if (on) Elem<T>::unpack(cur[j], x);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
-          if (m >> i & 1u) e[i] = Elem<T>::from_float(-INFINITY);
+        for (int e = 0; e < VEC; ++e) g[e] = Elem<G>::from_float(on ? ex2((x[e] - ref) * scale) * cw : 0.f);
+        if (inside || (aligned && R.whole(i))) {
+          if constexpr (sizeof(G) * VEC == 16) __stcs(reinterpret_cast<uint4*>(out + e0), *reinterpret_cast<const uint4*>(g));
+          else __stcs(reinterpret_cast<uint2*>(out + e0), *reinterpret_cast<const uint2*>(g));
+        } else {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            if (e0 + e >= 0 && e0 + e < p.V) out[e0 + e] = g[e];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kVecPerLane; ++j) cur[j] = nxt[j];
+    }
+    if (on) {
+      __syncthreads();   // the kept entries' gradients replace what the loop stored there
+      if (tid < p.K && sh.pv[tid] != -1.f) {
+        const int place = sh.idx[tid] - place0;
+        if (place >= 0 && place < nblk * kBlockPlaces)
+          out[sh.idx[tid]] = Elem<G>::from_float(w * (q_scale * ex2((sh.z[tid] - q_ref) * scale) - sh.pv[tid]));
       }
     }
-  };
-  stat_row<T, false>(R, br, p.inv_tau * kLog2e, p.inv_tau, sh.part, &sh.cta, mark, leave_out, Nothing());
-  cluster.sync();
-  Stat v = stat_empty();
-  if (rank == 0) v = stat_cluster(cluster, &sh.cta, c, p.inv_tau);
-  cluster.sync();   // the other CTAs' shared memory is read until here
-  if (rank == 0) finish_row<T, kTail>(sh, p, row, true, v, 0.f, 0.f);
-}
-
-// The second kernel: c CTAs a row, one warp a block at a time.
-template <typename T, typename G>
-__global__ void __launch_bounds__(kThreads, 4) distill_gradient_kernel(const DistillArgs p, int c) {
-  constexpr int VEC = Elem<T>::VEC;
-  constexpr int kBlockPlaces = kBlockVecs * VEC;
-  const int row = (int)(blockIdx.x / c), rank = (int)(blockIdx.x % c);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const WsView ws = ws_view(p.ws, p.N, p.K);
-  const Row<T> R(static_cast<const T*>(p.logits) + (size_t)row * p.row_stride, p.V);
-  const BlockRange br = block_range(R.nvec, rank, c);
-  const int lo = max(br.begin * kBlockPlaces - R.shift, 0), hi = min(br.end * kBlockPlaces - R.shift, p.V);
-  const float scale = p.inv_tau * kLog2e;
-  const bool on = scored(p, row);
-  uint4 cur[kVecPerLane], nxt[kVecPerLane];
-  int b = br.begin + warp;
-  if (on && b < br.end) R.load_block(b, lane, cur);
-  pdl_wait();
-  const float4 k = __ldcg(ws.coef + row);
-  const bool live = k.z != 0.f;
-  const float ref = k.x, cw = k.y;
-  int kept = -1;
-  float kept_g = 0.f;
-  if (live && tid < p.K) {
-    kept = __ldcg(ws.kept_at + (size_t)row * p.K + tid);
-    kept_g = __ldcg(ws.kept_g + (size_t)row * p.K + tid);
   }
-  G* out = static_cast<G*>(p.dlogits) + (size_t)row * p.V;
-  // an output row whose vectors start where the logits' do is stored by vectors
-  const bool aligned = ((reinterpret_cast<uintptr_t>(out) - R.shift * sizeof(G)) & (VEC * sizeof(G) - 1)) == 0;
-  for (; b < br.end; b += kWarps) {
-    if (live && b + kWarps < br.end) R.load_block(b + kWarps, lane, nxt);
-    const bool inside = aligned && R.inside(b);
-#pragma unroll
-    for (int j = 0; j < kVecPerLane; ++j) {
-      const int i = b * kBlockVecs + j * 32 + lane, e0 = R.first_entry(i);
-      alignas(16) G g[VEC];
-      float x[VEC];
-      if (live) Elem<T>::unpack(cur[j], x);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) g[e] = Elem<G>::from_float(live ? ex2((x[e] - ref) * scale) * cw : 0.f);
-      if (inside || (aligned && R.whole(i))) {
-        if constexpr (sizeof(G) * VEC == 16) __stcs(reinterpret_cast<uint4*>(out + e0), *reinterpret_cast<const uint4*>(g));
-        else __stcs(reinterpret_cast<uint2*>(out + e0), *reinterpret_cast<const uint2*>(g));
-      } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          if (e0 + e >= 0 && e0 + e < p.V) out[e0 + e] = g[e];
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < kVecPerLane; ++j) cur[j] = nxt[j];
-  }
-  if (live) {
-    __syncthreads();   // the kept entries' gradients replace what the loop stored there
-    if (kept >= lo && kept < hi) out[kept] = Elem<G>::from_float(kept_g);
-  }
-}
-
-template <typename T>
-cudaError_t launch_sum(const DistillArgs& a, int sms, cudaStream_t stream) {
-  constexpr int kBlockPlaces = kBlockVecs * Elem<T>::VEC;
-  const int nblk = div_up(a.V, kBlockPlaces) + 1;
-  // (a backward pass seldom sums a row)
-  const int least = div_up(nblk, kMarkedPlaces / kBlockPlaces);
-  int c = 1;
-  if (a.stats_in == nullptr) c = cluster_for(a.N, nblk, least, sms);
-  else while (c < least) c *= 2;
-  const bool tail = a.teacher_lse != nullptr;
-  const int smem = tail ? div_up(nblk, c) * (kBlockPlaces / 8 + 1) : 0;
-  auto kern = tail ? distill_sum_kernel<T, true> : distill_sum_kernel<T, false>;
-  return launch_rows(kern, a.N, c, smem, stream, a);
+  if (pass) cluster_wait();   // the others have read this one's
 }
 
 template <typename T, typename G>
 cudaError_t launch(const DistillArgs& a, cudaStream_t stream) {
+  constexpr int kBlockPlaces = kBlockVecs * Elem<T>::VEC;
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  if ((e = launch_sum<T>(a, sms, stream)) != cudaSuccess || a.dlogits == nullptr) return e;
-  const int nblk = div_up(a.V, kBlockVecs * Elem<T>::VEC) + 1;
-  const int c = div_up(nblk, 8 * kWarps);   // at most eight blocks a warp
-  if ((long long)a.N * c > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-  return launch_pdl(distill_gradient_kernel<T, G>, dim3((unsigned)a.N * c), dim3(kThreads), 0, stream, a, c);
+  const int nblk = div_up(a.V, kBlockPlaces) + 1;
+  int least = div_up(nblk, kMarkedPlaces / kBlockPlaces);
+  if (a.stats_in != nullptr) {
+    least = std::max(least, std::min(div_up(nblk, 8 * kWarps), 8));   // eight blocks a warp, or more
+  } else if (a.dlogits != nullptr) {
+    const long long flight = (long long)a.V * (long long)sizeof(T) * std::min(a.N, kCtasPerSm * sms);
+    least = std::max(least, (int)std::min<long long>((flight + kFlightBytes - 1) / kFlightBytes, kMaxCluster));
+  }
+  const int c = cluster_for(a.N, nblk, least, sms);
+  const bool tail = a.teacher_lse != nullptr;
+  const int smem = tail ? div_up(nblk, c) * (kBlockPlaces / 8 + 1) : 0;
+  return launch_rows(tail ? distill_kernel<T, G, true> : distill_kernel<T, G, false>, a.N, c, smem, stream, a);
 }
 
 }  // namespace
-
-size_t distill_workspace_bytes(int N, int V, int K) {
-  (void)V;
-  return ws_view(nullptr, N, K).total;
-}
 
 cudaError_t launch_distill(const DistillArgs& a, cudaStream_t stream) {
   if (a.dtype == DSPARK_F32)

@@ -291,9 +291,7 @@ struct DistillArgs {
   const float* stats_in;      // [N][2]: the backward pass alone (no loss, no stats)
   void* dlogits;              // [N][V] dense or null; may be the logits
   int gdtype;
-  void* ws;                   // distill_workspace_bytes(N, V, K)
 };
-size_t distill_workspace_bytes(int N, int V, int K);
 cudaError_t launch_distill(const DistillArgs& a, cudaStream_t stream);
 
 }  // namespace dspark

@@ -81,12 +81,27 @@ struct Elem<__half> {
   }
 };
 
+// How long L2 should hold what a load brings in.
+enum class Hold { kNormal, kLong, kShort };
+template <Hold H>
 __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
   uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
+  if constexpr (H == Hold::kNormal) {
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+  } else {
+    uint64_t policy;
+    if constexpr (H == Hold::kLong)
+      asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(policy));
+    else
+      asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p), "l"(policy)
+                 : "memory");
+  }
   return v;
 }
 
@@ -110,7 +125,10 @@ struct Row {
     return e0 >= 0 && e0 + Elem<T>::VEC <= V;
   }
   // Vector i with -inf in the places outside the row (i >= nvec: all of them).
-  __device__ __forceinline__ uint4 load(int i) const { return whole(i) ? ld_stream(base + i) : load_edge(i); }
+  template <Hold H = Hold::kNormal>
+  __device__ __forceinline__ uint4 load(int i) const {
+    return whole(i) ? ld_stream<H>(base + i) : load_edge(i);
+  }
   __device__ __noinline__ uint4 load_edge(int i) const {
     uint4 v = make_uint4(Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf);
     T* p = reinterpret_cast<T*>(&v);
@@ -124,14 +142,15 @@ struct Row {
     return first_entry(b * kBlockVecs) >= 0 && first_entry((b + 1) * kBlockVecs) <= V;
   }
   // This lane's vectors of block b.
+  template <Hold H = Hold::kNormal>
   __device__ __forceinline__ void load_block(int b, int lane, uint4 (&r)[kVecPerLane]) const {
     const int i0 = b * kBlockVecs + lane;
     if (inside(b)) {
 #pragma unroll
-      for (int j = 0; j < kVecPerLane; ++j) r[j] = ld_stream(base + i0 + j * 32);
+      for (int j = 0; j < kVecPerLane; ++j) r[j] = ld_stream<H>(base + i0 + j * 32);
     } else {
 #pragma unroll
-      for (int j = 0; j < kVecPerLane; ++j) r[j] = load(i0 + j * 32);
+      for (int j = 0; j < kVecPerLane; ++j) r[j] = load<H>(i0 + j * 32);
     }
   }
 };
@@ -318,21 +337,21 @@ __device__ __forceinline__ void cta_stat(const LaneStat& st, float inv, Stat* pa
 }
 
 // The state of this CTA's blocks of a row, read from global memory, in *out
-// (behind a barrier).  before() runs once the first loads are in flight;
+// (behind a barrier).  before() runs once the first two blocks' loads are in flight;
 // each(b, vectors) may change a block's vectors before they are taken in, and
 // seen(b, lane maximum, block maximum) sees what the block holds.  The next
-// block's loads are in flight while one is taken in.
-template <typename T, bool kEntropy, typename Before, typename Each, typename Seen>
+// blocks' loads are in flight while one is taken in.
+template <typename T, bool kEntropy, Hold H = Hold::kNormal, typename Before, typename Each, typename Seen>
 __device__ __forceinline__ void stat_row(const Row<T>& R, const BlockRange& br, float scale, float inv, Stat* part,
                                          Stat* out, Before before, Each each, Seen seen) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   LaneStat st = lane_stat_empty();
   uint4 cur[kVecPerLane], nxt[kVecPerLane];
   int b = br.begin + warp;
-  if (b < br.end) R.load_block(b, lane, cur);
+  if (b < br.end) R.template load_block<H>(b, lane, cur);
+  if (b + kWarps < br.end) R.template load_block<H>(b + kWarps, lane, nxt);
   before();
   for (; b < br.end; b += kWarps) {
-    if (b + kWarps < br.end) R.load_block(b + kWarps, lane, nxt);
     each(b, cur);
     const float lm = lane_max(cur, (const T*)nullptr);
     const float bm = warp_max_nan(lm);
@@ -340,6 +359,7 @@ __device__ __forceinline__ void stat_row(const Row<T>& R, const BlockRange& br, 
     stat_block<T, kEntropy>(st, cur, bm, scale);
 #pragma unroll
     for (int j = 0; j < kVecPerLane; ++j) cur[j] = nxt[j];
+    if (b + 2 * kWarps < br.end) R.template load_block<H>(b + 2 * kWarps, lane, nxt);
   }
   cta_stat(st, inv, part, out);
 }
@@ -372,13 +392,17 @@ __device__ __forceinline__ bool stat_bad(const Stat& v) { return !(v.m < INFINIT
 // lost beside it) they take the row's state anew.
 constexpr float kLargeLse = 1024.f;
 
-// CTAs a row (a power of two): at least `least`, and for few rows as many more
-// as give each SM about two while every warp keeps a block.
+// CTAs a row: at least `least` (1 to 16), and for few rows as many more as give
+// each SM about two while every warp keeps a block.
 inline int cluster_for(int rows, int nblk, int least, int sms) {
-  int c = 1;
-  while (c < kMaxCluster && (c < least || ((long long)rows * c <= sms && nblk > kWarps * c))) c *= 2;
+  int c = least;
+  while (2 * c <= kMaxCluster && (long long)rows * c <= sms && nblk > kWarps * c) c *= 2;
   return c;
 }
+
+// The cluster's barrier in its two halves.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // Launches kern with clusters of c CTAs, c * rows of them.
 template <typename... KArgs, typename... Args>

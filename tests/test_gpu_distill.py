@@ -188,9 +188,8 @@ def test_bad_rows_are_reported():
     S[1, 3] = math.inf
     i[2, 1] = 999
     i[3, 5] = -2
-    ws = ds.distill_workspace(5, 999, 6, "cuda")
-    loss, stats, grad = ds.distill_loss(S, i, v, teacher_lse=t, grad=True, ws=ws)
-    back = ds.distill_loss_backward(S, i, v, clean[1], torch.ones(5, device="cuda"), teacher_lse=t, ws=ws)
+    loss, stats, grad = ds.distill_loss(S, i, v, teacher_lse=t, grad=True)
+    back = ds.distill_loss_backward(S, i, v, clean[1], torch.ones(5, device="cuda"), teacher_lse=t)
     assert torch.isnan(loss[:4]).all() and torch.isnan(grad[:4]).all()
     assert torch.isnan(back[2:4]).all() and torch.isfinite(back[4]).all()
     assert torch.equal(loss[4], clean[0][4]) and torch.equal(grad[4], clean[2][4])

@@ -63,14 +63,12 @@ def test_token_logprobs_backward_arguments(lib):
 def test_distill_arguments(lib):
     p, odd = _fake(), _fake(0x10002)
 
-    def call(logits=p, dtype=0, stride=100, ti=p, tv=p, N=4, R=2, V=100, K=5, tau=1.0, loss=p, stats=p, dl=p, gd=0,
-             ws=_fake(0x100000), n=1 << 30):
+    def call(logits=p, dtype=0, stride=100, ti=p, tv=p, N=4, R=2, V=100, K=5, tau=1.0, loss=p, stats=p, dl=p, gd=0):
         return lib.dspark_distill_loss(logits, dtype, stride, ti, tv, None, None, None, N, R, V, K, tau, loss, stats,
-                                       dl, gd, ws, n, None)
+                                       dl, gd, None)
 
-    def back(stats=p, g=p, dl=p, K=5, tau=1.0, ws=_fake(0x100000), n=1 << 30):
-        return lib.dspark_distill_loss_backward(p, 0, 100, p, p, stats, g, None, None, 4, 2, 100, K, tau, dl, 0, ws, n,
-                                                None)
+    def back(stats=p, g=p, dl=p, K=5, tau=1.0):
+        return lib.dspark_distill_loss_backward(p, 0, 100, p, p, stats, g, None, None, 4, 2, 100, K, tau, dl, 0, None)
 
     for kw in (dict(logits=None), dict(ti=None), dict(tv=None), dict(loss=None), dict(stats=None), dict(K=0),
                dict(tau=0.0), dict(tau=-1.0), dict(tau=float("inf")), dict(tau=float("nan")), dict(tau=1e-44),
@@ -79,11 +77,6 @@ def test_distill_arguments(lib):
     for kw in (dict(K=129), dict(gd=2), dict(dtype=1, gd=0), dict(dtype=2, gd=1)):
         assert call(**kw) == ds.ERR_UNSUPPORTED, kw
     assert call(N=0, R=1) == ds.OK
-    need = lib.dspark_distill_workspace_size(4, 100, 5)
-    assert need > 0 and lib.dspark_distill_workspace_size(0, 100, 5) == 0
-    for f in (call, back):
-        for kw in (dict(ws=None), dict(ws=_fake(0x100010)), dict(n=need - 1)):
-            assert f(**kw) == ds.ERR_WORKSPACE, kw
     for kw in (dict(stats=None), dict(g=None), dict(dl=None), dict(K=0), dict(tau=0.0)):
         assert back(**kw) == ds.ERR_INVALID, kw
 
