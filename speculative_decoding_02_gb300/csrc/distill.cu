@@ -208,12 +208,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
         }
       }
     };
-    stat_row<T, false, Hold::kLong>(R, br, scale, p.inv_tau, sh.part, &sh.cta, before, leave_out, Nothing());
-    cluster_arrive();
+    stat_row<T, false, false, Hold::kLong>(R, br, scale, p.inv_tau, sh.part, &sh.cta, before, leave_out, Nothing());
+    cluster_arrive(c);
     first_block();
-    cluster_wait();
+    cluster_wait(c);
     const Stat rest = stat_cluster(cluster, &sh.cta, c, p.inv_tau);
-    cluster_arrive();   // (this CTA has read the others' shared memory)
+    cluster_arrive(c);   // (this CTA has read the others' shared memory)
     const Stat all = kTail ? stat_reduce<2>(lane & 1 ? kept.stat : rest, p.inv_tau) : rest;
     const bool bad = kept.bad || (kept.any && stat_bad(all));
     const bool none = all.m == -INFINITY;
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
       }
     }
   }
-  if (pass) cluster_wait();   // the others have read this one's
+  if (pass && c > 1) cluster_wait(c);   // the others have read this one's
 }
 
 template <typename T, typename G>

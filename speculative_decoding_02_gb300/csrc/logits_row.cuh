@@ -184,35 +184,39 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// The largest of a lane's four vectors of a block (NaN if one is).
-__device__ __forceinline__ float lane_max(const uint4 (&r)[kVecPerLane], const float*) {
-  float m = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < kVecPerLane; ++j) {
-    float f[4];
-    Elem<float>::unpack(r[j], f);
-    m = max_nan(m, max_nan(max_nan(f[0], f[1]), max_nan(f[2], f[3])));
-  }
-  return m;
+// The largest of a vector's entries (NaN if one is).
+__device__ __forceinline__ float vec_max(uint4 r, const float*) {
+  float f[4];
+  Elem<float>::unpack(r, f);
+  return max_nan(max_nan(f[0], f[1]), max_nan(f[2], f[3]));
 }
 template <typename T2>
-__device__ __forceinline__ T2 lane_max2(const uint4 (&r)[kVecPerLane]) {
-  T2 m = *reinterpret_cast<const T2*>(&r[0].x);
-#pragma unroll
-  for (int j = 0; j < kVecPerLane; ++j) {
-    const T2* q = reinterpret_cast<const T2*>(&r[j]);
-    m = __hmax2_nan(m, __hmax2_nan(__hmax2_nan(q[0], q[1]), __hmax2_nan(q[2], q[3])));
-  }
-  return m;
+__device__ __forceinline__ T2 vec_max2(const uint4& r) {
+  const T2* q = reinterpret_cast<const T2*>(&r);
+  return __hmax2_nan(__hmax2_nan(q[0], q[1]), __hmax2_nan(q[2], q[3]));
+}
+__device__ __forceinline__ float vec_max(uint4 r, const __nv_bfloat16*) {
+  const __nv_bfloat162 m = vec_max2<__nv_bfloat162>(r);
+  return max_nan(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float vec_max(uint4 r, const __half*) {
+  const __half2 m = vec_max2<__half2>(r);
+  return max_nan(__low2float(m), __high2float(m));
+}
+// The largest of a lane's four vectors of a block.
+__device__ __forceinline__ float lane_max(const uint4 (&r)[kVecPerLane], const float* t) {
+  return max_nan(max_nan(vec_max(r[0], t), vec_max(r[1], t)), max_nan(vec_max(r[2], t), vec_max(r[3], t)));
+}
+template <typename T2>
+__device__ __forceinline__ float lane_max2(const uint4 (&r)[kVecPerLane]) {
+  const T2 m = __hmax2_nan(__hmax2_nan(vec_max2<T2>(r[0]), vec_max2<T2>(r[1])),
+                           __hmax2_nan(vec_max2<T2>(r[2]), vec_max2<T2>(r[3])));
+  return max_nan(__low2float(m), __high2float(m));
 }
 __device__ __forceinline__ float lane_max(const uint4 (&r)[kVecPerLane], const __nv_bfloat16*) {
-  const __nv_bfloat162 m = lane_max2<__nv_bfloat162>(r);
-  return max_nan(__low2float(m), __high2float(m));
+  return lane_max2<__nv_bfloat162>(r);
 }
-__device__ __forceinline__ float lane_max(const uint4 (&r)[kVecPerLane], const __half*) {
-  const __half2 m = lane_max2<__half2>(r);
-  return max_nan(__low2float(m), __high2float(m));
-}
+__device__ __forceinline__ float lane_max(const uint4 (&r)[kVecPerLane], const __half*) { return lane_max2<__half2>(r); }
 
 // Softmax state: maximum, sum exp(x - m), sum exp(x - m) (m - x).
 struct Stat {
@@ -338,10 +342,11 @@ __device__ __forceinline__ void cta_stat(const LaneStat& st, float inv, Stat* pa
 
 // The state of this CTA's blocks of a row, read from global memory, in *out
 // (behind a barrier).  before() runs once the first two blocks' loads are in flight;
-// each(b, vectors) may change a block's vectors before they are taken in, and
-// seen(b, lane maximum, block maximum) sees what the block holds.  The next
-// blocks' loads are in flight while one is taken in.
-template <typename T, bool kEntropy, Hold H = Hold::kNormal, typename Before, typename Each, typename Seen>
+// each(b, vectors) may change a block's vectors before they are taken in.  With
+// kSeen seen(b, lane maximum, float4) sees a block's maxima: those of its four
+// quarters (one vector of every lane).  The next blocks' loads are in flight
+// while one is taken in.
+template <typename T, bool kEntropy, bool kSeen, Hold H = Hold::kNormal, typename Before, typename Each, typename Seen>
 __device__ __forceinline__ void stat_row(const Row<T>& R, const BlockRange& br, float scale, float inv, Stat* part,
                                          Stat* out, Before before, Each each, Seen seen) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -353,9 +358,19 @@ __device__ __forceinline__ void stat_row(const Row<T>& R, const BlockRange& br, 
   before();
   for (; b < br.end; b += kWarps) {
     each(b, cur);
-    const float lm = lane_max(cur, (const T*)nullptr);
-    const float bm = warp_max_nan(lm);
-    seen(b, lm, bm);
+    float bm;
+    if constexpr (kSeen) {
+      static_assert(kVecPerLane == 4, "four quarters");
+      float v[4], q[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = vec_max(cur[j], (const T*)nullptr);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q[j] = warp_max_nan(v[j]);
+      bm = max_nan(max_nan(q[0], q[1]), max_nan(q[2], q[3]));
+      seen(b, max_nan(max_nan(v[0], v[1]), max_nan(v[2], v[3])), make_float4(q[0], q[1], q[2], q[3]));
+    } else {
+      bm = warp_max_nan(lane_max(cur, (const T*)nullptr));
+    }
     stat_block<T, kEntropy>(st, cur, bm, scale);
 #pragma unroll
     for (int j = 0; j < kVecPerLane; ++j) cur[j] = nxt[j];
@@ -368,6 +383,7 @@ __device__ __forceinline__ void stat_row(const Row<T>& R, const BlockRange& br, 
 // same on every lane; behind a cluster barrier, and another one has to follow
 // before a CTA leaves.
 __device__ __forceinline__ Stat stat_cluster(cg::cluster_group& cluster, Stat* cta, int c, float inv) {
+  if (c == 1) return *cta;
   const int lane = threadIdx.x & 31;
   Stat v = stat_reduce<kMaxCluster>(lane < c ? *cluster.map_shared_rank(cta, lane) : stat_empty(), inv);
   v.m = __shfl_sync(0xffffffffu, v.m, 0);
@@ -376,11 +392,24 @@ __device__ __forceinline__ Stat stat_cluster(cg::cluster_group& cluster, Stat* c
   return v;
 }
 
+// The cluster's barrier, whole and in its two halves (one CTA: the CTA's).
+__device__ __forceinline__ void cluster_arrive(int c) {
+  if (c > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait(int c) {
+  if (c > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  else __syncthreads();
+}
+__device__ __forceinline__ void cluster_meet(int c) {
+  cluster_arrive(c);
+  cluster_wait(c);
+}
+
 // A hook of stat_row that does nothing.
 struct Nothing {
   __device__ __forceinline__ void operator()() const {}
   __device__ __forceinline__ void operator()(int, uint4 (&)[kVecPerLane]) const {}
-  __device__ __forceinline__ void operator()(int, float, float) const {}
+  __device__ __forceinline__ void operator()(int, float, float4) const {}
 };
 
 // A NaN or +inf was in the row.
@@ -399,10 +428,6 @@ inline int cluster_for(int rows, int nblk, int least, int sms) {
   while (2 * c <= kMaxCluster && (long long)rows * c <= sms && nblk > kWarps * c) c *= 2;
   return c;
 }
-
-// The cluster's barrier in its two halves.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // Launches kern with clusters of c CTAs, c * rows of them.
 template <typename... KArgs, typename... Args>

@@ -5,18 +5,22 @@
 //   dx_v = g_logp (1[v = t] - p_v) - g_H p_v (log p_v + H)
 //
 // Forward: one pass over the row (logits_row.cuh); HBM bounds it.  A cluster
-// of 1 to 8 CTAs takes a row; their states and top lists meet in CTA 0 through
+// of 1 to 16 CTAs takes a row; their states and candidates meet in CTA 0 through
 // distributed shared memory.  The top entries cost the pass one maximum per
-// lane and one stored maximum per block:
-//   1. the K-th largest of the CTA's 256 lane maxima is a lower bound of the row
-//      part's K-th largest entry (K distinct entries are at least that large);
-//   2. only the blocks whose maximum reaches it are read again (from L2), and
-//      their entries that reach it become candidates, about K (1 + K / 512)
-//      of them in a row of no particular order;
+// lane and one stored maximum per quarter of a block:
+//   1. the K-th largest of the lanes' maxima (256 of each CTA), or a little less
+//      by a histogram, is a lower bound of the row's K-th largest entry (K
+//      distinct entries are at least that large);
+//   2. only the quarters whose maximum reaches it are read again (from L2), and
+//      their entries that reach it become candidates: hardly more than K in a
+//      row of no particular order;
 //   3. a candidate's rank is the number of larger ones (64-bit keys of value,
-//      then lower index, so no two are equal and ties go to the lowest index).
-// Rows whose candidates overflow the buffer (thousands of equal or ascending
-// entries) find the K-th largest key by bisection over its 64 bits instead.
+//      then lower index, so no two are equal and ties go to the lowest index);
+//      more than 512 of them are sorted instead.
+// Where the candidates overflow their buffer (thousands of equal or ascending
+// entries) each CTA finds its own K largest by bisection over the keys' bits.
+#include <float.h>
+
 #include "logits_row.cuh"
 
 namespace dspark {
@@ -24,25 +28,25 @@ namespace {
 
 using namespace lrow;
 
-constexpr int kMaxBlocks = 1024;     // blocks of one CTA's part of a row
+constexpr int kMaxBlocks = 512;      // blocks of one CTA's part of a row
 constexpr int kCandidates = 4096;
-constexpr int kRankDirect = 512;     // candidates ranked by counting; more are bisected first
-// the order key (see argmax_key) of -inf, which is never an alternative
-constexpr uint32_t kNegInfOrder = 0x007FFFFFu;
-
+constexpr int kRankDirect = 512;     // candidates ranked by counting; more are sorted
 struct Shared {
   Stat part[kWarps];
   Stat cta;
-  int ncand, nlist, count;
-  float bmax[kMaxBlocks];
-  unsigned long long cand[kCandidates];
-  unsigned long long list[kMaxTop];
+  int count[2][kWarps];
+  int ncand;
+  float lane_max[kThreads];                   // each lane's largest entry
+  float2 range[kWarps];
+  int bins[256];
+  int cut;
+  float4 quarter[kMaxBlocks];                 // maxima of each block's quarters
+  unsigned long long cand[kCandidates];       // (CTA 0's)
   unsigned long long sorted[kMaxTop];
 };
 static_assert(sizeof(Shared) <= 48 * 1024, "static shared memory");
-static_assert(kMaxCluster * kMaxTop <= kCandidates, "CTA 0 gathers every list in its candidate buffer");
+static_assert(kMaxCluster * kMaxTop <= kCandidates, "the lists of all CTAs");
 
-__device__ __forceinline__ uint32_t order32(float x) { return (uint32_t)(argmax_key(x + 0.0f, 0) >> 32); }
 __device__ __forceinline__ unsigned long long entry_key(float x, int v) { return argmax_key(x + 0.0f, v); }
 
 // The token of a row and whether the row is scored.
@@ -59,121 +63,184 @@ __device__ __forceinline__ bool row_token(const LogprobArgs& p, int row, int* to
   return true;
 }
 
-// Adds up `mine` over the CTA (every thread gets the sum).
-__device__ __forceinline__ int cta_sum(int mine, int* slot) {
+// Adds up `mine` over the CTA (every thread gets the sum) with one barrier;
+// calls alternate `which`.
+__device__ __forceinline__ int cta_sum(Shared& sh, int which, int mine) {
   const int w = __reduce_add_sync(0xffffffffu, mine);
+  if ((threadIdx.x & 31) == 0) sh.count[which][threadIdx.x >> 5] = w;
   __syncthreads();
-  if (threadIdx.x == 0) *slot = 0;
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) atomicAdd(slot, w);
-  __syncthreads();
-  return *slot;
-}
-
-// The K-th largest key: the largest 64-bit value that at least K keys reach,
-// bit by bit.  count(t) gives this thread's share of the keys >= t.
-template <typename Count>
-__device__ unsigned long long kth_largest(int K, int* slot, Count count) {
-  unsigned long long t = 0;
-  for (int bit = 63; bit >= 0; --bit) {
-    const unsigned long long c = t | (1ull << bit);
-    if (cta_sum(count(c), slot) >= K) t = c;
-  }
-  return t;
-}
-
-__device__ __forceinline__ void append(Shared& sh, unsigned long long key) {
-  const int i = atomicAdd(&sh.nlist, 1);
-  if (i < kMaxTop) sh.list[i] = key;
-}
-
-__device__ __forceinline__ float order_value(uint32_t o) { return argmax_key_value((unsigned long long)o << 32); }
-
-// Calls f(key) for every entry that reaches the order t0, block by block of
-// this warp's.
-template <typename T, typename F>
-__device__ __forceinline__ void for_candidates(const Row<T>& R, const BlockRange& br, const float* bmax, uint32_t t0,
-                                               int warp, int lane, F f) {
-  const float least = order_value(t0);
-  const int mine = br.begin + warp;   // this warp's blocks: mine, mine + kWarps, ...
-  for (int b0 = mine; b0 < br.end; b0 += 32 * kWarps) {
-    const int bl = b0 + lane * kWarps;
-    unsigned hit = __ballot_sync(0xffffffffu, bl < br.end && !(bmax[bl < br.end ? bl - br.begin : 0] < least));
-    for (; hit != 0; hit &= hit - 1) {
-      const int b = b0 + (__ffs(hit) - 1) * kWarps;
-      uint4 r[kVecPerLane];
-      R.load_block(b, lane, r);
-      if (lane_max(r, (const T*)nullptr) < least) continue;
+  int s = 0;
 #pragma unroll
-      for (int j = 0; j < kVecPerLane; ++j) {
+  for (int i = 0; i < kWarps; ++i) s += sh.count[which][i];
+  return s;
+}
+
+// Calls f(key) for every entry of this warp's blocks that reaches `least`.
+template <typename T, typename F>
+__device__ __forceinline__ void for_candidates(const Shared& sh, const Row<T>& R, const BlockRange& br, float least, F f) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // eight blocks at a time, a lane for each of their 32 quarters
+  for (int b0 = br.begin + warp; b0 < br.end; b0 += 8 * kWarps) {
+    const int bl = b0 + (lane >> 2) * kWarps;
+    const float* q = reinterpret_cast<const float*>(sh.quarter + (bl < br.end ? bl - br.begin : 0));
+    unsigned hit = __ballot_sync(0xffffffffu, bl < br.end && !(q[lane & 3] < least));
+    auto vec_of = [&](unsigned h) {
+      const int l = __ffs(h) - 1;
+      return (b0 + (l >> 2) * kWarps) * kBlockVecs + (l & 3) * 32 + lane;
+    };
+    uint4 nxt = make_uint4(0, 0, 0, 0);
+    if (hit != 0) nxt = R.load(vec_of(hit));
+    while (hit != 0) {
+      const int i = vec_of(hit);
+      const uint4 r = nxt;
+      hit &= hit - 1;
+      if (hit != 0) nxt = R.load(vec_of(hit));
+      if (!(vec_max(r, (const T*)nullptr) < least)) {
         float v[Elem<T>::VEC];
-        Elem<T>::unpack(r[j], v);
-        const int e0 = R.first_entry(b * kBlockVecs + j * 32 + lane);
+        Elem<T>::unpack(r, v);
 #pragma unroll
         for (int e = 0; e < Elem<T>::VEC; ++e)
-          if (v[e] >= least) f(entry_key(v[e], e0 + e));
+          if (v[e] >= least) f(entry_key(v[e], R.first_entry(i) + e));
       }
+      __syncwarp();
     }
-    __syncwarp();
   }
 }
 
-// The CTA's K largest entries, in no order, into sh.list; their count into
-// sh.nlist.  tmax: the largest entry this thread has read.
-template <typename T>
-__device__ void cta_top(Shared& sh, const Row<T>& R, const BlockRange& br, float tmax, int K, int warp, int lane) {
-  const int tid = threadIdx.x;
-  const uint32_t mine = order32(tmax);
-  uint32_t t0 = 0;
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t c = t0 | (1u << bit);
-    const int n = __syncthreads_count(mine >= c);
-    if (n >= K) t0 = c;
-    if (n >= K && n <= K + K / 8) break;   // (any lower bound will do)
+// A lower bound of the row's K-th largest entry: about the K-th largest of the
+// cluster's lane maxima.  They are counted in 256 bins of equal width between
+// the smallest and the largest; the bound is the smallest one in the bins down
+// to that of the K-th.  Fewer than K maxima above -inf: the lowest number.
+__device__ __forceinline__ float lower_bound(Shared& sh, cg::cluster_group& cluster, int c, int K) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  static_assert(kThreads == 256, "a bin for every thread");
+  float v[kMaxCluster];
+  float lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) {
+    v[r] = -INFINITY;
+    if (r < c) v[r] = c == 1 ? sh.lane_max[tid] : cluster.map_shared_rank(sh.lane_max, r)[tid];
+    if (v[r] > -INFINITY) lo = fminf(lo, v[r]);
+    hi = fmaxf(hi, v[r]);
   }
-  t0 = max(t0, kNegInfOrder + 1);
-  if (tid == 0) sh.ncand = sh.nlist = 0;
+  sh.bins[tid] = 0;
+  asm volatile("redux.sync.min.f32 %0, %0, 0xffffffff;" : "+f"(lo));
+  asm volatile("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(hi));
+  if (lane == 0) sh.range[warp] = make_float2(lo, hi);
   __syncthreads();
-  for_candidates(R, br, sh.bmax, t0, warp, lane, [&](unsigned long long key) {
-    const int i = atomicAdd(&sh.ncand, 1);
-    if (i < kCandidates) sh.cand[i] = key;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    lo = fminf(lo, sh.range[w].x);
+    hi = fmaxf(hi, sh.range[w].y);
+  }
+  const float scale = 255.f / (hi - lo);   // (0 * inf below where they are equal: bin 0)
+  int bin[kMaxCluster];
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) {
+    if (r >= c) break;
+    bin[r] = v[r] > -INFINITY ? min(max((int)((v[r] - lo) * scale), 0), 255) : -1;
+    if (bin[r] >= 0) atomicAdd(&sh.bins[bin[r]], 1);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    // lane l: bins 255 - 8 l and the seven below; their sum and that of all above
+    int n[8], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += n[i] = sh.bins[255 - 8 * lane - i];
+    int upto = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off *= 2) {
+      const int o = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += o;
+    }
+    int above = upto - sum;
+    if (above < K && upto >= K) {
+      int i = 0;
+      while (above + n[i] < K) above += n[i++];
+      sh.cut = 255 - 8 * lane - i;
+    }
+    if (lane == 31 && upto < K) sh.cut = -1;
+  }
+  __syncthreads();
+  const int cut = sh.cut;
+  float least = INFINITY;
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) {
+    if (r >= c) break;
+    if (bin[r] >= cut && bin[r] >= 0) least = fminf(least, v[r]);
+  }
+  asm volatile("redux.sync.min.f32 %0, %0, 0xffffffff;" : "+f"(least));
+  if (lane == 0) sh.range[warp].x = least;   // (everyone has read the range)
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) least = fminf(least, sh.range[w].x);
+  return cut < 0 ? -FLT_MAX : least;
+}
+
+// This CTA's K largest entries into to[0 .. K - 1], in no order, zeros behind
+// them; for rows whose candidates overflow.  The K-th largest key is the largest
+// 64-bit value that at least K keys reach, bit by bit.
+template <typename T>
+__device__ __noinline__ void top_by_bisection(Shared& sh, const Row<T>& R, const BlockRange& br, float least, int K,
+                                              unsigned long long* to) {
+  unsigned long long kth = 0;
+  for (int bit = 63; bit >= 0; --bit) {
+    const unsigned long long t = kth | (1ull << bit);
+    int mine = 0;
+    for_candidates(sh, R, br, least, [&](unsigned long long key) { mine += key >= t; });
+    if (cta_sum(sh, bit & 1, mine) >= K) kth = t;
+  }
+  int* n = sh.count[0];
+  __syncthreads();
+  if (threadIdx.x == 0) *n = 0;
+  for (int i = threadIdx.x; i < K; i += kThreads) to[i] = 0ull;
+  __syncthreads();
+  for_candidates(sh, R, br, least, [&](unsigned long long key) {
+    if (key < kth) return;
+    const int i = atomicAdd(n, 1);
+    if (i < K) to[i] = key;
   });
-  __syncthreads();
-  const int n = sh.ncand;
+}
+
+// The K largest of sh.cand[0 .. n - 1] into sh.sorted, largest first, zeros
+// behind them.
+__device__ __forceinline__ void rank_candidates(Shared& sh, int n, int K) {
+  const int tid = threadIdx.x;
   if (n <= kRankDirect) {
+    if (tid < K) sh.sorted[tid] = 0ull;
+    __syncthreads();
     for (int i = tid; i < n; i += kThreads) {
       const unsigned long long key = sh.cand[i];
-      int rank = 0;
-      for (int j = 0; j < n; ++j) rank += sh.cand[j] > key;
-      if (rank < K) sh.list[rank] = key;
+      int at = 0;
+      for (int j = 0; j < n; ++j) at += sh.cand[j] > key;
+      if (key != 0ull && at < K) sh.sorted[at] = key;
     }
-    if (tid == 0) sh.nlist = min(n, K);
     __syncthreads();
     return;
   }
-  // (more than kRankDirect >= K candidates: exactly K keys reach the K-th)
-  if (n <= kCandidates) {
-    const unsigned long long kth = kth_largest(K, &sh.count, [&](unsigned long long t) {
-      int c = 0;
-      for (int i = tid; i < n; i += kThreads) c += sh.cand[i] >= t;
-      return c;
-    });
-    for (int i = tid; i < n; i += kThreads)
-      if (sh.cand[i] >= kth) append(sh, sh.cand[i]);
-  } else {
-    const unsigned long long kth = kth_largest(K, &sh.count, [&](unsigned long long t) {
-      int c = 0;
-      for_candidates(R, br, sh.bmax, max(t0, (uint32_t)(t >> 32)), warp, lane,
-                     [&](unsigned long long key) { c += key >= t; });
-      return c;
-    });
-    for_candidates(R, br, sh.bmax, max(t0, (uint32_t)(kth >> 32)), warp, lane, [&](unsigned long long key) {
-      if (key >= kth) append(sh, key);
-    });
+  // a bitonic network over the next power of two
+  int m = 2 * kRankDirect;
+  while (m < n) m *= 2;
+  for (int i = n + tid; i < m; i += kThreads) sh.cand[i] = 0ull;
+  for (int k = 2; k <= m; k *= 2) {
+    for (int j = k / 2; j > 0; j /= 2) {
+      __syncthreads();
+      for (int i = tid; i < m / 2; i += kThreads) {
+        const int lo = 2 * j * (i / j) + i % j, hi = lo + j;
+        const unsigned long long a = sh.cand[lo], b = sh.cand[hi];
+        if ((a < b) == ((lo & k) == 0)) {
+          sh.cand[lo] = b;
+          sh.cand[hi] = a;
+        }
+      }
+    }
   }
   __syncthreads();
+  if (tid < K) sh.sorted[tid] = sh.cand[tid];
+  __syncthreads();
 }
-static_assert(kRankDirect >= kMaxTop, "the bisection needs at least K candidates");
+static_assert(kCandidates >= 2 * kRankDirect && (kCandidates & (kCandidates - 1)) == 0 && kRankDirect >= kMaxTop,
+              "the sorted lengths are powers of two up to the buffer's");
 
 template <typename T, bool kTop>
 __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs p) {
@@ -181,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
   cg::cluster_group cluster = cg::this_cluster();
   const int c = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int row = (int)(blockIdx.x / c);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
   int tok = -1;
   if (!row_token(p, row, &tok)) {
     // not scored: zeros, and no alternatives
@@ -201,17 +268,33 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
   const BlockRange br = block_range(R.nvec, rank, c);
 
   float tmax = -INFINITY;
-  stat_row<T, true>(R, br, kLog2e, 1.f, sh.part, &sh.cta, Nothing(), Nothing(), [&](int b, float lm, float bm) {
-    if (kTop) {
-      tmax = fmaxf(tmax, lm);
-      if (lane == 0) sh.bmax[b - br.begin] = bm;
-    }
+  if (kTop && tid == 0) sh.ncand = 0;
+  stat_row<T, true, kTop>(R, br, kLog2e, 1.f, sh.part, &sh.cta, Nothing(), Nothing(), [&](int b, float lm, float4 q) {
+    tmax = fmaxf(tmax, lm);
+    if (lane == 0) sh.quarter[b - br.begin] = q;
   });
-  if (kTop) cta_top<T>(sh, R, br, tmax, p.K, warp, lane);
-
-  cluster.sync();
+  if (kTop) sh.lane_max[tid] = tmax;
+  cluster_meet(c);
+  const Stat v = stat_cluster(cluster, &sh.cta, c, 1.f);
+  if (kTop) {
+    const float least = lower_bound(sh, cluster, c, p.K);
+    int* ncand = c == 1 ? &sh.ncand : cluster.map_shared_rank(&sh.ncand, 0);
+    unsigned long long* cand = c == 1 ? sh.cand : cluster.map_shared_rank(sh.cand, 0);
+    for_candidates(sh, R, br, least, [&](unsigned long long key) {
+      const int i = atomicAdd(ncand, 1);
+      if (i < kCandidates) cand[i] = key;
+    });
+    cluster_meet(c);
+    int n = *ncand;
+    if (n > kCandidates) {
+      cluster_meet(c);   // (every CTA has read the count)
+      top_by_bisection(sh, R, br, least, p.K, cand + rank * p.K);
+      cluster_meet(c);
+      n = c * p.K;
+    }
+    if (rank == 0) rank_candidates(sh, n, p.K);
+  }
   if (rank == 0) {
-    const Stat v = stat_cluster(cluster, &sh.cta, c, 1.f);
     const bool bad = stat_bad(v);
     const bool none = v.m == -INFINITY;   // every entry is -inf
     const float ls = none ? 0.f : logf(v.s);
@@ -224,37 +307,14 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
       p.entropy[row] = bad ? nan : (none ? 0.f : fmaxf(ls + v.t / v.s, 0.f));
       p.lse[row] = bad ? nan : v.m + ls;
     }
-    if (kTop) {
-      // the c lists as one, then each key's rank
-      const unsigned long long* keys = sh.list;
-      int n = min(sh.nlist, p.K);
-      if (c > 1) {
-        for (int i = tid; i < c * p.K; i += kThreads) {
-          const int r = i / p.K, j = i - r * p.K;
-          const bool has = j < min(*cluster.map_shared_rank(&sh.nlist, r), p.K);
-          sh.cand[i] = has ? cluster.map_shared_rank(sh.list, r)[j] : 0ull;
-        }
-        keys = sh.cand;
-        n = c * p.K;
-      }
-      if (tid < p.K) sh.sorted[tid] = 0ull;
-      __syncthreads();
-      for (int i = tid; i < n; i += kThreads) {
-        const unsigned long long key = keys[i];
-        int at = 0;
-        for (int j = 0; j < n; ++j) at += keys[j] > key;
-        if (key != 0ull && at < p.K) sh.sorted[at] = key;
-      }
-      __syncthreads();
-      if (tid < p.K) {
-        const unsigned long long key = sh.sorted[tid];
-        const bool has = key != 0ull && !bad;
-        p.top_idx[(size_t)row * p.K + tid] = has ? argmax_key_index(key) : -1;
-        p.top_logp[(size_t)row * p.K + tid] = bad ? nan : (has ? (argmax_key_value(key) - v.m) - ls : -INFINITY);
-      }
+    if (kTop && tid < p.K) {
+      const unsigned long long key = sh.sorted[tid];
+      const bool has = key != 0ull && !bad;
+      p.top_idx[(size_t)row * p.K + tid] = has ? argmax_key_index(key) : -1;
+      p.top_logp[(size_t)row * p.K + tid] = bad ? nan : (has ? (argmax_key_value(key) - v.m) - ls : -INFINITY);
     }
   }
-  cluster.sync();   // the other CTAs' shared memory is read until here
+  if (c > 1) cluster_meet(c);   // a CTA's shared memory is read until here
 }
 
 // The gradient, one warp a block at a time: HBM bounds it (one read, one
@@ -282,10 +342,10 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_backward_kernel(const Lo
   float ref = on ? p.lse[row] : -INFINITY, ls = 0.f;
   if (ref != ref) gl = nan;
   if (fabsf(ref) > kLargeLse && ref != -INFINITY) {
-    stat_row<T, false>(R, br, kLog2e, 1.f, part, &cta, Nothing(), Nothing(), Nothing());
-    cluster.sync();
+    stat_row<T, false, false>(R, br, kLog2e, 1.f, part, &cta, Nothing(), Nothing(), Nothing());
+    cluster_meet(c);
     const Stat v = stat_cluster(cluster, &cta, c, 1.f);
-    cluster.sync();
+    cluster_meet(c);
     if (stat_bad(v)) gl = nan;
     ref = v.m;
     ls = logf(v.s);
