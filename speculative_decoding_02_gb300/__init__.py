@@ -623,6 +623,12 @@ def markov_logits(U, W1, W2, anchor, x, dtype=torch.float32, ws=None, out=None):
 
 def head_workspace(B, gamma, V, device):
     """A workspace of markov_head_backward for these sizes."""
+    ws = _head_workspace(B, gamma, V, device)
+    ws[:256].zero_()
+    return ws
+
+
+def _head_workspace(B, gamma, V, device):
     n = int(_load().dspark_head_workspace_size(B, gamma, V))
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
 
@@ -635,7 +641,7 @@ def markov_head_backward(dlogits, W1, W2, anchor, x, ws=None):
     dev, B, G, V, r = _head_args(dlogits, "dlogits", torch.bfloat16, W1, W2, anchor, x)
     dW1 = torch.empty((V, r), dtype=torch.float32, device=dev)
     dW2 = torch.empty((V, r), dtype=torch.float32, device=dev)
-    ws = head_workspace(B, G, V, dev) if ws is None else ws
+    ws = _head_workspace(B, G, V, dev) if ws is None else ws   # (its status word is nobody's)
     _launch(L.dspark_markov_head_backward, "markov_head_backward", dev, dlogits.data_ptr(), W1.data_ptr(),
             W2.data_ptr(), _dt(W1, "W1"), anchor.data_ptr(), x.data_ptr(), B, G, V, r, dW1.data_ptr(), dW2.data_ptr(),
             ws.data_ptr(), ws.numel())

@@ -316,41 +316,54 @@ markov_logits_tc(const __grid_constant__ CUtensorMap w_map, const __grid_constan
 }
 
 // ---------------------------------------------------------------------------
-// Weight gradients.  One kernel for both products, each an accumulation over K
-// in stages of 64 into kHalves accumulators of 128 x 256:
-//   kW2:  dW2 tile [128 kHalves v, 256] over K = rows n:  A = D^T (the stage
-//         holds [64 n][64 v] boxes, M-major), B = E [64 n][256] (N-major)
-//   else: part of dE [128 kHalves n, 256] over a range of K = v:  A = D ([128 n]
-//         [64 v] boxes, K-major), B = W2 [64 v][256] (N-major)
+// Weight gradients.  One kernel for both products, on pairs of CTAs
+// (cta_group::2): a tile of 256 x 256, 128 rows of it in each CTA's tensor
+// memory, accumulated over K in stages of 64.  Each CTA copies its 128 rows of
+// A and one half of B (128 of the 256 columns):
+//   kW2:  dW2 tile [256 v, 256] over K = rows n:  A = D^T (the stage holds
+//         [64 n][64 v] boxes, M-major), B = E [64 n][256] (N-major)
+//   else: part of dE [256 n, 256] over a range of K = v:  A = D ([128 n][64 v]
+//         boxes, K-major), B = W2 [64 v][256] (N-major)
+//
+//   warp 0     TMA producer of its CTA; all copies of a stage count on the
+//              first CTA's barrier;
+//   warp 1     of the first CTA: MMA issuer for both;
+//   warps 2-9  a thread owns a row and 128 columns.
+//
+// The tensor cores truncate when they add to an accumulator, which over the
+// 128 additions of 2048 rows came to a relative error of 1e-5 (2-norm), an order
+// more than fp32 products have.  So an accumulator takes kChunk stages only (12
+// additions) and the epilogue adds it, rounded, to sums in registers, while
+// the next one fills (two of them).
 // ---------------------------------------------------------------------------
-constexpr int BThreads = 64 + 128;
-
-template <int kHalves>
-struct BShape {
-  static constexpr int kABytes = kHalves * HM * 64 * 2;
-  static constexpr int kBBytes = HK * 64 * 2;
-  static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = kHalves == 2 ? 3 : 4;
-  static constexpr int kSmem = 1024 + kStages * kStageBytes + 256;
-  static_assert(kSmem <= kMaxSmem, "shared memory");
-};
+constexpr int BEpiWarps = 8;
+constexpr int BThreads = 64 + 32 * BEpiWarps;
+constexpr int BStages = 6;
+constexpr int kChunk = 3;
+constexpr int BABytes = HM * 64 * 2;           // 16384: 128 rows of A
+constexpr int BBBytes = HK / 2 * 64 * 2;       // 16384: 128 columns of B
+constexpr int BStageBytes = BABytes + BBBytes;
+constexpr int BSmemBytes = 1024 + BStages * BStageBytes + 256;
+constexpr uint32_t BTmemCols = 512;            // two accumulators of 256 columns
+static_assert(BSmemBytes <= kMaxSmem, "shared memory");
 
 struct __align__(8) BBars {
-  uint64_t full[4], empty[4];
-  uint64_t acc_full, acc_empty, drain;
+  uint64_t full[BStages], empty[BStages];
+  uint64_t acc_full[2], acc_empty[2];
   uint32_t tmem_base;
   int abort;
 };
 static_assert(sizeof(BBars) <= 256, "barrier block");
 
 struct GradParams {
-  float* out;        // kW2: dW2 [V][256]; else partials [splits][rows][256]
+  float* out;        // kW2: dW2 [V][256]; else parts [splits][rows][256]
+  float* zero;       // kW2: dW1 [V][256], which is cleared along
   int* status;
   int rows;          // kW2: V; else the rows of this chunk of D
   int row0;          // else: the chunk's first row of D
   int ksteps;        // 64-wide steps of K
-  int tiles;         // kW2: tiles of 128 kHalves v; else row groups
-  int splits;        // else: parts of K (tiles * splits CTAs)
+  int tiles;         // kW2: tiles of 256 v; else groups of 256 rows
+  int splits;        // else: parts of K (tiles * splits pairs)
 };
 
 // A matrix in 128-byte swizzled boxes of [K rows][64 of M or N]: 8 rows of K
@@ -361,130 +374,206 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t 
 }
 constexpr uint32_t kAMajorM = 1u << 15, kBMajorN = 1u << 16;   // instruction descriptor: not K-major
 
-template <bool kW2, int kHalves>
-__global__ void __launch_bounds__(BThreads, 1)
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address, in the cluster's window, of the same place in CTA `rank`.
+__device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void arrive_in_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// tma_g2s_2d of a CTA pair: the bytes count on a barrier of either CTA.
+__device__ __forceinline__ void tma_pair_2d(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on `bar` of both CTAs when the MMAs issued so far are done.
+__device__ __forceinline__ void umma_pair_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// 32 bytes, a whole sector of L2.
+__device__ __forceinline__ void st_8(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+template <bool kW2>
+__global__ void __launch_bounds__(BThreads, 1) __cluster_dims__(2, 1, 1)
 head_grad_tc(const __grid_constant__ CUtensorMap d_map, const __grid_constant__ CUtensorMap b_map, const GradParams p) {
-  using S = BShape<kHalves>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  BBars* bars = reinterpret_cast<BBars*>(smem + S::kStages * S::kStageBytes);
+  BBars* bars = reinterpret_cast<BBars*>(smem + BStages * BStageBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   volatile int* abort = &bars->abort;
-  constexpr uint32_t kCols = kHalves * 256;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S::kStages; ++s) { mbar_init(&bars->full[s], 1); mbar_init(&bars->empty[s], 1); }
-    mbar_init(&bars->acc_full, 1);
-    mbar_init(&bars->acc_empty, 4);
-    mbar_init(&bars->drain, 1);
+    for (int s = 0; s < BStages; ++s) { mbar_init(&bars->full[s], 1); mbar_init(&bars->empty[s], 1); }
+    for (int s = 0; s < 2; ++s) { mbar_init(&bars->acc_full[s], 1); mbar_init(&bars->acc_empty[s], 2 * BEpiWarps); }
     bars->abort = 0;
     fence_mbar_init();
     prefetch_tensormap(&d_map);
     prefetch_tensormap(&b_map);
   }
-  if (warp == 1) tmem_alloc(&bars->tmem_base, kCols);
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars->tmem_base)),
+                 "r"(BTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
   tc_fence_before();
   __syncthreads();
+  cluster_meet();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+  pdl_trigger();
+  pdl_wait();
 
-  // this CTA's tiles and, of each, its steps of K
-  const int tile0 = kW2 ? blockIdx.x : blockIdx.x / p.splits;
-  const int tile_step = kW2 ? gridDim.x : p.tiles;
-  const int split = kW2 ? 0 : blockIdx.x % p.splits;
+  // this pair's tiles and, of each, its steps of K
+  const int tile0 = kW2 ? pair : pair / p.splits;
+  const int tile_step = kW2 ? pairs : p.tiles;
+  const int split = kW2 ? 0 : pair % p.splits;
   const int k0 = kW2 ? 0 : (int)((long long)p.ksteps * split / p.splits);
   const int k1 = kW2 ? p.ksteps : (int)((long long)p.ksteps * (split + 1) / p.splits);
 
   if (warp == 0) {
+    // ------------------------------------------------------------ producer
     if (lane == 0) {
       const uint64_t pol_d = policy_evict_first(), pol_b = policy_evict_last();
       uint32_t i = 0;
       bool ok = true;
       for (int tile = tile0; tile < p.tiles && ok; tile += tile_step) {
+        const int m0 = (tile * 2 + rank) * HM;
         for (int k = k0; k < k1; ++k, ++i) {
-          const int s = i % S::kStages;
-          ok = mbar_wait(&bars->empty[s], ((i / S::kStages) & 1) ^ 1, abort, p.status);
+          const int s = i % BStages;
+          ok = mbar_wait(&bars->empty[s], ((i / BStages) & 1) ^ 1, abort, p.status);
           if (!ok) break;
-          unsigned char* a = smem + s * S::kStageBytes;
-          unsigned char* b = a + S::kABytes;
-          mbar_arrive_expect_tx(&bars->full[s], S::kStageBytes);
+          unsigned char* a = smem + s * BStageBytes;
+          const uint32_t full = in_cta(&bars->full[s], 0);
+          if (rank == 0) mbar_arrive_expect_tx(&bars->full[s], 2 * BStageBytes);
           if (kW2) {
-            for (int j = 0; j < 2 * kHalves; ++j)
-              tma_g2s_2d(a + j * 8192, &d_map, tile * HM * kHalves + j * 64, k * 64, &bars->full[s], pol_d);
+            for (int j = 0; j < 2; ++j) tma_pair_2d(a + j * 8192, &d_map, m0 + j * 64, k * 64, full, pol_d);
           } else {
-            for (int j = 0; j < kHalves; ++j)
-              tma_g2s_2d(a + j * 16384, &d_map, k * 64, p.row0 + (tile * kHalves + j) * HM, &bars->full[s], pol_d);
+            tma_pair_2d(a, &d_map, k * 64, p.row0 + m0, full, pol_d);
           }
-          for (int j = 0; j < HK / 64; ++j) tma_g2s_2d(b + j * 8192, &b_map, j * 64, k * 64, &bars->full[s], pol_b);
+          for (int j = 0; j < 2; ++j)
+            tma_pair_2d(a + BABytes + j * 8192, &b_map, (rank * 2 + j) * 64, k * 64, full, pol_b);
         }
       }
-      if (*abort) {
-        for (int s = 0; s < S::kStages; ++s) {
-          const uint32_t n = (i + S::kStages - 1 - s) / S::kStages;
-          if (n > 0) mbar_drain(&bars->full[s], (n - 1) & 1);
-        }
+      // every stage is consumed before the CTA leaves (on a timeout: as far as
+      // the wait's limit goes, which is longer than any copy takes)
+      for (int s = 0; s < BStages; ++s) {
+        const uint32_t n = (i + BStages - 1 - s) / BStages;
+        if (n > 0) mbar_drain(&bars->empty[s], (n - 1) & 1);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(HM, HK) | kBMajorN | (kW2 ? kAMajorM : 0u);
-      uint32_t i = 0, done = 0;
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(2 * HM, HK) | kBMajorN | (kW2 ? kAMajorM : 0u);
+      uint32_t i = 0, chunk = 0;
       bool ok = true;
-      for (int tile = tile0; tile < p.tiles && ok; tile += tile_step, ++done) {
-        if (!(ok = mbar_wait(&bars->acc_empty, (done & 1) ^ 1, abort, p.status))) break;
-        tc_fence_after();
-        for (int k = k0; k < k1; ++k, ++i) {
-          const int s = i % S::kStages;
-          if (!(ok = mbar_wait(&bars->full[s], (i / S::kStages) & 1, abort, p.status))) break;
+      for (int tile = tile0; tile < p.tiles && ok; tile += tile_step) {
+        for (int k = k0; k < k1 && ok; ++chunk) {
+          const int buf = chunk & 1, kend = min(k + kChunk, k1);
+          ok = mbar_wait(&bars->acc_empty[buf], ((chunk >> 1) & 1) ^ 1, abort, p.status);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a = smem_u32(smem + s * S::kStageBytes);
-          const uint64_t bd = sw128_mnmajor_desc(a + S::kABytes, 8192);
-#pragma unroll
-          for (int h = 0; h < kHalves; ++h) {
-            const uint64_t ad = kW2 ? sw128_mnmajor_desc(a + h * 16384, 8192) : sw128_kmajor_desc(a + h * 16384);
+          for (int kf = k; k < kend; ++k, ++i) {
+            const int s = i % BStages;
+            ok = mbar_wait(&bars->full[s], (i / BStages) & 1, abort, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t a = smem_u32(smem + s * BStageBytes);
+            const uint64_t ad = kW2 ? sw128_mnmajor_desc(a, 8192) : sw128_kmajor_desc(a);
+            const uint64_t bd = sw128_mnmajor_desc(a + BABytes, 8192);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)   // 16 of K: two 1024-byte groups, or 32 bytes of a K-major row
-              umma_bf16(tmem + h * 256, ad + (uint64_t)(kk * (kW2 ? 128 : 2)), bd + (uint64_t)(kk * 128), idesc,
-                        k != k0 || kk != 0);
+              umma_pair(tmem + buf * HK, ad + (uint64_t)(kk * (kW2 ? 128 : 2)), bd + (uint64_t)(kk * 128), idesc,
+                        k != kf || kk != 0);
+            umma_pair_commit(&bars->empty[s]);
           }
-          umma_commit(&bars->empty[s]);
+          if (ok) umma_pair_commit(&bars->acc_full[buf]);
         }
-        if (ok) umma_commit(&bars->acc_full);
       }
-      umma_commit(&bars->drain);
-      mbar_drain(&bars->drain, 0);
     }
     __syncwarp();
   } else {
-    const int q = warp & 3;
-    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
-    uint32_t done = 0;
-    for (int tile = tile0; tile < p.tiles; tile += tile_step, ++done) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&bars->acc_full, done & 1, abort, p.status))) break;
-      tc_fence_after();
-      for (int h = 0; h < kHalves; ++h) {
-        const int row = (tile * kHalves + h) * HM + q * 32 + lane;
-        float4* o = reinterpret_cast<float4*>(p.out + ((size_t)split * (kW2 ? 0 : p.rows) + row) * HK);
-        for (int c = 0; c < HK / 32; ++c) {
-          float v[32];
-          tmem_load_cols<32>(lanes + h * 256 + c * 32, v);
-          if (row < p.rows) {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3, h = (warp - 2) >> 2;
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + h * 128;
+    const int nchunks = (k1 - k0 + kChunk - 1) / kChunk;
+    uint32_t chunk = 0;
+    bool ok = true;
+    for (int tile = tile0; tile < p.tiles && ok; tile += tile_step) {
+      float acc[128];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              o[c * 8 + j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-          }
+      for (int j = 0; j < 128; ++j) acc[j] = 0.f;
+      for (int n = 0; n < nchunks && ok; ++n, ++chunk) {
+        const int buf = chunk & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->acc_full[buf], (chunk >> 1) & 1, abort, p.status));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float v[32];
+          tmem_load_cols<32>(lanes + buf * HK + j * 32, v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) acc[j * 32 + e] += v[e];
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_in_cluster(in_cta(&bars->acc_empty[buf], 0));
+      }
+      const int row = (tile * 2 + rank) * HM + q * 32 + lane;
+      if (ok && row < p.rows) {
+        float* o = p.out + ((size_t)split * (kW2 ? 0 : p.rows) + row) * HK + h * 128;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) st_8(o + j * 8, acc + j * 8);
+        if (kW2) {
+          const float none[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          float* z = p.zero + (size_t)row * HK + h * 128;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) st_8(z + j * 8, none);
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->acc_empty);
     }
   }
   tc_fence_before();
   __syncthreads();
+  cluster_meet();   // neither CTA's memory is used past here
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, kCols);
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(BTmemCols) : "memory");
 }
 
 // E [N][256] and the previous tokens [N] (-1: none), a warp per row.
@@ -492,6 +581,7 @@ __global__ void __launch_bounds__(256) gather_rows(const __nv_bfloat16* __restri
                                                    const int32_t* __restrict__ x, int N, int G, int V,
                                                    uint4* __restrict__ E, int32_t* __restrict__ prev, int* status) {
   const int n = (int)((blockIdx.x * (long long)blockDim.x + threadIdx.x) >> 5), lane = threadIdx.x & 31;
+  pdl_trigger();
   if (n >= N) return;
   const int tok = previous_token(anchor, x, n, G, V, status);
   E[(size_t)n * 32 + lane] =
@@ -499,28 +589,42 @@ __global__ void __launch_bounds__(256) gather_rows(const __nv_bfloat16* __restri
   if (lane == 0) prev[n] = tok;
 }
 
+// dE of a chunk of rows: the sum of its parts, into the first.
+__global__ void __launch_bounds__(256) sum_parts(float4* part, int rows, int splits) {
+  pdl_trigger();
+  pdl_wait();
+  const size_t n = (size_t)rows * (HK / 4), i = blockIdx.x * (size_t)256 + threadIdx.x;
+  if (i >= n) return;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) {
+    const float4 v = part[s * n + i];
+    a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+  }
+  part[i] = a;
+}
+
 // dW1 of a chunk of rows: the block of a token's first row in the chunk adds
-// the K parts of every row of that token, in order of the rows, to dW1[token].
-__global__ void __launch_bounds__(HK) scatter_rows(const float* __restrict__ part, const int32_t* __restrict__ prev,
-                                                   int rows, int splits, float* __restrict__ dW1) {
+// dE of every row of that token, in order of the rows, to dW1[token].
+__global__ void __launch_bounds__(HK) scatter_rows(const float* dE, const int32_t* prev,
+                                                   int rows, float* dW1) {
+  pdl_trigger();
+  pdl_wait();
   const int n = blockIdx.x, tok = prev[n];
   if (tok < 0) return;
-  __shared__ int later[HK];
   bool earlier = false;
   for (int j = threadIdx.x; j < n; j += HK) earlier = earlier || prev[j] == tok;
   if (__syncthreads_or(earlier)) return;
+  __shared__ unsigned hits[HK / 32];
   float acc = 0.f;
   for (int j0 = n; j0 < rows; j0 += HK) {
     const int j = j0 + threadIdx.x;
-    const bool same = j < rows && prev[j] == tok;
-    if (!__syncthreads_or(same)) continue;
-    later[threadIdx.x] = same;
+    const unsigned h = __ballot_sync(0xffffffffu, j < rows && prev[j] == tok);
+    if ((threadIdx.x & 31) == 0) hits[threadIdx.x >> 5] = h;
     __syncthreads();
-    for (int i = 0; i < HK && j0 + i < rows; ++i) {
-      if (!later[i]) continue;
-#pragma unroll 8
-      for (int s = 0; s < splits; ++s) acc += part[((size_t)s * rows + j0 + i) * HK + threadIdx.x];
-    }
+    for (int w = 0; w < HK / 32; ++w)
+      for (unsigned left = hits[w]; left != 0; left &= left - 1)
+        acc += dE[(size_t)(j0 + w * 32 + __ffs(left) - 1) * HK + threadIdx.x];
     __syncthreads();
   }
   dW1[(size_t)tok * HK + threadIdx.x] += acc;
@@ -560,38 +664,27 @@ int sm_count() {
   return sms;
 }
 
-template <bool kW2, int kHalves>
-cudaError_t launch_grad(int grid, const CUtensorMap& d, const CUtensorMap& b, const GradParams& p, cudaStream_t stream) {
-  auto kern = head_grad_tc<kW2, kHalves>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, BShape<kHalves>::kSmem);
+template <bool kW2>
+cudaError_t launch_grad(int pairs, const CUtensorMap& d, const CUtensorMap& b, const GradParams& p, cudaStream_t stream) {
+  auto kern = head_grad_tc<kW2>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, BSmemBytes);
   if (e != cudaSuccess) return e;
-  kern<<<grid, BThreads, BShape<kHalves>::kSmem, stream>>>(d, b, p);
-  return cudaGetLastError();
+  return launch_pdl(kern, dim3(2 * pairs), dim3(BThreads), BSmemBytes, stream, d, b, p);
 }
 
 // Rows of D whose dE parts the workspace holds at a time, and parts of K for
 // them: one CTA an SM.
 constexpr int kChunkRows = 4096;
-constexpr int kMaxCtas = 160;
-struct GradPlan {
-  int halves, groups, splits;
-};
-GradPlan plan_chunk(int rows, int V, int sms) {
-  GradPlan g;
-  g.halves = rows > HM ? 2 : 1;
-  g.groups = div_up(rows, g.halves * HM);
-  g.splits = std::max(1, std::min(std::min(sms, kMaxCtas) / g.groups, div_up(V, 64)));
-  return g;
-}
+constexpr int kMaxPairs = 80;
 
 }  // namespace
 
 // Workspace: status word, previous tokens, E, the dE parts of a chunk.
 size_t head_workspace_bytes(int N, int V) {
-  // rows * splits of a chunk (plan_chunk): at most 256 rows for each CTA, and
-  // at most kMaxCtas or V / 64 parts of the rows there are
-  const size_t splits = std::min(kMaxCtas, div_up(V, 64));
-  const size_t parts = std::min<size_t>((size_t)kMaxCtas * 2 * HM, splits * std::min(N, kChunkRows));
+  // rows * splits of a chunk: at most 256 rows for each pair, and at most
+  // kMaxPairs or V / 64 parts of the rows there are
+  const size_t splits = std::min(kMaxPairs, div_up(V, 64));
+  const size_t parts = std::min<size_t>((size_t)kMaxPairs * 2 * HM, splits * std::min(N, kChunkRows));
   return 256 + align256(4ull * N) + align256(512ull * N) + align256(1024ull * parts);
 }
 
@@ -637,45 +730,45 @@ cudaError_t launch_markov_head_backward(const HeadBackwardArgs& a, cudaStream_t 
   char* E = ws + 256 + align256(4ull * N);
   float* part = reinterpret_cast<float*>(E + align256(512ull * N));
   cudaError_t e;
-  if ((e = cudaMemsetAsync(status, 0, sizeof(int), stream)) != cudaSuccess) return e;
-  if ((e = cudaMemsetAsync(a.dW1, 0, sizeof(float) * HK * (size_t)a.V, stream)) != cudaSuccess) return e;
   gather_rows<<<(unsigned)div_up(N, 8), 256, 0, stream>>>(static_cast<const __nv_bfloat16*>(a.W1), a.anchor, a.x, N,
                                                          a.G, a.V, reinterpret_cast<uint4*>(E), prev, status);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
 
-  // dW2: one tile of 256 (or, while those leave SMs idle, 128) v per CTA at a time
+  // dW2 (and zeros into dW1)
+  const int pairs = std::min(sms / 2, kMaxPairs);
   CUtensorMap dm, bm;
   if ((e = make_bf16_map(a.dlogits, N, a.V, 64, &dm)) != cudaSuccess) return e;
   if ((e = make_bf16_map(E, N, HK, 64, &bm)) != cudaSuccess) return e;
   GradParams p{};
   p.out = a.dW2;
+  p.zero = a.dW1;
   p.status = status;
   p.rows = a.V;
   p.ksteps = div_up(N, 64);
-  const int halves = div_up(a.V, 2 * HM) >= sms ? 2 : 1;
-  p.tiles = div_up(a.V, halves * HM);
+  p.tiles = div_up(a.V, 2 * HM);
   p.splits = 1;
-  const int grid = std::min(p.tiles, sms);
-  e = halves == 2 ? launch_grad<true, 2>(grid, dm, bm, p, stream) : launch_grad<true, 1>(grid, dm, bm, p, stream);
-  if (e != cudaSuccess) return e;
+  if ((e = launch_grad<true>(std::min(p.tiles, pairs), dm, bm, p, stream)) != cudaSuccess) return e;
 
   // dE and dW1, a chunk of rows at a time
   if ((e = make_bf16_map(a.dlogits, N, a.V, HM, &dm)) != cudaSuccess) return e;
   if ((e = make_bf16_map(a.W2, a.V, HK, 64, &bm)) != cudaSuccess) return e;
   for (int r0 = 0; r0 < N; r0 += kChunkRows) {
     const int rows = std::min(N - r0, kChunkRows);
-    const GradPlan g = plan_chunk(rows, a.V, sms);
     p.out = part;
     p.rows = rows;
     p.row0 = r0;
     p.ksteps = div_up(a.V, 64);
-    p.tiles = g.groups;
-    p.splits = g.splits;
-    e = g.halves == 2 ? launch_grad<false, 2>(g.groups * g.splits, dm, bm, p, stream)
-                      : launch_grad<false, 1>(g.groups * g.splits, dm, bm, p, stream);
+    p.tiles = div_up(rows, 2 * HM);
+    p.splits = std::max(1, std::min(pairs / p.tiles, p.ksteps));
+    if ((e = launch_grad<false>(p.tiles * p.splits, dm, bm, p, stream)) != cudaSuccess) return e;
+    if (p.splits > 1) {
+      e = launch_pdl(sum_parts, dim3((unsigned)div_up(rows * (HK / 4), 256)), dim3(256), 0, stream,
+                     reinterpret_cast<float4*>(part), rows, p.splits);
+      if (e != cudaSuccess) return e;
+    }
+    e = launch_pdl(scatter_rows, dim3((unsigned)rows), dim3(HK), 0, stream, (const float*)part, (const int32_t*)(prev + r0),
+                   rows, a.dW1);
     if (e != cudaSuccess) return e;
-    scatter_rows<<<rows, HK, 0, stream>>>(part, prev + r0, rows, g.splits, a.dW1);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
