@@ -529,8 +529,8 @@ int dspark_markov_logits(const float* U, const void* W1, const void* W2, int wdt
  *   dW1[t, i] = sum_{(b,k): x_{k-1} = t} sum_v dlogits[b, k-1, v] * W2[v, i]
  * Out: dW1_out, dW2_out [V, r] f32, wholly written; sums in fp32, in an order
  * that depends on the sizes alone.  A previous token outside [0, V) takes no
- * part and records DSPARK_ERR_INVALID.  Same limits as dspark_markov_logits;
- * dW1_out and dW2_out 32-byte aligned.
+ * part and records DSPARK_ERR_INVALID.  Same limits as dspark_markov_logits
+ * (every tensor 16-byte aligned).
  * Workspace: dspark_head_workspace_size bytes (0 when a size is not positive or
  * out of range), 256-byte aligned, its status word zero at first.
  */

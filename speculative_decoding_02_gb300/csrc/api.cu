@@ -422,7 +422,7 @@ int dspark_markov_head_backward(const void* dlogits, const void* W1, const void*
   DSPARK_TRY(check_shapes(B, gamma, V, r));
   DSPARK_TRY(check_dtype(wdtype));
   if (!dlogits || !W1 || !W2 || !anchor || !x || !dW1_out || !dW2_out) return DSPARK_ERR_INVALID;
-  if (!aligned(dlogits, 16) || !aligned(W1, 16) || !aligned(W2, 16) || !aligned(dW1_out, 32) || !aligned(dW2_out, 32))
+  if (!aligned(dlogits, 16) || !aligned(W1, 16) || !aligned(W2, 16) || !aligned(dW1_out, 16) || !aligned(dW2_out, 16))
     return DSPARK_ERR_INVALID;
   if (!draft_tc_supported(wdtype, r, V)) return DSPARK_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < head_workspace_bytes(B * gamma, V))

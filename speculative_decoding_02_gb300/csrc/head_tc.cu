@@ -65,7 +65,7 @@ __device__ __forceinline__ int previous_token(const int32_t* anchor, const int32
 //              they gather the next E.
 // ---------------------------------------------------------------------------
 constexpr int GN = 64;             // columns of a tile
-constexpr int GUStages = 4, GWStages = 2;
+constexpr int GUStages = 5, GWStages = 2;
 constexpr int GEpiWarps = 8;
 constexpr int GThreads = 64 + 32 * GEpiWarps;
 constexpr int GUBytes = HM * GN * 4;     // 32768
@@ -159,7 +159,7 @@ markov_logits_tc(const __grid_constant__ CUtensorMap w_map, const __grid_constan
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      const uint64_t pol_w = policy_evict_last(), pol_u = policy_evict_first();
+      const uint64_t pol_w = policy_evict_last(), pol_u = policy_evict_normal();
       uint32_t i = 0;
       bool ok = true;
       for (long long u = u0; u < u1; ++u, ++i) {
@@ -328,22 +328,26 @@ markov_logits_tc(const __grid_constant__ CUtensorMap w_map, const __grid_constan
 //   warp 0     TMA producer of its CTA; all copies of a stage count on the
 //              first CTA's barrier;
 //   warp 1     of the first CTA: MMA issuer for both;
-//   warps 2-9  a thread owns a row and 128 columns.
+//   warps 2-17 a thread owns a row and 64 columns; at a tile's end they go to
+//              shared memory by boxes of 16 rows x 32 columns and out by TMA.
 //
 // The tensor cores truncate when they add to an accumulator, which over the
 // 128 additions of 2048 rows came to a relative error of 1e-5 (2-norm), an order
-// more than fp32 products have.  So an accumulator takes kChunk stages only (12
+// more than fp32 products have.  So an accumulator takes kChunk stages only (32
 // additions) and the epilogue adds it, rounded, to sums in registers, while
 // the next one fills (two of them).
 // ---------------------------------------------------------------------------
-constexpr int BEpiWarps = 8;
+constexpr int BEpiWarps = 16;
 constexpr int BThreads = 64 + 32 * BEpiWarps;
-constexpr int BStages = 6;
-constexpr int kChunk = 3;
+constexpr int BStages = 5;
+constexpr int kChunk = 8;
 constexpr int BABytes = HM * 64 * 2;           // 16384: 128 rows of A
 constexpr int BBBytes = HK / 2 * 64 * 2;       // 16384: 128 columns of B
 constexpr int BStageBytes = BABytes + BBBytes;
-constexpr int BSmemBytes = 1024 + BStages * BStageBytes + 256;
+constexpr int BBoxRows = 16;
+constexpr int BBoxBytes = BBoxRows * 32 * 4;   // of an epilogue warp's output
+constexpr int BZeroBytes = 4096;
+constexpr int BSmemBytes = 1024 + BStages * BStageBytes + BEpiWarps * BBoxBytes + BZeroBytes + 256;
 constexpr uint32_t BTmemCols = 512;            // two accumulators of 256 columns
 static_assert(BSmemBytes <= kMaxSmem, "shared memory");
 
@@ -354,9 +358,9 @@ struct __align__(8) BBars {
   int abort;
 };
 static_assert(sizeof(BBars) <= 256, "barrier block");
+static_assert(BZeroBytes == 4 * HK * 4, "four rows of dW1");
 
 struct GradParams {
-  float* out;        // kW2: dW2 [V][256]; else parts [splits][rows][256]
   float* zero;       // kW2: dW1 [V][256], which is cleared along
   int* status;
   int rows;          // kW2: V; else the rows of this chunk of D
@@ -364,6 +368,7 @@ struct GradParams {
   int ksteps;        // 64-wide steps of K
   int tiles;         // kW2: tiles of 256 v; else groups of 256 rows
   int splits;        // else: parts of K (tiles * splits pairs)
+  bool wait_last;    // nothing here depends on the kernel before, but a kernel ends after it
 };
 
 // A matrix in 128-byte swizzled boxes of [K rows][64 of M or N]: 8 rows of K
@@ -418,19 +423,15 @@ __device__ __forceinline__ void umma_pair_commit(uint64_t* bar) {
       "h"((uint16_t)3)
       : "memory");
 }
-// 32 bytes, a whole sector of L2.
-__device__ __forceinline__ void st_8(float* p, const float* v) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-               : "memory");
-}
-
 template <bool kW2>
 __global__ void __launch_bounds__(BThreads, 1) __cluster_dims__(2, 1, 1)
-head_grad_tc(const __grid_constant__ CUtensorMap d_map, const __grid_constant__ CUtensorMap b_map, const GradParams p) {
+head_grad_tc(const __grid_constant__ CUtensorMap d_map, const __grid_constant__ CUtensorMap b_map,
+             const __grid_constant__ CUtensorMap o_map, const GradParams p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  BBars* bars = reinterpret_cast<BBars*>(smem + BStages * BStageBytes);
+  unsigned char* boxes = smem + BStages * BStageBytes;
+  unsigned char* zeros = boxes + BEpiWarps * BBoxBytes;
+  BBars* bars = reinterpret_cast<BBars*>(zeros + BZeroBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   volatile int* abort = &bars->abort;
@@ -442,7 +443,10 @@ head_grad_tc(const __grid_constant__ CUtensorMap d_map, const __grid_constant__ 
     fence_mbar_init();
     prefetch_tensormap(&d_map);
     prefetch_tensormap(&b_map);
+    prefetch_tensormap(&o_map);
   }
+  for (int i = threadIdx.x; i < BZeroBytes / 4; i += BThreads) reinterpret_cast<float*>(zeros)[i] = 0.f;
+  fence_proxy_async_smem();
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars->tmem_base)),
                  "r"(BTmemCols)
@@ -455,24 +459,28 @@ head_grad_tc(const __grid_constant__ CUtensorMap d_map, const __grid_constant__ 
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   pdl_trigger();
-  pdl_wait();
+  if (!p.wait_last) pdl_wait();
 
-  // this pair's tiles and, of each, its steps of K
+  // this pair's tiles and, of each, its steps of K: split, split + kstep, ...
   const int tile0 = kW2 ? pair : pair / p.splits;
   const int tile_step = kW2 ? pairs : p.tiles;
   const int split = kW2 ? 0 : pair % p.splits;
-  const int k0 = kW2 ? 0 : (int)((long long)p.ksteps * split / p.splits);
-  const int k1 = kW2 ? p.ksteps : (int)((long long)p.ksteps * (split + 1) / p.splits);
+  // (the parts of K are interleaved, so that the pairs read neighbouring 128-byte
+  // pieces of a row of D at about the same time)
+  const int kstep = kW2 ? 1 : p.splits;
+  const int nk = (p.ksteps - split + kstep - 1) / kstep;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      const uint64_t pol_d = policy_evict_first(), pol_b = policy_evict_last();
+      // (a copy of 128-byte pieces brings its neighbours into L2 as well, which
+      // evict_first would drop before the pair next to this one reads them)
+      const uint64_t pol_d = policy_evict_normal(), pol_b = policy_evict_last();
       uint32_t i = 0;
       bool ok = true;
       for (int tile = tile0; tile < p.tiles && ok; tile += tile_step) {
         const int m0 = (tile * 2 + rank) * HM;
-        for (int k = k0; k < k1; ++k, ++i) {
+        for (int k = split; k < p.ksteps; k += kstep, ++i) {
           const int s = i % BStages;
           ok = mbar_wait(&bars->empty[s], ((i / BStages) & 1) ^ 1, abort, p.status);
           if (!ok) break;
@@ -503,8 +511,8 @@ head_grad_tc(const __grid_constant__ CUtensorMap d_map, const __grid_constant__ 
       uint32_t i = 0, chunk = 0;
       bool ok = true;
       for (int tile = tile0; tile < p.tiles && ok; tile += tile_step) {
-        for (int k = k0; k < k1 && ok; ++chunk) {
-          const int buf = chunk & 1, kend = min(k + kChunk, k1);
+        for (int k = 0; k < nk && ok; ++chunk) {
+          const int buf = chunk & 1, kend = min(k + kChunk, nk);
           ok = mbar_wait(&bars->acc_empty[buf], ((chunk >> 1) & 1) ^ 1, abort, p.status);
           if (!ok) break;
           tc_fence_after();
@@ -530,14 +538,15 @@ head_grad_tc(const __grid_constant__ CUtensorMap d_map, const __grid_constant__ 
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, h = (warp - 2) >> 2;
-    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + h * 128;
-    const int nchunks = (k1 - k0 + kChunk - 1) / kChunk;
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + h * 64;
+    unsigned char* box = boxes + (warp - 2) * BBoxBytes;
+    const int nchunks = (nk + kChunk - 1) / kChunk;
     uint32_t chunk = 0;
     bool ok = true;
     for (int tile = tile0; tile < p.tiles && ok; tile += tile_step) {
-      float acc[128];
+      float acc[64];
 #pragma unroll
-      for (int j = 0; j < 128; ++j) acc[j] = 0.f;
+      for (int j = 0; j < 64; ++j) acc[j] = 0.f;
       for (int n = 0; n < nchunks && ok; ++n, ++chunk) {
         const int buf = chunk & 1;
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->acc_full[buf], (chunk >> 1) & 1, abort, p.status));
@@ -545,29 +554,56 @@ head_grad_tc(const __grid_constant__ CUtensorMap d_map, const __grid_constant__ 
         tc_fence_after();
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float v[32];
-          tmem_load_cols<32>(lanes + buf * HK + j * 32, v);
+          float v[16];
+          tmem_load_cols<16>(lanes + buf * HK + j * 16, v);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) acc[j * 32 + e] += v[e];
+          for (int e = 0; e < 16; ++e) acc[j * 16 + e] += v[e];
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_in_cluster(in_cta(&bars->acc_empty[buf], 0));
       }
-      const int row = (tile * 2 + rank) * HM + q * 32 + lane;
-      if (ok && row < p.rows) {
-        float* o = p.out + ((size_t)split * (kW2 ? 0 : p.rows) + row) * HK + h * 128;
+      if (!ok) break;
+      // this warp's 32 rows and 64 columns by boxes, 128-byte swizzled (chunk j
+      // of row r at j ^ (r & 7)); rows past the output's end are clipped
+      const int row = (tile * 2 + rank) * HM + q * 32;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) st_8(o + j * 8, acc + j * 8);
-        if (kW2) {
-          const float none[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          float* z = p.zero + (size_t)row * HK + h * 128;
+      for (int j = 0; j < 2; ++j) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) st_8(z + j * 8, none);
+        for (int g = 0; g < 32 / BBoxRows; ++g) {
+          if (lane == 0) bulk_wait_read<0>();   // the box before is out
+          __syncwarp();
+          if (lane / BBoxRows == g) {
+            const int r = lane % BBoxRows;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<float4*>(box + r * 128 + ((e ^ (r & 7)) << 4)) =
+                  make_float4(acc[j * 32 + 4 * e], acc[j * 32 + 4 * e + 1], acc[j * 32 + 4 * e + 2],
+                              acc[j * 32 + 4 * e + 3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && row + g * BBoxRows < p.rows) {
+            tma_s2g_3d(&o_map, box, h * 64 + j * 32, row + g * BBoxRows, split);
+            bulk_commit();
+          }
         }
       }
+      if (kW2 && lane == 0) {
+        // zeros into 8 of the 32 rows of dW1
+        for (int i = 0; i < 2; ++i) {
+          const int z = row + h * 8 + i * 4, n = min(4, p.rows - z);
+          if (n > 0)
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(p.zero + (size_t)z * HK),
+                         "r"(smem_u32(zeros)), "r"(n * HK * 4)
+                         : "memory");
+        }
+        bulk_commit();
+      }
     }
+    if (lane == 0) bulk_wait_read<0>();
   }
+  if (p.wait_last) pdl_wait();
   tc_fence_before();
   __syncthreads();
   cluster_meet();   // neither CTA's memory is used past here
@@ -612,20 +648,40 @@ __global__ void __launch_bounds__(HK) scatter_rows(const float* dE, const int32_
   pdl_wait();
   const int n = blockIdx.x, tok = prev[n];
   if (tok < 0) return;
+  // bit i: row i * HK + threadIdx.x has this token
+  unsigned mine = 0;
+#pragma unroll 4
+  for (int i = 0; i < div_up(rows, HK); ++i) {
+    const int j = i * HK + threadIdx.x;
+    if ((j < rows ? prev[j] : -1) == tok) mine |= 1u << i;
+  }
   bool earlier = false;
-  for (int j = threadIdx.x; j < n; j += HK) earlier = earlier || prev[j] == tok;
+  for (unsigned left = mine; left != 0; left &= left - 1) earlier |= (__ffs(left) - 1) * HK + (int)threadIdx.x < n;
   if (__syncthreads_or(earlier)) return;
   __shared__ unsigned hits[HK / 32];
+  __shared__ int list[HK];
   float acc = 0.f;
-  for (int j0 = n; j0 < rows; j0 += HK) {
-    const int j = j0 + threadIdx.x;
-    const unsigned h = __ballot_sync(0xffffffffu, j < rows && prev[j] == tok);
-    if ((threadIdx.x & 31) == 0) hits[threadIdx.x >> 5] = h;
+  for (int i0 = n / HK; i0 < div_up(rows, HK); ++i0) {
+    const int j = i0 * HK + threadIdx.x, warp = threadIdx.x >> 5;
+    const bool same = mine >> i0 & 1u;
+    if (!__syncthreads_or(same)) continue;
+    const unsigned h = __ballot_sync(0xffffffffu, same);
+    if ((threadIdx.x & 31) == 0) hits[warp] = h;
     __syncthreads();
-    for (int w = 0; w < HK / 32; ++w)
-      for (unsigned left = hits[w]; left != 0; left &= left - 1)
-        acc += dE[(size_t)(j0 + w * 32 + __ffs(left) - 1) * HK + threadIdx.x];
+    int before = 0, count = 0;
+    for (int w = 0; w < HK / 32; ++w) {
+      if (w < warp) before += __popc(hits[w]);
+      count += __popc(hits[w]);
+    }
+    if (same) list[before + __popc(h & ((1u << (threadIdx.x & 31)) - 1u))] = j;
     __syncthreads();
+    for (int i = 0; i < count; i += 8) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = i + u < count ? dE[(size_t)list[i + u] * HK + threadIdx.x] : 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) acc += v[u];
+    }
   }
   dW1[(size_t)tok * HK + threadIdx.x] += acc;
 }
@@ -665,16 +721,29 @@ int sm_count() {
 }
 
 template <bool kW2>
-cudaError_t launch_grad(int pairs, const CUtensorMap& d, const CUtensorMap& b, const GradParams& p, cudaStream_t stream) {
+cudaError_t launch_grad(int pairs, const CUtensorMap& d, const CUtensorMap& b, float* out, const GradParams& p,
+                        cudaStream_t stream) {
+  // the output [splits][rows][256] in boxes of 16 x 32, 128-byte swizzled
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  CUtensorMap o;
+  cuuint64_t dims[3] = {(cuuint64_t)HK, (cuuint64_t)p.rows, (cuuint64_t)p.splits};
+  cuuint64_t strides[2] = {(cuuint64_t)HK * 4, (cuuint64_t)HK * 4 * p.rows};
+  cuuint32_t box[3] = {32, BBoxRows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  if (enc(&o, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
   auto kern = head_grad_tc<kW2>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, BSmemBytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(2 * pairs), dim3(BThreads), BSmemBytes, stream, d, b, p);
+  return launch_pdl(kern, dim3(2 * pairs), dim3(BThreads), BSmemBytes, stream, d, b, o, p);
 }
 
 // Rows of D whose dE parts the workspace holds at a time, and parts of K for
 // them: one CTA an SM.
 constexpr int kChunkRows = 4096;
+static_assert(kChunkRows / HK <= 32, "scatter_rows keeps a bit for every HK rows");
 constexpr int kMaxPairs = 80;
 
 }  // namespace
@@ -682,8 +751,8 @@ constexpr int kMaxPairs = 80;
 // Workspace: status word, previous tokens, E, the dE parts of a chunk.
 size_t head_workspace_bytes(int N, int V) {
   // rows * splits of a chunk: at most 256 rows for each pair, and at most
-  // kMaxPairs or V / 64 parts of the rows there are
-  const size_t splits = std::min(kMaxPairs, div_up(V, 64));
+  // kMaxPairs or V / (64 kChunk) parts of the rows there are
+  const size_t splits = std::min(kMaxPairs, div_up(div_up(V, 64), kChunk));
   const size_t parts = std::min<size_t>((size_t)kMaxPairs * 2 * HM, splits * std::min(N, kChunkRows));
   return 256 + align256(4ull * N) + align256(512ull * N) + align256(1024ull * parts);
 }
@@ -740,27 +809,27 @@ cudaError_t launch_markov_head_backward(const HeadBackwardArgs& a, cudaStream_t 
   if ((e = make_bf16_map(a.dlogits, N, a.V, 64, &dm)) != cudaSuccess) return e;
   if ((e = make_bf16_map(E, N, HK, 64, &bm)) != cudaSuccess) return e;
   GradParams p{};
-  p.out = a.dW2;
   p.zero = a.dW1;
   p.status = status;
   p.rows = a.V;
   p.ksteps = div_up(N, 64);
   p.tiles = div_up(a.V, 2 * HM);
   p.splits = 1;
-  if ((e = launch_grad<true>(std::min(p.tiles, pairs), dm, bm, p, stream)) != cudaSuccess) return e;
+  if ((e = launch_grad<true>(std::min(p.tiles, pairs), dm, bm, a.dW2, p, stream)) != cudaSuccess) return e;
 
   // dE and dW1, a chunk of rows at a time
   if ((e = make_bf16_map(a.dlogits, N, a.V, HM, &dm)) != cudaSuccess) return e;
   if ((e = make_bf16_map(a.W2, a.V, HK, 64, &bm)) != cudaSuccess) return e;
   for (int r0 = 0; r0 < N; r0 += kChunkRows) {
     const int rows = std::min(N - r0, kChunkRows);
-    p.out = part;
     p.rows = rows;
     p.row0 = r0;
     p.ksteps = div_up(a.V, 64);
     p.tiles = div_up(rows, 2 * HM);
-    p.splits = std::max(1, std::min(pairs / p.tiles, p.ksteps));
-    if ((e = launch_grad<false>(p.tiles * p.splits, dm, bm, p, stream)) != cudaSuccess) return e;
+    // (a part of K shorter than one chunk costs more in sum_parts than it gives)
+    p.splits = std::max(1, std::min(pairs / p.tiles, div_up(p.ksteps, kChunk)));
+    p.wait_last = r0 == 0;   // (a later chunk's parts replace those of the one before)
+    if ((e = launch_grad<false>(p.tiles * p.splits, dm, bm, part, p, stream)) != cudaSuccess) return e;
     if (p.splits > 1) {
       e = launch_pdl(sum_parts, dim3((unsigned)div_up(rows * (HK / 4), 256)), dim3(256), 0, stream,
                      reinterpret_cast<float4*>(part), rows, p.splits);
