@@ -37,7 +37,7 @@ struct Shared {
   Stat part[kWarps];
   Stat cta;               // of this CTA's part, outside the kept entries with a tail
   // the row's kept entries
-  int idx[kMaxTop];       // -1: absent
+  alignas(16) int idx[kMaxTop];   // -1: absent
   float p[kMaxTop];       // the teacher's probability
   float logp[kMaxTop];
   float pv[kMaxTop];      // p(v) at the first entry of its index, -1 elsewhere
@@ -68,15 +68,15 @@ __device__ __forceinline__ float cta_max(Shared& sh, int which, float v) {
 }
 
 // The teacher's side of a row and the student's logits there, by the CTA, into
-// sh; returns the state of the kept entries (with a tail), the rest's mass,
-// whether an index is out of range and whether an entry has mass.
+// sh; returns the state of the kept entries (with a tail, if `state`), the
+// rest's mass, whether an index is out of range and whether an entry has mass.
 struct Kept {
   Stat stat;
   float p_rest;
   bool bad, any;
 };
 template <typename T, bool kTail>
-__device__ __forceinline__ Kept load_kept(Shared& sh, const DistillArgs& p, int row, const T* rp) {
+__device__ __forceinline__ Kept load_kept(Shared& sh, const DistillArgs& p, int row, const T* rp, bool state) {
   const int tid = threadIdx.x;
   int idx = -1;
   float val = -INFINITY, z = 0.f;
@@ -113,16 +113,27 @@ __device__ __forceinline__ Kept load_kept(Shared& sh, const DistillArgs& p, int 
   const float total = cta_add(sh, 2, pk);
   r.p_rest = kTail ? (total > 1.f ? 0.f : 1.f - total) : 0.f;   // (a NaN total stays one)
   // p(v): equal indices add up in the first of them
-  float pv = 0.f;
+  float pv = pk;
   bool first = idx >= 0;
-  for (int k = 0; first && k < p.K; ++k) {
-    if (sh.idx[k] != idx) continue;
-    first = k >= tid;
-    pv += sh.p[k];
+  if (first) {
+    int equal = 0;
+#pragma unroll 4
+    for (int k = 0; k < p.K; k += 4) {
+      const int4 i = *reinterpret_cast<const int4*>(sh.idx + k);
+      equal += (i.x == idx) + (i.y == idx) + (i.z == idx) + (i.w == idx);
+    }
+    if (equal > 1) {
+      pv = 0.f;
+      for (int k = 0; first && k < p.K; ++k) {
+        if (sh.idx[k] != idx) continue;
+        first = k >= tid;
+        pv += sh.p[k];
+      }
+    }
   }
   if (tid < kMaxTop) sh.pv[tid] = first ? pv : -1.f;
   r.stat = stat_empty();
-  if (kTail) {
+  if (kTail && state) {
     r.stat.m = cta_max(sh, 3, first ? z : -INFINITY);
     r.stat.s = cta_add(sh, 0, first && r.stat.m != -INFINITY ? expf((z - r.stat.m) * p.inv_tau) : 0.f);
   }
@@ -183,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
         for (int k = tid; k < words; k += kThreads) marked[k] = 0;
         for (int k = tid; k < nblk; k += kThreads) block_marked[k] = 0;
       }
-      kept = load_kept<T, kTail>(sh, p, row, rp);
+      kept = load_kept<T, kTail>(sh, p, row, rp, true);
       if constexpr (kTail) {
         const int place = tid < p.K && sh.idx[tid] >= 0 ? sh.idx[tid] - place0 : -1;
         if (place >= 0 && place < nblk * kBlockPlaces) {
@@ -244,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
     }
   } else if (on) {
     first_block();
-    kept = load_kept<T, kTail>(sh, p, row, rp);
+    kept = load_kept<T, kTail>(sh, p, row, rp, false);
     // the references in units of the logits, with what their rounding lost
     on = (kept.any || kept.bad) && lse_in != -INFINITY;
     q_ref = on ? lse_in * p.tau : 0.f;
