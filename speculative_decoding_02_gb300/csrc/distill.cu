@@ -277,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
     G* out = static_cast<G*>(p.dlogits) + (size_t)row * p.V;
     // an output row whose vectors start where the logits' do is stored by vectors
     const bool aligned = ((reinterpret_cast<uintptr_t>(out) - R.shift * sizeof(G)) & (VEC * sizeof(G) - 1)) == 0;
+    const uint64_t ref2 = pack2(-ref, -ref), scale2 = pack2(scale, scale), cw2 = pack2(cw, cw);
     for (; b >= br.begin + warp; b -= kWarps) {
       if (on && b - kWarps >= br.begin + warp) R.template load_block<Hold::kShort>(b - kWarps, lane, nxt);
       const bool inside = aligned && R.inside(b);
@@ -287,7 +288,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
         float x[VEC];
         if (on) Elem<T>::unpack(cur[j], x);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) g[e] = Elem<G>::from_float(on ? ex2((x[e] - ref) * scale) * cw : 0.f);
+        for (int e = 0; e < VEC; e += 2) {
+          float u = 0.f, v = 0.f;
+          if (on) {
+            unpack2(mul2(add2(pack2(x[e], x[e + 1]), ref2), scale2), u, v);
+            unpack2(mul2(pack2(ex2(u), ex2(v)), cw2), u, v);
+          }
+          put2(g + e, u, v);
+        }
         if (inside || (aligned && R.whole(i))) {
           if constexpr (sizeof(G) * VEC == 16) __stcs(reinterpret_cast<uint4*>(out + e0), *reinterpret_cast<const uint4*>(g));
           else __stcs(reinterpret_cast<uint2*>(out + e0), *reinterpret_cast<const uint2*>(g));

@@ -268,6 +268,15 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
+// Two results, rounded, next to each other.
+__device__ __forceinline__ void put2(float* g, float a, float b) { g[0] = a; g[1] = b; }
+__device__ __forceinline__ void put2(__nv_bfloat16* g, float a, float b) {
+  *reinterpret_cast<__nv_bfloat162*>(g) = __floats2bfloat162_rn(a, b);
+}
+__device__ __forceinline__ void put2(__half* g, float a, float b) {
+  *reinterpret_cast<__half2*>(g) = __floats2half2_rn(a, b);
+}
+
 // A lane's running state: the warp's maximum, and the sums of its even and odd
 // entries (t with the opposite sign).
 struct LaneStat {

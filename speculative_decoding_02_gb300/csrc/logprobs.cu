@@ -353,7 +353,16 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_backward_kernel(const Lo
   const bool zero = ref == -INFINITY;   // not scored, or no entry above -inf
   const float a = gh != 0.f ? fmaf(gh, p.entropy[row], gl) : gl;
   const bool aligned = ((reinterpret_cast<uintptr_t>(out) - R.shift * sizeof(T)) & 15) == 0;
+  // the token's own entry is stored last, over what the loop leaves there; its
+  // logit is read first, for out may be the logits
+  const int place0 = br.begin * kBlockVecs * VEC - R.shift;
+  const bool last = threadIdx.x == 0 && !zero && tok >= place0 && tok < place0 + (br.end - br.begin) * kBlockVecs * VEC;
+  const float xt = last && tok < p.V ? Elem<T>::to_float(R.row[max(tok, 0)]) : 0.f;
+  __syncthreads();
+  const uint64_t ref2 = pack2(-ref, -ref), ls2 = pack2(-ls, -ls), scale2 = pack2(kLog2e, kLog2e);
+  const uint64_t gh2 = pack2(-gh, -gh), a2 = pack2(-a, -a);
   for (int b = br.begin + warp; b < br.end; b += kWarps) {
+    const bool inside = aligned && R.inside(b);
     uint4 r[kVecPerLane];
     if (!zero) R.load_block(b, lane, r);
 #pragma unroll
@@ -362,20 +371,21 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_backward_kernel(const Lo
       alignas(16) T g[VEC];
       if (zero) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) g[e] = Elem<T>::from_float(0.f);
+        for (int e = 0; e < VEC; e += 2) put2(g + e, 0.f, 0.f);
       } else {
         float x[VEC];
         Elem<T>::unpack(r[j], x);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float d = fmaxf((x[e] - ref) - ls, -1000.f);   // (an entry of -inf: p = 0, gradient 0)
-          const float pr = ex2(d * kLog2e);
-          float v = -pr * fmaf(gh, d, a);
-          if (e0 + e == tok) v += gl;
-          g[e] = Elem<T>::from_float(v);
+        for (int e = 0; e < VEC; e += 2) {
+          float u, v;
+          unpack2(add2(add2(pack2(x[e], x[e + 1]), ref2), ls2), u, v);
+          const uint64_t d = pack2(fmaxf(u, -1000.f), fmaxf(v, -1000.f));   // (an entry of -inf: p = 0, gradient 0)
+          unpack2(mul2(d, scale2), u, v);
+          unpack2(mul2(pack2(ex2(u), ex2(v)), fma2(gh2, d, a2)), u, v);
+          put2(g + e, u, v);
         }
       }
-      if (aligned && R.whole(i)) {
+      if (inside || (aligned && R.whole(i))) {
         __stcs(reinterpret_cast<uint4*>(out + e0), *reinterpret_cast<const uint4*>(g));
       } else {
 #pragma unroll
@@ -383,6 +393,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_backward_kernel(const Lo
           if (e0 + e >= 0 && e0 + e < p.V) out[e0 + e] = g[e];
       }
     }
+  }
+  __syncthreads();
+  if (last && tok >= 0 && tok < p.V) {
+    const float d = fmaxf((xt - ref) - ls, -1000.f);
+    out[tok] = Elem<T>::from_float(gl - ex2(d * kLog2e) * fmaf(gh, d, a));
   }
 }
 
