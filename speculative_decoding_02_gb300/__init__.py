@@ -177,6 +177,7 @@ def _sized(t, what, shape):
 
 
 _ws_cache = {}
+_ws_views = {}
 
 
 def workspace_size(B, gamma, V):
@@ -185,6 +186,9 @@ def workspace_size(B, gamma, V):
 
 def workspace(B, gamma, V, device):
     """A cached, 256-byte aligned device workspace for these sizes."""
+    view = _ws_views.get((B, gamma, V, device))
+    if view is not None:
+        return view
     n = workspace_size(B, gamma, V)
     key = (torch.device(device), n)
     ws = _ws_cache.get(key)
@@ -192,7 +196,8 @@ def workspace(B, gamma, V, device):
         ws = torch.zeros(n + 256, dtype=torch.uint8, device=device)
         _ws_cache[key] = ws
     off = (-ws.data_ptr()) % 256
-    return ws[off:off + n]
+    view = _ws_views[(B, gamma, V, device)] = ws[off:off + n]
+    return view
 
 
 def _round_dev(round_dev, dev):

@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
   const bool backward = p.stats_in != nullptr, grad = p.dlogits != nullptr;
   const float nan = __int_as_float(0x7FC00000);
   const float scale = p.inv_tau * kLog2e;
+  const uint64_t drop = tc::policy_evict_first();   // of what is read for the last time
   const T* rp = static_cast<const T*>(p.logits) + (size_t)row * p.row_stride;
   const Row<T> R(rp, p.V);
   const BlockRange br = block_range(R.nvec, rank, c);
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
   uint4 cur[kVecPerLane], nxt[kVecPerLane];
   int b = nblk > warp ? br.begin + warp + (nblk - 1 - warp) / kWarps * kWarps : -1;
   auto first_block = [&]() {
-    if (grad && b >= 0) R.template load_block<Hold::kShort>(b, lane, cur);
+    if (grad && b >= 0) R.load_block(b, lane, cur, drop);
   };
 
   if (pass) {
@@ -219,7 +220,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
         }
       }
     };
-    stat_row<T, false, false, Hold::kLong>(R, br, scale, p.inv_tau, sh.part, &sh.cta, before, leave_out, Nothing());
+    // (with a gradient to come L2 is asked to keep the row for it)
+    stat_row<T, false, false>(R, br, scale, p.inv_tau, grad ? tc::policy_evict_last() : drop, sh.part, &sh.cta, before,
+                              leave_out, Nothing());
     cluster_arrive(c);
     first_block();
     cluster_wait(c);
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
     const bool aligned = ((reinterpret_cast<uintptr_t>(out) - R.shift * sizeof(G)) & (VEC * sizeof(G) - 1)) == 0;
     const uint64_t ref2 = pack2(-ref, -ref), scale2 = pack2(scale, scale), cw2 = pack2(cw, cw);
     for (; b >= br.begin + warp; b -= kWarps) {
-      if (on && b - kWarps >= br.begin + warp) R.template load_block<Hold::kShort>(b - kWarps, lane, nxt);
+      if (on && b - kWarps >= br.begin + warp) R.load_block(b - kWarps, lane, nxt, drop);
       const bool inside = aligned && R.inside(b);
 #pragma unroll
       for (int j = 0; j < kVecPerLane; ++j) {

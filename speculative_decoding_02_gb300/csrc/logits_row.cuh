@@ -23,6 +23,7 @@
 #include <cuda_fp16.h>
 
 #include "kernels.h"
+#include "tc_common.cuh"
 
 namespace dspark {
 namespace lrow {
@@ -81,27 +82,23 @@ struct Elem<__half> {
   }
 };
 
-// How long L2 should hold what a load brings in.
-enum class Hold { kNormal, kLong, kShort };
-template <Hold H>
-__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+// A 16-byte load past L1; a policy (createpolicy) says how long L2 holds it, and
+// none costs no register.
+struct NoPolicy {};
+__device__ __forceinline__ uint4 ld_stream(const uint4* p, NoPolicy) {
   uint4 v;
-  if constexpr (H == Hold::kNormal) {
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p)
-                 : "memory");
-  } else {
-    uint64_t policy;
-    if constexpr (H == Hold::kLong)
-      asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(policy));
-    else
-      asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
-    asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p), "l"(policy)
-                 : "memory");
-  }
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 ld_stream(const uint4* p, uint64_t policy) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p), "l"(policy)
+               : "memory");
   return v;
 }
 
@@ -125,9 +122,9 @@ struct Row {
     return e0 >= 0 && e0 + Elem<T>::VEC <= V;
   }
   // Vector i with -inf in the places outside the row (i >= nvec: all of them).
-  template <Hold H = Hold::kNormal>
-  __device__ __forceinline__ uint4 load(int i) const {
-    return whole(i) ? ld_stream<H>(base + i) : load_edge(i);
+  template <typename P>
+  __device__ __forceinline__ uint4 load(int i, P policy) const {
+    return whole(i) ? ld_stream(base + i, policy) : load_edge(i);
   }
   __device__ __noinline__ uint4 load_edge(int i) const {
     uint4 v = make_uint4(Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf);
@@ -142,15 +139,15 @@ struct Row {
     return first_entry(b * kBlockVecs) >= 0 && first_entry((b + 1) * kBlockVecs) <= V;
   }
   // This lane's vectors of block b.
-  template <Hold H = Hold::kNormal>
-  __device__ __forceinline__ void load_block(int b, int lane, uint4 (&r)[kVecPerLane]) const {
+  template <typename P>
+  __device__ __forceinline__ void load_block(int b, int lane, uint4 (&r)[kVecPerLane], P policy) const {
     const int i0 = b * kBlockVecs + lane;
     if (inside(b)) {
 #pragma unroll
-      for (int j = 0; j < kVecPerLane; ++j) r[j] = ld_stream<H>(base + i0 + j * 32);
+      for (int j = 0; j < kVecPerLane; ++j) r[j] = ld_stream(base + i0 + j * 32, policy);
     } else {
 #pragma unroll
-      for (int j = 0; j < kVecPerLane; ++j) r[j] = load<H>(i0 + j * 32);
+      for (int j = 0; j < kVecPerLane; ++j) r[j] = load(i0 + j * 32, policy);
     }
   }
 };
@@ -355,15 +352,15 @@ __device__ __forceinline__ void cta_stat(const LaneStat& st, float inv, Stat* pa
 // kSeen seen(b, lane maximum, float4) sees a block's maxima: those of its four
 // quarters (one vector of every lane).  The next blocks' loads are in flight
 // while one is taken in.
-template <typename T, bool kEntropy, bool kSeen, Hold H = Hold::kNormal, typename Before, typename Each, typename Seen>
-__device__ __forceinline__ void stat_row(const Row<T>& R, const BlockRange& br, float scale, float inv, Stat* part,
+template <typename T, bool kEntropy, bool kSeen, typename P, typename Before, typename Each, typename Seen>
+__device__ __forceinline__ void stat_row(const Row<T>& R, const BlockRange& br, float scale, float inv, P policy, Stat* part,
                                          Stat* out, Before before, Each each, Seen seen) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   LaneStat st = lane_stat_empty();
   uint4 cur[kVecPerLane], nxt[kVecPerLane];
   int b = br.begin + warp;
-  if (b < br.end) R.template load_block<H>(b, lane, cur);
-  if (b + kWarps < br.end) R.template load_block<H>(b + kWarps, lane, nxt);
+  if (b < br.end) R.load_block(b, lane, cur, policy);
+  if (b + kWarps < br.end) R.load_block(b + kWarps, lane, nxt, policy);
   before();
   for (; b < br.end; b += kWarps) {
     each(b, cur);
@@ -383,7 +380,7 @@ __device__ __forceinline__ void stat_row(const Row<T>& R, const BlockRange& br, 
     stat_block<T, kEntropy>(st, cur, bm, scale);
 #pragma unroll
     for (int j = 0; j < kVecPerLane; ++j) cur[j] = nxt[j];
-    if (b + 2 * kWarps < br.end) R.template load_block<H>(b + 2 * kWarps, lane, nxt);
+    if (b + 2 * kWarps < br.end) R.load_block(b + 2 * kWarps, lane, nxt, policy);
   }
   cta_stat(st, inv, part, out);
 }

@@ -89,12 +89,12 @@ __device__ __forceinline__ void for_candidates(const Shared& sh, const Row<T>& R
       return (b0 + (l >> 2) * kWarps) * kBlockVecs + (l & 3) * 32 + lane;
     };
     uint4 nxt = make_uint4(0, 0, 0, 0);
-    if (hit != 0) nxt = R.load(vec_of(hit));
+    if (hit != 0) nxt = R.load(vec_of(hit), NoPolicy());
     while (hit != 0) {
       const int i = vec_of(hit);
       const uint4 r = nxt;
       hit &= hit - 1;
-      if (hit != 0) nxt = R.load(vec_of(hit));
+      if (hit != 0) nxt = R.load(vec_of(hit), NoPolicy());
       if (!(vec_max(r, (const T*)nullptr) < least)) {
         float v[Elem<T>::VEC];
         Elem<T>::unpack(r, v);
@@ -269,10 +269,15 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
 
   float tmax = -INFINITY;
   if (kTop && tid == 0) sh.ncand = 0;
-  stat_row<T, true, kTop>(R, br, kLog2e, 1.f, sh.part, &sh.cta, Nothing(), Nothing(), [&](int b, float lm, float4 q) {
+  auto seen = [&](int b, float lm, float4 q) {
     tmax = fmaxf(tmax, lm);
     if (lane == 0) sh.quarter[b - br.begin] = q;
-  });
+  };
+  // (some of the row is read again for its alternatives)
+  if constexpr (kTop)
+    stat_row<T, true, true>(R, br, kLog2e, 1.f, NoPolicy(), sh.part, &sh.cta, Nothing(), Nothing(), seen);
+  else
+    stat_row<T, true, false>(R, br, kLog2e, 1.f, tc::policy_evict_first(), sh.part, &sh.cta, Nothing(), Nothing(), Nothing());
   if (kTop) sh.lane_max[tid] = tmax;
   cluster_meet(c);
   const Stat v = stat_cluster(cluster, &sh.cta, c, 1.f);
@@ -342,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_backward_kernel(const Lo
   float ref = on ? p.lse[row] : -INFINITY, ls = 0.f;
   if (ref != ref) gl = nan;
   if (fabsf(ref) > kLargeLse && ref != -INFINITY) {
-    stat_row<T, false, false>(R, br, kLog2e, 1.f, part, &cta, Nothing(), Nothing(), Nothing());
+    stat_row<T, false, false>(R, br, kLog2e, 1.f, NoPolicy(), part, &cta, Nothing(), Nothing(), Nothing());
     cluster_meet(c);
     const Stat v = stat_cluster(cluster, &cta, c, 1.f);
     cluster_meet(c);
@@ -364,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_backward_kernel(const Lo
   for (int b = br.begin + warp; b < br.end; b += kWarps) {
     const bool inside = aligned && R.inside(b);
     uint4 r[kVecPerLane];
-    if (!zero) R.load_block(b, lane, r);
+    if (!zero) R.load_block(b, lane, r, NoPolicy());
 #pragma unroll
     for (int j = 0; j < kVecPerLane; ++j) {
       const int i = b * kBlockVecs + j * 32 + lane, e0 = R.first_entry(i);
