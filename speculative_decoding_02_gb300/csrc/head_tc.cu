@@ -94,6 +94,7 @@ struct LogitParams {
   int ntiles;        // column tiles
   int tail_tile;     // the column tile that comes and goes as [rows x 32] boxes (V % 32 != 0), else -1
   long long units;
+  int per;           // CTAs of a row tile, or 0
 };
 
 __device__ __forceinline__ void tma_s2g_2d(const CUtensorMap* map, const void* src, int c0, int c1) {
@@ -133,7 +134,12 @@ markov_logits_tc(const __grid_constant__ CUtensorMap w_map, const __grid_constan
   unsigned char* W_s = U_s + GUStages * GUBytes;
   GBars* bars = reinterpret_cast<GBars*>(W_s + GWStages * GWBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long u0 = p.units * blockIdx.x / gridDim.x, u1 = p.units * (blockIdx.x + 1) / gridDim.x;
+  // this CTA's tiles u = row tile * ntiles + column tile: with per > 0 every
+  // per-th of one row tile, else a contiguous range
+  const int step = max(p.per, 1);
+  const long long row0 = p.per > 0 ? (long long)(blockIdx.x / p.per) * p.ntiles : 0;
+  const long long u0 = p.per > 0 ? row0 + blockIdx.x % p.per : p.units * blockIdx.x / gridDim.x;
+  const long long u1 = p.per > 0 ? row0 + p.ntiles : p.units * (blockIdx.x + 1) / gridDim.x;
   volatile int* abort = &bars->abort;
 
   if (threadIdx.x == 0) {
@@ -162,7 +168,7 @@ markov_logits_tc(const __grid_constant__ CUtensorMap w_map, const __grid_constan
       const uint64_t pol_w = policy_evict_last(), pol_u = policy_evict_normal();
       uint32_t i = 0;
       bool ok = true;
-      for (long long u = u0; u < u1; ++u, ++i) {
+      for (long long u = u0; u < u1; u += step, ++i) {
         const int m0 = (int)(u / p.ntiles) * HM, t = (int)(u % p.ntiles), v0 = t * GN;
         const int sw = i % GWStages, su = i % GUStages;
         ok = mbar_wait(&bars->empty_w[sw], ((i / GWStages) & 1) ^ 1, abort, p.status);
@@ -202,7 +208,7 @@ markov_logits_tc(const __grid_constant__ CUtensorMap w_map, const __grid_constan
       uint32_t i = 0, em = 0;
       int m = -1;
       bool ok = true;
-      for (long long u = u0; u < u1 && ok; ++u, ++i) {
+      for (long long u = u0; u < u1 && ok; u += step, ++i) {
         if ((int)(u / p.ntiles) != m) {
           m = (int)(u / p.ntiles);
           if (!(ok = mbar_wait(&bars->e_full, em++ & 1, abort, p.status))) break;
@@ -236,7 +242,7 @@ markov_logits_tc(const __grid_constant__ CUtensorMap w_map, const __grid_constan
     bool ok = true;
     // (a warp whose wait gave up goes on through the tiles' barriers, which the
     // others may be at, and does nothing else)
-    for (long long u = u0; u < u1; ++u, ++i) {
+    for (long long u = u0; u < u1; u += step, ++i) {
       const int t = (int)(u % p.ntiles);
       const int acc = i & 1, su = i % GUStages;
       unsigned char* tile = U_s + su * GUBytes;
@@ -782,7 +788,13 @@ cudaError_t launch_markov_logits(const MarkovLogitArgs& a, cudaStream_t stream) 
   p.units = (long long)div_up(N, HM) * p.ntiles;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorUnknown;
-  const int grid = (int)std::min<long long>(p.units, sms);
+  // CTAs side by side on one row tile read neighbouring columns at about the
+  // same time; where whole groups of them would leave more than a tenth of the
+  // SMs idle, contiguous ranges
+  const int mtiles = div_up(N, HM);
+  p.per = mtiles <= sms ? std::min(sms / mtiles, p.ntiles) : 0;
+  if (p.per > 0 && p.per < p.ntiles && 10 * mtiles * p.per < 9 * sms) p.per = 0;
+  const int grid = p.per > 0 ? mtiles * p.per : (int)std::min<long long>(p.units, sms);
   auto kern = a.odtype == DSPARK_F32 ? markov_logits_tc<DSPARK_F32> : markov_logits_tc<DSPARK_BF16>;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GSmemBytes)) != cudaSuccess) return e;
   kern<<<grid, GThreads, GSmemBytes, stream>>>(w, u, u4, o, o4, p);
