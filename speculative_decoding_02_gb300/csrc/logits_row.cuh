@@ -362,25 +362,28 @@ __device__ __forceinline__ void stat_row(const Row<T>& R, const BlockRange& br, 
   if (b < br.end) R.load_block(b, lane, cur, policy);
   if (b + kWarps < br.end) R.load_block(b + kWarps, lane, nxt, policy);
   before();
-  for (; b < br.end; b += kWarps) {
-    each(b, cur);
+  auto take = [&](int k, uint4(&v)[kVecPerLane]) {
+    each(k, v);
     float bm;
     if constexpr (kSeen) {
       static_assert(kVecPerLane == 4, "four quarters");
-      float v[4], q[4];
+      float m[4], q[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = vec_max(cur[j], (const T*)nullptr);
+      for (int j = 0; j < 4; ++j) m[j] = vec_max(v[j], (const T*)nullptr);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) q[j] = warp_max_nan(v[j]);
+      for (int j = 0; j < 4; ++j) q[j] = warp_max_nan(m[j]);
       bm = max_nan(max_nan(q[0], q[1]), max_nan(q[2], q[3]));
-      seen(b, max_nan(max_nan(v[0], v[1]), max_nan(v[2], v[3])), make_float4(q[0], q[1], q[2], q[3]));
+      seen(k, max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3])), make_float4(q[0], q[1], q[2], q[3]));
     } else {
-      bm = warp_max_nan(lane_max(cur, (const T*)nullptr));
+      bm = warp_max_nan(lane_max(v, (const T*)nullptr));
     }
-    stat_block<T, kEntropy>(st, cur, bm, scale);
-#pragma unroll
-    for (int j = 0; j < kVecPerLane; ++j) cur[j] = nxt[j];
-    if (b + 2 * kWarps < br.end) R.load_block(b + 2 * kWarps, lane, nxt, policy);
+    stat_block<T, kEntropy>(st, v, bm, scale);
+    if (k + 2 * kWarps < br.end) R.load_block(k + 2 * kWarps, lane, v, policy);
+  };
+  // (two blocks a turn, each in registers of its own)
+  for (; b < br.end; b += 2 * kWarps) {
+    take(b, cur);
+    if (b + kWarps < br.end) take(b + kWarps, nxt);
   }
   cta_stat(st, inv, part, out);
 }
