@@ -280,34 +280,47 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
     G* out = static_cast<G*>(p.dlogits) + (size_t)row * p.V;
     // an output row whose vectors start where the logits' do is stored by vectors
     const bool aligned = ((reinterpret_cast<uintptr_t>(out) - R.shift * sizeof(G)) & (VEC * sizeof(G) - 1)) == 0;
+    auto store = [&](int k, int j, bool inside, const G(&g)[VEC]) {
+      const int i = k * kBlockVecs + j * 32 + lane, e0 = R.first_entry(i);
+      if (inside || (aligned && R.whole(i))) {
+        if constexpr (sizeof(G) * VEC == 16) __stcs(reinterpret_cast<uint4*>(out + e0), *reinterpret_cast<const uint4*>(g));
+        else __stcs(reinterpret_cast<uint2*>(out + e0), *reinterpret_cast<const uint2*>(g));
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (e0 + e >= 0 && e0 + e < p.V) out[e0 + e] = g[e];
+      }
+    };
+    if (!on) {
+      alignas(16) G none[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; e += 2) put2(none + e, 0.f, 0.f);
+      for (; b >= br.begin + warp; b -= kWarps) {
+#pragma unroll
+        for (int j = 0; j < kVecPerLane; ++j) store(b, j, aligned && R.inside(b), none);
+      }
+    }
     const uint64_t ref2 = pack2(-ref, -ref), scale2 = pack2(scale, scale), cw2 = pack2(cw, cw);
-    for (; b >= br.begin + warp; b -= kWarps) {
-      if (on && b - kWarps >= br.begin + warp) R.load_block(b - kWarps, lane, nxt, drop);
-      const bool inside = aligned && R.inside(b);
+    auto gradient = [&](int k, const uint4(&r)[kVecPerLane]) {
+      const bool inside = aligned && R.inside(k);
 #pragma unroll
       for (int j = 0; j < kVecPerLane; ++j) {
-        const int i = b * kBlockVecs + j * 32 + lane, e0 = R.first_entry(i);
         alignas(16) G g[VEC];
         float x[VEC];
-        if (on) Elem<T>::unpack(cur[j], x);
+        Elem<T>::unpack(r[j], x);
 #pragma unroll
         for (int e = 0; e < VEC; e += 2) {
-          float u = 0.f, v = 0.f;
-          if (on) {
-            unpack2(mul2(add2(pack2(x[e], x[e + 1]), ref2), scale2), u, v);
-            unpack2(mul2(pack2(ex2(u), ex2(v)), cw2), u, v);
-          }
+          float u, v;
+          unpack2(mul2(add2(pack2(x[e], x[e + 1]), ref2), scale2), u, v);
+          unpack2(mul2(pack2(ex2(u), ex2(v)), cw2), u, v);
           put2(g + e, u, v);
         }
-        if (inside || (aligned && R.whole(i))) {
-          if constexpr (sizeof(G) * VEC == 16) __stcs(reinterpret_cast<uint4*>(out + e0), *reinterpret_cast<const uint4*>(g));
-          else __stcs(reinterpret_cast<uint2*>(out + e0), *reinterpret_cast<const uint2*>(g));
-        } else {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e)
-            if (e0 + e >= 0 && e0 + e < p.V) out[e0 + e] = g[e];
-        }
+        store(k, j, inside, g);
       }
+    };
+    for (; b >= br.begin + warp; b -= kWarps) {
+      if (b - kWarps >= br.begin + warp) R.load_block(b - kWarps, lane, nxt, drop);
+      gradient(b, cur);
 #pragma unroll
       for (int j = 0; j < kVecPerLane; ++j) cur[j] = nxt[j];
     }

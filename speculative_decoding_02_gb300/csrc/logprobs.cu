@@ -364,45 +364,57 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_backward_kernel(const Lo
   const bool last = threadIdx.x == 0 && !zero && tok >= place0 && tok < place0 + (br.end - br.begin) * kBlockVecs * VEC;
   const float xt = last && tok < p.V ? Elem<T>::to_float(R.row[max(tok, 0)]) : 0.f;
   __syncthreads();
-  const uint64_t ref2 = pack2(-ref, -ref), ls2 = pack2(-ls, -ls), scale2 = pack2(kLog2e, kLog2e);
-  const uint64_t gh2 = pack2(-gh, -gh), a2 = pack2(-a, -a);
-  for (int b = br.begin + warp; b < br.end; b += kWarps) {
+  auto store = [&](int b, int j, bool inside, const T(&g)[VEC]) {
+    const int i = b * kBlockVecs + j * 32 + lane, e0 = R.first_entry(i);
+    if (inside || (aligned && R.whole(i))) {
+      __stcs(reinterpret_cast<uint4*>(out + e0), *reinterpret_cast<const uint4*>(g));
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (e0 + e >= 0 && e0 + e < p.V) out[e0 + e] = g[e];
+    }
+  };
+  if (zero) {
+    alignas(16) T none[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) put2(none + e, 0.f, 0.f);
+    for (int b = br.begin + warp; b < br.end; b += kWarps) {
+#pragma unroll
+      for (int j = 0; j < kVecPerLane; ++j) store(b, j, aligned && R.inside(b), none);
+    }
+    return;
+  }
+  // with d = x - ref and f = exp(-ls): -p (a + g_H (d - ls)) = exp(d) (-f (a - g_H ls) - f g_H d)
+  const float f = expf(-ls), c0 = -f * fmaf(-gh, ls, a), c1 = -f * gh;
+  const uint64_t ref2 = pack2(-ref, -ref), scale2 = pack2(kLog2e, kLog2e), c02 = pack2(c0, c0), c12 = pack2(c1, c1);
+  auto gradient = [&](int b, const uint4(&r)[kVecPerLane]) {
     const bool inside = aligned && R.inside(b);
-    uint4 r[kVecPerLane];
-    if (!zero) R.load_block(b, lane, r, NoPolicy());
 #pragma unroll
     for (int j = 0; j < kVecPerLane; ++j) {
-      const int i = b * kBlockVecs + j * 32 + lane, e0 = R.first_entry(i);
       alignas(16) T g[VEC];
-      if (zero) {
+      float x[VEC];
+      Elem<T>::unpack(r[j], x);
 #pragma unroll
-        for (int e = 0; e < VEC; e += 2) put2(g + e, 0.f, 0.f);
-      } else {
-        float x[VEC];
-        Elem<T>::unpack(r[j], x);
-#pragma unroll
-        for (int e = 0; e < VEC; e += 2) {
-          float u, v;
-          unpack2(add2(add2(pack2(x[e], x[e + 1]), ref2), ls2), u, v);
-          const uint64_t d = pack2(fmaxf(u, -1000.f), fmaxf(v, -1000.f));   // (an entry of -inf: p = 0, gradient 0)
-          unpack2(mul2(d, scale2), u, v);
-          unpack2(mul2(pack2(ex2(u), ex2(v)), fma2(gh2, d, a2)), u, v);
-          put2(g + e, u, v);
-        }
+      for (int e = 0; e < VEC; e += 2) {
+        float u, v;
+        unpack2(add2(pack2(x[e], x[e + 1]), ref2), u, v);
+        const uint64_t d = pack2(fmaxf(u, -1000.f), fmaxf(v, -1000.f));   // (an entry of -inf: p = 0, gradient 0)
+        unpack2(mul2(d, scale2), u, v);
+        unpack2(mul2(pack2(ex2(u), ex2(v)), fma2(c12, d, c02)), u, v);
+        put2(g + e, u, v);
       }
-      if (inside || (aligned && R.whole(i))) {
-        __stcs(reinterpret_cast<uint4*>(out + e0), *reinterpret_cast<const uint4*>(g));
-      } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          if (e0 + e >= 0 && e0 + e < p.V) out[e0 + e] = g[e];
-      }
+      store(b, j, inside, g);
     }
+  };
+  for (int b = br.begin + warp; b < br.end; b += kWarps) {
+    uint4 r[kVecPerLane];
+    R.load_block(b, lane, r, NoPolicy());
+    gradient(b, r);
   }
   __syncthreads();
   if (last && tok >= 0 && tok < p.V) {
-    const float d = fmaxf((xt - ref) - ls, -1000.f);
-    out[tok] = Elem<T>::from_float(gl - ex2(d * kLog2e) * fmaf(gh, d, a));
+    const float d = fmaxf(xt - ref, -1000.f);
+    out[tok] = Elem<T>::from_float(fmaf(ex2(d * kLog2e), fmaf(c1, d, c0), gl));
   }
 }
 
