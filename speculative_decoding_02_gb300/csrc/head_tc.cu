@@ -789,11 +789,13 @@ cudaError_t launch_markov_logits(const MarkovLogitArgs& a, cudaStream_t stream) 
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorUnknown;
   // CTAs side by side on one row tile read neighbouring columns at about the
-  // same time; where whole groups of them would leave more than a tenth of the
-  // SMs idle, contiguous ranges
+  // same time, which DRAM serves faster than one range a CTA: 393 against 449 us
+  // at 16 row tiles of 151936 columns, 163 against 181 at 60 of 16384 although
+  // that leaves a fifth of the SMs idle.  With one CTA a row tile there are no
+  // neighbours (297 against 301 at 100 row tiles): ranges, on every SM.
   const int mtiles = div_up(N, HM);
-  p.per = mtiles <= sms ? std::min(sms / mtiles, p.ntiles) : 0;
-  if (p.per > 0 && p.per < p.ntiles && 10 * mtiles * p.per < 9 * sms) p.per = 0;
+  p.per = std::min(sms / mtiles, p.ntiles);
+  if (p.per == 1 && p.ntiles > 1) p.per = 0;
   const int grid = p.per > 0 ? mtiles * p.per : (int)std::min<long long>(p.units, sms);
   auto kern = a.odtype == DSPARK_F32 ? markov_logits_tc<DSPARK_F32> : markov_logits_tc<DSPARK_BF16>;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GSmemBytes)) != cudaSuccess) return e;

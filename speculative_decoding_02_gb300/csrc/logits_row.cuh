@@ -430,11 +430,14 @@ __device__ __forceinline__ bool stat_bad(const Stat& v) { return !(v.m < INFINIT
 // lost beside it) they take the row's state anew.
 constexpr float kLargeLse = 1024.f;
 
-// CTAs a row: at least `least` (1 to 16), and for few rows as many more as give
-// each SM about two while every warp keeps a block.
+// CTAs a row: at least `least` (1 to 16), and for few rows up to 8 as long as
+// every warp keeps a block and the SMs have about two each.  Rows of 151936
+// fp32 entries with 20 alternatives: one row takes 21 us by one CTA, 9.5 by 8 and
+// 9.7 by 16; 16 rows 21, 10.6 and 15.7; 152 rows 31 by one each, 24 by 2 and 30
+// by 4; 304 rows 38, 36 and 51.
 inline int cluster_for(int rows, int nblk, int least, int sms) {
   int c = least;
-  while (2 * c <= kMaxCluster && (long long)rows * c <= sms && nblk > kWarps * c) c *= 2;
+  while (2 * c <= 8 && (long long)rows * c <= sms && nblk > kWarps * c) c *= 2;
   return c;
 }
 

@@ -428,7 +428,9 @@ template <typename T>
 cudaError_t backward(const LogprobBackwardArgs& a, cudaStream_t stream) {
   const int nblk = div_up(div_up(a.V, Elem<T>::VEC) + 1, kBlockVecs);
   int c = 1;
-  while (c < 8 && nblk > 2 * kWarps * c) c *= 2;   // two blocks a warp and more
+  while (c < 8 && nblk > 2 * kWarps * c) c *= 2;
+  // (two blocks a warp and more: 640 rows of 151936 take 145 us by one CTA each,
+  // 124, 119 and 115 by 2, 4 and 8)
   return launch_rows(logprobs_backward_kernel<T>, a.N, c, 0, stream, a);
 }
 
