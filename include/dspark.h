@@ -462,7 +462,8 @@ int dspark_emitted_logprobs(const void* T, int dtype, const int32_t* x, const in
  *   dx_v = g_logp (1[v = t] - p_v) - g_entropy p_v (log p_v + entropy)
  * from its lse and entropy outputs.  g_logp, g_entropy [N] f32 (either may be
  * NULL: 0; entropy is needed with g_entropy).  A row that does not count gets
- * zeros; a token of -1 has no g_logp part.
+ * zeros; a token of -1 has no g_logp part.  Of a row whose |lse| is above 1024
+ * (where its rounding would show) the lse is taken again from the logits.
  * Out: dlogits_out [N, V] dense, of the logits' type; it may be the logits
  * themselves when those are dense, and may not overlap them otherwise.
  */
@@ -500,7 +501,8 @@ int dspark_distill_loss(const void* logits, int dtype, int64_t row_stride, const
 
 /*
  * The gradient of dspark_distill_loss alone, from its stats output and an
- * upstream gradient g [N] f32 (in the place of weight).
+ * upstream gradient g [N] f32 (in the place of weight).  Of a row whose |lse|
+ * is above 1024 the statistics are taken again from the logits.
  */
 int dspark_distill_loss_backward(const void* logits, int dtype, int64_t row_stride, const int32_t* top_idx,
                                  const float* top_val, const float* stats, const float* g,

@@ -620,7 +620,7 @@ def markov_logits(U, W1, W2, anchor, x, dtype=torch.float32, ws=None, out=None):
     if dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
     out = _gradient_out(out, U, dtype)
-    ws = workspace(B, G, V, dev) if ws is None else ws
+    ws = workspace(B, G, V, dev) if ws is None else _need(ws, "ws", torch.uint8, dev)
     _launch(L.dspark_markov_logits, "markov_logits", dev, U.data_ptr(), W1.data_ptr(), W2.data_ptr(), _dt(W1, "W1"),
             anchor.data_ptr(), x.data_ptr(), B, G, V, r, out.data_ptr(), _ROW_DTYPES[dtype], ws.data_ptr(), ws.numel())
     return out
@@ -646,7 +646,8 @@ def markov_head_backward(dlogits, W1, W2, anchor, x, ws=None):
     dev, B, G, V, r = _head_args(dlogits, "dlogits", torch.bfloat16, W1, W2, anchor, x)
     dW1 = torch.empty((V, r), dtype=torch.float32, device=dev)
     dW2 = torch.empty((V, r), dtype=torch.float32, device=dev)
-    ws = _head_workspace(B, G, V, dev) if ws is None else ws   # (its status word is nobody's)
+    # (the status word of a workspace of the call's own is nobody's)
+    ws = _head_workspace(B, G, V, dev) if ws is None else _need(ws, "ws", torch.uint8, dev)
     _launch(L.dspark_markov_head_backward, "markov_head_backward", dev, dlogits.data_ptr(), W1.data_ptr(),
             W2.data_ptr(), _dt(W1, "W1"), anchor.data_ptr(), x.data_ptr(), B, G, V, r, dW1.data_ptr(), dW2.data_ptr(),
             ws.data_ptr(), ws.numel())

@@ -19,7 +19,16 @@
 // loss needs one pass; the gradient a second one over the same part by the same
 // CTA, backwards, which L2 still holds when the rows in flight fit there, so
 // that HBM sees about one read and one write.  What depends on the teacher
-// alone is worked out while the first block's loads are under way.
+// alone is worked out while the first blocks' loads are under way.
+//
+// Measured (GB300, 2048 rows of 151936 and 64 kept entries, the kernel alone):
+// the loss 194 us in fp32 (6.4 TB/s) and 118 us in bf16; with its gradient 455 us
+// (one read and one write at 5.5 TB/s; HBM reads 1.57 GB for 1.24, L2 keeping
+// most of the 92 MB in flight) and 254 us; the gradient alone 383 and 200 us.
+// Two passes through HBM (a kernel for the sums, one for the gradients) took
+// 600 us; parts held in shared memory between the passes 830 us and more, for
+// their copies, barriers and passes hardly overlap; tasks in an order that
+// leaves L2 a short reuse distance 730 us, for their waits.
 #include <algorithm>
 
 #include "logits_row.cuh"
@@ -31,7 +40,9 @@ using namespace lrow;
 
 constexpr int kCtasPerSm = 4;
 constexpr int kMarkedPlaces = 262144;           // of a CTA's part of a row: a bitmap of 32 KB
-constexpr long long kFlightBytes = 96ll << 20;  // of the rows in flight with a gradient
+// of the rows in flight with a gradient: the step above takes 453 to 456 us for
+// 75 to 96 MB, 471 for 130 to 160 (L2 keeps less) and took 590 for one CTA a row
+constexpr long long kFlightBytes = 96ll << 20;
 
 struct Shared {
   Stat part[kWarps];
@@ -346,6 +357,7 @@ cudaError_t launch(const DistillArgs& a, cudaStream_t stream) {
   int least = div_up(nblk, kMarkedPlaces / kBlockPlaces);
   if (a.stats_in != nullptr) {
     least = std::max(least, std::min(div_up(nblk, 8 * kWarps), 8));   // eight blocks a warp, or more
+    // (1400 rows of 50257 fp16 entries: 71 us so, 73 and 94 with four and two)
   } else if (a.dlogits != nullptr) {
     const long long flight = (long long)a.V * (long long)sizeof(T) * std::min(a.N, kCtasPerSm * sms);
     least = std::max(least, (int)std::min<long long>((flight + kFlightBytes - 1) / kFlightBytes, kMaxCluster));

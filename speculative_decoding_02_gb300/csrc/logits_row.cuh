@@ -13,9 +13,10 @@
 // log s + t / s); a block whose maximum is above m rescales both first.  Two
 // entries share each packed fp32 addition, product and fused product.
 //
-// CTAs of 256 threads, four or five to an SM, rather than two of 512: a row's
+// CTAs of 256 threads, four to an SM, rather than two of 512: a row's
 // barriers and short serial phases (merging states, choosing alternatives, the
-// teacher's side) then overlap with the other rows' streams.
+// teacher's side) then overlap with the other rows' streams (2048 bf16 rows of
+// 129280 with 64 alternatives: 171 us against 210).
 #pragma once
 
 #include <cooperative_groups.h>

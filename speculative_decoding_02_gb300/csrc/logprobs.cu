@@ -19,6 +19,13 @@
 //      more than 512 of them are sorted instead.
 // Where the candidates overflow their buffer (thousands of equal or ascending
 // entries) each CTA finds its own K largest by bisection over the keys' bits.
+//
+// Measured (GB300, the kernel alone): 2048 rows of 151936 take 185 us in fp32
+// (6.7 TB/s, the copy rate) and 111 us in bf16 (5.6 TB/s: 7.6 instructions an
+// entry fill the issue slots), with 20 alternatives 208 and 131 us; one row takes
+// 5 us, with 20 alternatives 8.5, with 128 10.5 us (latency: two cluster
+// barriers, the histogram's four, one read of L2).  The gradients of those rows
+// take 366 us in fp32 (6.8 TB/s) and 205 us in bf16 (6.1 TB/s).
 #include <float.h>
 
 #include "logits_row.cuh"

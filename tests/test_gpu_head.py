@@ -204,6 +204,41 @@ def test_training_step(tail):
         assert abs(diff - float((dw.to(F64) * d).sum())) < tol
 
 
+def test_a_round_feeds_training():
+    """What the round verified, straight into the head's gradients: the target's
+    alternatives of the verified positions as the teacher, the drafted tokens as
+    the prefix; positions past a request's verify length take no part."""
+    from speculative_decoding_02_gb300 import workloads as wl
+
+    w = wl.custom(B=16, gamma=4, V=4096, r=256, H=64, wdtype=torch.bfloat16, u_sigma=3.0, seed=5, sps_b0=32.0,
+                  sps_kind="steps")
+    inp = wl.make_inputs(w, 0, "cuda")
+    U, T, W1, W2, anchor = (inp[k] for k in ("U", "T", "W1", "W2", "anchor"))
+    out = ds.round(U, T, W1, W2, inp["h"], inp["w"], anchor, seed=w.seed, sps=inp["sps"], mode=w.mode)
+    B, G, V = U.shape
+    none = torch.full((B, G + 1), -1, dtype=torch.int32, device="cuda")
+    _, _, _, idx, lp = ds.token_logprobs(T, none, top_k=64, rows=out.ell)
+    idx, lp = idx[:, :G].contiguous(), lp[:, :G].contiguous()
+    l = ds.markov_logits(U, W1, W2, anchor, out.x)
+    loss, stats, dl = ds.distill_loss(l, idx, lp, teacher_lse=torch.zeros(B, G, device="cuda"), rows=out.ell,
+                                      grad=True, grad_dtype=torch.bfloat16)
+    dW1, dW2 = ds.markov_head_backward(dl, W1, W2, anchor, out.x)
+    on = (torch.arange(G, device="cuda")[None] < out.ell[:, None]).reshape(-1)
+    assert on.any() and not on.all()
+    z = l.view(-1, V)[on].to(F64)
+    want, _, grad, size, gsize = ref.distill(z, idx.view(-1, 64)[on], lp.view(-1, 64)[on], 1.0,
+                                             torch.zeros(int(on.sum()), device="cuda"), None)
+    e = ref.base_error(V, 60.0) + 64 * ref.U + 4 * ref.U * 40
+    ref.assert_close(loss.view(-1)[on], want, e * size, "loss")
+    assert (loss.view(-1)[~on] == 0).all() and (dl.view(-1, V)[~on] == 0).all()
+    prev = _prev(anchor, out.x)[on]
+    w1, w2 = W1[prev].to(F64), W2.to(F64)
+    tol = lambda s: 2 ** -8 * 1.01 * s + 1e-6
+    ref.assert_close(dW2, grad.T @ w1, tol(grad.abs().T @ w1.abs()), "dW2")
+    zero = torch.zeros((V, R), dtype=F64, device="cuda")
+    ref.assert_close(dW1, zero.index_add(0, prev, grad @ w2), tol(zero.index_add(0, prev, grad.abs() @ w2.abs())), "dW1")
+
+
 def test_refusals():
     B, G, V = 2, 3, 256
     W1, W2 = _weights(V, 1)
@@ -220,6 +255,9 @@ def test_refusals():
         assert e.value.code == ds.ERR_UNSUPPORTED
     with pytest.raises(TypeError):
         ds.markov_head_backward(U, W1, W2, anchor, x)
+    for ws in (torch.zeros(1024, device="cuda"), torch.zeros(1024, dtype=torch.uint8)):
+        with pytest.raises((ValueError, TypeError)):
+            ds.markov_logits(U, W1, W2, anchor, x, ws=ws)
     with pytest.raises(ds.DSparkError) as e:
         ds.markov_head_backward(U.bfloat16(), W1, W2, anchor, x, ws=torch.empty(512, dtype=torch.uint8, device="cuda"))
     assert e.value.code == ds.ERR_WORKSPACE

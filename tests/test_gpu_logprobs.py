@@ -231,6 +231,23 @@ def test_emitted_tokens_of_a_round():
         assert (logp[b, n[b] + 1:] == 0).all() and (idx[b, n[b] + 1:] == -1).all()
 
 
+def test_shapes():
+    # leading dimensions of any number, among them none
+    x = ref.logits(6, 777, torch.float16, 3)
+    tok = _tokens(6, 777, 1)
+    want = ds.token_logprobs(x, tok, top_k=4)
+    got = ds.token_logprobs(x.view(3, 1, 2, 777), tok.view(3, 1, 2), top_k=4)
+    assert got[0].shape == (3, 1, 2) and got[3].shape == (3, 1, 2, 4)
+    assert all(torch.equal(a.reshape(b.shape), b) for a, b in zip(got, want))
+    one = ds.token_logprobs(x[0], tok[0], top_k=4)
+    assert one[0].shape == () and one[3].shape == (4,)
+    d = ds.token_logprobs_backward(x[0], tok[0], one[2], g_logp=torch.ones((), device="cuda"))
+    assert d.shape == (777,)
+    # a part of a vocabulary, and requests of which a part is taken
+    assert torch.equal(ds.token_logprobs(x[:, 5:], tok.clamp(max=700))[2],
+                       ds.token_logprobs(x[:, 5:].contiguous(), tok.clamp(max=700))[2])
+
+
 def test_no_rows():
     x = torch.empty((0, 100), device="cuda")
     tok = torch.empty((0,), dtype=torch.int32, device="cuda")
