@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
       const float q_rest = expf((rest.m - all.m) * p.inv_tau) * rest.s / all.s;
       cw = rest.m == -INFINITY ? 0.f : w * ((q_rest - kept.p_rest) / rest.s);
     }
-    on = (kept.any || bad) && !none;
+    on = bad || (kept.any && !none);
     if (bad) cw = q_scale = nan;
     if (!backward && rank == 0) {
       const float pk = tid < p.K ? sh.p[tid] : 0.f;

@@ -195,6 +195,19 @@ def test_bad_rows_are_reported():
     assert torch.equal(loss[4], clean[0][4]) and torch.equal(grad[4], clean[2][4])
 
 
+@pytest.mark.parametrize("tail", [False, True])
+def test_a_bad_index_in_an_empty_row_is_reported(tail):
+    S = ref.logits(3, 700, torch.float32, 1)
+    i, v, t, _ = _teacher(S, 6, 1.0, tail, 5)
+    S[0] = S[1] = -math.inf
+    i[0, 2] = 700
+    loss, stats, grad = ds.distill_loss(S, i, v, teacher_lse=t, grad=True)
+    back = ds.distill_loss_backward(S, i, v, stats, torch.ones(3, device="cuda"), teacher_lse=t)
+    assert torch.isnan(loss[0]) and torch.isnan(grad[0]).all() and torch.isnan(back[0]).all()
+    assert loss[1] == 0 and (grad[1] == 0).all() and (back[1] == 0).all()
+    assert torch.isfinite(grad[2]).all() and torch.isfinite(back[2]).all()
+
+
 def test_top_alternatives_are_a_teacher():
     # the target's own alternatives, kept by token_logprobs, as the teacher at
     # temperature 1: at the same logits loss and gradient vanish up to rounding
