@@ -348,7 +348,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_backward_kernel(const Lo
   const int tok = on ? p.tokens[row] : -1;
   const float nan = __int_as_float(0x7FC00000);
   float gl = on && p.g_logp != nullptr && tok != -1 ? p.g_logp[row] : 0.f;
-  if (tok < -1 || tok >= p.V) gl = nan;
+  const bool bad_tok = tok < -1 || tok >= p.V;
+  if (bad_tok) gl = nan;
   const float gh = on && p.g_entropy != nullptr ? p.g_entropy[row] : 0.f;
   // p_v = exp(x_v - ref - ls)
   float ref = on ? p.lse[row] : -INFINITY, ls = 0.f;
@@ -362,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_backward_kernel(const Lo
     ref = v.m;
     ls = logf(v.s);
   }
-  const bool zero = ref == -INFINITY;   // not scored, or no entry above -inf
+  const bool zero = ref == -INFINITY && !bad_tok;   // not scored, or no entry above -inf
   const float a = gh != 0.f ? fmaf(gh, p.entropy[row], gl) : gl;
   const bool aligned = ((reinterpret_cast<uintptr_t>(out) - R.shift * sizeof(T)) & 15) == 0;
   // the token's own entry is stored last, over what the loop leaves there; its

@@ -142,6 +142,17 @@ def test_tokens_absent_and_out_of_range():
     assert (g[0] == 0).all() and torch.isnan(g[1]).all() and torch.isnan(g[2]).all() and torch.isfinite(g[3]).all()
 
 
+def test_a_bad_token_of_an_empty_row_is_reported():
+    x = ref.logits(4, 600, torch.float32, 5)
+    x[:3] = -math.inf
+    tok = torch.tensor([600, 3, -1, 4], dtype=torch.int32, device="cuda")
+    lp, H, lse, *_ = ds.token_logprobs(x, tok)
+    one = torch.ones(4, device="cuda")
+    g = ds.token_logprobs_backward(x, tok, lse, H, one, one)
+    assert torch.isnan(lp[0]) and torch.isnan(g[0]).all()
+    assert (g[1:3] == 0).all() and torch.isfinite(g[3]).all()
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("N,V", [(1, 1), (4, 33), (6, 4099), (3, 50257), (1, 262144)])
 @pytest.mark.parametrize("entropy", [False, True])
