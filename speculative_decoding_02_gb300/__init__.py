@@ -390,6 +390,7 @@ def sts_fit(z, ell, acc, grid):
     return T, e
 
 
+_INT_MAX = 2 ** 31 - 1   # of the library's sizes; a larger one would wrap around on its way there
 _ROW_DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 
@@ -426,6 +427,8 @@ def _row_args(logits, rows, what="logits"):
         raise ValueError(f"{what} must be [..., V] with V >= 1, got {list(logits.shape)}")
     lead, V = tuple(logits.shape[:-1]), logits.shape[-1]
     N = math.prod(lead)
+    if max(N, V) > _INT_MAX:
+        raise DSparkError(ERR_UNSUPPORTED, f"{what} of {list(logits.shape)}")
     if V > 1 and N > 0 and logits.stride(-1) != 1:
         raise ValueError(f"{what} must have entries of a row next to each other")
     stride = V
@@ -543,6 +546,8 @@ def _distill_args(logits, top_idx, top_val, teacher_lse, rows, temperature):
     if top_idx.dim() != len(lead) + 1 or top_idx.shape[-1] < 1:
         raise ValueError(f"top_idx must be {list(lead)} + [K], got {list(top_idx.shape)}")
     K = top_idx.shape[-1]
+    if K > _INT_MAX:
+        raise DSparkError(ERR_UNSUPPORTED, f"top_idx of {list(top_idx.shape)}")
     _sized(top_idx, "top_idx", (*lead, K)); _sized(top_val, "top_val", (*lead, K))
     _row_vector(teacher_lse, "teacher_lse", lead, dev)
     if not 0.0 < temperature < math.inf:

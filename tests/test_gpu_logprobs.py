@@ -291,6 +291,18 @@ def test_refusals():
         ds.token_logprobs_backward(x, tok, lse, g_logp=g, out=torch.empty_like(x, dtype=torch.bfloat16))
 
 
+def test_sizes_past_32_bits_are_refused():
+    # (their low 32 bits are a size that would be taken)
+    big = torch.empty((1, 2 ** 32 + 8), dtype=torch.bfloat16, device="cuda")
+    tok = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for call in (lambda: ds.token_logprobs(big, tok), lambda: ds.token_logprobs(big[:, :2 ** 31], tok)):
+        with pytest.raises(ds.DSparkError) as e:
+            call()
+        assert e.value.code == ds.ERR_UNSUPPORTED
+    del big
+    torch.cuda.empty_cache()
+
+
 def test_streams_and_graphs():
     x = [ref.logits(40, 30011, torch.bfloat16, s) for s in range(2)]
     tok = _tokens(40, 30011, 1)
