@@ -474,7 +474,7 @@ int dspark_token_logprobs_backward(const void* logits, int dtype, int64_t row_st
 
 /*
  * Kullback-Leibler loss of a student's logits against a teacher's K kept logits
- * (1 <= K <= 128) at a temperature tau > 0.  With z = logits / tau, q =
+ * (1 <= K <= 128) at a temperature tau (1e-30 <= tau <= 1e30).  With z = logits / tau, q =
  * softmax(z), entries (i_k, t_k) = (top_idx, top_val) [N, K] (index -1: absent):
  *  - teacher_lse NULL: p = softmax(t / tau) over the kept entries and
  *      loss = sum_k p_k (log p_k - log q_{i_k});
@@ -516,8 +516,8 @@ int dspark_distill_loss_backward(const void* logits, int dtype, int64_t row_stri
  * as a tensor [B, gamma, V] of type ldtype (DSPARK_F32 or DSPARK_BF16, rounded
  * once).  l_out may be U itself when ldtype is DSPARK_F32.  A previous token
  * outside [0, V) adds nothing and records DSPARK_ERR_INVALID.  Tensor-core path
- * only (bf16 weights, r = 256, V >= 192; U, W1, W2, l_out 16-byte aligned),
- * else DSPARK_ERR_UNSUPPORTED.  Workspace: its status word (256 bytes).
+ * only (bf16 weights, r = 256, V >= 192), else DSPARK_ERR_UNSUPPORTED; U, W1, W2
+ * and l_out 16-byte aligned.  Workspace: its status word (256 bytes).
  */
 int dspark_markov_logits(const float* U, const void* W1, const void* W2, int wdtype,
                          const int32_t* anchor, const int32_t* x, int B, int gamma, int V, int r,

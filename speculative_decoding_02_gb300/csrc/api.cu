@@ -1,7 +1,6 @@
 // The C ABI of libdspark: host-side argument checks, workspace checks and the
 // enqueueing of the per-round kernels.  Every entry point validates its sizes
 // and pointers before it enqueues anything and never synchronises the stream.
-#include <math.h>
 #include <stdint.h>
 
 #include "kernels.h"
@@ -94,9 +93,8 @@ int top_checks(int N, int V, int top_k, const float* logp_out, const float* entr
 int distill_checks(const void* logits, int dtype, int64_t row_stride, const int32_t* top_idx, const float* top_val,
                    int N, int R, int V, int K, float temperature, const void* dlogits, int gdtype) {
   DSPARK_TRY(rows_checks(logits, dtype, row_stride, N, R, V));
-  // (a temperature whose reciprocal overflows is none)
-  if (K <= 0 || !(temperature > 0.f) || !(temperature < INFINITY) || !(1.f / temperature < INFINITY))
-    return DSPARK_ERR_INVALID;
+  // (so that 1 / tau log2 e and an lse's product with tau stay in fp32's range)
+  if (K <= 0 || !(temperature >= 1e-30f && temperature <= 1e30f)) return DSPARK_ERR_INVALID;
   if (K > kMaxTop) return DSPARK_ERR_UNSUPPORTED;
   if (N > 0 && (!top_idx || !top_val)) return DSPARK_ERR_INVALID;
   if (dlogits) {

@@ -221,6 +221,31 @@ def test_top_alternatives_are_a_teacher():
     ref.assert_close(stats[:, 0], lse.double(), e + 2 * ref.U * lse.abs().double(), "lse")
 
 
+@pytest.mark.parametrize("tau", [1e-30, 1e30])
+def test_extreme_temperatures(tau):
+    # hot: every entry has the same probability, to a relative 1e-29; cold: the
+    # largest entry has all of it, on both sides
+    N, V, K = 3, 1500, 8
+    S = torch.rand((N, V), generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+    S[:, 7] = 2.0
+    top = S.topk(K)
+    i, v = top.indices.to(torch.int32), top.values
+    loss, stats, grad = ds.distill_loss(S, i, v, temperature=tau, grad=True)
+    back = ds.distill_loss_backward(S, i, v, stats, torch.ones(N, device="cuda"), temperature=tau)
+    e = ref.base_error(V, 0.0) + K * ref.U
+    if tau > 1:
+        want = torch.full((N, V), 1.0 / V, dtype=torch.float64, device="cuda")
+        want.scatter_add_(1, top.indices, torch.full((N, K), -1.0 / K, dtype=torch.float64, device="cuda"))
+        want /= float(torch.tensor(tau))
+        ref.assert_close(loss, torch.full((N,), math.log(V / K), dtype=torch.float64, device="cuda"), e * (2 + 2 * math.log(V)),
+                         "loss")
+        # (4 U log V more for the rounded lse)
+        for g in (grad, back):
+            ref.assert_close(g, want, (e + 4 * ref.U * math.log(V)) * (1.0 / V + 1.0 / K) / tau, "gradient")
+    else:
+        assert (loss == 0).all() and (grad == 0).all() and (back == 0).all()
+
+
 def test_no_rows_and_refusals():
     S = ref.logits(4, 100, torch.float32, 1)
     i, v, t, w = _teacher(S, 6, 1.0, True, 5)

@@ -71,7 +71,7 @@ def test_distill_arguments(lib):
         return lib.dspark_distill_loss_backward(p, 0, 100, p, p, stats, g, None, None, 4, 2, 100, K, tau, dl, 0, None)
 
     for kw in (dict(logits=None), dict(ti=None), dict(tv=None), dict(loss=None), dict(stats=None), dict(K=0),
-               dict(tau=0.0), dict(tau=-1.0), dict(tau=float("inf")), dict(tau=float("nan")), dict(tau=1e-44),
+               dict(tau=0.0), dict(tau=-1.0), dict(tau=float("inf")), dict(tau=float("nan")), dict(tau=1e-44), dict(tau=4e-39), dict(tau=9e-31), dict(tau=1.1e30), dict(tau=3e38),
                dict(dl=odd), dict(R=3), dict(stride=99), dict(dtype=4)):
         assert call(**kw) == ds.ERR_INVALID, kw
     for kw in (dict(K=129), dict(gd=2), dict(dtype=1, gd=0), dict(dtype=2, gd=1)):
