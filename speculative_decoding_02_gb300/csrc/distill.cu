@@ -22,7 +22,7 @@
 // alone is worked out while the first blocks' loads are under way.
 //
 // Measured (GB300, 2048 rows of 151936 and 64 kept entries, the kernel alone):
-// the loss 194 us in fp32 (6.4 TB/s) and 118 us in bf16; with its gradient 455 us
+// the loss 187 us in fp32 (6.7 TB/s) and 108 us in bf16; with its gradient 455 us
 // (one read and one write at 5.5 TB/s; HBM reads 1.57 GB for 1.24, L2 keeping
 // most of the 92 MB in flight) and 254 us; the gradient alone 383 and 200 us.
 // Two passes through HBM (a kernel for the sums, one for the gradients) took
@@ -38,7 +38,6 @@ namespace {
 
 using namespace lrow;
 
-constexpr int kCtasPerSm = 4;
 constexpr int kMarkedPlaces = 262144;           // of a CTA's part of a row: a bitmap of 32 KB
 // of the rows in flight with a gradient: the step above takes 453 to 456 us for
 // 75 to 96 MB, 471 for 130 to 160 (L2 keeps less) and took 590 for one CTA a row
@@ -156,7 +155,7 @@ __device__ __forceinline__ Kept load_kept(Shared& sh, const DistillArgs& p, int 
 // kTail: the teacher's lse is given.  With p.stats_in the backward pass alone,
 // which takes the row's state anew only where its lse is too large to be used.
 template <typename T, typename G, bool kTail>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const DistillArgs p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const DistillArgs p, int ahead) {
   constexpr int VEC = Elem<T>::VEC;
   constexpr int kBlockPlaces = kBlockVecs * VEC;
   __shared__ Shared sh;
@@ -198,6 +197,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
     if (grad && b >= 0) R.load_block(b, lane, cur, drop);
   };
 
+  // the row that takes this CTA's place (without a second pass, which needs L2 for
+  // the rows in flight)
+  auto next = [&]() {
+    if (tid == 0 && row + ahead < p.N && ahead > 0) prefetch_row(rp + (size_t)ahead * p.row_stride, p.V, backward ? 2 : 4);
+  };
   if (pass) {
     const int words = nblk * (kBlockPlaces / 32);
     unsigned char* block_marked = reinterpret_cast<unsigned char*>(marked + words);
@@ -233,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
     };
     // (with a gradient to come L2 is asked to keep the row for it)
     stat_row<T, false, false>(R, br, scale, p.inv_tau, grad ? tc::policy_evict_last() : drop, sh.part, &sh.cta, before,
-                              leave_out, Nothing());
+                              leave_out, Nothing(), next);
     cluster_arrive(c);
     first_block();
     cluster_wait(c);
@@ -335,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
 #pragma unroll
       for (int j = 0; j < kVecPerLane; ++j) cur[j] = nxt[j];
     }
+    if (backward) next();
     if (on) {
       __syncthreads();   // the kept entries' gradients replace what the loop stored there
       if (tid < p.K && sh.pv[tid] != -1.f) {
@@ -363,9 +368,11 @@ cudaError_t launch(const DistillArgs& a, cudaStream_t stream) {
     least = std::max(least, (int)std::min<long long>((flight + kFlightBytes - 1) / kFlightBytes, kMaxCluster));
   }
   const int c = cluster_for(a.N, nblk, least, sms);
+  const bool two_passes = a.dlogits != nullptr && a.stats_in == nullptr;
+  const int ahead = c == 1 && a.lens == nullptr && !two_passes ? kCtasPerSm * sms : 0;
   const bool tail = a.teacher_lse != nullptr;
   const int smem = tail ? div_up(nblk, c) * (kBlockPlaces / 8 + 1) : 0;
-  return launch_rows(tail ? distill_kernel<T, G, true> : distill_kernel<T, G, false>, a.N, c, smem, stream, a);
+  return launch_rows(tail ? distill_kernel<T, G, true> : distill_kernel<T, G, false>, a.N, c, smem, stream, a, ahead);
 }
 
 }  // namespace

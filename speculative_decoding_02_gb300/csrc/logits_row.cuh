@@ -36,7 +36,14 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kVecPerLane = 4;
 constexpr int kBlockVecs = 32 * kVecPerLane;
 constexpr int kMaxCluster = 16;
+constexpr int kCtasPerSm = 4;
 constexpr float kLog2e = 1.4426950408889634f;
+
+// Word i of a vector.
+__device__ __forceinline__ uint32_t word(uint4 r, int i) {
+  const uint32_t lo = i & 1 ? r.y : r.x, hi = i & 1 ? r.w : r.z;
+  return i & 2 ? hi : lo;
+}
 
 template <typename T>
 struct Elem;
@@ -50,6 +57,8 @@ struct Elem<float> {
     f[0] = __uint_as_float(r.x); f[1] = __uint_as_float(r.y);
     f[2] = __uint_as_float(r.z); f[3] = __uint_as_float(r.w);
   }
+  // Entry e of a vector.
+  static __device__ __forceinline__ float entry(uint4 r, int e) { return __uint_as_float(word(r, e)); }
 };
 template <>
 struct Elem<__nv_bfloat16> {
@@ -65,6 +74,8 @@ struct Elem<__nv_bfloat16> {
       f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
   }
+  // Entry e of a vector.
+  static __device__ __forceinline__ float entry(uint4 r, int e) { return __uint_as_float(word(r, e >> 1) >> 16 * (e & 1) << 16); }
 };
 template <>
 struct Elem<__half> {
@@ -81,6 +92,8 @@ struct Elem<__half> {
       f[2 * i + 1] = p.y;
     }
   }
+  // Entry e of a vector.
+  static __device__ __forceinline__ float entry(uint4 r, int e) { return __half2float(__ushort_as_half((unsigned short)(word(r, e >> 1) >> 16 * (e & 1)))); }
 };
 
 // A 16-byte load past L1; a policy (createpolicy) says how long L2 holds it, and
@@ -101,6 +114,21 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p, uint64_t policy) {
                : "l"(p), "l"(policy)
                : "memory");
   return v;
+}
+
+// Asks L2 for the start of a row that a CTA will take soon: 1 / part of it, 64 KB
+// at most.  The CTAs of a launch take in rows of one length in step, and so come
+// to the end of one together, where nothing is asked of HBM until they have
+// begun the next (3 of 30 us at 151936 bf16 entries).  2048 rows of those take 101
+// us so and 109 without (fp32: 179 and 190; 105 by 128 KB, 106 by 16 KB); 10000
+// rows of 32000 128 us by a quarter of a row, 132 without, 145 by the whole.
+constexpr uint64_t kAheadBytes = 65536;
+template <typename T>
+__device__ __forceinline__ void prefetch_row(const T* row, int V, int part) {
+  const uint64_t a = ((uint64_t)__cvta_generic_to_global(row) + 15) & ~15ull;
+  const uint64_t n = min((uint64_t)V * sizeof(T) / part, kAheadBytes) & ~15ull;   // (a - row < 16 bytes: inside the row)
+  if (n > 16)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a), "r"((uint32_t)n - 16) : "memory");
 }
 
 // A row as its vectors: `base` is the row's address rounded down to 16 bytes.
@@ -348,14 +376,15 @@ __device__ __forceinline__ void cta_stat(const LaneStat& st, float inv, Stat* pa
 }
 
 // The state of this CTA's blocks of a row, read from global memory, in *out
-// (behind a barrier).  before() runs once the first two blocks' loads are in flight;
+// (behind a barrier).  before() runs once the first two blocks' loads are in flight
+// and last() behind the last block;
 // each(b, vectors) may change a block's vectors before they are taken in.  With
 // kSeen seen(b, lane maximum, float4) sees a block's maxima: those of its four
 // quarters (one vector of every lane).  The next blocks' loads are in flight
 // while one is taken in.
-template <typename T, bool kEntropy, bool kSeen, typename P, typename Before, typename Each, typename Seen>
+template <typename T, bool kEntropy, bool kSeen, typename P, typename Before, typename Each, typename Seen, typename Last>
 __device__ __forceinline__ void stat_row(const Row<T>& R, const BlockRange& br, float scale, float inv, P policy, Stat* part,
-                                         Stat* out, Before before, Each each, Seen seen) {
+                                         Stat* out, Before before, Each each, Seen seen, Last last) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   LaneStat st = lane_stat_empty();
   uint4 cur[kVecPerLane], nxt[kVecPerLane];
@@ -386,6 +415,7 @@ __device__ __forceinline__ void stat_row(const Row<T>& R, const BlockRange& br, 
     take(b, cur);
     if (b + kWarps < br.end) take(b + kWarps, nxt);
   }
+  last();
   cta_stat(st, inv, part, out);
 }
 

@@ -11,19 +11,22 @@
 //   1. the K-th largest of the lanes' maxima (256 of each CTA), or a little less
 //      by a histogram, is a lower bound of the row's K-th largest entry (K
 //      distinct entries are at least that large);
-//   2. only the quarters whose maximum reaches it are read again (from L2), and
-//      their entries that reach it become candidates: hardly more than K in a
-//      row of no particular order;
+//   2. only the quarters whose maximum reaches it are read again, and their
+//      entries that reach it become candidates: hardly more than K in a row of no
+//      particular order.  A list of the quarters deals them out evenly to the
+//      warps, four at a time, so that few loads' latencies follow each other (64
+//      alternatives: 147 us by each warp's own, one ahead; 138 by four of its
+//      own, 133 by the list);
 //   3. a candidate's rank is the number of larger ones (64-bit keys of value,
 //      then lower index, so no two are equal and ties go to the lowest index);
 //      more than 512 of them are sorted instead.
 // Where the candidates overflow their buffer (thousands of equal or ascending
 // entries) each CTA finds its own K largest by bisection over the keys' bits.
 //
-// Measured (GB300, the kernel alone): 2048 rows of 151936 take 185 us in fp32
-// (6.7 TB/s, the copy rate) and 111 us in bf16 (5.6 TB/s: 7.6 instructions an
-// entry fill the issue slots), with 20 alternatives 208 and 131 us; one row takes
-// 5 us, with 20 alternatives 8.5, with 128 10.5 us (latency: two cluster
+// Measured (GB300, the kernel alone): 2048 rows of 151936 take 179 us in fp32
+// (7.0 TB/s) and 102 us in bf16 (6.1 TB/s), with 20 alternatives 192 and 117 us,
+// with 64 205 and 131 us (about 100 instructions a candidate and 8000 a row of
+// the 40000 of its sums, in phases that no load overlaps); one row takes 5 us, with 20 alternatives 8.5, with 128 10.5 us (latency: two cluster
 // barriers, the histogram's four, one read of L2).  The gradients of those rows
 // take 366 us in fp32 (6.8 TB/s) and 205 us in bf16 (6.1 TB/s).
 #include <float.h>
@@ -37,17 +40,19 @@ using namespace lrow;
 
 constexpr int kMaxBlocks = 512;      // blocks of one CTA's part of a row
 constexpr int kCandidates = 4096;
+constexpr int kHits = 4;             // quarters that a warp reads again at a time (2: 139 us, 4: 133, 6: 136, 8: 138)
 constexpr int kRankDirect = 512;     // candidates ranked by counting; more are sorted
 struct Shared {
   Stat part[kWarps];
   Stat cta;
   int count[2][kWarps];
-  int ncand;
+  int ncand, nhits;
   float lane_max[kThreads];                   // each lane's largest entry
   float2 range[kWarps];
   int bins[256];
   int cut;
   float4 quarter[kMaxBlocks];                 // maxima of each block's quarters
+  unsigned short hits[4 * kMaxBlocks];        // quarters that are read again
   unsigned long long cand[kCandidates];       // (CTA 0's)
   unsigned long long sorted[kMaxTop];
 };
@@ -70,6 +75,15 @@ __device__ __forceinline__ bool row_token(const LogprobArgs& p, int row, int* to
   return true;
 }
 
+// Places behind *n, counted on, for the lanes that want one.
+__device__ __forceinline__ int warp_slots(int* n, bool want) {
+  const int lane = threadIdx.x & 31;
+  const unsigned b = __ballot_sync(0xffffffffu, want);
+  int at = 0;
+  if (lane == 0 && b != 0) at = atomicAdd(n, __popc(b));
+  return __shfl_sync(0xffffffffu, at, 0) + __popc(b & ((1u << lane) - 1u));
+}
+
 // Adds up `mine` over the CTA (every thread gets the sum) with one barrier;
 // calls alternate `which`.
 __device__ __forceinline__ int cta_sum(Shared& sh, int which, int mine) {
@@ -82,34 +96,62 @@ __device__ __forceinline__ int cta_sum(Shared& sh, int which, int mine) {
   return s;
 }
 
-// Calls f(key) for every entry of this warp's blocks that reaches `least`.
+// The quarters of this CTA's blocks whose maximum reaches `least`, into sh.hits
+// (in any order; behind a barrier).
+__device__ __forceinline__ void find_quarters(Shared& sh, const BlockRange& br, float least) {
+  const int lane = threadIdx.x & 31, n = 4 * (br.end - br.begin);
+  const float* q = reinterpret_cast<const float*>(sh.quarter);
+  for (int i0 = threadIdx.x - lane; i0 < n; i0 += kThreads) {
+    const bool hit = i0 + lane < n && !(q[i0 + lane] < least);
+    const int at = warp_slots(&sh.nhits, hit);
+    if (hit) sh.hits[at] = (unsigned short)(i0 + lane);
+  }
+  __syncthreads();
+}
+
+// Calls f(has, key), with the whole warp, until every entry of this warp's share
+// of the quarters that reaches `least` has been a lane's key with has.
 template <typename T, typename F>
 __device__ __forceinline__ void for_candidates(const Shared& sh, const Row<T>& R, const BlockRange& br, float least, F f) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // eight blocks at a time, a lane for each of their 32 quarters
-  for (int b0 = br.begin + warp; b0 < br.end; b0 += 8 * kWarps) {
-    const int bl = b0 + (lane >> 2) * kWarps;
-    const float* q = reinterpret_cast<const float*>(sh.quarter + (bl < br.end ? bl - br.begin : 0));
-    unsigned hit = __ballot_sync(0xffffffffu, bl < br.end && !(q[lane & 3] < least));
-    auto vec_of = [&](unsigned h) {
-      const int l = __ffs(h) - 1;
-      return (b0 + (l >> 2) * kWarps) * kBlockVecs + (l & 3) * 32 + lane;
-    };
-    uint4 nxt = make_uint4(0, 0, 0, 0);
-    if (hit != 0) nxt = R.load(vec_of(hit), NoPolicy());
-    while (hit != 0) {
-      const int i = vec_of(hit);
-      const uint4 r = nxt;
-      hit &= hit - 1;
-      if (hit != 0) nxt = R.load(vec_of(hit), NoPolicy());
-      if (!(vec_max(r, (const T*)nullptr) < least)) {
-        float v[Elem<T>::VEC];
-        Elem<T>::unpack(r, v);
+  const int n = sh.nhits;
+  for (int h = warp; h < n; h += kHits * kWarps) {
+    // (their loads are under way together)
+    uint4 r[kHits];
+    int i[kHits];
 #pragma unroll
-        for (int e = 0; e < Elem<T>::VEC; ++e)
-          if (v[e] >= least) f(entry_key(v[e], R.first_entry(i) + e));
+    for (int u = 0; u < kHits; ++u) {
+      i[u] = 0;
+      r[u] = make_uint4(Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf);
+      if (h + u * kWarps < n) {
+        i[u] = br.begin * kBlockVecs + sh.hits[h + u * kWarps] * 32 + lane;
+        r[u] = R.load(i[u], NoPolicy());
       }
-      __syncwarp();
+    }
+    unsigned mine = 0;   // those of this lane's vectors that reach `least`
+#pragma unroll
+    for (int u = 0; u < kHits; ++u) mine |= (!(vec_max(r[u], (const T*)nullptr) < least) ? 1u : 0u) << u;
+    while (__any_sync(0xffffffffu, mine != 0)) {
+      // one vector of each lane, then one entry of each lane at a time
+      uint4 q = r[0];
+      int at = i[0];
+#pragma unroll
+      for (int u = 1; u < kHits; ++u)
+        if (!(mine & ((1u << u) - 1u))) {
+          q = r[u];
+          at = i[u];
+        }
+      unsigned es = 0;
+      float v[Elem<T>::VEC];
+      Elem<T>::unpack(q, v);
+#pragma unroll
+      for (int e = 0; e < Elem<T>::VEC; ++e) es |= (mine != 0 && v[e] >= least ? 1u : 0u) << e;
+      mine &= mine - 1;
+      while (__any_sync(0xffffffffu, es != 0)) {
+        const int e = max(__ffs(es) - 1, 0);
+        f(es != 0, entry_key(Elem<T>::entry(q, e), R.first_entry(at) + e));
+        es &= es - 1;
+      }
     }
   }
 }
@@ -194,7 +236,7 @@ __device__ __noinline__ void top_by_bisection(Shared& sh, const Row<T>& R, const
   for (int bit = 63; bit >= 0; --bit) {
     const unsigned long long t = kth | (1ull << bit);
     int mine = 0;
-    for_candidates(sh, R, br, least, [&](unsigned long long key) { mine += key >= t; });
+    for_candidates(sh, R, br, least, [&](bool has, unsigned long long key) { mine += has && key >= t; });
     if (cta_sum(sh, bit & 1, mine) >= K) kth = t;
   }
   int* n = sh.count[0];
@@ -202,8 +244,8 @@ __device__ __noinline__ void top_by_bisection(Shared& sh, const Row<T>& R, const
   if (threadIdx.x == 0) *n = 0;
   for (int i = threadIdx.x; i < K; i += kThreads) to[i] = 0ull;
   __syncthreads();
-  for_candidates(sh, R, br, least, [&](unsigned long long key) {
-    if (key < kth) return;
+  for_candidates(sh, R, br, least, [&](bool has, unsigned long long key) {
+    if (!has || key < kth) return;
     const int i = atomicAdd(n, 1);
     if (i < K) to[i] = key;
   });
@@ -250,7 +292,7 @@ static_assert(kCandidates >= 2 * kRankDirect && (kCandidates & (kCandidates - 1)
               "the sorted lengths are powers of two up to the buffer's");
 
 template <typename T, bool kTop>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const LogprobArgs p, int ahead) {
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int c = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -275,16 +317,20 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
   const BlockRange br = block_range(R.nvec, rank, c);
 
   float tmax = -INFINITY;
-  if (kTop && tid == 0) sh.ncand = 0;
+  if (kTop && tid == 0) sh.ncand = sh.nhits = 0;
   auto seen = [&](int b, float lm, float4 q) {
     tmax = fmaxf(tmax, lm);
     if (lane == 0) sh.quarter[b - br.begin] = q;
   };
   // (some of the row is read again for its alternatives)
+  // (the row that takes this CTA's place)
+  auto next = [&]() {
+    if (tid == 0 && row + ahead < p.N && ahead > 0) prefetch_row(rp + (size_t)ahead * p.row_stride, p.V, 4);
+  };
   if constexpr (kTop)
-    stat_row<T, true, true>(R, br, kLog2e, 1.f, NoPolicy(), sh.part, &sh.cta, Nothing(), Nothing(), seen);
+    stat_row<T, true, true>(R, br, kLog2e, 1.f, NoPolicy(), sh.part, &sh.cta, Nothing(), Nothing(), seen, next);
   else
-    stat_row<T, true, false>(R, br, kLog2e, 1.f, tc::policy_evict_first(), sh.part, &sh.cta, Nothing(), Nothing(), Nothing());
+    stat_row<T, true, false>(R, br, kLog2e, 1.f, tc::policy_evict_first(), sh.part, &sh.cta, Nothing(), Nothing(), Nothing(), next);
   if (kTop) sh.lane_max[tid] = tmax;
   cluster_meet(c);
   const Stat v = stat_cluster(cluster, &sh.cta, c, 1.f);
@@ -292,9 +338,10 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
     const float least = lower_bound(sh, cluster, c, p.K);
     int* ncand = c == 1 ? &sh.ncand : cluster.map_shared_rank(&sh.ncand, 0);
     unsigned long long* cand = c == 1 ? sh.cand : cluster.map_shared_rank(sh.cand, 0);
-    for_candidates(sh, R, br, least, [&](unsigned long long key) {
-      const int i = atomicAdd(ncand, 1);
-      if (i < kCandidates) cand[i] = key;
+    find_quarters(sh, br, least);
+    for_candidates(sh, R, br, least, [&](bool has, unsigned long long key) {
+      const int i = warp_slots(ncand, has);
+      if (has && i < kCandidates) cand[i] = key;
     });
     cluster_meet(c);
     int n = *ncand;
@@ -333,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
 // write).  An output row whose vectors start where the logits' do is stored by
 // vectors, any other entry by entry.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_backward_kernel(const LogprobBackwardArgs p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_backward_kernel(const LogprobBackwardArgs p) {
   constexpr int VEC = Elem<T>::VEC;
   __shared__ Stat part[kWarps], cta;
   cg::cluster_group cluster = cg::this_cluster();
@@ -355,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_backward_kernel(const Lo
   float ref = on ? p.lse[row] : -INFINITY, ls = 0.f;
   if (ref != ref) gl = nan;
   if (fabsf(ref) > kLargeLse && ref != -INFINITY) {
-    stat_row<T, false, false>(R, br, kLog2e, 1.f, NoPolicy(), part, &cta, Nothing(), Nothing(), Nothing());
+    stat_row<T, false, false>(R, br, kLog2e, 1.f, NoPolicy(), part, &cta, Nothing(), Nothing(), Nothing(), Nothing());
     cluster_meet(c);
     const Stat v = stat_cluster(cluster, &cta, c, 1.f);
     cluster_meet(c);
@@ -427,9 +474,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_backward_kernel(const Lo
 }
 
 template <typename T>
-cudaError_t forward(const LogprobArgs& a, int c, cudaStream_t stream) {
-  return a.K > 0 ? launch_rows(logprobs_kernel<T, true>, a.N, c, 0, stream, a)
-                 : launch_rows(logprobs_kernel<T, false>, a.N, c, 0, stream, a);
+cudaError_t forward(const LogprobArgs& a, int c, int ahead, cudaStream_t stream) {
+  return a.K > 0 ? launch_rows(logprobs_kernel<T, true>, a.N, c, 0, stream, a, ahead)
+                 : launch_rows(logprobs_kernel<T, false>, a.N, c, 0, stream, a, ahead);
 }
 
 template <typename T>
@@ -451,9 +498,11 @@ cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t stream) {
   const int per_block = kBlockVecs * (a.dtype == DSPARK_F32 ? 4 : 8);
   const int nblk = div_up(a.V, per_block) + 1;
   const int c = cluster_for(a.N, nblk, div_up(nblk, kMaxBlocks), sms);
-  if (a.dtype == DSPARK_F32) return forward<float>(a, c, stream);
-  if (a.dtype == DSPARK_BF16) return forward<__nv_bfloat16>(a, c, stream);
-  return forward<__half>(a, c, stream);
+  // the CTAs that run at a time, where they are rows that all count
+  const int ahead = c == 1 && a.lens == nullptr && a.n == nullptr ? kCtasPerSm * sms : 0;
+  if (a.dtype == DSPARK_F32) return forward<float>(a, c, ahead, stream);
+  if (a.dtype == DSPARK_BF16) return forward<__nv_bfloat16>(a, c, ahead, stream);
+  return forward<__half>(a, c, ahead, stream);
 }
 
 cudaError_t launch_token_logprobs_backward(const LogprobBackwardArgs& a, cudaStream_t stream) {

@@ -73,6 +73,15 @@ def test_against_64_bits(dtype, tail, N, V, K, tau):
     _check(S, *(lambda i, v, t, w: (i, v, tau, t, w))(*_teacher(S, K, tau, tail, V)))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("N,V", [(1300, 3), (1301, 41), (1300, 1037)])
+def test_more_rows_than_run_at_once(dtype, tail, N, V):
+    S = ref.logits(N, V, dtype, N)
+    i, v, t, w = _teacher(S, min(V, 9), 1.0, tail, V)
+    _check(S, i, v, 1.0, t, w)
+
+
 @pytest.mark.parametrize("tail", [False, True])
 def test_bf16_gradient_of_fp32_logits(tail):
     S = ref.logits(5, 3001, torch.float32, 1)

@@ -63,6 +63,12 @@ def test_against_64_bits(dtype, N, V, K):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N,V,K", [(1300, 3, 1), (1301, 41, 3), (1300, 1037, 20), (2000, 4097, 0)])
+def test_more_rows_than_run_at_once(dtype, N, V, K):
+    _check(ref.logits(N, V, dtype, N), _tokens(N, V, V), K)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("off,pad", [(1, 0), (3, 5), (0, 1), (7, 9)])
 def test_strided_rows(dtype, off, pad):
     N, V = 6, 1500 + pad
