@@ -664,21 +664,24 @@ __global__ void __launch_bounds__(HK) scatter_rows(const float* dE, const int32_
   if (tok < 0) return;
   // bit i: row i * HK + threadIdx.x has this token
   unsigned mine = 0;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = 0; i < div_up(rows, HK); ++i) {
     const int j = i * HK + threadIdx.x;
     if ((j < rows ? prev[j] : -1) == tok) mine |= 1u << i;
   }
-  bool earlier = false;
-  for (unsigned left = mine; left != 0; left &= left - 1) earlier |= (__ffs(left) - 1) * HK + (int)threadIdx.x < n;
-  if (__syncthreads_or(earlier)) return;
-  __shared__ unsigned hits[HK / 32];
+  __shared__ unsigned some[HK / 32], hits[HK / 32];
   __shared__ int list[HK];
+  const int warp = threadIdx.x >> 5;
+  const unsigned warp_has = __reduce_or_sync(0xffffffffu, mine);
+  if ((threadIdx.x & 31) == 0) some[warp] = warp_has;
+  if (__syncthreads_or(mine != 0 && (__ffs(mine) - 1) * HK + (int)threadIdx.x < n)) return;   // not the first
+  unsigned all = 0;
+  for (int w = 0; w < HK / 32; ++w) all |= some[w];
   float acc = 0.f;
-  for (int i0 = n / HK; i0 < div_up(rows, HK); ++i0) {
-    const int j = i0 * HK + threadIdx.x, warp = threadIdx.x >> 5;
+  for (unsigned left = all; left != 0; left &= left - 1) {
+    const int i0 = __ffs(left) - 1, j = i0 * HK + threadIdx.x;
     const bool same = mine >> i0 & 1u;
-    if (!__syncthreads_or(same)) continue;
+    if (left != all) __syncthreads();   // (the list before has been read)
     const unsigned h = __ballot_sync(0xffffffffu, same);
     if ((threadIdx.x & 31) == 0) hits[warp] = h;
     __syncthreads();
