@@ -17,19 +17,21 @@
 //
 // A cluster of 1 to 16 CTAs takes a row (logits_row.cuh) and HBM bounds it.  The
 // loss needs one pass; the gradient a second one over the same part by the same
-// CTA, backwards, which L2 still holds when the rows in flight fit there, so
-// that HBM sees about one read and one write.  What depends on the teacher
-// alone is worked out while the first blocks' loads are under way.
+// CTA, backwards: its last blocks are still in shared memory (fp32), and L2 holds
+// the others when the rows in flight fit there, so that HBM sees about one read and
+// one write.  What depends on the teacher alone is worked out while the first
+// blocks' loads are under way.
 //
 // Measured (GB300, 2048 rows of 151936 and 64 kept entries, the kernel alone):
-// the loss 187 us in fp32 (6.7 TB/s) and 108 us in bf16; with its gradient 455 us
-// (one read and one write at 5.5 TB/s; HBM reads 1.57 GB for 1.24, L2 keeping
-// most of the 92 MB in flight) and 254 us; the gradient alone 383 and 200 us.
+// the loss 187 us in fp32 (6.7 TB/s) and 108 us in bf16; with its gradient 444 us
+// (one read and one write at 5.6 TB/s; HBM reads 1.49 GB for 1.24, L2 keeping
+// most of the 92 MB in flight) and 253 us; the gradient alone 383 and 200 us.
 // Two passes through HBM (a kernel for the sums, one for the gradients) took
 // 600 us; parts held in shared memory between the passes 830 us and more, for
 // their copies, barriers and passes hardly overlap; tasks in an order that
 // leaves L2 a short reuse distance 730 us, for their waits.
 #include <algorithm>
+#include <type_traits>
 
 #include "logits_row.cuh"
 
@@ -38,6 +40,11 @@ namespace {
 
 using namespace lrow;
 
+// of shared memory a CTA, so that four leave L1 the room that their loads in flight
+// take: the step takes 456 us with nothing held between the passes, 450 with 23
+// KB, 444 with 31, 445 with 39 and 488 with 55.  fp32 alone: in bf16, where each
+// block has more entries to work on, the copy costs what it saves (253 and 258)
+constexpr int kSmemPerCta = 31 * 1024;
 constexpr int kMarkedPlaces = 262144;           // of a CTA's part of a row: a bitmap of 32 KB
 // of the rows in flight with a gradient: the step above takes 453 to 456 us for
 // 75 to 96 MB, 471 for 130 to 160 (L2 keeps less) and took 590 for one CTA a row
@@ -154,12 +161,13 @@ __device__ __forceinline__ Kept load_kept(Shared& sh, const DistillArgs& p, int 
 
 // kTail: the teacher's lse is given.  With p.stats_in the backward pass alone,
 // which takes the row's state anew only where its lse is too large to be used.
-template <typename T, typename G, bool kTail>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const DistillArgs p, int ahead) {
+// kStash: the part's last `stash` blocks stay in shared memory between the passes.
+template <typename T, typename G, bool kTail, bool kStash>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const DistillArgs p, int ahead, int stash) {
   constexpr int VEC = Elem<T>::VEC;
   constexpr int kBlockPlaces = kBlockVecs * VEC;
   __shared__ Shared sh;
-  extern __shared__ uint32_t marked[];   // kTail: one bit per place of the part, then a byte per block
+  extern __shared__ uint4 dynamic[];   // `stash` blocks; kTail: one bit per place of the part, then a byte per block
   cg::cluster_group cluster = cg::this_cluster();
   const int c = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int row = (int)(blockIdx.x / c);
@@ -173,6 +181,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
   const BlockRange br = block_range(R.nvec, rank, c);
   const int place0 = br.begin * kBlockPlaces - R.shift;   // entry at the part's first place
   const int nblk = br.end - br.begin;
+  const int stash_from = br.end - (kStash ? stash : 0);
+  uint32_t* marked = reinterpret_cast<uint32_t*>(dynamic + (kStash ? stash : 0) * kBlockVecs);
   const int group = row / p.R;
   bool on = p.lens == nullptr || row - group * p.R < p.lens[group];
   float lse_in = 0.f, lse_rest_in = 0.f;
@@ -193,8 +203,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
   // to be in L2.  Its first block is under way while the CTAs meet.
   uint4 cur[kVecPerLane], nxt[kVecPerLane];
   int b = nblk > warp ? br.begin + warp + (nblk - 1 - warp) / kWarps * kWarps : -1;
+  auto load_again = [&](int k, uint4(&r)[kVecPerLane]) {
+    if (!kStash || k < stash_from) {
+      R.load_block(k, lane, r, drop);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVecPerLane; ++j) r[j] = dynamic[(k - stash_from) * kBlockVecs + j * 32 + lane];
+    }
+  };
   auto first_block = [&]() {
-    if (grad && b >= 0) R.load_block(b, lane, cur, drop);
+    if (grad && b >= 0) load_again(b, cur);
   };
 
   // the row that takes this CTA's place (without a second pass, which needs L2 for
@@ -221,6 +239,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
       }
     };
     auto leave_out = [&](int b, uint4(&cur)[kVecPerLane]) {
+      if (kStash && b >= stash_from) {
+#pragma unroll
+        for (int j = 0; j < kVecPerLane; ++j) dynamic[(b - stash_from) * kBlockVecs + j * 32 + lane] = cur[j];
+      }
       if constexpr (kTail) {
         if (!block_marked[b - br.begin]) return;
 #pragma unroll
@@ -236,7 +258,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
       }
     };
     // (with a gradient to come L2 is asked to keep the row for it)
-    stat_row<T, false, false>(R, br, scale, p.inv_tau, grad ? tc::policy_evict_last() : drop, sh.part, &sh.cta, before,
+    const uint64_t keep = grad ? tc::policy_evict_last() : drop;
+    std::conditional_t<kStash, SplitPolicy, uint64_t> policy;
+    if constexpr (kStash) policy = SplitPolicy{keep, drop, stash_from};
+    else policy = keep;
+    stat_row<T, false, false>(R, br, scale, p.inv_tau, policy, sh.part, &sh.cta, before,
                               leave_out, Nothing(), next);
     cluster_arrive(c);
     first_block();
@@ -334,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
       }
     };
     for (; b >= br.begin + warp; b -= kWarps) {
-      if (b - kWarps >= br.begin + warp) R.load_block(b - kWarps, lane, nxt, drop);
+      if (b - kWarps >= br.begin + warp) load_again(b - kWarps, nxt);
       gradient(b, cur);
 #pragma unroll
       for (int j = 0; j < kVecPerLane; ++j) cur[j] = nxt[j];
@@ -371,8 +397,18 @@ cudaError_t launch(const DistillArgs& a, cudaStream_t stream) {
   const bool two_passes = a.dlogits != nullptr && a.stats_in == nullptr;
   const int ahead = c == 1 && a.lens == nullptr && !two_passes ? kCtasPerSm * sms : 0;
   const bool tail = a.teacher_lse != nullptr;
-  const int smem = tail ? div_up(nblk, c) * (kBlockPlaces / 8 + 1) : 0;
-  return launch_rows(tail ? distill_kernel<T, G, true> : distill_kernel<T, G, false>, a.N, c, smem, stream, a, ahead);
+  const int marks = tail ? (div_up(nblk, c) * (kBlockPlaces / 8 + 1) + 15) & ~15 : 0;
+  if constexpr (sizeof(T) == 4) {
+    if (two_passes) {
+      const int room = std::max(0, kSmemPerCta - (int)sizeof(Shared) - marks);
+      const int stash = std::min(room / (kBlockVecs * 16), nblk / c);
+      const int smem = stash * kBlockVecs * 16 + marks;
+      return launch_rows(tail ? distill_kernel<T, G, true, true> : distill_kernel<T, G, false, true>, a.N, c, smem,
+                         stream, a, ahead, stash);
+    }
+  }
+  return launch_rows(tail ? distill_kernel<T, G, true, false> : distill_kernel<T, G, false, false>, a.N, c, marks,
+                     stream, a, ahead, 0);
 }
 
 }  // namespace

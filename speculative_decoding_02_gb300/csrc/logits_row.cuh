@@ -131,6 +131,15 @@ __device__ __forceinline__ void prefetch_row(const T* row, int V, int part) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a), "r"((uint32_t)n - 16) : "memory");
 }
 
+// One policy for the blocks before `from`, another from there on.
+struct SplitPolicy {
+  uint64_t before, behind;
+  int from;
+};
+__device__ __forceinline__ NoPolicy policy_of(NoPolicy p, int) { return p; }
+__device__ __forceinline__ uint64_t policy_of(uint64_t p, int) { return p; }
+__device__ __forceinline__ uint64_t policy_of(const SplitPolicy& p, int b) { return b < p.from ? p.before : p.behind; }
+
 // A row as its vectors: `base` is the row's address rounded down to 16 bytes.
 template <typename T>
 struct Row {
@@ -389,8 +398,8 @@ __device__ __forceinline__ void stat_row(const Row<T>& R, const BlockRange& br, 
   LaneStat st = lane_stat_empty();
   uint4 cur[kVecPerLane], nxt[kVecPerLane];
   int b = br.begin + warp;
-  if (b < br.end) R.load_block(b, lane, cur, policy);
-  if (b + kWarps < br.end) R.load_block(b + kWarps, lane, nxt, policy);
+  if (b < br.end) R.load_block(b, lane, cur, policy_of(policy, b));
+  if (b + kWarps < br.end) R.load_block(b + kWarps, lane, nxt, policy_of(policy, b + kWarps));
   before();
   auto take = [&](int k, uint4(&v)[kVecPerLane]) {
     each(k, v);
@@ -408,7 +417,7 @@ __device__ __forceinline__ void stat_row(const Row<T>& R, const BlockRange& br, 
       bm = warp_max_nan(lane_max(v, (const T*)nullptr));
     }
     stat_block<T, kEntropy>(st, v, bm, scale);
-    if (k + 2 * kWarps < br.end) R.load_block(k + 2 * kWarps, lane, v, policy);
+    if (k + 2 * kWarps < br.end) R.load_block(k + 2 * kWarps, lane, v, policy_of(policy, k + 2 * kWarps));
   };
   // (two blocks a turn, each in registers of its own)
   for (; b < br.end; b += 2 * kWarps) {

@@ -67,7 +67,7 @@ def _check(S, idx, val, tau, tl, w, gdtype=None):
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("N,V,K,tau", [(1, 1, 1, 1.0), (3, 5, 2, 2.0), (2, 130, 128, 0.7), (5, 4099, 64, 1.0),
                                        (4, 50257, 50, 1.5), (1, 151936, 64, 1.0), (310, 2051, 7, 4.0),
-                                       (2, 300007, 16, 1.0), (1, 2097152, 100, 1.0)])
+                                       (2, 300007, 16, 1.0), (1, 2097152, 100, 1.0), (160, 261000, 5, 1.0)])
 def test_against_64_bits(dtype, tail, N, V, K, tau):
     S = ref.logits(N, V, dtype, N * V)
     _check(S, *(lambda i, v, t, w: (i, v, tau, t, w))(*_teacher(S, K, tau, tail, V)))
