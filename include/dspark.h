@@ -485,7 +485,8 @@ int dspark_token_logprobs_backward(const void* logits, int dtype, int64_t row_st
  * dspark_token_logprobs' top_idx, top_logp and teacher_lse = 0 are such entries
  * at tau = 1.  An index may repeat (each entry is a term of its own); one
  * outside [-1, V) makes the row's outputs NaN.  A row none of whose entries has
- * mass does not count.
+ * mass does not count.  p_k and p_r are taken in 64 bits, so a p_r much smaller
+ * than fp32's step at 1 keeps its digits.
  * Out: loss_out [N] f32; stats_out [N, 2] f32, the lse of z and that of its
  * entries outside the kept ones (the lse again with teacher_lse NULL).
  * dlogits_out (may be NULL) [N, V] dense, type gdtype (the logits' type, or

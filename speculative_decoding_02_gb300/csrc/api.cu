@@ -104,6 +104,9 @@ int distill_checks(const void* logits, int dtype, int64_t row_stride, const int3
   return DSPARK_OK;
 }
 
+// What 1 / v in fp32 leaves of it.
+float inverse_low(float v) { return (float)(1. / v - (double)(1.f / v)); }
+
 }  // namespace
 
 extern "C" {
@@ -438,7 +441,8 @@ int dspark_distill_loss(const void* logits, int dtype, int64_t row_stride, const
   if (N == 0) return DSPARK_OK;
   if (!loss_out || !stats_out) return DSPARK_ERR_INVALID;
   DistillArgs a{logits, dtype, row_stride, top_idx, top_val, teacher_lse, weight, lens, N, R, V, K, temperature,
-                1.f / temperature, loss_out, stats_out, nullptr, dlogits_out, dlogits_out ? gdtype : dtype};
+                1.f / temperature, inverse_low(temperature), loss_out, stats_out, nullptr, dlogits_out,
+                dlogits_out ? gdtype : dtype};
   return cuda_status(launch_distill(a, (cudaStream_t)stream));
 }
 
@@ -451,7 +455,7 @@ int dspark_distill_loss_backward(const void* logits, int dtype, int64_t row_stri
   if (N == 0) return DSPARK_OK;
   if (!stats || !g || !dlogits_out) return DSPARK_ERR_INVALID;
   DistillArgs a{logits, dtype, row_stride, top_idx, top_val, teacher_lse, g, lens, N, R, V, K, temperature,
-                1.f / temperature, nullptr, nullptr, stats, dlogits_out, gdtype};
+                1.f / temperature, inverse_low(temperature), nullptr, nullptr, stats, dlogits_out, gdtype};
   return cuda_status(launch_distill(a, (cudaStream_t)stream));
 }
 

@@ -30,6 +30,9 @@
 // 600 us; parts held in shared memory between the passes 830 us and more, for
 // their copies, barriers and passes hardly overlap; tasks in an order that
 // leaves L2 a short reuse distance 730 us, for their waits.
+#include <float.h>
+#include <limits.h>
+
 #include <algorithm>
 #include <type_traits>
 
@@ -60,6 +63,7 @@ struct Shared {
   float pv[kMaxTop];      // p(v) at the first entry of its index, -1 elsewhere
   float z[kMaxTop];       // the student's logit
   float red[4][kWarps];
+  int2 mass[kMaxTop / 32];   // sums of the teacher's probabilities (rest_mass)
 };
 
 // Sums over the CTA (every thread gets them): slot `which` of sh.red.
@@ -82,6 +86,95 @@ __device__ __forceinline__ float cta_max(Shared& sh, int which, float v) {
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) s = max_nan(s, sh.red[which][w]);
   return s;
+}
+
+// A number as the sum of two floats, l below half a step of h (T. J. Dekker, "A
+// floating-point technique for extending the available precision", 1971; the exact
+// sum of any two numbers is D. E. Knuth's).  The _rn forms are never fused.
+struct Pair {
+  float h, l;
+};
+__device__ __forceinline__ Pair sum_of(float a, float b) {
+  const float s = __fadd_rn(a, b), v = __fsub_rn(s, a);
+  return Pair{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, v)), __fsub_rn(b, v))};
+}
+__device__ __forceinline__ Pair sum_of_ordered(float a, float b) {   // |a| >= |b|
+  const float s = __fadd_rn(a, b);
+  return Pair{s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ Pair product_of(Pair a, Pair b) {
+  const float h = __fmul_rn(a.h, b.h);
+  return Pair{h, fmaf(a.h, b.l, fmaf(a.l, b.h, fmaf(a.h, b.h, -h)))};
+}
+constexpr __device__ Pair pair_of(double v) { return Pair{(float)v, (float)(v - (double)(float)v)}; }
+
+// t / tau - lse.
+__device__ __forceinline__ Pair teacher_log(float t, const DistillArgs& p, float lse) {
+  // (a difference that cancels may be smaller than what the product's rounding left)
+  const float u = __fmul_rn(t, p.inv_tau);
+  const Pair s = sum_of(u, -lse);
+  const float l = __fadd_rn(s.l, fmaf(t, p.inv_tau, -u) + t * p.inv_tau_low);
+  return fabsf(s.h) <= FLT_MAX ? sum_of(s.h, l) : Pair{s.h, 0.f};
+}
+
+// e^t for -80 <= t <= 0: t = n ln 2 + r with |r| <= 0.35 and the Taylor series of
+// e^r, its terms from r^7 in single floats.  Off by 1e-14 at most, of 1 (and by
+// 3e-13 of its value), over 2e7 arguments.
+__device__ __forceinline__ Pair exp_of(Pair t) {
+  constexpr double kLn2 = 0.693147180559945309417;
+  constexpr float kLn2a = 0.693145751953125f;   // 15 bits: its products with n are exact
+  constexpr float kLn2b = (float)(kLn2 - kLn2a), kLn2c = (float)(kLn2 - kLn2a - kLn2b);
+  const float n = rintf(t.h * kLog2e);
+  const float m = __fmul_rn(n, kLn2b);
+  const Pair d = sum_of(fmaf(-n, kLn2a, t.h), -m);
+  const Pair r = sum_of_ordered(d.h, d.l - fmaf(n, kLn2b, -m) + t.l - n * kLn2c);
+  float f = 1.f / 479001600.f;
+  f = fmaf(f, r.h, 1.f / 39916800.f);
+  f = fmaf(f, r.h, 1.f / 3628800.f);
+  f = fmaf(f, r.h, 1.f / 362880.f);
+  f = fmaf(f, r.h, 1.f / 40320.f);
+  f = fmaf(f, r.h, 1.f / 5040.f);
+  Pair q{f, 0.f};
+  constexpr Pair kTerms[5] = {pair_of(1. / 720), pair_of(1. / 120), pair_of(1. / 24), pair_of(1. / 6), pair_of(0.5)};
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    const Pair x = product_of(q, r), y = sum_of_ordered(kTerms[i].h, x.h);
+    q = Pair{y.h, __fadd_rn(y.l, __fadd_rn(x.l, kTerms[i].l))};
+  }
+  q = product_of(product_of(r, r), q);
+  const Pair e = sum_of_ordered(r.h, q.h);
+  const Pair y = sum_of_ordered(1.f, e.h);
+  const float scale = __int_as_float(((int)n + 127) << 23);
+  return Pair{y.h * scale, __fadd_rn(y.l, __fadd_rn(e.l, __fadd_rn(q.l, r.l))) * scale};
+}
+
+// What a teacher's probabilities leave of 1.  It is all of the gradient outside the kept
+// entries, and 1 - sum p in 32 bits is off by 2^-24 of 1, however little it is:
+// 3e-4 of it where they hold 99.98 %, all of it past 99.99999 %.  So each is
+// taken in two floats and the sums in whole numbers, p = (i + j 2^-26) 2^-25: 64
+// bits in all (double exponentials: the step below 448 us instead of 444, a short
+// row's gradient alone 61 instead of 59).
+constexpr int kMassNan = INT_MIN;
+__device__ __forceinline__ int2 warp_mass(bool has, Pair t) {
+  int i = 0, j = 0;
+  if (has && t.h >= -80.f) {
+    const Pair p = t.h < 0.f ? exp_of(t) : Pair{1.f, 0.f};   // (one of 1 or more leaves nothing)
+    i = __float2int_rn(p.h * 0x1p25f);
+    j = __float2int_rn(fmaf(p.l, 0x1p25f, fmaf(p.h, 0x1p25f, -(float)i)) * 0x1p26f);
+  }
+  i = __reduce_add_sync(0xffffffffu, i);
+  j = __reduce_add_sync(0xffffffffu, j);
+  return make_int2(__any_sync(0xffffffffu, has && t.h != t.h) ? kMassNan : i, j);
+}
+__device__ __forceinline__ float rest_mass(const int2* mass) {
+  long long left = 1ll << 51;
+  bool nan = false;
+#pragma unroll
+  for (int w = 0; w < kMaxTop / 32; ++w) {
+    left -= mass[w].x * (1ll << 26) + mass[w].y;
+    nan |= mass[w].x == kMassNan;
+  }
+  return nan ? __int_as_float(0x7FC00000) : (left > 0 ? (float)left * 0x1p-51f : 0.f);
 }
 
 // The teacher's side of a row and the student's logits there, by the CTA, into
@@ -110,25 +203,30 @@ __device__ __forceinline__ Kept load_kept(Shared& sh, const DistillArgs& p, int 
     }
   }
   if (tid < kMaxTop) sh.idx[tid] = idx;
+  // the teacher's probabilities once more for their sum, by the warps that hold
+  // no entry, beside the search for equal indices
+  static_assert(kThreads >= 2 * kMaxTop, "a second thread for every entry");
+  const int k2 = tid - (kThreads - kMaxTop);
+  Pair t2{-INFINITY, 0.f};
+  if (kTail && k2 >= 0 && k2 < p.K) t2 = teacher_log(p.top_val[(size_t)row * p.K + k2], p, p.teacher_lse[row]);
   Kept r;
   // log p_k and p_k (products and differences rounded once)
   float t = -INFINITY, base = 0.f;
   if (kTail) {
-    if (val != -INFINITY) t = fmaf(val, p.inv_tau, -p.teacher_lse[row]);
+    if (val != -INFINITY) t = teacher_log(val, p, p.teacher_lse[row]).h;
   } else {
     const float m = cta_max(sh, 0, val);
     if (val != -INFINITY) t = (val - m) * p.inv_tau;
     base = logf(cta_add(sh, 1, t == -INFINITY ? 0.f : expf(t)));
   }
   const float logp = t == -INFINITY ? -INFINITY : t - base;
-  const float pk = t == -INFINITY ? 0.f : expf(logp);
   if (tid < kMaxTop) {
-    sh.p[tid] = pk;
+    sh.p[tid] = t == -INFINITY ? 0.f : expf(logp);
     sh.logp[tid] = logp;
     sh.z[tid] = z;
   }
-  const float total = cta_add(sh, 2, pk);
-  r.p_rest = kTail ? (total > 1.f ? 0.f : 1.f - total) : 0.f;   // (a NaN total stays one)
+  __syncthreads();
+  const float pk = tid < kMaxTop ? sh.p[tid] : 0.f;
   // p(v): equal indices add up in the first of them
   float pv = pk;
   bool first = idx >= 0;
@@ -149,6 +247,10 @@ __device__ __forceinline__ Kept load_kept(Shared& sh, const DistillArgs& p, int 
     }
   }
   if (tid < kMaxTop) sh.pv[tid] = first ? pv : -1.f;
+  if (kTail && k2 >= 0) {
+    const int2 m = warp_mass(k2 < p.K && sh.idx[k2] >= 0, t2);
+    if ((tid & 31) == 0) sh.mass[k2 >> 5] = m;
+  }
   r.stat = stat_empty();
   if (kTail && state) {
     r.stat.m = cta_max(sh, 3, first ? z : -INFINITY);
@@ -156,6 +258,7 @@ __device__ __forceinline__ Kept load_kept(Shared& sh, const DistillArgs& p, int 
   }
   r.any = __syncthreads_or(val != -INFINITY);
   r.bad = __syncthreads_or(bad);
+  r.p_rest = kTail ? rest_mass(sh.mass) : 0.f;
   return r;
 }
 

@@ -286,6 +286,7 @@ struct DistillArgs {
   const int32_t* lens;
   int N, R, V, K;
   float tau, inv_tau;
+  float inv_tau_low;          // what inv_tau leaves of 1 / tau
   float* loss;                // [N]
   float* stats;               // [N][2]
   const float* stats_in;      // [N][2]: the backward pass alone (no loss, no stats)

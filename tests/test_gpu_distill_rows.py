@@ -1,0 +1,184 @@
+"""Distillation with each row held to bounds of its own: rows whose entries
+outside the kept ones are masked by finite values, rows far from zero, masked,
+absent and repeated entries, and teachers that kept almost all of their mass.
+
+The reference subtracts a row's maximum before anything else, so that log V is
+not lost beside a mask of the type's lowest value, and every bound follows from
+differences to that maximum, never from the size of the logits."""
+import math
+
+import pytest
+import torch
+
+import speculative_decoding_02_gb300 as ds
+
+import _rows as ref
+
+pytestmark = pytest.mark.gpu
+
+F64, U = torch.float64, ref.U
+FLT_MAX = torch.finfo(torch.float32).max
+DTYPES = [torch.float32, torch.bfloat16, torch.float16]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from speculative_decoding_02_gb300 import build
+    build.build()
+    ds.library()
+
+
+def f32(v):
+    """A temperature as the library gets it."""
+    return float(torch.tensor(v, dtype=torch.float32))
+
+
+def _finite(t):
+    return torch.where(torch.isfinite(t), t, torch.zeros_like(t))
+
+
+def _states(z, tau):
+    """Maximum, distances (z - max) / tau, log of the sum and the relative error of
+    the sum for each row: base_error without its span, and five steps of a
+    term's distance (x - m, 1 / tau, log2 e and two products) weighted as in the sum."""
+    m = z.amax(-1, keepdim=True)
+    none = m == -math.inf
+    d = torch.where(none, torch.full_like(z, -math.inf), (z - torch.where(none, torch.zeros_like(m), m)) / tau)
+    e = torch.exp(d)
+    s = e.sum(-1, keepdim=True)
+    ls = torch.where(none, torch.zeros_like(s), s.log())
+    weighted = (e * _finite(d).abs()).sum(-1, keepdim=True) / s.clamp(min=1.0)
+    return m, d, ls, ref.base_error(z.shape[-1], 0.0) + 5 * U * weighted
+
+
+def _want(S, idx, val, tau, tlse, w):
+    """(loss, its bound), (stats, their bound), (gradient, its bound, the additional
+    bound of the gradient from rounded stats); tau as the library gets it."""
+    N, V = S.shape
+    K = idx.shape[1]
+    z = S.to(F64)
+    present = (idx >= 0)
+    ii = idx.long().clamp(min=0)
+    t = torch.where(present, val.to(F64) / tau, torch.full((N, K), -math.inf, dtype=F64, device=S.device))
+    any_ = (t > -math.inf).any(-1)
+    tm = torch.where(any_[:, None], t.amax(-1, keepdim=True), torch.zeros(N, 1, dtype=F64, device=S.device))
+    norm = tlse.to(F64)[:, None] if tlse is not None else tm + torch.where(
+        any_[:, None], torch.exp(t - tm).sum(-1, keepdim=True), torch.ones_like(tm)).log()
+    lp = t - norm
+    p = torch.exp(lp)
+    # relative error of p_k: its argument (product, difference, rounded), the
+    # kept entries' sum where it divides by one, the exponential
+    ep = U * (4 * _finite(t - tm).abs() + 2 * _finite(lp).abs() + 40)
+    m, d, ls, ea = _states(z, tau)
+    on = any_ & (m.squeeze(1) > -math.inf)
+    q = torch.exp(d - ls)
+    dk = d.gather(1, ii)
+    gap = torch.where(p > 0, lp - (dk - ls), torch.zeros_like(p))
+    loss = (p * gap).sum(-1)
+    part = p * (ea + 6 * U * (_finite(dk).abs() + ls + _finite(lp).abs()) + ep * (1 + gap.abs()) + 16 * U * gap.abs())
+    eloss = torch.where(torch.isfinite(part), part, torch.zeros_like(part)).sum(-1)
+    mass = torch.zeros_like(z).scatter_add_(1, ii, p * present)
+    emass = torch.zeros_like(z).scatter_add_(1, ii, p * ep * present)
+    inside = torch.zeros_like(z).scatter_add_(1, ii, present.to(F64)) > 0
+    lse = m / tau + ls
+    rest, erest = lse, ea + 4 * U * (m / tau).abs() + 2 * U * ls
+    estat = torch.cat([erest, erest], 1)
+    eq = ea + 5 * U * _finite(d).abs() + 10 * U
+    grad, egrad = q - mass, q * eq + emass
+    late = 6 * U * (lse.abs() + ls) * torch.ones_like(q) * q
+    if tlse is not None:
+        pr = (1 - p.sum(-1, keepdim=True)).clamp(min=0)
+        epr = (K + _finite(t).abs().amax(-1, keepdim=True)) * 2.0 ** -51
+        mr, dr, lsr, er = _states(z.masked_fill(inside, -math.inf), tau)
+        below = torch.where(mr > -math.inf, (m - mr) / tau, torch.zeros_like(m))
+        lqr = torch.where(mr > -math.inf, lsr - ls - below, torch.full_like(m, -math.inf))
+        qr = torch.exp(lqr)
+        r = torch.exp(dr - lsr)
+        term = torch.where(pr > 0, pr * (pr.log() - lqr), torch.zeros_like(pr)).squeeze(1)
+        loss = loss + term
+        eterm = pr * (ea + er + 6 * U * (below + ls + lsr) + 16 * U * _finite(lqr).abs()) + \
+            (epr + 2 * U * pr) * (1 + _finite(pr.log()).abs() + _finite(lqr).abs())
+        eloss = eloss + eterm.squeeze(1) + 16 * U * _finite(term).abs()
+        rest = torch.where(mr > -math.inf, mr / tau + lsr, torch.full_like(mr, -math.inf))
+        estat = torch.cat([estat[:, :1], er + 4 * U * _finite(mr / tau).abs() + 2 * U * lsr], 1)
+        grad = torch.where(inside, grad, r * (qr - pr))
+        outside = r * ((qr + pr) * (ea + er + 5 * U * _finite(dr).abs() + 10 * U) + qr * 5 * U * below + epr)
+        egrad = torch.where(inside, egrad, outside)
+        late = torch.where(inside, late, r * (qr + pr) * 6 * U * (lse.abs() + _finite(rest).abs() + ls + lsr))
+    stats = torch.cat([lse, rest], 1)
+    stats = torch.where(torch.isfinite(stats), stats.clamp(-FLT_MAX, FLT_MAX), stats)
+    off = torch.where(any_, torch.full((N,), -math.inf, dtype=F64, device=S.device), torch.zeros(N, dtype=F64, device=S.device))
+    stats = torch.where(on[:, None], stats, off[:, None])
+    # (past 1024 the stats are not used)
+    used = ((stats.abs() <= 1024) | ~torch.isfinite(stats)).all(-1, keepdim=True)
+    late = torch.where(used, late, torch.zeros_like(late))
+    weight = (w.to(F64) if w is not None else torch.ones(N, dtype=F64, device=S.device))[:, None] / tau
+    gate = lambda a: torch.where(on[:, None], a * weight, torch.zeros_like(a))
+    # (exponentials below 2^-126 are 0)
+    loss = torch.where(loss > FLT_MAX, torch.full_like(loss, math.inf), loss)
+    return ((torch.where(on, loss, torch.zeros_like(loss)), eloss), (stats, torch.where(torch.isfinite(estat), estat, torch.zeros_like(estat))),
+            (gate(grad), gate(egrad) + 2.0 ** -125 * (1 + weight), gate(late)))
+
+
+def _check(S, idx, val, tau, tl, w, gdtype=None):
+    tau = f32(tau)
+    gd = S.dtype if gdtype is None else gdtype
+    (wl, el), (ws, es), (wg, eg, late) = _want(S, idx, val, tau, tl, w)
+    loss, stats, grad = ds.distill_loss(S, idx, val, temperature=tau, teacher_lse=tl, weight=w, grad=True, grad_dtype=gdtype)
+    ref.assert_close(loss, wl, el, "loss")
+    ref.assert_close(stats, ws, es, "stats")
+    rounding = 1.01 * ref.HALF[gd] * wg.abs() + ref.TINY[gd]
+    ref.assert_close(grad, wg, 1.01 * eg + rounding, "gradient")
+    alone = ds.distill_loss(S, idx, val, temperature=tau, teacher_lse=tl)
+    ref.assert_close(alone[0], wl, el, "loss alone")
+    g = torch.ones(len(S), device="cuda") if w is None else w
+    back = ds.distill_loss_backward(S, idx, val, stats, g, temperature=tau, teacher_lse=tl, grad_dtype=gdtype)
+    ref.assert_close(back, wg, 1.01 * (eg + late) + rounding, "gradient alone")
+    return loss, stats, grad, back
+
+
+def _case(N, V, K, dtype, seed, tau=1.0, share=0.7):
+    """Student rows, and a teacher whose kept entries carry `share` of its mass."""
+    S = ref.logits(N, V, dtype, seed)
+    g = torch.Generator(device="cuda").manual_seed(seed + 1)
+    idx = torch.stack([torch.randperm(V, generator=g, device="cuda")[:K] for _ in range(N)]).to(torch.int32)
+    val = torch.empty((N, K), device="cuda").normal_(0, 2, generator=g)
+    tl = torch.logsumexp(val / f32(tau), -1) - math.log(share)
+    w = torch.rand(N, generator=g, device="cuda") + 0.1
+    return S, idx, val, tl, w
+
+
+def _almost_all(kept, left, shift, tau, N, K, device="cuda"):
+    """val [N, K] and teacher_lse [N] of a teacher with about `left` of its mass
+    outside, and the mass that these rounded inputs leave there."""
+    g = torch.Generator().manual_seed(5)
+    p = torch.softmax(3.0 * torch.randn((N, K), generator=g, dtype=F64), -1) if kept == "peaked" else \
+        torch.softmax(torch.log(0.5 + torch.rand((N, K), generator=g, dtype=F64)), -1)
+    tl = torch.full((N,), shift, dtype=torch.float32)
+    val = (tau * ((p * (1 - left)).log() + shift)).float()
+    rest = 1 - torch.exp(val.to(F64) / tau - tl.to(F64)[:, None]).sum(-1)
+    return val.to(device), tl.to(device), rest
+
+
+LEFT = [(1e-2, 0.0), (1e-2, 12.0), (1e-4, 0.0), (1e-4, 12.0), (1e-5, 0.0), (1e-6, 0.0), (3e-7, 0.0)]
+
+
+@pytest.mark.parametrize("kept", ["peaked", "spread"])
+@pytest.mark.parametrize("left,shift", LEFT)
+@pytest.mark.parametrize("tau", [1.0, 0.7, 3.0])
+def test_teachers_that_kept_almost_all(kept, left, shift, tau):
+    """The remaining mass p_r is all of the gradient outside the kept entries
+    where the student has nothing there, and 1 - sum p in 32 bits is off by 2^-24
+    of 1, however small p_r is."""
+    N, V, K = 4, 20000, 64
+    val, tl, rest = _almost_all(kept, left, shift, f32(tau), N, K)
+    assert (rest > left / 4).all() and (rest < 4 * left).all()
+    S = ref.logits(N, V, torch.float32, 2)
+    idx = S.topk(K).indices.to(torch.int32)
+    S.scatter_add_(1, idx.long(), torch.full((N, K), 60.0 * tau, device="cuda"))
+    _, _, grad, back = _check(S, idx, val, tau, tl, None)
+    outside = torch.ones_like(S, dtype=torch.bool).scatter_(1, idx.long(), False)
+    for got in (grad, back):
+        total = -(got.to(F64) * outside).sum(-1).cpu() * f32(tau)
+        assert ((total - rest).abs() < 1e-4 * rest).all()
+    _check(S, idx, val, tau, tl, None, torch.bfloat16)
