@@ -488,7 +488,8 @@ int dspark_token_logprobs_backward(const void* logits, int dtype, int64_t row_st
  * mass does not count.  p_k and p_r are taken in 64 bits, so a p_r much smaller
  * than fp32's step at 1 keeps its digits.
  * Out: loss_out [N] f32; stats_out [N, 2] f32, the lse of z and that of its
- * entries outside the kept ones (the lse again with teacher_lse NULL).
+ * entries outside the kept ones (the lse again with teacher_lse NULL), -inf
+ * where every entry is and else held in fp32's finite range.
  * dlogits_out (may be NULL) [N, V] dense, type gdtype (the logits' type, or
  * DSPARK_BF16 for fp32 logits): weight[i] * d loss_i / d logits, weight [N] f32
  * or NULL (1); zeros in rows that do not count.  It may be the logits

@@ -88,6 +88,12 @@ __device__ __forceinline__ float cta_max(Shared& sh, int which, float v) {
   return s;
 }
 
+// A state's log-sum-exp, held in fp32's finite range unless the state is empty: a
+// row of the lowest value at a temperature below 1 is none.
+__device__ __forceinline__ float finite_lse(float m, float inv_tau, float ls) {
+  return m == -INFINITY ? m : fminf(fmaxf(fmaf(m, inv_tau, ls), -FLT_MAX), FLT_MAX);
+}
+
 // A number as the sum of two floats, l below half a step of h (T. J. Dekker, "A
 // floating-point technique for extending the available precision", 1971; the exact
 // sum of any two numbers is D. E. Knuth's).  The _rn forms are never fused.
@@ -389,10 +395,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
     if (bad) cw = q_scale = nan;
     if (!backward && rank == 0) {
       const float pk = tid < p.K ? sh.p[tid] : 0.f;
-      float L = cta_add(sh, 1, !(pk == 0.f) ? pk * (sh.logp[tid] - ((sh.z[tid] - q_ref) * p.inv_tau - ls)) : 0.f);
-      const float lse = fmaf(all.m, p.inv_tau, ls);
-      const float lse_rest = rest.m == -INFINITY ? -INFINITY : fmaf(rest.m, p.inv_tau, logf(rest.s));
-      if (kTail && !(kept.p_rest == 0.f)) L += kept.p_rest * (logf(kept.p_rest) - (lse_rest - lse));
+      // p (log p - log q) with -log q = distance / tau + ls; the distance is taken
+      // down by p first, for over tau alone it may pass fp32's range
+      float L = cta_add(sh, 1, !(pk == 0.f) ? fmaf(pk * (q_ref - sh.z[tid]), p.inv_tau, pk * (sh.logp[tid] + ls)) : 0.f);
+      const float ls_rest = logf(rest.s);
+      const float lse = finite_lse(all.m, p.inv_tau, ls), lse_rest = finite_lse(rest.m, p.inv_tau, ls_rest);
+      if (kTail && !(kept.p_rest == 0.f)) {
+        // (log q_r not as lse_rest - lse: of rows far from zero the two keep no fraction)
+        const float below = rest.m == -INFINITY ? INFINITY : kept.p_rest * (all.m - rest.m);
+        L += fmaf(below, p.inv_tau, kept.p_rest * (logf(kept.p_rest) + (ls - ls_rest)));
+      }
       if (tid == 0) {
         const bool counts = kept.any || bad;
         p.loss[row] = bad ? nan : (on ? L : 0.f);

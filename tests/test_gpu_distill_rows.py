@@ -148,6 +148,22 @@ def _case(N, V, K, dtype, seed, tau=1.0, share=0.7):
     return S, idx, val, tl, w
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tau", [1.0, 0.5, 0.01, 3.0])
+@pytest.mark.parametrize("level", [1e9, -1e9, 3000.0, -3000.0, "lowest"])
+def test_rows_far_from_zero(dtype, tau, level):
+    level = torch.finfo(dtype).min if level == "lowest" else level
+    if abs(level) > torch.finfo(dtype).max:
+        level = math.copysign(6e4, level)
+    S, idx, val, tl, w = _case(3, 100, 50, dtype, 3, tau)
+    S[0] = level                                   # one value, half of its entries kept
+    S[1] += level                                  # what of the row the type leaves
+    if level < -1e5:
+        S[1, ::3] = 0.0
+    _check(S, idx, val, tau, tl, w)
+    _check(S, idx, val, tau, None, w)
+
+
 def _almost_all(kept, left, shift, tau, N, K, device="cuda"):
     """val [N, K] and teacher_lse [N] of a teacher with about `left` of its mass
     outside, and the mass that these rounded inputs leave there."""
