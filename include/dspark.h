@@ -503,8 +503,8 @@ int dspark_distill_loss(const void* logits, int dtype, int64_t row_stride, const
 
 /*
  * The gradient of dspark_distill_loss alone, from its stats output and an
- * upstream gradient g [N] f32 (in the place of weight).  Of a row whose |lse|
- * is above 1024 the statistics are taken again from the logits.
+ * upstream gradient g [N] f32 (in the place of weight).  Of a row one of whose
+ * stats is above 1024 in size they are taken again from the logits.
  */
 int dspark_distill_loss_backward(const void* logits, int dtype, int64_t row_stride, const int32_t* top_idx,
                                  const float* top_val, const float* stats, const float* g,

@@ -269,7 +269,7 @@ __device__ __forceinline__ Kept load_kept(Shared& sh, const DistillArgs& p, int 
 }
 
 // kTail: the teacher's lse is given.  With p.stats_in the backward pass alone,
-// which takes the row's state anew only where its lse is too large to be used.
+// which takes the row's state anew only where one of its stats is too large to be used.
 // kStash: the part's last `stash` blocks stay in shared memory between the passes.
 template <typename T, typename G, bool kTail, bool kStash>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const DistillArgs p, int ahead, int stash) {
@@ -299,7 +299,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(const Dis
     lse_in = p.stats_in[2 * (size_t)row];
     lse_rest_in = p.stats_in[2 * (size_t)row + 1];
   }
-  const bool pass = on && (!backward || (lse_in != -INFINITY && fabsf(lse_in) > kLargeLse));
+  // (the second one is the tail's reference: masks of finite values outside the
+  // kept entries leave it far from zero beside an ordinary lse)
+  const bool pass = on && (!backward || lse_is_large(lse_in) || (kTail && lse_is_large(lse_rest_in)));
 
   Kept kept;
   kept.any = kept.bad = false;

@@ -467,8 +467,9 @@ __device__ __forceinline__ bool stat_bad(const Stat& v) { return !(v.m < INFINIT
 // The backward passes take p_v = exp(x_v - lse) from an lse rounded to fp32,
 // which is off by |lse| 2^-24 of its value: past this size (rows far from
 // zero, and rows that a mask of the type's lowest value fills, whose log V is
-// lost beside it) they take the row's state anew.
+// lost beside it) they take the row's state anew.  An empty row's -inf is exact.
 constexpr float kLargeLse = 1024.f;
+__device__ __forceinline__ bool lse_is_large(float lse) { return lse != -INFINITY && fabsf(lse) > kLargeLse; }
 
 // CTAs a row: at least `least` (1 to 16), and for few rows up to 8 as long as
 // every warp keeps a block and the SMs have about two each.  Rows of 151936

@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_backward_kernel
   // p_v = exp(x_v - ref - ls)
   float ref = on ? p.lse[row] : -INFINITY, ls = 0.f;
   if (ref != ref) gl = nan;
-  if (fabsf(ref) > kLargeLse && ref != -INFINITY) {
+  if (lse_is_large(ref)) {
     stat_row<T, false, false>(R, br, kLog2e, 1.f, NoPolicy(), part, &cta, Nothing(), Nothing(), Nothing(), Nothing());
     cluster_meet(c);
     const Stat v = stat_cluster(cluster, &cta, c, 1.f);

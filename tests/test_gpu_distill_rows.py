@@ -148,6 +148,26 @@ def _case(N, V, K, dtype, seed, tau=1.0, share=0.7):
     return S, idx, val, tl, w
 
 
+MASKS = [-math.inf, -1e4, -3e3, -1e9, "lowest"]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tau", [1.0, 0.5])
+@pytest.mark.parametrize("mask", MASKS)
+def test_entries_outside_the_kept_ones_masked(dtype, tau, mask):
+    fill = torch.finfo(dtype).min if mask == "lowest" else mask
+    if abs(fill) > torch.finfo(dtype).max and fill != -math.inf:
+        pytest.skip("not a value of the type")
+    for N, V, K in ((4, 5003, 8), (2, 151936, 64)):
+        S, idx, val, tl, w = _case(N, V, K, dtype, 7, tau)
+        kept = S.gather(1, idx.long())
+        S[:] = fill
+        S[1, : V // 2] = -math.inf                 # masks of two kinds
+        S.scatter_(1, idx.long(), kept)
+        _check(S, idx, val, tau, tl, w)
+        _check(S, idx, val, tau, None, w)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("tau", [1.0, 0.5, 0.01, 3.0])
 @pytest.mark.parametrize("level", [1e9, -1e9, 3000.0, -3000.0, "lowest"])
