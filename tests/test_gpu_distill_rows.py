@@ -184,6 +184,33 @@ def test_rows_far_from_zero(dtype, tau, level):
     _check(S, idx, val, tau, None, w)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("gdtype", [None, torch.bfloat16])
+def test_masked_empty_absent_and_repeated(dtype, tail, gdtype):
+    if gdtype is not None and dtype != torch.float32:
+        pytest.skip("the gradient has the logits' type")
+    N, V, K = 10, 1500, 8
+    S, i, v, t, w = _case(N, V, K, dtype, 11)
+    S[0] = -math.inf                               # nothing left in the student
+    S[1, ::2] = -math.inf
+    i[1] = torch.arange(1, 2 * K, 2, dtype=torch.int32, device="cuda")
+    S[2] = torch.finfo(dtype).min                  # uniform
+    S[3, 5:] = torch.finfo(dtype).min              # all but entries that are kept
+    i[3] = torch.arange(K, dtype=torch.int32, device="cuda").clamp(max=4)
+    i[4, 3:] = -1                                  # absent entries
+    i[5] = -1                                      # no teacher: the row does not count
+    i[6] = i[6, 0]                                 # one index K times
+    i[7, 1] = i[7, 0]
+    v[8, 2] = -math.inf                            # an entry without mass
+    S[9] = -math.inf                               # nothing outside the kept entries, and no mass there either
+    S[9, i[9].long()] = 1.0
+    t[9] = torch.logsumexp(v[9], -1) - 1e-3
+    loss, _, grad, back = _check(S, i, v, 1.0, t if tail else None, w, gdtype)
+    for row in (0, 5):
+        assert loss[row] == 0 and (grad[row] == 0).all() and (back[row] == 0).all()
+
+
 def _almost_all(kept, left, shift, tau, N, K, device="cuda"):
     """val [N, K] and teacher_lse [N] of a teacher with about `left` of its mass
     outside, and the mass that these rounded inputs leave there."""
