@@ -615,17 +615,47 @@ def _head_args(logits, what, dtype, W1, W2, anchor, x):
     return dev, B, G, V, r
 
 
+_head_status = {}
+
+
+def head_status(device):
+    """The status word of the calls of markov_logits on this device that were
+    given no ws, for read_status.  (A call that is captured into a graph before
+    the device has one takes a word of its own, which nobody reads: call this
+    first, or give it a ws.)"""
+    dev = torch.device(device)
+    if dev.index is None:
+        dev = torch.device(dev.type, torch.cuda.current_device())
+    st = _head_status.get(dev)
+    if st is None:
+        st = torch.zeros(256, dtype=torch.uint8, device=dev)
+        # (cleared before another stream's call can record in it)
+        torch.cuda.current_stream(dev).synchronize()
+        _head_status[dev] = st
+    return st
+
+
+def _status_without_ws(dev):
+    st = _head_status.get(dev)
+    if st is None:
+        with torch.cuda.device(dev):
+            capturing = torch.cuda.is_current_stream_capturing()
+        st = torch.zeros(256, dtype=torch.uint8, device=dev) if capturing else head_status(dev)
+    return st
+
+
 def markov_logits(U, W1, W2, anchor, x, dtype=torch.float32, ws=None, out=None):
     """l [B, G, V] = U + W1[x_{k-1}] W2^T (x_0 = anchor), the logits the draft
     samples from at tokens x [B, G], as float32 or bfloat16.  out: a tensor to
     write, which may be U itself (float32).  Tensor-core path only (bf16
-    weights, r = 256)."""
+    weights, r = 256).  ws: 256 zeroed bytes to read_status of; by default
+    errors are recorded in head_status."""
     L = _load()
     dev, B, G, V, r = _head_args(U, "U", torch.float32, W1, W2, anchor, x)
     if dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
     out = _gradient_out(out, U, dtype)
-    ws = workspace(B, G, V, dev) if ws is None else _need(ws, "ws", torch.uint8, dev)
+    ws = _status_without_ws(dev) if ws is None else _need(ws, "ws", torch.uint8, dev)
     _launch(L.dspark_markov_logits, "markov_logits", dev, U.data_ptr(), W1.data_ptr(), W2.data_ptr(), _dt(W1, "W1"),
             anchor.data_ptr(), x.data_ptr(), B, G, V, r, out.data_ptr(), _ROW_DTYPES[dtype], ws.data_ptr(), ws.numel())
     return out

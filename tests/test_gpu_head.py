@@ -297,3 +297,28 @@ def test_streams_and_graphs():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, w))
+
+
+def _bad_tokens(B, G, V):
+    anchor, x = _tokens(B, G, V, 3)
+    anchor[1], x[2, 1] = -1, V
+    return anchor, x
+
+
+def test_errors_of_logits_without_a_workspace():
+    """They are kept for whoever asks, and are not a round's: its cached
+    workspace for the same sizes is neither written nor made."""
+    B, G, V = 6, 3, 1160
+    W1, W2 = _weights(V, 1)
+    anchor, x = _bad_tokens(B, G, V)
+    U = torch.empty((B, G, V), device="cuda").normal_(0, 3, generator=_gen(1))
+    rounds = ds.workspace(B, G, V, U.device)
+    cached = len(ds._ws_cache)
+    assert ds.read_status(rounds) == ds.OK
+    ds.markov_logits(U, W1, W2, anchor, x)
+    assert ds.read_status(rounds) == ds.OK
+    status = ds.head_status("cuda")
+    assert ds.read_status(status) == ds.ERR_INVALID and ds.read_status(status) == ds.OK
+    good, y = _tokens(B, G, V, 3)
+    ds.markov_logits(torch.zeros((B, G, V + 8), device="cuda"), *_weights(V + 8, 2), good, y)
+    assert ds.read_status(ds.head_status(U.device)) == ds.OK and len(ds._ws_cache) == cached
