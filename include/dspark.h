@@ -545,6 +545,16 @@ int dspark_markov_head_backward(const void* dlogits, const void* W1, const void*
                                 void* stream);
 
 /*
+ * dspark_markov_head_backward with its status word in status (device, 4-byte
+ * aligned, zero at first; NULL: the workspace's), so that an error outlives a
+ * workspace that is freed behind the call.
+ */
+int dspark_markov_head_backward_ex(const void* dlogits, const void* W1, const void* W2, int wdtype,
+                                   const int32_t* anchor, const int32_t* x, int B, int gamma, int V, int r,
+                                   int32_t* status, float* dW1_out, float* dW2_out, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
  * The Markov draft without a caller workspace.  The method has no counterpart:
  * this entry serves callers that cannot allocate device memory at the time of
  * the call (an engine whose pool owns all of HBM, a plugin given no allocator,

@@ -108,6 +108,8 @@ def _load():
     L.dspark_markov_logits.restype = i32
     L.dspark_markov_head_backward.argtypes = [vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp, sz, vp]
     L.dspark_markov_head_backward.restype = i32
+    L.dspark_markov_head_backward_ex.argtypes = [vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp]
+    L.dspark_markov_head_backward_ex.restype = i32
     L.dspark_distill_loss.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, vp, vp, vp, i32, vp]
     L.dspark_distill_loss.restype = i32
     L.dspark_distill_loss_backward.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, vp,
@@ -619,10 +621,10 @@ _head_status = {}
 
 
 def head_status(device):
-    """The status word of the calls of markov_logits on this device that were
-    given no ws, for read_status.  (A call that is captured into a graph before
-    the device has one takes a word of its own, which nobody reads: call this
-    first, or give it a ws.)"""
+    """The status word of the calls of markov_logits and markov_head_backward on
+    this device that were given no ws, for read_status.  (A call that is captured
+    into a graph before the device has one takes a word of its own, which
+    nobody reads: call this first, or give it a ws.)"""
     dev = torch.device(device)
     if dev.index is None:
         dev = torch.device(dev.type, torch.cuda.current_device())
@@ -676,16 +678,19 @@ def _head_workspace(B, gamma, V, device):
 def markov_head_backward(dlogits, W1, W2, anchor, x, ws=None):
     """dW1, dW2 [V, r] f32 from the gradient dlogits [B, G, V] bf16 of
     markov_logits.  ws: a head_workspace to keep (and read_status of); by
-    default one is allocated for the call."""
+    default one is allocated for the call and errors are recorded in head_status."""
     L = _load()
     dev, B, G, V, r = _head_args(dlogits, "dlogits", torch.bfloat16, W1, W2, anchor, x)
     dW1 = torch.empty((V, r), dtype=torch.float32, device=dev)
     dW2 = torch.empty((V, r), dtype=torch.float32, device=dev)
-    # (the status word of a workspace of the call's own is nobody's)
-    ws = _head_workspace(B, G, V, dev) if ws is None else _need(ws, "ws", torch.uint8, dev)
-    _launch(L.dspark_markov_head_backward, "markov_head_backward", dev, dlogits.data_ptr(), W1.data_ptr(),
-            W2.data_ptr(), _dt(W1, "W1"), anchor.data_ptr(), x.data_ptr(), B, G, V, r, dW1.data_ptr(), dW2.data_ptr(),
-            ws.data_ptr(), ws.numel())
+    status = None
+    if ws is None:
+        ws, status = _head_workspace(B, G, V, dev), _status_without_ws(dev)
+    else:
+        _need(ws, "ws", torch.uint8, dev)
+    _launch(L.dspark_markov_head_backward_ex, "markov_head_backward", dev, dlogits.data_ptr(), W1.data_ptr(),
+            W2.data_ptr(), _dt(W1, "W1"), anchor.data_ptr(), x.data_ptr(), B, G, V, r, _address(status), dW1.data_ptr(),
+            dW2.data_ptr(), ws.data_ptr(), ws.numel())
     return dW1, dW2
 
 

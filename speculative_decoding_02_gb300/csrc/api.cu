@@ -416,20 +416,30 @@ int dspark_markov_logits(const float* U, const void* W1, const void* W2, int wdt
   return cuda_status(launch_markov_logits(a, (cudaStream_t)stream));
 }
 
-int dspark_markov_head_backward(const void* dlogits, const void* W1, const void* W2, int wdtype,
-                                const int32_t* anchor, const int32_t* x, int B, int gamma, int V, int r,
-                                float* dW1_out, float* dW2_out, void* workspace, size_t workspace_bytes,
-                                void* stream) {
+int dspark_markov_head_backward_ex(const void* dlogits, const void* W1, const void* W2, int wdtype,
+                                   const int32_t* anchor, const int32_t* x, int B, int gamma, int V, int r,
+                                   int32_t* status, float* dW1_out, float* dW2_out, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
   DSPARK_TRY(check_shapes(B, gamma, V, r));
   DSPARK_TRY(check_dtype(wdtype));
   if (!dlogits || !W1 || !W2 || !anchor || !x || !dW1_out || !dW2_out) return DSPARK_ERR_INVALID;
   if (!aligned(dlogits, 16) || !aligned(W1, 16) || !aligned(W2, 16) || !aligned(dW1_out, 16) || !aligned(dW2_out, 16))
     return DSPARK_ERR_INVALID;
+  if (!aligned(status, 4)) return DSPARK_ERR_INVALID;
   if (!draft_tc_supported(wdtype, r, V)) return DSPARK_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < head_workspace_bytes(B * gamma, V))
     return DSPARK_ERR_WORKSPACE;
-  HeadBackwardArgs a{dlogits, W1, W2, anchor, x, B, gamma, V, dW1_out, dW2_out, workspace};
+  HeadBackwardArgs a{dlogits, W1, W2, anchor, x, B, gamma, V, dW1_out, dW2_out, workspace,
+                     status ? status : ws_ptr<int>(workspace, 0)};
   return cuda_status(launch_markov_head_backward(a, (cudaStream_t)stream));
+}
+
+int dspark_markov_head_backward(const void* dlogits, const void* W1, const void* W2, int wdtype,
+                                const int32_t* anchor, const int32_t* x, int B, int gamma, int V, int r,
+                                float* dW1_out, float* dW2_out, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  return dspark_markov_head_backward_ex(dlogits, W1, W2, wdtype, anchor, x, B, gamma, V, r, nullptr, dW1_out, dW2_out,
+                                        workspace, workspace_bytes, stream);
 }
 
 int dspark_distill_loss(const void* logits, int dtype, int64_t row_stride, const int32_t* top_idx,

@@ -819,7 +819,7 @@ cudaError_t launch_markov_head_backward(const HeadBackwardArgs& a, cudaStream_t 
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorUnknown;
   char* ws = static_cast<char*>(a.ws);
-  int* status = reinterpret_cast<int*>(ws);
+  int* status = a.status;
   int32_t* prev = reinterpret_cast<int32_t*>(ws + 256);
   char* E = ws + 256 + align256(4ull * N);
   float* part = reinterpret_cast<float*>(E + align256(512ull * N));

@@ -271,6 +271,7 @@ struct HeadBackwardArgs {
   float* dW1;              // [V][256]
   float* dW2;
   void* ws;                // head_workspace_bytes(B * G, V)
+  int* status;
 };
 size_t head_workspace_bytes(int N, int V);
 cudaError_t launch_markov_head_backward(const HeadBackwardArgs& a, cudaStream_t stream);

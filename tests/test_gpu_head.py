@@ -322,3 +322,43 @@ def test_errors_of_logits_without_a_workspace():
     good, y = _tokens(B, G, V, 3)
     ds.markov_logits(torch.zeros((B, G, V + 8), device="cuda"), *_weights(V + 8, 2), good, y)
     assert ds.read_status(ds.head_status(U.device)) == ds.OK and len(ds._ws_cache) == cached
+
+
+def test_errors_of_gradients_without_a_workspace():
+    B, G, V = 6, 3, 1160
+    W1, W2 = _weights(V, 1)
+    anchor, x = _bad_tokens(B, G, V)
+    D = torch.empty((B, G, V), device="cuda").normal_(0, 3, generator=_gen(1)).bfloat16()
+    status = ds.head_status("cuda")
+    assert ds.read_status(status) == ds.OK
+    _check_backward(D, W1, W2, anchor, x)
+    assert ds.read_status(status) == ds.ERR_INVALID
+    _check_backward(D, W1, W2, *_tokens(B, G, V, 3))
+    assert ds.read_status(status) == ds.OK
+    # a workspace of the caller's keeps its own errors
+    ws = ds.head_workspace(B, G, V, "cuda")
+    _check_backward(D, W1, W2, anchor, x, ws=ws)
+    assert ds.read_status(status) == ds.OK and ds.read_status(ws) == ds.ERR_INVALID
+
+
+@pytest.mark.parametrize("first", [False, True])
+def test_captured_calls_without_a_workspace(first, monkeypatch):
+    B, G, V = 6, 3, 1160
+    W1, W2 = _weights(V, 1)
+    anchor, x = _bad_tokens(B, G, V)
+    U = torch.empty((B, G, V), device="cuda").normal_(0, 3, generator=_gen(1))
+    D = U.bfloat16()
+    want = (ds.markov_logits(U, W1, W2, anchor, x), *ds.markov_head_backward(D, W1, W2, anchor, x))
+    ds.read_status(ds.head_status("cuda"))
+    if first:   # as on a device where nothing has run before the capture
+        monkeypatch.setattr(ds, "_head_status", {})
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = (ds.markov_logits(U, W1, W2, anchor, x), *ds.markov_head_backward(D, W1, W2, anchor, x))
+    for _ in range(2):
+        for t in out:
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+        assert ds.read_status(ds.head_status("cuda")) == (ds.OK if first else ds.ERR_INVALID)

@@ -87,3 +87,19 @@ def test_binding_refuses_host_tensors(lib):
         ds.token_logprobs(x, tok)
     with pytest.raises(ValueError):
         ds.distill_loss(x, tok[:, None], x[:, :1])
+
+
+def test_head_backward_arguments(lib):
+    p, odd = _fake(), _fake(0x10002)
+
+    def call(d=p, W1=p, W2=p, wdtype=1, anchor=p, x=p, B=2, G=3, V=256, r=256, status=None, dW1=p, dW2=p, ws=p, n=1 << 30):
+        return lib.dspark_markov_head_backward_ex(d, W1, W2, wdtype, anchor, x, B, G, V, r, status, dW1, dW2, ws, n, None)
+
+    for kw in (dict(d=None), dict(W1=None), dict(W2=None), dict(anchor=None), dict(x=None), dict(dW1=None), dict(dW2=None),
+               dict(d=odd), dict(W1=odd), dict(W2=odd), dict(dW1=odd), dict(dW2=odd), dict(status=odd), dict(wdtype=2),
+               dict(B=0), dict(G=0), dict(V=0)):
+        assert call(**kw) == ds.ERR_INVALID, kw
+    for kw in (dict(wdtype=0), dict(r=128), dict(V=184), dict(V=260)):
+        assert call(**kw) == ds.ERR_UNSUPPORTED, kw
+    for kw in (dict(ws=None), dict(ws=odd), dict(n=256)):
+        assert call(**kw) == ds.ERR_WORKSPACE, kw
