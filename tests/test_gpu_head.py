@@ -362,3 +362,22 @@ def test_captured_calls_without_a_workspace(first, monkeypatch):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want))
         assert ds.read_status(ds.head_status("cuda")) == (ds.OK if first else ds.ERR_INVALID)
+
+
+@pytest.mark.parametrize("B,G,V", [(128, 16, 20000), (128, 16, 2048), (16, 4, 60000)])
+def test_accumulators_are_promoted_in_time(B, G, V):
+    """The tensor cores truncate when they add to an accumulator: half a step, or
+    0.36 * 2^-23 of its value on average (1 / m over mantissas m in [1, 2) averages
+    0.72), always towards zero.  After j additions of terms of no particular sign it
+    is about sqrt(j) of them, so n additions lose 0.36 * 2^-23 * 2/3 n of the sum:
+    9.2e-7 for the 32 of one accumulator, after which sums are rounded (1.5e-7 at
+    most beside it).  Twice as many additions gave 1.3e-6."""
+    W1, W2 = _weights(V, 1)
+    anchor, x = _tokens(B, G, V, 3)
+    D = torch.empty((B, G, V), device="cuda").normal_(0, 1, generator=_gen(2)).bfloat16()
+    dW1, dW2 = ds.markov_head_backward(D, W1, W2, anchor, x)
+    prev, d = _prev(anchor, x), D.view(-1, V).to(F64)
+    w2 = d.T @ W1[prev].to(F64)
+    w1 = torch.zeros((V, R), dtype=F64, device="cuda").index_add(0, prev, d @ W2.to(F64))
+    for got, want in ((dW1, w1), (dW2, w2)):
+        assert float((got.to(F64) - want).norm() / want.norm()) < 1e-6
