@@ -485,8 +485,8 @@ int dspark_token_logprobs_backward(const void* logits, int dtype, int64_t row_st
  * dspark_token_logprobs' top_idx, top_logp and teacher_lse = 0 are such entries
  * at tau = 1.  An index may repeat (each entry is a term of its own); one
  * outside [-1, V) makes the row's outputs NaN.  A row none of whose entries has
- * mass does not count.  p_k and p_r are taken in 64 bits, so a p_r much smaller
- * than fp32's step at 1 keeps its digits.
+ * mass does not count.  p_r is taken to 1e-13 of 1, so that one far below fp32's
+ * step there keeps its digits.
  * Out: loss_out [N] f32; stats_out [N, 2] f32, the lse of z and that of its
  * entries outside the kept ones (the lse again with teacher_lse NULL), -inf
  * where every entry is and else held in fp32's finite range.
@@ -527,13 +527,15 @@ int dspark_markov_logits(const float* U, const void* W1, const void* W2, int wdt
 
 /*
  * The gradients of both weights from the gradient of those logits, dlogits
- * [B, gamma, V] bf16 (as dspark_distill_loss and dspark_token_logprobs_backward
- * give it; the gradient of U is dlogits itself):
+ * [B, gamma, V] bf16 (as dspark_distill_loss gives it with gdtype DSPARK_BF16, and
+ * dspark_token_logprobs_backward for bf16 logits; the gradient of U is dlogits
+ * itself):
  *   dW2[v, i] = sum_{b,k} dlogits[b, k-1, v] * W1[x_{k-1}, i]
  *   dW1[t, i] = sum_{(b,k): x_{k-1} = t} sum_v dlogits[b, k-1, v] * W2[v, i]
  * Out: dW1_out, dW2_out [V, r] f32, wholly written; sums in fp32, in an order
- * that depends on the sizes alone.  A previous token outside [0, V) takes no
- * part and records DSPARK_ERR_INVALID.  Same limits as dspark_markov_logits
+ * that depends on the sizes alone.  A position whose previous token lies outside
+ * [0, V) takes no part, if its dlogits are finite, and records
+ * DSPARK_ERR_INVALID.  Same limits as dspark_markov_logits
  * (every tensor 16-byte aligned).
  * Workspace: dspark_head_workspace_size bytes (0 when a size is not positive or
  * out of range), 256-byte aligned, its status word zero at first.

@@ -4,7 +4,9 @@ Argument marshalling only: every step of the path runs in the library's CUDA
 kernels.  Tensors must be contiguous CUDA tensors on one device; outputs are
 allocated with torch on that device and every call is enqueued on the current
 torch stream.  If the compiled library is missing, every call raises
-``DSparkError`` -- there is no CPU fallback.
+``DSparkError`` -- there is no CPU fallback.  Autograd does not see these calls:
+their outputs require no gradient, whatever their inputs do, and the gradients
+are calls of their own (the _backward forms, and distill_loss with grad).
 
 Entry points (same names as the C ABI in include/dspark.h; the optional
 arguments of markov_draft, schedule, verify and round map to the C ABI's _ex
@@ -13,6 +15,7 @@ forms):
   acceptance_label, sts_fit, token_logprobs, emitted_logprobs,
   token_logprobs_backward, distill_loss, distill_loss_backward,
   markov_logits, markov_head_backward
+head_status is the word in which the last two record errors without a workspace.
 """
 import ctypes
 import math

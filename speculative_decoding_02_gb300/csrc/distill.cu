@@ -22,10 +22,11 @@
 // one write.  What depends on the teacher alone is worked out while the first
 // blocks' loads are under way.
 //
-// Measured (GB300, 2048 rows of 151936 and 64 kept entries, the kernel alone):
-// the loss 187 us in fp32 (6.7 TB/s) and 108 us in bf16; with its gradient 444 us
-// (one read and one write at 5.6 TB/s; HBM reads 1.49 GB for 1.24, L2 keeping
-// most of the 92 MB in flight) and 253 us; the gradient alone 383 and 200 us.
+// Measured (GB300, 2048 rows of 151936 and 64 kept entries with the teacher's lse,
+// four calls in a graph): the loss 183 us in fp32 (6.8 TB/s) and 104 us in bf16;
+// with its gradient 442 us (one read and one write at 5.6 TB/s; HBM reads 1.49 GB
+// for 1.24, L2 keeping most of the 92 MB in flight), 370 us where that is bf16 and
+// 245 us for bf16 logits (5.1 TB/s); the gradient alone 380 and 197 us.
 // Two passes through HBM (a kernel for the sums, one for the gradients) took
 // 600 us; parts held in shared memory between the passes 830 us and more, for
 // their copies, barriers and passes hardly overlap; tasks in an order that
@@ -157,9 +158,9 @@ __device__ __forceinline__ Pair exp_of(Pair t) {
 // What a teacher's probabilities leave of 1.  It is all of the gradient outside the kept
 // entries, and 1 - sum p in 32 bits is off by 2^-24 of 1, however little it is:
 // 3e-4 of it where they hold 99.98 %, all of it past 99.99999 %.  So each is
-// taken in two floats and the sums in whole numbers, p = (i + j 2^-26) 2^-25: 64
-// bits in all (double exponentials: the step below 448 us instead of 444, a short
-// row's gradient alone 61 instead of 59).
+// taken in two floats and the sums in whole numbers, p = (i + j 2^-26) 2^-25.
+// (With double exponentials the step of 2048 rows of 151936 took 448 us, so 443 as
+// with sums in 32 bits; the gradient alone of 1400 fp16 rows of 50257 61, so 58.)
 constexpr int kMassNan = INT_MIN;
 __device__ __forceinline__ int2 warp_mass(bool has, Pair t) {
   int i = 0, j = 0;

@@ -16,7 +16,8 @@
 // CTAs of 256 threads, four to an SM, rather than two of 512: a row's
 // barriers and short serial phases (merging states, choosing alternatives, the
 // teacher's side) then overlap with the other rows' streams (2048 bf16 rows of
-// 129280 with 64 alternatives: 171 us against 210).
+// 129280 with 64 alternatives, as the kernel was when both sizes were timed: 171 us
+// against 210; it takes 116 now).
 #pragma once
 
 #include <cooperative_groups.h>

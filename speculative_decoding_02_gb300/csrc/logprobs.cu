@@ -322,12 +322,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
     tmax = fmaxf(tmax, lm);
     if (lane == 0) sh.quarter[b - br.begin] = q;
   };
-  // (some of the row is read again for its alternatives)
   // (the row that takes this CTA's place)
   auto next = [&]() {
     if (tid == 0 && row + ahead < p.N && ahead > 0) prefetch_row(rp + (size_t)ahead * p.row_stride, p.V, 4);
   };
-  if constexpr (kTop)
+  if constexpr (kTop)   // (some of the row is read again, so L2 is not asked to drop it)
     stat_row<T, true, true>(R, br, kLog2e, 1.f, NoPolicy(), sh.part, &sh.cta, Nothing(), Nothing(), seen, next);
   else
     stat_row<T, true, false>(R, br, kLog2e, 1.f, tc::policy_evict_first(), sh.part, &sh.cta, Nothing(), Nothing(), Nothing(), next);
