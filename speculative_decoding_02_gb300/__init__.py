@@ -636,7 +636,7 @@ def head_status(device):
         st = torch.zeros(256, dtype=torch.uint8, device=dev)
         # (cleared before another stream's call can record in it)
         torch.cuda.current_stream(dev).synchronize()
-        _head_status[dev] = st
+        st = _head_status.setdefault(dev, st)   # (the one that another thread made meanwhile)
     return st
 
 
