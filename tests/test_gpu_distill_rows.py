@@ -245,3 +245,26 @@ def test_teachers_that_kept_almost_all(kept, left, shift, tau):
         total = -(got.to(F64) * outside).sum(-1).cpu() * f32(tau)
         assert ((total - rest).abs() < 1e-4 * rest).all()
     _check(S, idx, val, tau, tl, None, torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_masked_rows_in_place_and_captured(dtype):
+    """The rows that the gradient alone reads again, written over themselves by
+    clusters of CTAs, of one wave and of several, and replayed from a graph."""
+    for N, V in ((3, 40961), (700, 2049), (2, 262144)):
+        S, idx, val, tl, w = _case(N, V, 24, dtype, 5)
+        kept = S.gather(1, idx.long())
+        S[::2] = torch.finfo(dtype).min
+        S.scatter_(1, idx.long(), kept)
+        _, stats, _ = ds.distill_loss(S, idx, val, teacher_lse=tl)
+        want = ds.distill_loss_backward(S, idx, val, stats, w, teacher_lse=tl)
+        got = S.clone()
+        assert ds.distill_loss_backward(got, idx, val, stats, w, teacher_lse=tl, out=got) is got
+        assert torch.equal(got, want)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = ds.distill_loss_backward(S, idx, val, stats, w, teacher_lse=tl)
+        out.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
