@@ -557,6 +557,55 @@ int dspark_markov_head_backward_ex(const void* dlogits, const void* W1, const vo
                                    size_t workspace_bytes, void* stream);
 
 /*
+ * Softmax cross entropy of hidden states under an output head, taken in pieces
+ * of the vocabulary: the logits z = h W^T are never kept ([blog] section 9
+ * trains a draft's hidden states under the target's head).
+ *
+ * h holds N rows of D values and W [V] rows of D, both of type DSPARK_BF16 or
+ * DSPARK_F16 (DSPARK_F32: DSPARK_ERR_UNSUPPORTED), rows h_stride and W_stride
+ * values apart (each >= D).  D % 8 == 0, D <= 16384; V <= 2^21, N <= 2^20; W
+ * 16-byte aligned with W_stride % 8 == 0, h of any element alignment.  A row's
+ * token tokens[i] is in [0, V), or -1: the row does not count.  Rows come in groups
+ * of R with lens as for the rows of logits: those past the first lens[g] do not
+ * count either.  Rows that do not count are gathered out before the products
+ * and cost next to nothing; their outputs are zeros.  A token outside [-1, V)
+ * records DSPARK_ERR_INVALID, its loss is NaN (its lse 0), its dh NaN, and it
+ * takes no part in dW.  A NaN or infinite h or W gives what the formulas give.
+ * status: the device word for errors (4-byte aligned, zero at first; NULL: the
+ * workspace's, its first word).  Workspace: dspark_linear_ce_workspace_size
+ * bytes, 256-byte aligned; `what` is 0 for the loss, else the gradients wanted.
+ *
+ * dspark_linear_cross_entropy: lse = log sum_v exp z_v, loss = lse - z_t, both
+ * [N] f32; products are exact and summed in fp32.
+ */
+#define DSPARK_WANT_DH 1
+#define DSPARK_WANT_DW 2
+size_t dspark_linear_ce_workspace_size(int N, int V, int D, int what);
+int dspark_linear_cross_entropy(const void* h, int64_t h_stride, const void* W, int64_t W_stride, int dtype,
+                                const int32_t* tokens, const int32_t* lens, int N, int R, int V, int D,
+                                float* loss_out, float* lse_out, int32_t* status, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/*
+ * The gradients of dspark_linear_cross_entropy from its lse and the upstream
+ * gradients g_loss and g_lse [N] f32 (g_lse may be NULL: 0):
+ *   s_v = (g_loss + g_lse) exp(z_v - lse) - g_loss 1[v = t],
+ *   dh = s W,  dW = s^T h.
+ * Out: dh_out [N, D] and dW_out [V, D] dense, of h's type, 16-byte aligned and
+ * wholly written; either may be NULL (a head that stays as it is), not both.
+ * They overlap no input.  The logits are formed again, and the slopes s of a
+ * piece of the vocabulary are rounded to h's type before the products (of fp16
+ * after scaling by a power of two); sums are fp32, in an order that depends on
+ * the sizes and on which rows count.  g_loss and g_lse of rows that do not count
+ * are not read.  N = 0 gives a dW of zeros.
+ */
+int dspark_linear_cross_entropy_backward(const void* h, int64_t h_stride, const void* W, int64_t W_stride, int dtype,
+                                         const int32_t* tokens, const int32_t* lens, const float* lse,
+                                         const float* g_loss, const float* g_lse, int N, int R, int V, int D,
+                                         void* dh_out, void* dW_out, int32_t* status, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/*
  * The Markov draft without a caller workspace.  The method has no counterpart:
  * this entry serves callers that cannot allocate device memory at the time of
  * the call (an engine whose pool owns all of HBM, a plugin given no allocator,

@@ -14,8 +14,9 @@ forms):
   markov_draft, confidence, schedule, verify, round, read_status,
   acceptance_label, sts_fit, token_logprobs, emitted_logprobs,
   token_logprobs_backward, distill_loss, distill_loss_backward,
-  markov_logits, markov_head_backward
-head_status is the word in which the last two record errors without a workspace.
+  markov_logits, markov_head_backward, linear_cross_entropy,
+  linear_cross_entropy_backward
+head_status is the word in which the last four record errors without a workspace.
 """
 import ctypes
 import math
@@ -118,6 +119,13 @@ def _load():
     L.dspark_distill_loss_backward.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, vp,
                                                i32, vp]
     L.dspark_distill_loss_backward.restype = i32
+    L.dspark_linear_ce_workspace_size.argtypes = [i32, i32, i32, i32]
+    L.dspark_linear_ce_workspace_size.restype = sz
+    L.dspark_linear_cross_entropy.argtypes = [vp, i64, vp, i64, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp]
+    L.dspark_linear_cross_entropy.restype = i32
+    L.dspark_linear_cross_entropy_backward.argtypes = [vp, i64, vp, i64, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp,
+                                                       vp, vp, vp, sz, vp]
+    L.dspark_linear_cross_entropy_backward.restype = i32
     L.dspark_read_status.argtypes = [vp, ctypes.POINTER(i32), vp]
     L.dspark_read_status.restype = i32
     L.dspark_selftest_wait_timeout.argtypes = [i32, vp, sz, vp]
@@ -624,8 +632,8 @@ _head_status = {}
 
 
 def head_status(device):
-    """The status word of the calls of markov_logits and markov_head_backward on
-    this device that were given no ws, for read_status.  (A call that is captured
+    """The status word of the calls of markov_logits, markov_head_backward and
+    linear_cross_entropy(_backward) on this device that were given no ws, for read_status.  (A call that is captured
     into a graph before the device has one takes a word of its own, which
     nobody reads: call this first, or give it a ws.)"""
     dev = torch.device(device)
@@ -695,6 +703,79 @@ def markov_head_backward(dlogits, W1, W2, anchor, x, ws=None):
             W2.data_ptr(), _dt(W1, "W1"), anchor.data_ptr(), x.data_ptr(), B, G, V, r, _address(status), dW1.data_ptr(),
             dW2.data_ptr(), ws.data_ptr(), ws.numel())
     return dW1, dW2
+
+
+def _hidden_args(h, W, tokens, rows):
+    """device, leading shape, N, R, V, D, both row strides and the dtype code of
+    hidden states and the head over them."""
+    dev, lead, N, R, D, h_stride, dt = _row_args(h, rows, "h")
+    if W is None or not W.is_cuda:
+        raise ValueError("W must be a CUDA tensor")
+    if W.device != dev:
+        raise ValueError(f"W is on {W.device}, expected {dev}")
+    if W.dtype != h.dtype:
+        raise TypeError(f"W must be {h.dtype}, got {W.dtype}")
+    if W.dim() != 2 or W.shape[0] < 1 or W.shape[1] != D:
+        raise ValueError(f"W must be [V, {D}] with V >= 1, got {list(W.shape)}")
+    _, _, V, _, _, W_stride, _ = _row_args(W, None, "W")
+    _row_vector(_need(tokens, "tokens"), "tokens", lead, dev, torch.int32)
+    return dev, lead, N, R, V, D, h_stride, W_stride, dt
+
+
+def _hidden_workspace(ws, N, V, D, what, dev):
+    """A workspace, and the word that errors are recorded in when it is not the caller's."""
+    if ws is not None:
+        return _need(ws, "ws", torch.uint8, dev), None
+    n = int(_load().dspark_linear_ce_workspace_size(N, V, D, what))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=dev), _status_without_ws(dev)
+
+
+def linear_ce_workspace(N, V, D, device, dh=False, dW=False):
+    """A workspace of linear_cross_entropy for N rows (dh and dW False), or of
+    linear_cross_entropy_backward for these gradients."""
+    n = int(_load().dspark_linear_ce_workspace_size(N, V, D, int(bool(dh)) + 2 * int(bool(dW))))
+    ws = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def linear_cross_entropy(h, W, tokens, rows=None, ws=None):
+    """loss, lse [...] f32: the softmax cross entropy of tokens [...] i32 (-1:
+    none) under the logits h W^T of hidden states h [..., D] and a head W [V, D]
+    (bfloat16 or float16; rows a fixed distance apart, W's on 16 bytes; D % 8 ==
+    0), which are formed in pieces of the vocabulary and not kept.
+    rows [B] i32, with h [B, R, D]: only the first rows[b] rows of b count.  Rows
+    that do not count, or have no token, cost next to nothing and give zeros.
+    ws: a linear_ce_workspace to keep (and read_status of); by default one is
+    allocated for the call and errors are recorded in head_status."""
+    L = _load()
+    dev, lead, N, R, V, D, h_stride, W_stride, dt = _hidden_args(h, W, tokens, rows)
+    loss, lse = (torch.empty(lead, dtype=torch.float32, device=dev) for _ in range(2))
+    ws, status = _hidden_workspace(ws, N, V, D, 0, dev)
+    _launch(L.dspark_linear_cross_entropy, "linear_cross_entropy", dev, h.data_ptr(), h_stride, W.data_ptr(), W_stride, dt,
+            tokens.data_ptr(), _address(rows), N, R, V, D, loss.data_ptr(), lse.data_ptr(), _address(status),
+            ws.data_ptr(), ws.numel())
+    return loss, lse
+
+
+def linear_cross_entropy_backward(h, W, tokens, lse, g_loss, g_lse=None, rows=None, dh=True, dW=True, ws=None):
+    """dh [..., D] and dW [V, D], of h's type (None where dh or dW is False), from
+    the lse of linear_cross_entropy and the upstream gradients g_loss and g_lse
+    [...] f32 (None: 0); the other arguments as for that call."""
+    L = _load()
+    dev, lead, N, R, V, D, h_stride, W_stride, dt = _hidden_args(h, W, tokens, rows)
+    _row_vector(_need(lse, "lse"), "lse", lead, dev)
+    _row_vector(_need(g_loss, "g_loss"), "g_loss", lead, dev)
+    _row_vector(g_lse, "g_lse", lead, dev)
+    if not dh and not dW:
+        raise ValueError("one of dh and dW is needed")
+    ws, status = _hidden_workspace(ws, N, V, D, int(bool(dh)) + 2 * int(bool(dW)), dev)
+    dh = torch.empty(h.shape, dtype=h.dtype, device=dev) if dh else None
+    dW = torch.empty((V, D), dtype=W.dtype, device=dev) if dW else None
+    _launch(L.dspark_linear_cross_entropy_backward, "linear_cross_entropy_backward", dev, h.data_ptr(), h_stride,
+            W.data_ptr(), W_stride, dt, tokens.data_ptr(), _address(rows), lse.data_ptr(), g_loss.data_ptr(),
+            _address(g_lse), N, R, V, D, _address(dh), _address(dW), _address(status), ws.data_ptr(), ws.numel())
+    return dh, dW
 
 
 class RoundOutputs:

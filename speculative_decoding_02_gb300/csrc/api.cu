@@ -90,6 +90,21 @@ int top_checks(int N, int V, int top_k, const float* logp_out, const float* entr
   return DSPARK_OK;
 }
 
+// The checks of a call on N rows of hidden states under a head of V rows.
+int hidden_checks(const void* h, int64_t h_stride, const void* W, int64_t W_stride, int dtype, const int32_t* tokens,
+                  int N, int R, int V, int D) {
+  if (dtype != DSPARK_F32 && dtype != DSPARK_BF16 && dtype != DSPARK_F16) return DSPARK_ERR_INVALID;
+  if (N < 0 || R <= 0 || V <= 0 || D <= 0) return DSPARK_ERR_INVALID;
+  if (dtype == DSPARK_F32 || N > kMaxHiddenRows || V > kMaxRowV || D > kMaxHidden || D % 8 != 0)
+    return DSPARK_ERR_UNSUPPORTED;
+  if (N % R != 0 || (N > 1 && h_stride < D) || (V > 1 && W_stride < D)) return DSPARK_ERR_INVALID;
+  if (N == 0) return DSPARK_OK;
+  if (!h || !W || !tokens || !aligned(h, 2)) return DSPARK_ERR_INVALID;
+  // (the head is read by tensor copies, whose rows start on 16 bytes)
+  if (!aligned(W, 16) || (V > 1 && (W_stride % 8 != 0 || W_stride >= (1ll << 38)))) return DSPARK_ERR_INVALID;
+  return DSPARK_OK;
+}
+
 int distill_checks(const void* logits, int dtype, int64_t row_stride, const int32_t* top_idx, const float* top_val,
                    int N, int R, int V, int K, float temperature, const void* dlogits, int gdtype) {
   DSPARK_TRY(rows_checks(logits, dtype, row_stride, N, R, V));
@@ -467,6 +482,51 @@ int dspark_distill_loss_backward(const void* logits, int dtype, int64_t row_stri
   DistillArgs a{logits, dtype, row_stride, top_idx, top_val, teacher_lse, g, lens, N, R, V, K, temperature,
                 1.f / temperature, inverse_low(temperature), nullptr, nullptr, stats, dlogits_out, gdtype};
   return cuda_status(launch_distill(a, (cudaStream_t)stream));
+}
+
+size_t dspark_linear_ce_workspace_size(int N, int V, int D, int what) {
+  if (N <= 0 || V <= 0 || D <= 0 || N > kMaxHiddenRows || V > kMaxRowV || D > kMaxHidden || D % 8 != 0 || what < 0 ||
+      what > 3)
+    return 0;
+  return linear_ce_workspace_bytes(N, V, D, what != 0, (what & DSPARK_WANT_DH) != 0);
+}
+
+int dspark_linear_cross_entropy(const void* h, int64_t h_stride, const void* W, int64_t W_stride, int dtype,
+                                const int32_t* tokens, const int32_t* lens, int N, int R, int V, int D,
+                                float* loss_out, float* lse_out, int32_t* status, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  DSPARK_TRY(hidden_checks(h, h_stride, W, W_stride, dtype, tokens, N, R, V, D));
+  if (N == 0) return DSPARK_OK;
+  if (!loss_out || !lse_out || !aligned(status, 4)) return DSPARK_ERR_INVALID;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < linear_ce_workspace_bytes(N, V, D, false, false))
+    return DSPARK_ERR_WORKSPACE;
+  LinearCeArgs a{};
+  a.h = h; a.h_stride = N > 1 ? h_stride : D; a.W = W; a.W_stride = V > 1 ? W_stride : D; a.dtype = dtype;
+  a.tokens = tokens; a.lens = lens; a.N = N; a.R = R; a.V = V; a.D = D;
+  a.loss = loss_out; a.lse_out = lse_out;
+  a.ws = workspace; a.status = status ? status : ws_ptr<int>(workspace, 0);
+  return cuda_status(launch_linear_ce(a, (cudaStream_t)stream));
+}
+
+int dspark_linear_cross_entropy_backward(const void* h, int64_t h_stride, const void* W, int64_t W_stride, int dtype,
+                                         const int32_t* tokens, const int32_t* lens, const float* lse,
+                                         const float* g_loss, const float* g_lse, int N, int R, int V, int D,
+                                         void* dh_out, void* dW_out, int32_t* status, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+  DSPARK_TRY(hidden_checks(h, h_stride, W, W_stride, dtype, tokens, N, R, V, D));
+  if (!aligned(dh_out, 16) || !aligned(dW_out, 16) || !aligned(status, 4)) return DSPARK_ERR_INVALID;
+  if (N == 0)   // no rows: a gradient of zeros
+    return dW_out ? cuda_status(cudaMemsetAsync(dW_out, 0, (size_t)V * D * 2, (cudaStream_t)stream)) : DSPARK_OK;
+  if (!lse || !g_loss || (!dh_out && !dW_out)) return DSPARK_ERR_INVALID;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < linear_ce_workspace_bytes(N, V, D, true, dh_out != nullptr))
+    return DSPARK_ERR_WORKSPACE;
+  LinearCeArgs a{};
+  a.h = h; a.h_stride = N > 1 ? h_stride : D; a.W = W; a.W_stride = V > 1 ? W_stride : D; a.dtype = dtype;
+  a.tokens = tokens; a.lens = lens; a.N = N; a.R = R; a.V = V; a.D = D;
+  a.lse_in = lse; a.g_loss = g_loss; a.g_lse = g_lse; a.dh = dh_out; a.dW = dW_out;
+  a.ws = workspace; a.status = status ? status : ws_ptr<int>(workspace, 0);
+  return cuda_status(launch_linear_ce_backward(a, (cudaStream_t)stream));
 }
 
 int dspark_selftest_wait_timeout(int mode, void* workspace, size_t workspace_bytes, void* stream) {

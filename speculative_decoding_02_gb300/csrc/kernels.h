@@ -296,4 +296,32 @@ struct DistillArgs {
 };
 cudaError_t launch_distill(const DistillArgs& a, cudaStream_t stream);
 
+// Cross entropy of hidden states under an output head, and its gradients: N
+// rows of D values of a 16-bit type, in groups of R as above.
+constexpr int kMaxHiddenRows = 1 << 20;
+constexpr int kMaxHidden = 1 << 14;   // D
+
+struct LinearCeArgs {
+  const void* h;           // [N] rows of D
+  long long h_stride;
+  const void* W;           // [V] rows of D
+  long long W_stride;
+  int dtype;               // DSPARK_BF16 or DSPARK_F16
+  const int32_t* tokens;   // [N], -1: none
+  const int32_t* lens;
+  int N, R, V, D;
+  float* loss;             // forward: [N] each
+  float* lse_out;
+  const float* lse_in;     // backward: [N] each
+  const float* g_loss;
+  const float* g_lse;      // or null: 0
+  void* dh;                // [N][D] or null
+  void* dW;                // [V][D] or null
+  int* status;
+  void* ws;                // linear_ce_workspace_bytes
+};
+size_t linear_ce_workspace_bytes(int N, int V, int D, bool backward, bool want_dh);
+cudaError_t launch_linear_ce(const LinearCeArgs& a, cudaStream_t stream);
+cudaError_t launch_linear_ce_backward(const LinearCeArgs& a, cudaStream_t stream);
+
 }  // namespace dspark

@@ -1,0 +1,780 @@
+// Softmax cross entropy of hidden states under an output head, in pieces of the
+// vocabulary, without keeping the logits, and its gradients: the loss a draft's
+// hidden states are trained with ("[DeepSeek-6] DSpark" blog, section 9).  For
+// the rows n that count, z = h W^T [N, V], t the row's token:
+//
+//   loss:      lse = log sum_v exp z_v,  loss = lse - z_t
+//   gradients: s_v = (g_loss + g_lse) exp(z_v - lse) - g_loss 1[v = t]
+//              dh = s W,  dW = s^T h
+//
+// Four products of 2 N V D operations (the gradients form z again), bound by the
+// tensor cores as soon as there are a few hundred rows and by the read of W below.
+// The rows that count are gathered first, so the others cost nothing.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "gemm_tc.cuh"
+
+namespace dspark {
+namespace {
+
+using namespace gemm;
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct Counts {
+  int n;            // rows that count
+  int splits;       // parts of dh
+  float scale;      // of the slopes, a power of two
+  float inv_scale;
+};
+
+// A row that counts, for its slopes.
+struct __align__(16) RowInfo {
+  float lse2;       // lse log2 e
+  float up, down;   // scale (g_loss + g_lse), scale g_loss
+  int token;
+};
+
+__host__ __device__ constexpr long long ceil_to(long long x, long long m) { return (x + m - 1) / m * m; }
+
+// ---------------------------------------------------------------------------
+// which rows count, and the rows themselves
+// ---------------------------------------------------------------------------
+struct ScanParams {
+  const int32_t* tokens;
+  const int32_t* lens;
+  int N, R, V;
+  float* loss;              // forward: written where a row does not count
+  float* lse;
+  const float* g_loss;      // backward
+  const float* g_lse;
+  bool half;                // fp16: the slopes are scaled
+  int dt, kx, wt, units, max_splits;
+  Counts* counts;
+  int32_t* list;            // [N]: the rows that count, in order
+  int32_t* slot;            // [N]: a row's place there; -1 none, -2 none and its token is out of range
+  int* status;
+};
+
+// The parts of K that give dh's tiles and dW's the earliest end: a tile takes
+// its steps of K and about 4 steps' time for its epilogue.
+__device__ int choose_splits(int mt, int dt, int kx, int wt, int n, int units, int most) {
+  const int tx = mt * dt, tw = wt * dt, kw = div_up(n, kStep);
+  int best = 1;
+  long long best_cost = -1;
+  for (int s = 1; s <= most; ++s) {
+    const long long cx = div_up(kx, s) + 4;
+    const long long waves = div_up(tx * s, units) * cx;
+    const long long all = ((long long)tx * s * cx + (long long)tw * (kw + 4) + units - 1) / units;
+    const long long cost = waves > all ? waves : all;
+    if (best_cost < 0 || cost < best_cost) best = s, best_cost = cost;
+  }
+  return best;
+}
+
+constexpr int kScanThreads = 1024, kScanEach = 8;
+
+// One block: the rows that count, in order.
+__global__ void __launch_bounds__(kScanThreads) ce_scan(const ScanParams p) {
+  __shared__ int sums[32], before[32];
+  __shared__ float most[32];
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int base = 0;
+  float g = 0.f;
+  for (long long n0 = 0; n0 < p.N; n0 += kScanThreads * kScanEach) {
+    const long long first = n0 + (long long)threadIdx.x * kScanEach;
+    unsigned on = 0;
+#pragma unroll
+    for (int j = 0; j < kScanEach; ++j) {
+      const long long n = first + j;
+      if (n >= p.N) break;
+      const int t = p.tokens[n];
+      const bool in = p.lens == nullptr || (int)(n % p.R) < p.lens[n / p.R];
+      if (in && t >= 0 && t < p.V) {
+        on |= 1u << j;
+        if (p.g_loss) {
+          const float a = p.g_loss[n], b = p.g_lse ? a + p.g_lse[n] : a;
+          g = fmaxf(g, fmaxf(fabsf(a), fabsf(b)));
+        }
+      } else {
+        const bool bad = in && t != -1;
+        if (bad) record_status(p.status, DSPARK_ERR_INVALID);
+        if (p.loss) {
+          p.loss[n] = bad ? __int_as_float(0x7fc00000) : 0.f;
+          p.lse[n] = 0.f;
+        }
+        if (p.slot) p.slot[n] = bad ? -2 : -1;
+      }
+    }
+    const int mine = __popc(on);
+    int incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+      int v = sums[lane];
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int u = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += u;
+      }
+      before[lane] = v;
+    }
+    __syncthreads();
+    int at = base + incl - mine + (warp > 0 ? before[warp - 1] : 0);
+    for (; on != 0; on &= on - 1, ++at) {
+      const long long n = first + __ffs(on) - 1;
+      p.list[at] = (int)n;
+      if (p.slot) p.slot[n] = at;
+    }
+    base += before[31];
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, d));
+  if (lane == 0) most[warp] = g;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 32; ++w) g = fmaxf(g, most[w]);
+    Counts c;
+    c.n = base;
+    c.splits = p.dt > 0 ? choose_splits(div_up(base, 256), p.dt, p.kx, p.wt, base, p.units, p.max_splits) : 1;
+    // fp16 holds 2^-24 to 65504: the slopes, at most twice the largest |g|, go
+    // up to 2^15, so that a probability of 2^-29 keeps its digits (bf16 has fp32's range)
+    int e = 0;
+    if (p.half && g > 0.f && g < INFINITY) {
+      frexpf(g, &e);   // g < 2^e
+      e = max(-100, min(100, 14 - e));
+    }
+    c.scale = ldexpf(1.f, e);
+    c.inv_scale = ldexpf(1.f, -e);
+    *p.counts = c;
+  }
+}
+
+struct GatherParams {
+  const unsigned short* h;
+  const unsigned short* W;
+  long long h_stride, W_stride;
+  const int32_t* tokens;
+  const int32_t* list;
+  const Counts* counts;
+  int D;
+  bool vec;                 // rows of h start on 16 bytes
+  unsigned short* rows;     // [..][D]
+  float* logit;             // forward: the token's logit
+  const float* lse;         // backward
+  const float* g_loss;
+  const float* g_lse;
+  RowInfo* info;
+};
+
+template <bool kBf16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (kBf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  else return __half22float2(*reinterpret_cast<__half2*>(&w));
+}
+
+template <bool kBf16>
+__device__ __forceinline__ float dot8(uint4 a, uint4 b, float s) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 u = unpack2<kBf16>(x[j]), v = unpack2<kBf16>(y[j]);
+    s = fmaf(u.x, v.x, s);
+    s = fmaf(u.y, v.y, s);
+  }
+  return s;
+}
+
+// A block per gathered row: the row, dense, and its token's logit (in fp32 from
+// the row itself: a loss is the difference of two logits that may be near each
+// other) or what its slopes need.  Rows up to the next multiple of 256 are zeros.
+template <bool kBf16>
+__global__ void __launch_bounds__(128) ce_gather(const GatherParams p) {
+  __shared__ float sums[4];
+  pdl_trigger();
+  pdl_wait();
+  const int j = blockIdx.x, n = p.counts->n;
+  if (j >= ceil_to(n, 256)) return;
+  uint4* out = reinterpret_cast<uint4*>(p.rows + (size_t)j * p.D);
+  const int chunks = p.D / 8;
+  if (j >= n) {
+    for (int c = threadIdx.x; c < chunks; c += 128) out[c] = make_uint4(0, 0, 0, 0);
+    if (p.info && threadIdx.x == 0) p.info[j] = RowInfo{0.f, 0.f, 0.f, -1};
+    return;
+  }
+  const int row = p.list[j], t = p.tokens[row];
+  const unsigned short* src = p.h + (size_t)row * p.h_stride;
+  const uint4* w = reinterpret_cast<const uint4*>(p.W + (size_t)t * p.W_stride);
+  float s = 0.f;
+  for (int c = threadIdx.x; c < chunks; c += 128) {
+    uint4 v;
+    if (p.vec) {
+      v = reinterpret_cast<const uint4*>(src)[c];
+    } else {
+      uint32_t x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = src[8 * c + 2 * e] | (uint32_t)src[8 * c + 2 * e + 1] << 16;
+      v = make_uint4(x[0], x[1], x[2], x[3]);
+    }
+    out[c] = v;
+    if (p.logit) s = dot8<kBf16>(v, __ldg(w + c), s);
+  }
+  if (p.logit) {
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) p.logit[j] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+  } else if (threadIdx.x == 0) {
+    const float g = p.g_loss[row], scale = p.counts->scale;
+    p.info[j] = RowInfo{p.lse[row] * kLog2e, scale * (p.g_lse ? g + p.g_lse[row] : g), scale * g, t};
+  }
+}
+
+// ---------------------------------------------------------------------------
+// forward
+// ---------------------------------------------------------------------------
+
+// z = h W^T by tiles; of a tile's rows, the maximum (in units of log 2) and the
+// sum of 2^(z log2 e - maximum) of its 256 columns.
+struct LossTiles {
+  CUtensorMap h, w;
+  static constexpr bool kPair = true;
+  static constexpr int kN = 256, kBoxBytes = 0, kExtraBytes = 2 * 4 * kRows * 8;
+  using Counts = int;
+  int* status;
+  bool bf16;
+  int chunk;
+  const dspark::Counts* live;
+  float2* part;          // [vocabulary tiles][ld]
+  long long ld;
+  int V, steps, vtiles;
+
+  __device__ int counts() const { return live->n; }
+  __device__ bool tile(int n, int unit, int units, int i, Tile& t) const {
+    // neighbouring units take the row tiles of the same columns, so that W
+    // comes once from HBM
+    const int mt = div_up(n, 256);
+    const long long u = (long long)i * units + unit;
+    if (u >= (long long)mt * vtiles) return false;
+    t.m0 = (int)(u % mt) * 256;
+    t.n0 = (int)(u / mt) * 256;
+    t.steps = steps;
+    t.a_mn = t.b_mn = false;
+    return true;
+  }
+  __device__ Src a(const Tile& t, int k) const { return Src{&h, t.m0, k * kStep}; }
+  __device__ Src b(const Tile& t, int k) const { return Src{&w, t.n0, k * kStep}; }
+
+  __device__ void epilogue(const Epi& e, const Tile& t, float (&z)[64]) const {
+    const int left = V - (t.n0 + e.col);
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 64; ++j) {
+      if (j >= left) z[j] = -INFINITY;
+      m = fmaxf(m, z[j]);
+    }
+    // (a row of -inf, or a quarter past the vocabulary's end: a sum of zeros)
+    m = m == -INFINITY ? m : m * kLog2e;
+    const float at = m == -INFINITY ? 0.f : m;
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < 64; ++j) s += ex2_approx(fmaf(z[j], kLog2e, -at));
+    // the four warps of these rows; two tables in turn, so that one barrier a tile is enough
+    float2* table = reinterpret_cast<float2*>(e.extra) + (e.n & 1) * 4 * kRows;
+    const int r = e.q * 32 + e.lane;
+    table[e.h * kRows + r] = make_float2(m, s);
+    named_bar_sync(1 + e.q, 128);
+    if (e.h == 0) {
+      float2 v[4];
+      float M = -INFINITY, S = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = table[i * kRows + r];
+        M = fmaxf(M, v[i].x);
+      }
+      const float top = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S += v[i].y * ex2_approx(v[i].x - top);
+      part[(size_t)(t.n0 / 256) * ld + t.m0 + e.row] = make_float2(M, S);
+    }
+  }
+};
+
+struct CombineParams {
+  const float2* part;
+  long long ld;
+  int vtiles;
+  const Counts* counts;
+  const float* logit;
+  const int32_t* list;
+  float* loss;
+  float* lse;
+};
+
+// 8 rows a block, 32 threads' tiles each.
+__global__ void __launch_bounds__(256) ce_combine(const CombineParams p) {
+  __shared__ float2 sums[32][8];
+  pdl_trigger();
+  pdl_wait();
+  const int r = threadIdx.x & 7, g = threadIdx.x >> 3, n = p.counts->n;
+  const int j = blockIdx.x * 8 + r;
+  if (blockIdx.x * 8 >= n) return;
+  float m = -INFINITY, s = 0.f;
+#pragma unroll 4
+  for (int v = g; v < p.vtiles; v += 32) {
+    const float2 x = p.part[(size_t)v * p.ld + j];
+    const float M = fmaxf(m, x.x), top = M == -INFINITY ? 0.f : M;
+    s = s * exp2f(m - top) + x.y * exp2f(x.x - top);
+    m = M;
+  }
+  sums[g][r] = make_float2(m, s);
+  __syncthreads();
+  if (threadIdx.x >= 8 || j >= n) return;
+  float M = -INFINITY, S = 0.f;
+  for (int i = 0; i < 32; ++i) M = fmaxf(M, sums[i][r].x);
+  const float top = M == -INFINITY ? 0.f : M;
+  for (int i = 0; i < 32; ++i) S += sums[i][r].y * exp2f(sums[i][r].x - top);
+  const int row = p.list[j];
+  const float l = log2f(S);
+  p.lse[row] = (M + l) * kLn2;
+  p.loss[row] = (fmaf(-p.logit[j], kLog2e, M) + l) * kLn2;
+}
+
+// ---------------------------------------------------------------------------
+// backward
+// ---------------------------------------------------------------------------
+
+// The slopes of a piece of the vocabulary, rounded to the operands' type for the
+// products that follow (a relative 2^-9 of each in bf16, 2^-12 in fp16, which
+// averages out over a sum; of the token's own, which is most of dh, the rounding
+// is kept apart and added to dh).
+struct SlopeTiles {
+  CUtensorMap h, w, out;
+  static constexpr bool kPair = true;
+  static constexpr int kN = 256, kBoxBytes = kStoreBox, kExtraBytes = 0;
+  using Counts = int;
+  int* status;
+  bool bf16;
+  int chunk;
+  const dspark::Counts* live;
+  const RowInfo* info;
+  float* corr;           // what the rounding of the token's slope took
+  int rows;              // of the slopes' matrix
+  int v0, V, steps, vtiles;
+
+  __device__ int counts() const { return live->n; }
+  __device__ bool tile(int n, int unit, int units, int i, Tile& t) const {
+    const int mt = div_up(n, 256);
+    const long long u = (long long)i * units + unit;
+    if (u >= (long long)mt * vtiles) return false;
+    t.m0 = (int)(u % mt) * 256;
+    t.n0 = (int)(u / mt) * 256;
+    t.steps = steps;
+    t.a_mn = t.b_mn = false;
+    return true;
+  }
+  __device__ Src a(const Tile& t, int k) const { return Src{&h, t.m0, k * kStep}; }
+  __device__ Src b(const Tile& t, int k) const { return Src{&w, v0 + t.n0, k * kStep}; }
+
+  __device__ void epilogue(const Epi& e, const Tile& t, float (&z)[64]) const {
+    const RowInfo r = info[t.m0 + e.row];
+    const int first = v0 + t.n0 + e.col, left = V - first, at = r.token - first;
+    uint32_t w[32];
+#pragma unroll
+    for (int j = 0; j < 64; j += 2) {
+      float x[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x[i] = j + i < left ? ex2_approx(fmaf(z[j + i], kLog2e, -r.lse2)) * r.up : 0.f;
+        if (j + i == at) x[i] -= r.down;
+      }
+      float2 back;
+      if (bf16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x[0], x[1]);
+        w[j / 2] = *reinterpret_cast<const uint32_t*>(&v);
+        back = unpack2<true>(w[j / 2]);
+      } else {
+        const __half2 v = __floats2half2_rn(x[0], x[1]);
+        w[j / 2] = *reinterpret_cast<const uint32_t*>(&v);
+        back = unpack2<false>(w[j / 2]);
+      }
+      if (j == at) corr[t.m0 + e.row] = x[0] - back.x;
+      if (j + 1 == at) corr[t.m0 + e.row] = x[1] - back.y;
+    }
+    store_16bit(e, &out, w, t.n0 + e.col, vtiles * 256, t.m0 + e.row0, rows);
+  }
+};
+
+// dh += s W and dW = s^T h of a piece, in one launch: first dh's tiles, in parts
+// of K, which are long, then dW's, dealt so that all units end at about the
+// same time.
+struct GradTiles {
+  CUtensorMap s_k, s_mn, w, h, dh, dW;
+  static constexpr bool kPair = true;
+  static constexpr int kN = 256, kBoxBytes = kStoreBox, kExtraBytes = 0;
+  struct Counts {
+    int mt, splits, kw, tx, tw, shared;
+    float inv_scale;
+  };
+  int* status;
+  bool bf16;
+  int chunk;
+  const dspark::Counts* live;
+  int rows;              // of the slopes' matrix
+  int v0, V, kx, wt;     // the piece: first column, of V; steps of K and (for dW) tiles of 256
+  int D, dt;             // tiles of D
+  bool want_dh, add;     // add: a piece came before
+
+  __device__ Counts counts() const {
+    const dspark::Counts l = *live;
+    Counts c;
+    c.mt = div_up(l.n, 256);
+    c.splits = l.splits;
+    c.kw = div_up(l.n, kStep);
+    c.tx = want_dh ? c.mt * dt * c.splits : 0;
+    c.tw = wt * dt;
+    c.inv_scale = l.inv_scale;
+    // dW tiles that every unit takes: those with one more of dh's take no
+    // more than these (see tile)
+    const int units = gridDim.x >> 1;
+    const float cx = (float)(div_up(kx, c.splits) + 4), cw = (float)(c.kw + 4);
+    const float all = (c.tx * cx + c.tw * cw) / units;
+    const int most = div_up(c.tx, units);
+    c.shared = min(max((int)((all - most * cx) / cw + 0.5f), 0), c.tw / units);
+    return c;
+  }
+  __device__ bool tile(const Counts& c, int unit, int units, int i, Tile& t) const {
+    const int more = c.tx % units;                      // the first `more` units take one more of dh's
+    const int own = c.tx / units + (unit < more ? 1 : 0);
+    if (i < own) {
+      const int u = i * units + unit, tiles = c.mt * dt;
+      t.kind = 0;
+      t.part = u / tiles;
+      const int each = div_up(kx, c.splits);
+      t.m0 = (u % tiles) % c.mt * 256;
+      t.n0 = (u % tiles) / c.mt * 256;
+      t.k0 = t.part * each;
+      t.steps = max(0, min(each, kx - t.k0));
+      t.a_mn = false;
+      t.b_mn = true;
+      return true;
+    }
+    i -= own;
+    int u;
+    if (i < c.shared) {
+      u = i * units + unit;
+    } else {
+      if (unit < more) return false;
+      u = c.shared * units + (i - c.shared) * (units - more) + unit - more;
+    }
+    if (u >= c.tw) return false;
+    t.kind = 1;
+    t.part = 0;
+    t.m0 = u / dt * 256;
+    t.n0 = u % dt * 256;
+    t.steps = c.kw;
+    t.a_mn = t.b_mn = true;
+    return true;
+  }
+  __device__ Src a(const Tile& t, int k) const {
+    if (t.kind == 1) return Src{&s_mn, t.m0, k * kStep};
+    return Src{&s_k, t.m0, (t.k0 + k) * kStep};
+  }
+  __device__ Src b(const Tile& t, int k) const {
+    if (t.kind == 1) return Src{&h, t.n0, k * kStep};
+    return Src{&w, t.n0, v0 + (t.k0 + k) * kStep};
+  }
+
+  __device__ void epilogue(const Epi& e, const Tile& t, float (&v)[64]) const {
+    if (t.kind == 0) {
+      store_fp32(e, &dh, v, t.n0 + e.col, D, t.m0 + e.row0, rows, t.part, add);
+      return;
+    }
+    const float scale = live->inv_scale;
+    uint32_t w[32];
+#pragma unroll
+    for (int j = 0; j < 64; j += 2) {
+      if (bf16) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(v[j] * scale, v[j + 1] * scale);
+        w[j / 2] = *reinterpret_cast<const uint32_t*>(&x);
+      } else {
+        const __half2 x = __floats2half2_rn(v[j] * scale, v[j + 1] * scale);
+        w[j / 2] = *reinterpret_cast<const uint32_t*>(&x);
+      }
+    }
+    store_16bit(e, &dW, w, t.n0 + e.col, D, v0 + t.m0 + e.row0, V);
+  }
+};
+
+struct FinishParams {
+  const float* part;        // [splits][rows][D]
+  long long rows;
+  const Counts* counts;
+  const int32_t* slot;
+  const float* corr;
+  const RowInfo* info;
+  const unsigned short* W;
+  long long W_stride;
+  int D;
+  unsigned short* dh;       // [N][D]
+};
+
+// dh of a row: the sum of its parts and what the rounding of its token's slope took.
+template <bool kBf16>
+__global__ void __launch_bounds__(128) ce_finish(const FinishParams p) {
+  pdl_trigger();
+  pdl_wait();
+  const int j = p.slot[blockIdx.x];
+  uint4* out = reinterpret_cast<uint4*>(p.dh + (size_t)blockIdx.x * p.D);
+  const int chunks = p.D / 8;
+  if (j < 0) {
+    const uint32_t v = j == -2 ? 0x7fff7fffu : 0u;   // NaN in either type
+    for (int c = threadIdx.x; c < chunks; c += 128) out[c] = make_uint4(v, v, v, v);
+    return;
+  }
+  const Counts counts = *p.counts;
+  const float corr = p.corr[j];
+  const uint4* w = reinterpret_cast<const uint4*>(p.W + (size_t)p.info[j].token * p.W_stride);
+  for (int c = threadIdx.x; c < chunks; c += 128) {
+    float a[8];
+    const uint4 x = __ldg(w + c);
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 u = unpack2<kBf16>(xs[e]);
+      a[2 * e] = corr * u.x;
+      a[2 * e + 1] = corr * u.y;
+    }
+    for (int s = 0; s < counts.splits; ++s) {
+      const float4* q = reinterpret_cast<const float4*>(p.part + ((size_t)s * p.rows + j) * p.D + 8 * c);
+      const float4 u = q[0], v = q[1];
+      a[0] += u.x; a[1] += u.y; a[2] += u.z; a[3] += u.w;
+      a[4] += v.x; a[5] += v.y; a[6] += v.z; a[7] += v.w;
+    }
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float lo = a[2 * e] * counts.inv_scale, hi = a[2 * e + 1] * counts.inv_scale;
+      if constexpr (kBf16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        o[e] = *reinterpret_cast<const uint32_t*>(&v);
+      } else {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        o[e] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+    }
+    out[c] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// workspace
+// ---------------------------------------------------------------------------
+constexpr long long kPieceBytes = 256ll << 20;   // of the slopes
+constexpr long long kPartBytes = 256ll << 20;    // of dh's parts
+constexpr int kMaxSplits = 16;
+
+struct Layout {
+  long long rows;                  // N, in whole row tiles
+  size_t counts, list, slot, info, logit, corr, h, part, slopes, dh, total;
+  int vtiles;                      // of the vocabulary
+  int piece;                       // columns of a piece (a multiple of 256)
+  int splits;                      // parts of dh at most
+};
+
+Layout layout(int N, int V, int D, bool backward, bool want_dh) {
+  Layout l{};
+  l.rows = ceil_to(N, 256);
+  l.vtiles = div_up(V, 256);
+  size_t at = 256;                 // the status word
+  auto take = [&](size_t bytes) {
+    const size_t a = at;
+    at += align256(bytes);
+    return a;
+  };
+  l.counts = take(sizeof(Counts));
+  l.list = take(4ull * N);
+  l.h = take(2ull * l.rows * D);
+  if (!backward) {
+    l.logit = take(4ull * N);
+    l.part = take(8ull * l.rows * l.vtiles);
+  } else {
+    l.slot = take(4ull * N);
+    l.info = take(16ull * l.rows);
+    l.corr = take(4ull * l.rows);
+    const long long most = std::max<long long>(256, kPieceBytes / (2 * l.rows) / 256 * 256);
+    const int pieces = (int)((V + most - 1) / most);
+    l.piece = (int)ceil_to((V + pieces - 1) / pieces, 256);
+    l.slopes = take(2ull * l.rows * l.piece);
+    if (want_dh) {
+      l.splits = (int)std::max<long long>(1, std::min<long long>(kMaxSplits, kPartBytes / (4 * l.rows * D)));
+      l.dh = take(4ull * l.splits * l.rows * D);
+    }
+  }
+  l.total = at;
+  return l;
+}
+
+}  // namespace
+
+size_t linear_ce_workspace_bytes(int N, int V, int D, bool backward, bool want_dh) {
+  return layout(N, V, D, backward, want_dh).total;
+}
+
+namespace {
+
+template <class K, class... A>
+cudaError_t small(K kern, long long grid, int block, cudaStream_t stream, const A&... args) {
+  return launch_pdl(kern, dim3((unsigned)grid), dim3((unsigned)block), 0, stream, args...);
+}
+
+#define CE_TRY(expr)                            \
+  do {                                          \
+    const cudaError_t _e = (expr);              \
+    if (_e != cudaSuccess) return _e;           \
+  } while (0)
+
+cudaError_t scan_and_gather(const LinearCeArgs& a, const Layout& l, char* ws, const ScanParams& s, GatherParams& g,
+                            cudaStream_t stream) {
+  ce_scan<<<1, kScanThreads, 0, stream>>>(s);
+  CE_TRY(cudaGetLastError());
+  g.h = static_cast<const unsigned short*>(a.h);
+  g.W = static_cast<const unsigned short*>(a.W);
+  g.h_stride = a.h_stride;
+  g.W_stride = a.W_stride;
+  g.tokens = a.tokens;
+  g.list = s.list;
+  g.counts = s.counts;
+  g.D = a.D;
+  g.vec = reinterpret_cast<uintptr_t>(a.h) % 16 == 0 && (a.N == 1 || a.h_stride % 8 == 0);
+  g.rows = reinterpret_cast<unsigned short*>(ws + l.h);
+  return small(a.dtype == DSPARK_BF16 ? ce_gather<true> : ce_gather<false>, l.rows, 128, stream, g);
+}
+
+ScanParams scan_params(const LinearCeArgs& a, const Layout& l, char* ws) {
+  ScanParams s{};
+  s.tokens = a.tokens;
+  s.lens = a.lens;
+  s.N = a.N; s.R = a.R; s.V = a.V;
+  s.half = a.dtype == DSPARK_F16;
+  s.counts = reinterpret_cast<Counts*>(ws + l.counts);
+  s.list = reinterpret_cast<int32_t*>(ws + l.list);
+  s.status = a.status;
+  return s;
+}
+
+}  // namespace
+
+cudaError_t launch_linear_ce(const LinearCeArgs& a, cudaStream_t stream) {
+  const Layout l = layout(a.N, a.V, a.D, false, false);
+  char* ws = static_cast<char*>(a.ws);
+  const bool bf16 = a.dtype == DSPARK_BF16;
+  ScanParams s = scan_params(a, l, ws);
+  s.loss = a.loss;
+  s.lse = a.lse_out;
+  GatherParams g{};
+  g.logit = reinterpret_cast<float*>(ws + l.logit);
+  CE_TRY(scan_and_gather(a, l, ws, s, g, stream));
+
+  LossTiles t{};
+  CE_TRY(map_16bit(g.rows, bf16, l.rows, a.D, a.D, kRows, &t.h));
+  CE_TRY(map_16bit(a.W, bf16, a.V, a.D, a.W_stride, kRows, &t.w));
+  t.status = a.status;
+  t.bf16 = bf16;
+  t.chunk = 8;
+  t.live = s.counts;
+  t.part = reinterpret_cast<float2*>(ws + l.part);
+  t.ld = l.rows;
+  t.V = a.V;
+  t.steps = div_up(a.D, kStep);
+  t.vtiles = l.vtiles;
+  const int units = max_units<LossTiles>();
+  if (units <= 0) return cudaErrorUnknown;
+  CE_TRY(launch(t, (int)std::min<long long>(units, l.rows / 256 * l.vtiles), stream));
+  CombineParams c{t.part, t.ld, l.vtiles, s.counts, g.logit, s.list, a.loss, a.lse_out};
+  return small(ce_combine, div_up(a.N, 8), 256, stream, c);
+}
+
+cudaError_t launch_linear_ce_backward(const LinearCeArgs& a, cudaStream_t stream) {
+  const bool want_dh = a.dh != nullptr, want_dW = a.dW != nullptr;
+  const Layout l = layout(a.N, a.V, a.D, true, want_dh);
+  char* ws = static_cast<char*>(a.ws);
+  const bool bf16 = a.dtype == DSPARK_BF16;
+  const int units = max_units<GradTiles>();
+  if (units <= 0) return cudaErrorUnknown;
+  ScanParams s = scan_params(a, l, ws);
+  s.slot = reinterpret_cast<int32_t*>(ws + l.slot);
+  s.g_loss = a.g_loss;
+  s.g_lse = a.g_lse;
+  s.dt = want_dh ? div_up(a.D, 256) : 0;
+  s.kx = l.piece / kStep;
+  s.wt = want_dW ? l.piece / 256 : 0;
+  s.units = units;
+  s.max_splits = l.splits;
+  GatherParams g{};
+  g.lse = a.lse_in;
+  g.g_loss = a.g_loss;
+  g.g_lse = a.g_lse;
+  g.info = reinterpret_cast<RowInfo*>(ws + l.info);
+  CE_TRY(scan_and_gather(a, l, ws, s, g, stream));
+
+  unsigned short* slopes = reinterpret_cast<unsigned short*>(ws + l.slopes);
+  SlopeTiles t{};
+  CE_TRY(map_16bit(g.rows, bf16, l.rows, a.D, a.D, kRows, &t.h));
+  CE_TRY(map_16bit(a.W, bf16, a.V, a.D, a.W_stride, kRows, &t.w));
+  CE_TRY(map_16bit(slopes, bf16, l.rows, l.piece, l.piece, kBoxRows, &t.out));
+  t.status = a.status;
+  t.bf16 = bf16;
+  t.chunk = 64;
+  t.live = s.counts;
+  t.info = g.info;
+  t.corr = reinterpret_cast<float*>(ws + l.corr);
+  t.rows = (int)l.rows;
+  t.V = a.V;
+  t.steps = div_up(a.D, kStep);
+
+  GradTiles d{};
+  CE_TRY(map_16bit(slopes, bf16, l.rows, l.piece, l.piece, kRows, &d.s_k));
+  CE_TRY(map_16bit(slopes, bf16, l.rows, l.piece, l.piece, kStep, &d.s_mn));
+  CE_TRY(map_16bit(a.W, bf16, a.V, a.D, a.W_stride, kStep, &d.w));
+  CE_TRY(map_16bit(g.rows, bf16, l.rows, a.D, a.D, kStep, &d.h));
+  d.dh = d.dW = d.w;
+  if (want_dh) CE_TRY(map_fp32(reinterpret_cast<float*>(ws + l.dh), l.splits, l.rows, a.D, &d.dh));
+  if (want_dW) CE_TRY(map_16bit(a.dW, bf16, a.V, a.D, a.D, kBoxRows, &d.dW));
+  d.status = a.status;
+  d.bf16 = bf16;
+  d.chunk = 64;
+  d.live = s.counts;
+  d.rows = (int)l.rows;
+  d.V = a.V;
+  d.D = a.D;
+  d.dt = div_up(a.D, 256);
+  d.want_dh = want_dh;
+
+  const long long mt = l.rows / 256;
+  for (int v0 = 0; v0 < a.V; v0 += l.piece) {
+    const int cols = std::min(l.piece, a.V - v0);
+    t.v0 = d.v0 = v0;
+    t.vtiles = div_up(cols, 256);
+    d.kx = div_up(cols, kStep);
+    d.wt = want_dW ? t.vtiles : 0;
+    d.add = v0 > 0;
+    CE_TRY(launch(t, (int)std::min<long long>(units, mt * t.vtiles), stream));
+    CE_TRY(launch(d, units, stream));
+  }
+  if (!want_dh) return cudaSuccess;
+  FinishParams f{reinterpret_cast<const float*>(ws + l.dh), l.rows, s.counts, s.slot, t.corr, g.info, g.W, a.W_stride, a.D,
+                 static_cast<unsigned short*>(a.dh)};
+  return small(bf16 ? ce_finish<true> : ce_finish<false>, a.N, 128, stream, f);
+}
+
+}  // namespace dspark
