@@ -606,6 +606,30 @@ int dspark_linear_cross_entropy_backward(const void* h, int64_t h_stride, const 
                                          size_t workspace_bytes, void* stream);
 
 /*
+ * An update orthogonalised by Newton-Schulz products, the step that the Muon
+ * optimiser takes for a weight matrix (of the heads above, or of a draft's layers):
+ * M [rows, cols] of type DSPARK_F32, DSPARK_BF16 or DSPARK_F16, rows row_stride
+ * values apart (>= cols; any element alignment), X = M / (|M|_F + eps), then
+ * `steps` (1..64) times
+ *   A = X X^T (X^T X where rows > cols),  X <- a X + (b A + c A A) X
+ *                                         (a X + X (b A + c A A)).
+ * Out: X [rows, cols], dense bf16, the rounded result of steps held to about
+ * 1e-3 of its 2-norm (fp16 operands, fp32 sums, X itself in 22 bits); it may not
+ * overlap M.  The shorter side is at most 16384, the longer 2^21 (rows or cols 0:
+ * nothing is done); a, b, c and eps >= 0 are finite.  Values of X, A or b A + c A A
+ * beyond 60 overflow to infinities: the coefficients have to keep the
+ * singular values, at most 1 at first, near 1.  A NaN or infinite value in M
+ * gives NaN or 0, as the formula does.
+ * status: the device word for errors (4-byte aligned, zero at first; NULL: the
+ * workspace's, its first word).  Workspace: dspark_newton_schulz_workspace_size
+ * bytes (0: unsupported sizes), 256-byte aligned.
+ */
+size_t dspark_newton_schulz_workspace_size(int rows, int cols);
+int dspark_newton_schulz(const void* M, int dtype, int64_t row_stride, int rows, int cols, int steps, float a, float b,
+                         float c, float eps, void* out, int32_t* status, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/*
  * The Markov draft without a caller workspace.  The method has no counterpart:
  * this entry serves callers that cannot allocate device memory at the time of
  * the call (an engine whose pool owns all of HBM, a plugin given no allocator,

@@ -15,8 +15,8 @@ forms):
   acceptance_label, sts_fit, token_logprobs, emitted_logprobs,
   token_logprobs_backward, distill_loss, distill_loss_backward,
   markov_logits, markov_head_backward, linear_cross_entropy,
-  linear_cross_entropy_backward
-head_status is the word in which the last four record errors without a workspace.
+  linear_cross_entropy_backward, newton_schulz
+head_status is the word in which the last five record errors without a workspace.
 """
 import ctypes
 import math
@@ -126,6 +126,10 @@ def _load():
     L.dspark_linear_cross_entropy_backward.argtypes = [vp, i64, vp, i64, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp,
                                                        vp, vp, vp, sz, vp]
     L.dspark_linear_cross_entropy_backward.restype = i32
+    L.dspark_newton_schulz_workspace_size.argtypes = [i32, i32]
+    L.dspark_newton_schulz_workspace_size.restype = sz
+    L.dspark_newton_schulz.argtypes = [vp, i32, i64, i32, i32, i32, f32, f32, f32, f32, vp, vp, vp, sz, vp]
+    L.dspark_newton_schulz.restype = i32
     L.dspark_read_status.argtypes = [vp, ctypes.POINTER(i32), vp]
     L.dspark_read_status.restype = i32
     L.dspark_selftest_wait_timeout.argtypes = [i32, vp, sz, vp]
@@ -633,7 +637,7 @@ _head_status = {}
 
 def head_status(device):
     """The status word of the calls of markov_logits, markov_head_backward and
-    linear_cross_entropy(_backward) on this device that were given no ws, for read_status.  (A call that is captured
+    linear_cross_entropy(_backward) and newton_schulz on this device that were given no ws, for read_status.  (A call that is captured
     into a graph before the device has one takes a word of its own, which
     nobody reads: call this first, or give it a ws.)"""
     dev = torch.device(device)
@@ -776,6 +780,43 @@ def linear_cross_entropy_backward(h, W, tokens, lse, g_loss, g_lse=None, rows=No
             W.data_ptr(), W_stride, dt, tokens.data_ptr(), _address(rows), lse.data_ptr(), g_loss.data_ptr(),
             _address(g_lse), N, R, V, D, _address(dh), _address(dW), _address(status), ws.data_ptr(), ws.numel())
     return dh, dW
+
+
+def newton_schulz_workspace(rows, cols, device):
+    """A workspace of newton_schulz for an update of these sizes."""
+    n = int(_load().dspark_newton_schulz_workspace_size(rows, cols))
+    ws = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def newton_schulz(update, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, ws=None):
+    """The update [rows, cols] (f32, bf16 or f16, rows a fixed distance apart)
+    orthogonalised: X = update / (its Frobenius norm + eps), then `steps` times
+    X <- a X + (b A + c A A) X with A = X X^T and (a, b, c) = coefficients; bfloat16.
+    The default coefficients, Muon's, bring the singular values to between 0.7 and
+    1.2 or so in five steps.  ws: a newton_schulz_workspace to keep (and
+    read_status of); by default one is allocated for the call and errors are
+    recorded in head_status."""
+    L = _load()
+    if update is not None and update.dim() != 2:
+        raise ValueError(f"update must be [rows, cols], got {list(update.shape)}")
+    if update is not None and update.is_cuda and update.numel() == 0:
+        return torch.empty(update.shape, dtype=torch.bfloat16, device=update.device)
+    dev, _, rows, _, cols, stride, dt = _row_args(update, None, "update")
+    a, b, c = coefficients
+    if not all(map(math.isfinite, (a, b, c, eps))) or eps < 0:
+        raise ValueError(f"coefficients and eps >= 0 must be finite, got {coefficients} and {eps}")
+    out = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    status = None
+    if ws is None:
+        n = int(L.dspark_newton_schulz_workspace_size(rows, cols))
+        ws, status = torch.empty(max(n, 256), dtype=torch.uint8, device=dev), _status_without_ws(dev)
+    else:
+        _need(ws, "ws", torch.uint8, dev)
+    _launch(L.dspark_newton_schulz, "newton_schulz", dev, update.data_ptr(), dt, stride, rows, cols, steps, a, b, c, eps,
+            out.data_ptr(), _address(status), ws.data_ptr(), ws.numel())
+    return out
 
 
 class RoundOutputs:

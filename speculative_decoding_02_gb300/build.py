@@ -17,7 +17,7 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libdspark.so")
 SOURCES = ["api.cu", "draft.cu", "draft_tc.cu", "label_tc.cu", "sched.cu", "verify.cu", "noalloc.cu", "sts.cu",
            "logprobs.cu", "distill.cu", "head_tc.cu",
-           "linear_ce.cu"]
+           "linear_ce.cu", "newton_schulz.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

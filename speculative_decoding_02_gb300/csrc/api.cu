@@ -3,6 +3,9 @@
 // and pointers before it enqueues anything and never synchronises the stream.
 #include <stdint.h>
 
+#include <algorithm>
+#include <cmath>
+
 #include "kernels.h"
 
 using namespace dspark;
@@ -527,6 +530,30 @@ int dspark_linear_cross_entropy_backward(const void* h, int64_t h_stride, const 
   a.lse_in = lse; a.g_loss = g_loss; a.g_lse = g_lse; a.dh = dh_out; a.dW = dW_out;
   a.ws = workspace; a.status = status ? status : ws_ptr<int>(workspace, 0);
   return cuda_status(launch_linear_ce_backward(a, (cudaStream_t)stream));
+}
+
+size_t dspark_newton_schulz_workspace_size(int rows, int cols) {
+  if (rows <= 0 || cols <= 0 || std::min(rows, cols) > kMaxNsSmall || std::max(rows, cols) > kMaxNsLarge) return 0;
+  return newton_schulz_workspace_bytes(rows, cols);
+}
+
+int dspark_newton_schulz(const void* M, int dtype, int64_t row_stride, int rows, int cols, int steps, float a, float b,
+                         float c, float eps, void* out, int32_t* status, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  if (dtype != DSPARK_F32 && dtype != DSPARK_BF16 && dtype != DSPARK_F16) return DSPARK_ERR_INVALID;
+  if (rows < 0 || cols < 0 || steps < 1) return DSPARK_ERR_INVALID;
+  if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c) || !(eps >= 0.f) || !std::isfinite(eps))
+    return DSPARK_ERR_INVALID;
+  if (rows == 0 || cols == 0) return DSPARK_OK;
+  if (std::min(rows, cols) > kMaxNsSmall || std::max(rows, cols) > kMaxNsLarge || steps > 64)
+    return DSPARK_ERR_UNSUPPORTED;
+  if (!M || !out || (rows > 1 && row_stride < cols)) return DSPARK_ERR_INVALID;
+  if (!aligned(M, dtype == DSPARK_F32 ? 4 : 2) || !aligned(out, 2) || !aligned(status, 4)) return DSPARK_ERR_INVALID;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < newton_schulz_workspace_bytes(rows, cols))
+    return DSPARK_ERR_WORKSPACE;
+  NewtonSchulzArgs n{M, dtype, rows > 1 ? row_stride : cols, rows, cols, steps, a, b, c, eps, out,
+                     status ? status : ws_ptr<int>(workspace, 0), workspace};
+  return cuda_status(launch_newton_schulz(n, (cudaStream_t)stream));
 }
 
 int dspark_selftest_wait_timeout(int mode, void* workspace, size_t workspace_bytes, void* stream) {

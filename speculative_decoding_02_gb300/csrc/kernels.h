@@ -324,4 +324,21 @@ size_t linear_ce_workspace_bytes(int N, int V, int D, bool backward, bool want_d
 cudaError_t launch_linear_ce(const LinearCeArgs& a, cudaStream_t stream);
 cudaError_t launch_linear_ce_backward(const LinearCeArgs& a, cudaStream_t stream);
 
+// An update orthogonalised by Newton-Schulz products.
+constexpr int kMaxNsSmall = 1 << 14;   // the shorter side
+constexpr int kMaxNsLarge = 1 << 21;
+
+struct NewtonSchulzArgs {
+  const void* M;           // [rows] rows of cols values
+  int dtype;
+  long long row_stride;
+  int rows, cols, steps;
+  float a, b, c, eps;
+  void* out;               // [rows][cols] bf16
+  int* status;
+  void* ws;                // newton_schulz_workspace_bytes
+};
+size_t newton_schulz_workspace_bytes(int rows, int cols);
+cudaError_t launch_newton_schulz(const NewtonSchulzArgs& a, cudaStream_t stream);
+
 }  // namespace dspark

@@ -1,4 +1,5 @@
-"""Host-side refusals of the cross entropy from hidden states: no GPU is touched."""
+"""Host-side refusals of the cross entropy from hidden states and of the
+orthogonalisation of an update: no GPU is touched."""
 import ctypes
 
 import pytest
@@ -77,3 +78,31 @@ def test_binding_refuses_host_tensors(lib):
         ds.linear_cross_entropy(h, W, t)
     with pytest.raises(ValueError):
         ds.linear_cross_entropy_backward(h, W, t, torch.zeros(2), torch.zeros(2))
+
+
+def test_newton_schulz_arguments(lib):
+    p = _fake()
+
+    def call(M=p, dtype=0, stride=30, rows=20, cols=30, steps=5, a=3.0, b=-4.0, c=2.0, eps=1e-7, out=p, status=None, ws=p,
+             n=BIG):
+        return lib.dspark_newton_schulz(M, dtype, stride, rows, cols, steps, a, b, c, eps, out, status, ws, n, None)
+
+    nan, inf = float("nan"), float("inf")
+    for kw in (dict(M=None), dict(M=_fake(0x10002)), dict(out=None), dict(out=_fake(0x10001)), dict(dtype=3), dict(dtype=-1),
+               dict(stride=29), dict(rows=-1), dict(cols=-1), dict(steps=0), dict(a=nan), dict(b=inf), dict(c=-inf),
+               dict(eps=-1e-9), dict(eps=nan), dict(eps=inf), dict(status=_fake(0x10002))):
+        assert call(**kw) == ds.ERR_INVALID, kw
+    for kw in (dict(rows=16385, cols=16385, stride=20000), dict(cols=(1 << 21) + 1, stride=1 << 22), dict(steps=65)):
+        assert call(**kw) == ds.ERR_UNSUPPORTED, kw
+    for kw in (dict(ws=None), dict(ws=_fake(0x10080)), dict(n=lib.dspark_newton_schulz_workspace_size(20, 30) - 1)):
+        assert call(**kw) == ds.ERR_WORKSPACE, kw
+    assert call(rows=0, M=None, out=None, ws=None) == ds.OK and call(cols=0, stride=0) == ds.OK
+    size = lib.dspark_newton_schulz_workspace_size
+    assert size(0, 4) == 0 and size(4, 0) == 0 and size(16385, 16385) == 0 and size(1, (1 << 21) + 1) == 0
+    # the largest: no overflow
+    assert 8 * 16384 * (1 << 21) < size(16384, 1 << 21) < (8 * 16384 * (1 << 21)) * 1.1
+
+
+def test_newton_schulz_refuses_host_tensors(lib):
+    with pytest.raises(ValueError):
+        ds.newton_schulz(torch.zeros(4, 4))
