@@ -27,6 +27,7 @@
 //     for all its threads; false when there is none
 //   Src a(tile, k), b(tile, k)          map and coordinates of step k
 //   void epilogue(Epi&, tile, acc)      every epilogue thread, converged
+//   void prefetch()                     of the tensor maps
 #pragma once
 
 #include <algorithm>
@@ -97,17 +98,32 @@ struct __align__(8) Bars {
 static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
 
 template <bool kPair>
-__device__ __forceinline__ void copy_box(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
-  const uint64_t policy = policy_evict_normal();
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
   if constexpr (kPair) {
-    tma_pair_2d(dst, map, c0, c1, bar, policy);
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
   } else {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
         : "memory");
   }
+}
+
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// mbar_wait of a converged warp.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
 }
 
 template <bool kPair>
@@ -130,12 +146,17 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
   unsigned char* boxes = smem + S::kStages * S::kStageBytes;
   unsigned char* extra = boxes + kEpiWarps * P::kBoxBytes;
   Bars* bars = reinterpret_cast<Bars*>(extra + P::kExtraBytes);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the same in a warp, which the compiler sees in a shuffle's result: the loops
+  // of the producer and the issuer are the whole warp's, on uniform registers, and
+  // one lane's the copies and MMAs.  A loop of one lane alone takes 600 cycles a
+  // step, more than the 512 of a pair's 256 x 256 x 64)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = kPair ? (int)cluster_rank() : 0;
   const int unit = kPair ? blockIdx.x >> 1 : blockIdx.x, units = kPair ? gridDim.x >> 1 : gridDim.x;
   volatile int* abort = &bars->abort;
 
   if (threadIdx.x == 0) {
+    p.prefetch();
     for (int s = 0; s < S::kStages; ++s) { mbar_init(&bars->full[s], 1); mbar_init(&bars->empty[s], 1); }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->acc_full[s], 1);
@@ -165,35 +186,41 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      uint32_t i = 0;
-      bool ok = true;
-      Tile t;
-      for (int n = 0; ok && p.tile(counts, unit, units, n, t); ++n) {
-        for (int k = 0; k < t.steps; ++k, ++i) {
-          const int s = i % S::kStages;
-          ok = mbar_wait(&bars->empty[s], ((i / S::kStages) & 1) ^ 1, abort, p.status);
-          if (!ok) break;
-          unsigned char* dst = smem + s * S::kStageBytes;
+    const uint32_t stages = smem_u32(smem);
+    uint32_t i = 0, s = 0, phase = 1;
+    bool ok = true;
+    Tile t;
+    for (int n = 0; ok && p.tile(counts, unit, units, n, t); ++n) {
+      for (int k = 0; k < t.steps; ++k, ++i) {
+        ok = warp_wait(&bars->empty[s], phase, abort, p.status);
+        if (!ok) break;
+        const Src a = p.a(t, k), b = p.b(t, k);
+        if (elect_one()) {
+          uint32_t dst = stages + s * S::kStageBytes;
           const uint32_t full = kPair ? in_cta(&bars->full[s], 0) : smem_u32(&bars->full[s]);
           if (rank == 0) mbar_arrive_expect_tx(&bars->full[s], (kPair ? 2 : 1) * S::kStageBytes);
-          const Src a = p.a(t, k), b = p.b(t, k);
           const int am = a.mn + rank * kRows, bn = b.mn + rank * S::kBRows;
           if (t.a_mn) {
+#pragma unroll
             for (int j = 0; j < kRows / 64; ++j) copy_box<kPair>(dst + j * 8192, a.map, am + j * 64, a.k, full);
           } else {
             copy_box<kPair>(dst, a.map, a.k, am, full);
           }
           dst += S::kABytes;
           if (t.b_mn) {
+#pragma unroll
             for (int j = 0; j < S::kBRows / 64; ++j) copy_box<kPair>(dst + j * 8192, b.map, bn + j * 64, b.k, full);
           } else {
             copy_box<kPair>(dst, b.map, b.k, bn, full);
           }
         }
+        __syncwarp();
+        if (++s == S::kStages) s = 0, phase ^= 1;
       }
-      // every stage is consumed before the CTA leaves (on a timeout: as far as
-      // the wait's limit goes, which is longer than any copy takes)
+    }
+    // every stage is consumed before the CTA leaves (on a timeout: as far as
+    // the wait's limit goes, which is longer than any copy takes)
+    if (lane == 0) {
       for (int s = 0; s < S::kStages; ++s) {
         const uint32_t n = (i + S::kStages - 1 - s) / S::kStages;
         if (n > 0) mbar_drain(&bars->empty[s], (n - 1) & 1);
@@ -202,35 +229,41 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       const uint32_t type = p.bf16 ? (1u << 7) | (1u << 10) : 0u;
       const uint32_t base = (1u << 4) | type | ((uint32_t)(P::kN >> 3) << 17) | ((uint32_t)(S::kM >> 4) << 24);
-      uint32_t i = 0, c = 0;
+      const uint32_t stages = smem_u32(smem);
+      uint32_t c = 0, s = 0, phase = 0;
       bool ok = true;
       Tile t;
       for (int n = 0; ok && p.tile(counts, unit, units, n, t); ++n) {
         const uint32_t idesc = base | (t.a_mn ? kAMajorM : 0u) | (t.b_mn ? kBMajorN : 0u);
         // 16 of K: 32 bytes of a K-major row, else two 1024-byte groups
-        const uint64_t da = t.a_mn ? 128 : 2, db = t.b_mn ? 128 : 2;
+        const uint32_t da = t.a_mn ? 128 : 2, db = t.b_mn ? 128 : 2;
+        const uint64_t ad0 = t.a_mn ? sw128_mnmajor_desc(stages, 8192) : sw128_kmajor_desc(stages);
+        const uint64_t bd0 = t.b_mn ? sw128_mnmajor_desc(stages + S::kABytes, 8192) : sw128_kmajor_desc(stages + S::kABytes);
         for (int k = 0; k < t.steps && ok; ++c) {
           const int buf = c & 1, kend = min(k + p.chunk, t.steps);
-          ok = mbar_wait(&bars->acc_empty[buf], ((c >> 1) & 1) ^ 1, abort, p.status);
+          ok = warp_wait(&bars->acc_empty[buf], ((c >> 1) & 1) ^ 1, abort, p.status);
           if (!ok) break;
           tc_fence_after();
-          for (int kf = k; k < kend; ++k, ++i) {
-            const int s = i % S::kStages;
-            ok = mbar_wait(&bars->full[s], (i / S::kStages) & 1, abort, p.status);
+          for (int kf = k; k < kend; ++k) {
+            ok = warp_wait(&bars->full[s], phase, abort, p.status);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t at = smem_u32(smem + s * S::kStageBytes);
-            const uint64_t ad = t.a_mn ? sw128_mnmajor_desc(at, 8192) : sw128_kmajor_desc(at);
-            const uint64_t bd = t.b_mn ? sw128_mnmajor_desc(at + S::kABytes, 8192) : sw128_kmajor_desc(at + S::kABytes);
+            // (shared memory addresses are below 2^18: no carry out of a descriptor's address field)
+            const uint64_t ad = ad0 + s * (S::kStageBytes / 16), bd = bd0 + s * (S::kStageBytes / 16);
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma<kPair>(tmem + buf * P::kN, ad + kk * da, bd + kk * db, idesc, k != kf || kk != 0);
-            commit<kPair>(&bars->empty[s]);
+              for (int kk = 0; kk < 4; ++kk)
+                mma<kPair>(tmem + buf * P::kN, ad + kk * da, bd + kk * db, idesc, k != kf || kk != 0);
+              commit<kPair>(&bars->empty[s]);
+            }
+            __syncwarp();
+            if (++s == S::kStages) s = 0, phase ^= 1;
           }
-          if (ok) commit<kPair>(&bars->acc_full[buf]);
+          if (ok && elect_one()) commit<kPair>(&bars->acc_full[buf]);
+          __syncwarp();
         }
       }
     }
@@ -258,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
       const int chunks = (t.steps + p.chunk - 1) / p.chunk;
       for (int j = 0; j < chunks && ok; ++j, ++c) {
         const int buf = c & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->acc_full[buf], (c >> 1) & 1, abort, p.status));
+        ok = warp_wait(&bars->acc_full[buf], (c >> 1) & 1, abort, p.status);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll

@@ -258,6 +258,10 @@ struct LossTiles {
   long long ld;
   int V, steps, vtiles;
 
+  __device__ void prefetch() const {
+    prefetch_tensormap(&h);
+    prefetch_tensormap(&w);
+  }
   __device__ int counts() const { return live->n; }
   __device__ bool tile(int n, int unit, int units, int i, Tile& t) const {
     // neighbouring units take the row tiles of the same columns, so that W
@@ -371,6 +375,11 @@ struct SlopeTiles {
   int rows;              // of the slopes' matrix
   int v0, V, steps, vtiles;
 
+  __device__ void prefetch() const {
+    prefetch_tensormap(&h);
+    prefetch_tensormap(&w);
+    prefetch_tensormap(&out);
+  }
   __device__ int counts() const { return live->n; }
   __device__ bool tile(int n, int unit, int units, int i, Tile& t) const {
     const int mt = div_up(n, 256);
@@ -434,6 +443,9 @@ struct GradTiles {
   int D, dt;             // tiles of D
   bool want_dh, add;     // add: a piece came before
 
+  __device__ void prefetch() const {
+    for (const CUtensorMap* m : {&s_k, &s_mn, &w, &h, &dh, &dW}) prefetch_tensormap(m);
+  }
   __device__ Counts counts() const {
     const dspark::Counts l = *live;
     Counts c;

@@ -195,6 +195,9 @@ struct NsTiles {
   bool vec;              // out takes stores of 16 bytes
   float ca, cb, cc;      // the coefficients
 
+  __device__ void prefetch() const {
+    for (const CUtensorMap* m : {&left, &left_low, &right, &right_low, &out0, &out1}) prefetch_tensormap(m);
+  }
   __device__ int counts() const { return 0; }
   __device__ bool tile(int, int unit, int units, int i, Tile& t) const {
     const int u = i * units + unit;
