@@ -17,6 +17,11 @@
 // (16 x 16: up to 3e-3), and the less a product's time depends on its length:
 // up to kHalvesSide every operand is taken in halves, high x high + high x low +
 // low x high, and the result is off by 1e-6 before its rounding.  Sums are fp32.
+//
+// The linear terms a X and b A are products too, with a diagonal tile as an operand
+// (of X's halves with ones, of A with b / c in halves), so that no epilogue
+// reads anything: its loads took 5 us of a tile for A, 10 for X, against 0.3 us for
+// each step of 64 of K.  B is kept as B / a.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -77,9 +82,12 @@ struct InputParams {
   int blocks;
   __half *hi, *lo;      // [rows][ld]
   long long ld;
+  __half* units;        // [3][256][256]: ones, b / c's halves on the diagonal
+  float ratio;          // b / c
 };
 
 constexpr int kNormThreads = 256;
+constexpr int kUnit = 256;   // side of a diagonal tile
 
 __device__ __forceinline__ double block_sum(double v, double* table) {
 #pragma unroll
@@ -118,7 +126,7 @@ __global__ void __launch_bounds__(kNormThreads) ns_norm(const InputParams p) {
   if (threadIdx.x == 0) p.partial[blockIdx.x] = s;
 }
 
-// X_0 in high and low halves.
+// X_0 in high and low halves, and the diagonal tiles.
 template <int kType>
 __global__ void __launch_bounds__(kNormThreads) ns_split(const InputParams p) {
   __shared__ double table[kNormThreads / 32];
@@ -127,6 +135,14 @@ __global__ void __launch_bounds__(kNormThreads) ns_split(const InputParams p) {
   double s = 0.0;
   for (int i = threadIdx.x; i < p.blocks; i += kNormThreads) s += p.partial[i];
   s = (double)kScale / (sqrt(block_sum(s, table)) + (double)p.eps);
+  const __half high = __float2half_rn(p.ratio * kScale), low = __float2half_rn(p.ratio * kScale - __half2float(high));
+  for (int i = blockIdx.x * kNormThreads + threadIdx.x; i < kUnit * kUnit; i += gridDim.x * kNormThreads) {
+    const bool on = i / kUnit == i % kUnit;
+    const __half zero = __float2half_rn(0.f);
+    p.units[i] = on ? __float2half_rn(kScale) : zero;
+    p.units[kUnit * kUnit + i] = on ? high : zero;
+    p.units[2 * kUnit * kUnit + i] = on ? low : zero;
+  }
   // s as a factor of fp32's range and a power of two in two halves (M may be
   // as small as fp32 goes)
   int e = 0;
@@ -180,6 +196,7 @@ struct NsTiles {
   using Counts = int;
 
   CUtensorMap left, left_low, right, right_low;
+  CUtensorMap unit, unit_low;   // the diagonal tile's halves (low: kSquare)
   CUtensorMap out0, out1;   // stores of 64 columns a warp
   int* status;
   bool bf16;             // false: fp16 operands
@@ -188,15 +205,17 @@ struct NsTiles {
   int rows, cols;        // of the product
   int mt, nt, steps, parts;
   int products;          // 1, or 3: high high, high low, low high
-  const __half *in0, *in1;   // kSquare: A's halves; kStepX, kLastX: X's (low: may be null)
+  int extra;             // products with the diagonal tile
+  bool unit_is_left;
+  const __half *in0, *in1;   // without the diagonal tile: A's halves, or X's (low: may be null); else null
   __half *to0, *to1;         // halves (low: may be null)
   __nv_bfloat16* out;
   long long ld, ld_out;  // of in and to (a multiple of 8); of out
   bool vec;              // out takes stores of 16 bytes
-  float ca, cb, cc;      // the coefficients
+  float ca, cb, cc;      // of X, A and the product
 
   __device__ void prefetch() const {
-    for (const CUtensorMap* m : {&left, &left_low, &right, &right_low, &out0, &out1}) prefetch_tensormap(m);
+    for (const CUtensorMap* m : {&left, &left_low, &right, &right_low, &unit, &unit_low, &out0, &out1}) prefetch_tensormap(m);
   }
   __device__ int counts() const { return 0; }
   __device__ bool tile(int, int unit, int units, int i, Tile& t) const {
@@ -223,16 +242,28 @@ struct NsTiles {
     t.part = part;
     t.kind = max(1, min(each, steps - part * each));   // steps of one product
     t.k0 = part * each;
-    t.steps = max(0, min(each, steps - t.k0)) * products;
+    t.steps = max(0, min(each, steps - t.k0)) * products + extra * unit_steps();
     t.a_mn = left_mn;
     t.b_mn = right_mn;
     return true;
   }
+  __device__ int unit_steps() const { return (unit_is_left ? kM : kN) / kStep; }
   __device__ Src a(const Tile& t, int k) const {
-    return Src{k >= 2 * t.kind ? &left_low : &left, t.m0, (t.k0 + k % t.kind) * kStep};
+    const int q = k / t.kind;
+    if (q < products) return Src{q == 2 ? &left_low : &left, t.m0, (t.k0 + k - q * t.kind) * kStep};
+    k -= products * t.kind;
+    const int u = k / unit_steps(), j = (k - u * unit_steps()) * kStep;
+    if (unit_is_left) return Src{&unit, 0, j};
+    // A with b / c, its low half, A's low half with b / c; X's halves
+    return Src{(kKind == kSquare ? u == 2 : u == 1) ? &left_low : &left, t.m0, t.n0 + j};
   }
   __device__ Src b(const Tile& t, int k) const {
-    return Src{k >= t.kind && k < 2 * t.kind ? &right_low : &right, t.n0, (t.k0 + k % t.kind) * kStep};
+    const int q = k / t.kind;
+    if (q < products) return Src{q == 1 ? &right_low : &right, t.n0, (t.k0 + k - q * t.kind) * kStep};
+    k -= products * t.kind;
+    const int u = k / unit_steps(), j = (k - u * unit_steps()) * kStep;
+    if (unit_is_left) return Src{u == 1 ? &right_low : &right, t.n0, t.m0 + j};
+    return Src{kKind == kSquare && u == 1 ? &unit_low : &unit, 0, j};
   }
 
   // 8 values of a row, zeros outside the matrix (whose rows are padded to 8)
@@ -246,6 +277,21 @@ struct NsTiles {
       const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&x[e]));
       v[2 * e] = u.x;
       v[2 * e + 1] = u.y;
+    }
+  }
+  // v = f v, or v = f v + g in without the diagonal tile
+  __device__ static __forceinline__ void scale(float (&v)[kCols], float f) {
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) v[j] *= f;
+  }
+  __device__ __forceinline__ void add_linear(float (&v)[kCols], int row, int col, float f, float g) const {
+#pragma unroll
+    for (int j = 0; j < kCols; j += 8) {
+      float hi[8], lo[8];
+      load8(in0, row, col + j, hi);
+      load8(in1, row, col + j, lo);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j + i] = fmaf(v[j + i], f, g * (hi[i] + lo[i]));
     }
   }
   __device__ static __forceinline__ void pack_high(const float (&v)[kCols], uint32_t (&w)[kCols / 2]) {
@@ -293,19 +339,8 @@ struct NsTiles {
       return;
     }
     if constexpr (kKind == kGram || kKind == kSquare) {
-#pragma unroll
-      for (int j = 0; j < kCols; j += 8) {
-        float hi[8], lo[8];
-        if constexpr (kKind == kSquare) {
-          load8(in0, row, col + j, hi);
-          load8(in1, row, col + j, lo);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if constexpr (kKind == kSquare) v[j + i] = fmaf(v[j + i], cc * kInvScale, cb * (hi[i] + lo[i]));
-          else v[j + i] *= kInvScale;
-        }
-      }
+      if (kKind == kSquare && in0 != nullptr) add_linear(v, row, col, cc * kInvScale, cb);
+      else scale(v, cc * kInvScale);
       const bool mirror = t.n0 + kN <= t.m0 && row < rows;   // above the diagonal
       pack_high(v, w);
       store_half(e, t, &out0, to0, w);
@@ -318,14 +353,8 @@ struct NsTiles {
       return;
     }
     if constexpr (kKind == kStepX || kKind == kLastX) {
-#pragma unroll
-      for (int j = 0; j < kCols; j += 8) {
-        float hi[8], lo[8];
-        load8(in0, row, col + j, hi);
-        load8(in1, row, col + j, lo);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[j + i] = fmaf(v[j + i], kInvScale, ca * (hi[i] + lo[i]));
-      }
+      if (in0 != nullptr) add_linear(v, row, col, kInvScale, ca);
+      else scale(v, ca * kInvScale);
       if constexpr (kKind == kStepX) {
         pack_high(v, w);
         store_half(e, t, &out0, to0, w);
@@ -385,7 +414,7 @@ struct Layout {
   long long ld, lda, ldp;   // of X, of A and B, of the parts
   int small;                // the shorter side
   int parts;                // of the Gram matrix's K at most
-  size_t partial, x[2][2], A[2], B[2], part, total;
+  size_t partial, units, x[2][2], A[2], B[2], part, total;
   bool halves;
 };
 
@@ -403,6 +432,7 @@ Layout layout(int rows, int cols) {
     return a;
   };
   l.partial = take(8ull * kNormBlocks);
+  l.units = take(3 * 2ull * kUnit * kUnit);
   for (auto& half : l.x)
     for (auto& x : half) x = take(2ull * rows * l.ld);
   l.halves = l.small <= kHalvesSide;
@@ -419,10 +449,13 @@ Layout layout(int rows, int cols) {
 // Everything one product needs but the tile's shape.
 struct Product {
   Kind kind;
-  const __half *left, *left_low, *right, *right_low;   // operands (low: null, or both)
+  const __half *left, *left_low, *right, *right_low;   // operands (both low halves: three products)
   long long left_rows, left_cols, left_ld, right_rows, right_cols, right_ld;
   bool left_mn, right_mn;
   int rows, cols, K;
+  const __half *unit, *unit_low;       // the diagonal tile's halves, or null
+  int extra;
+  bool unit_is_left;
   const __half *in0, *in1;
   __half *to0, *to1;
   long long ld;
@@ -450,11 +483,19 @@ cudaError_t launch_product(const Product& q, cudaStream_t stream) {
   p.left_low = p.left;
   p.right_low = p.right;
   p.products = 1;
-  if (q.left_low) {
-    p.products = 3;
+  if (q.left_low && q.right_low) p.products = 3;
+  if (q.left_low)
     NS_TRY(map_16bit(q.left_low, false, q.left_rows, q.left_cols, q.left_ld, q.left_mn ? kStep : kRows, &p.left_low));
+  if (q.right_low)
     NS_TRY(map_16bit(q.right_low, false, q.right_rows, q.right_cols, q.right_ld, q.right_mn ? kStep : Shape<P>::kBRows,
                      &p.right_low));
+  p.unit = p.unit_low = p.left;
+  p.extra = kKind == kGramPart || !q.unit ? 0 : q.extra;
+  p.unit_is_left = q.unit_is_left;
+  if (p.extra) {
+    const int box = q.unit_is_left ? kRows : Shape<P>::kBRows;
+    NS_TRY(map_16bit(q.unit, false, kUnit, kUnit, kUnit, box, &p.unit));
+    if (q.unit_low) NS_TRY(map_16bit(q.unit_low, false, kUnit, kUnit, kUnit, box, &p.unit_low));
   }
   p.status = q.status;
   p.bf16 = false;
@@ -498,7 +539,7 @@ cudaError_t choose_product(const Product& q, int sms, cudaStream_t stream) {
   auto cost = [&](int tm, int tn, int units, double step, double more) {
     const double mt = div_up(q.rows, tm), nt = div_up(q.cols, tn);
     const double tiles = sym ? (double)tm / tn * mt * (mt + 1) / 2 : mt * nt;
-    return std::max(1.0, std::ceil(tiles / units)) * (div_up(q.K, kStep) * (q.left_low ? 3 : 1) * step + more);
+    return std::max(1.0, std::ceil(tiles / units)) * (div_up(q.K, kStep) * (q.left_low && q.right_low ? 3 : 1) * step + more);
   };
   const double big = cost(256, 256, sms / 2, 0.34, 2.0), mid = cost(128, 128, sms, 0.17, 1.4),
                low = cost(128, 64, sms, 0.12, 1.0);
@@ -545,6 +586,13 @@ cudaError_t launch_newton_schulz(const NewtonSchulzArgs& a, cudaStream_t stream)
   in.hi = x[0][0];
   in.lo = x[0][1];
   in.ld = l.ld;
+  in.units = reinterpret_cast<__half*>(ws + l.units);
+  // the linear terms are products with a diagonal tile as long as all its
+  // values and B / a stay well within fp16, else an epilogue adds them
+  const float most = 16.f;
+  const bool fold = std::fabs(a.b) <= most * std::fabs(a.c) && std::fabs(a.b) <= most * std::fabs(a.a) &&
+                    std::fabs(a.c) <= most * std::fabs(a.a) && a.a != 0.f && a.c != 0.f;
+  in.ratio = fold ? a.b / a.c : 0.f;
   if (a.dtype == DSPARK_F32) NS_TRY(launch_input<DSPARK_F32>(in, stream));
   else if (a.dtype == DSPARK_BF16) NS_TRY(launch_input<DSPARK_BF16>(in, stream));
   else NS_TRY(launch_input<DSPARK_F16>(in, stream));
@@ -552,11 +600,12 @@ cudaError_t launch_newton_schulz(const NewtonSchulzArgs& a, cudaStream_t stream)
   const bool tall = a.rows > a.cols;
   const int small = l.small, large = std::max(a.rows, a.cols);
   Product q{};
-  q.a = a.a; q.b = a.b; q.c = a.c;
   q.status = a.status;
   for (int i = 0; i < a.steps; ++i) {
     __half *hi = x[i & 1][0], *lo = x[i & 1][1];
     // A
+    q.unit = q.unit_low = q.in0 = q.in1 = nullptr;
+    q.c = 1.f;
     q.left = q.right = hi;
     q.left_low = q.right_low = l.halves ? lo : nullptr;
     q.left_rows = q.right_rows = a.rows;
@@ -589,25 +638,43 @@ cudaError_t launch_newton_schulz(const NewtonSchulzArgs& a, cudaStream_t stream)
     q.left_ld = q.right_ld = l.lda;
     q.left_mn = q.right_mn = false;
     q.K = small;
-    q.in0 = A[0];
-    q.in1 = A[1];
+    if (fold) {
+      q.unit = in.units + kUnit * kUnit;
+      q.unit_low = in.units + 2 * kUnit * kUnit;
+      q.extra = l.halves ? 3 : 2;
+      q.unit_is_left = false;
+      q.c = a.c / a.a;
+    } else {
+      q.in0 = A[0];
+      q.in1 = A[1];
+      q.b = a.b;
+      q.c = a.c;
+    }
     q.to0 = B[0];
     q.to1 = B[1];
     NS_TRY(choose_product<kSquare>(q, sms, stream));
     // X
     Product s = q;
     if (tall) {
-      s.left = hi; s.left_low = l.halves ? lo : nullptr; s.left_rows = a.rows; s.left_cols = a.cols; s.left_ld = l.ld;
+      s.left = hi; s.left_low = lo; s.left_rows = a.rows; s.left_cols = a.cols; s.left_ld = l.ld;
       s.right = B[0]; s.right_low = B[1];
     } else {
       s.left = B[0]; s.left_low = B[1];
-      s.right = hi; s.right_low = l.halves ? lo : nullptr; s.right_rows = a.rows; s.right_cols = a.cols; s.right_ld = l.ld;
+      s.right = hi; s.right_low = lo; s.right_rows = a.rows; s.right_cols = a.cols; s.right_ld = l.ld;
       s.right_mn = true;
     }
     s.rows = a.rows;
     s.cols = a.cols;
-    s.in0 = hi;
-    s.in1 = lo;
+    s.a = a.a;
+    if (fold) {
+      s.unit = in.units;
+      s.unit_low = nullptr;
+      s.extra = 2;
+      s.unit_is_left = !tall;
+    } else {
+      s.in0 = hi;
+      s.in1 = lo;
+    }
     s.ld = l.ld;
     s.to0 = x[1 - (i & 1)][0];
     s.to1 = x[1 - (i & 1)][1];
