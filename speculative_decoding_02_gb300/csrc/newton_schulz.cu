@@ -79,6 +79,7 @@ struct InputParams {
   bool vec;             // rows of M start on 4 of its values
   float eps;
   double* partial;      // [blocks] sums of squares
+  int* counters;        // cleared for the kernels that follow
   int blocks;
   __half *hi, *lo;      // [rows][ld]
   long long ld;
@@ -87,25 +88,18 @@ struct InputParams {
 };
 
 constexpr int kNormThreads = 256;
+constexpr int kPrograms = 64, kCounters = 2048;   // counters of programs, and of tiles whose K is split
 constexpr int kUnit = 256;   // side of a diagonal tile
-
-__device__ __forceinline__ double block_sum(double v, double* table) {
-#pragma unroll
-  for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
-  if ((threadIdx.x & 31) == 0) table[threadIdx.x >> 5] = v;
-  __syncthreads();
-  double s = 0.0;
-  for (int w = 0; w < kNormThreads / 32; ++w) s += table[w];
-  return s;
-}
 
 // Sums of squares of values of any size: fp32 sums of three ranges, each scaled
 // so that no square leaves fp32's range, joined in 64 bits.
 template <int kType>
 __global__ void __launch_bounds__(kNormThreads) ns_norm(const InputParams p) {
-  __shared__ double table[kNormThreads / 32];
+  __shared__ float3 table[kNormThreads / 32];
   pdl_trigger();
   pdl_wait();
+  for (int i = blockIdx.x * kNormThreads + threadIdx.x; i < kPrograms + kCounters; i += gridDim.x * kNormThreads)
+    p.counters[i] = 0;
   const int chunks = (p.cols + 3) / 4;
   const long long all = (long long)p.rows * chunks;
   float small = 0.f, middle = 0.f, large = 0.f;
@@ -122,19 +116,44 @@ __global__ void __launch_bounds__(kNormThreads) ns_norm(const InputParams p) {
       else middle = fmaf(t, t, middle);   // (and NaN)
     }
   }
-  const double s = block_sum((double)middle + (double)large * 0x1p176 + (double)small * 0x1p-176, table);
-  if (threadIdx.x == 0) p.partial[blockIdx.x] = s;
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) {
+    small += __shfl_xor_sync(0xffffffffu, small, d);
+    middle += __shfl_xor_sync(0xffffffffu, middle, d);
+    large += __shfl_xor_sync(0xffffffffu, large, d);
+  }
+  if ((threadIdx.x & 31) == 0) table[threadIdx.x >> 5] = make_float3(small, middle, large);
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  // (64-bit arithmetic is slow here: one thread's)
+  small = middle = large = 0.f;
+  for (int w = 0; w < kNormThreads / 32; ++w) small += table[w].x, middle += table[w].y, large += table[w].z;
+  p.partial[blockIdx.x] = (double)middle + (double)large * 0x1p176 + (double)small * 0x1p-176;
 }
 
 // X_0 in high and low halves, and the diagonal tiles.
 template <int kType>
 __global__ void __launch_bounds__(kNormThreads) ns_split(const InputParams p) {
-  __shared__ double table[kNormThreads / 32];
+  __shared__ float factors[3];
   pdl_trigger();
   pdl_wait();
-  double s = 0.0;
-  for (int i = threadIdx.x; i < p.blocks; i += kNormThreads) s += p.partial[i];
-  s = (double)kScale / (sqrt(block_sum(s, table)) + (double)p.eps);
+  if (threadIdx.x < 32) {
+    // (64-bit arithmetic is slow here: one warp's)
+    double s = 0.0;
+    for (int i = threadIdx.x; i < p.blocks; i += 32) s += p.partial[i];
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
+    if (threadIdx.x == 0) {
+      s = (double)kScale / (sqrt(s) + (double)p.eps);
+      // as a factor of fp32's range and a power of two in two halves (M may be as
+      // small as fp32 goes)
+      int e = 0;
+      if (isfinite(s) && s > 0.0) s = frexp(s, &e);
+      factors[0] = (float)s;
+      factors[1] = ldexpf(1.f, e / 2);
+      factors[2] = ldexpf(1.f, e - e / 2);
+    }
+  }
   const __half high = __float2half_rn(p.ratio * kScale), low = __float2half_rn(p.ratio * kScale - __half2float(high));
   for (int i = blockIdx.x * kNormThreads + threadIdx.x; i < kUnit * kUnit; i += gridDim.x * kNormThreads) {
     const bool on = i / kUnit == i % kUnit;
@@ -143,12 +162,8 @@ __global__ void __launch_bounds__(kNormThreads) ns_split(const InputParams p) {
     p.units[kUnit * kUnit + i] = on ? high : zero;
     p.units[2 * kUnit * kUnit + i] = on ? low : zero;
   }
-  // s as a factor of fp32's range and a power of two in two halves (M may be
-  // as small as fp32 goes)
-  int e = 0;
-  if (isfinite(s) && s > 0.0) s = frexp(s, &e);
-  const int e0 = e / 2;
-  const float f = (float)s, p0 = ldexpf(1.f, e0), p1 = ldexpf(1.f, e - e0);
+  __syncthreads();
+  const float f = factors[0], p0 = factors[1], p1 = factors[2];
   const int chunks = (p.cols + 3) / 4;
   const long long all = (long long)p.rows * chunks;
 #pragma unroll 4
@@ -213,6 +228,7 @@ struct NsTiles {
   long long ld, ld_out;  // of in and to (a multiple of 8); of out
   bool vec;              // out takes stores of 16 bytes
   float ca, cb, cc;      // of X, A and the product
+  float diag;            // kSquare: added on the diagonal (times 2^10)
 
   __device__ void prefetch() const {
     for (const CUtensorMap* m : {&left, &left_low, &right, &right_low, &unit, &unit_low, &out0, &out1}) prefetch_tensormap(m);
@@ -341,6 +357,11 @@ struct NsTiles {
     if constexpr (kKind == kGram || kKind == kSquare) {
       if (kKind == kSquare && in0 != nullptr) add_linear(v, row, col, cc * kInvScale, cb);
       else scale(v, cc * kInvScale);
+      if (kKind == kSquare && diag != 0.f) {
+#pragma unroll
+        for (int j = 0; j < kCols; ++j)
+          if (col + j == row) v[j] += diag;
+      }
       const bool mirror = t.n0 + kN <= t.m0 && row < rows;   // above the diagonal
       pack_high(v, w);
       store_half(e, t, &out0, to0, w);
@@ -405,6 +426,384 @@ __global__ void __launch_bounds__(256) ns_join(const JoinParams p) {
 }
 
 // ---------------------------------------------------------------------------
+// several products in one launch
+//
+// Products of a few hundred rows take 8 to 10 us each as kernels of their own,
+// of which 2 are spent on K: the rest is the next kernel's start behind the last
+// store, its first copies and its parameters.  Here persistent CTAs (a cooperative
+// launch) go from product to product: a tile's stores are followed by an increment
+// of a counter in global memory, and a product's copies wait until the counter
+// shows all tiles that it reads (bounded, as every wait).  Tiles are 128 x 64, a
+// CTA each; K may be split, the last CTA to finish a tile's part adds the parts
+// up in their order.
+// ---------------------------------------------------------------------------
+constexpr int kMaxOps = 24, kMaxMaps = 32;   // of a launch
+constexpr int kOpM = 128, kOpN = 64, kOpCols = kOpN / 4;
+constexpr int kOpGroup = 4;           // steps of K in a stage, which the waits and commits of a step are shared by
+constexpr int kOpStages = 2;
+constexpr int kOpStepBytes = (kOpM + kOpN) * 128, kOpStageBytes = kOpGroup * kOpStepBytes;
+constexpr int kOpRowsBytes = kOpM * 128;
+constexpr int kOpSmem = 1024 + kOpStages * kOpStageBytes + kOpRowsBytes + kBarBytes;
+static_assert(kOpSmem + 1024 + 24 * 160 <= kMaxSmem, "shared memory (and the static part)");
+
+// One product of a program.  Its sum over K is that of segments, each a pair of
+// maps and a number of steps: up to three products of halves, then up to three with
+// a diagonal tile.
+struct Op {
+  short left[3], right[3];     // maps
+  short unit[3], of[3];        // maps of the diagonal tiles and of their other factors
+  short products, extra, steps, unit_steps;   // steps: of a product's K
+  bool left_mn, right_mn, unit_is_left, symmetric, vec;
+  int rows, cols, mt, nt;
+  int tiles, parts;            // work items: tiles * parts
+  int base;                    // what the counter has to show first
+  int first;                   // the CTA that takes its first item
+  int split_counter;           // of its first tile
+  float scale, diag;           // result = scale sum + diag on the diagonal
+  long long ld, ld_part, ld_out;
+  __half *to0, *to1;           // halves (low: may be null)
+  __nv_bfloat16* out;          // or the last X
+  float* part;
+};
+
+struct Program {
+  CUtensorMap maps[kMaxMaps];
+  Op ops[kMaxOps];
+  int map_count, count;
+  int* counter;                // tiles done
+  int* split_counters;
+  int* status;
+};
+
+struct Item {
+  int m0, n0, part, tile, k0, steps;
+};
+
+__device__ __forceinline__ bool item_of(const Op& op, int unit, int units, int i, Item& t) {
+  const int u = (unit >= op.first ? unit - op.first : unit + units - op.first) + i * units;
+  if (u >= op.tiles * op.parts) return false;
+  t.part = u / op.tiles;
+  t.tile = u - t.part * op.tiles;
+  int m, n;
+  if (op.symmetric) {   // tiles on or below the diagonal: two more for each row tile
+    const int w = t.tile / 2;
+    m = (int)((sqrtf(8.f * w + 1.f) - 1.f) * 0.5f);
+    while (m * (m + 1) / 2 > w) --m;
+    while ((m + 1) * (m + 2) / 2 <= w) ++m;
+    n = t.tile - m * (m + 1);
+  } else {
+    n = t.tile / op.mt;
+    m = t.tile - n * op.mt;
+  }
+  t.m0 = m * kOpM;
+  t.n0 = n * kOpN;
+  const int each = div_up(op.steps, op.parts);
+  t.k0 = t.part * each;
+  t.steps = max(0, min(each, op.steps - t.k0));
+  return true;
+}
+__device__ __forceinline__ int steps_of(const Op& op, const Item& t) {
+  return t.steps * op.products + op.extra * op.unit_steps;
+}
+
+// Until `counter` shows `least`; a converged warp.  What other CTAs stored before
+// they counted is seen by this warp's loads and its copies (the async proxy).
+__device__ __forceinline__ bool wait_count(const int* counter, int least, volatile int* abort, int* status) {
+  bool ok = true;
+  const uint64_t t0 = globaltimer();
+  for (unsigned polls = 0;; ++polls) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+    if (v >= least) break;
+    if (polls % 16 != 15) continue;
+    if (*abort) { ok = false; break; }
+    if (globaltimer() - t0 > kWaitLimitNs) {
+      *abort = 1;
+      record_status(status, DSPARK_ERR_TIMEOUT);
+      ok = false;
+      break;
+    }
+  }
+  ok = __all_sync(0xffffffffu, ok);
+  asm volatile("fence.proxy.async;" ::: "memory");
+  return ok;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) ns_program(const __grid_constant__ Program p) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  unsigned char* rows_s = smem + kOpStages * kOpStageBytes;   // a tile's rows on their way out
+  Bars* bars = reinterpret_cast<Bars*>(rows_s + kOpRowsBytes);
+  __shared__ int last_part;
+  // (in shared memory: a read of the parameters that misses their small cache takes 200 cycles)
+  __shared__ Op ops[kMaxOps];
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int unit = blockIdx.x, units = gridDim.x;
+  volatile int* abort = &bars->abort;
+  constexpr int kChunk = 8;
+  static_assert(kChunk % kOpGroup == 0, "whole groups in a chunk");
+  for (int i = threadIdx.x; i < p.count * (int)(sizeof(Op) / 4); i += kThreads)
+    reinterpret_cast<int*>(ops)[i] = reinterpret_cast<const int*>(p.ops)[i];
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kOpStages; ++s) { mbar_init(&bars->full[s], 1); mbar_init(&bars->empty[s], 1); }
+    for (int s = 0; s < 2; ++s) { mbar_init(&bars->acc_full[s], 1); mbar_init(&bars->acc_empty[s], kEpiWarps); }
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(&bars->tmem_base, 2 * kOpN);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    static_assert(kMaxMaps <= 32, "a lane each");
+    if (lane < p.map_count) prefetch_tensormap(&p.maps[lane]);
+    const uint32_t stages = smem_u32(smem);
+    uint32_t i = 0, s = 0, phase = 1;
+    bool ok = true;
+    Item t;
+    for (int o = 0; o < p.count && ok; ++o) {
+      const Op& op = ops[o];
+      const bool left_mn = op.left_mn, right_mn = op.right_mn;
+      for (int n = 0; ok && item_of(op, unit, units, n, t); ++n) {
+        if (n == 0 && op.base > 0 && !(ok = wait_count(p.counter, op.base, abort, p.status))) break;
+        int left = steps_of(op, t), q = 0, in = 0;    // steps to go; segment, its steps to go
+        const CUtensorMap *lm = nullptr, *rm = nullptr;
+        int lr = 0, lk = 0, rr = 0, rk = 0;
+        while (left > 0) {
+          const int group = min(left, kOpGroup);
+          left -= group;
+          ok = warp_wait(&bars->empty[s], phase, abort, p.status);
+          if (!ok) break;
+          uint32_t dst = stages + s * kOpStageBytes;
+          const uint32_t full = smem_u32(&bars->full[s]);
+          if (elect_one()) mbar_arrive_expect_tx(&bars->full[s], group * kOpStepBytes);
+          __syncwarp();
+          for (int g = 0; g < group; ++g, dst += kOpStepBytes) {
+            if (in == 0) {   // the next segment
+              lr = t.m0;
+              rr = t.n0;
+              lk = rk = t.k0 * kStep;
+              if (q < op.products) {
+                in = t.steps;
+                lm = &p.maps[op.left[q]];
+                rm = &p.maps[op.right[q]];
+              } else {
+                const int x = q - op.products;
+                in = op.unit_steps;
+                lm = &p.maps[op.unit_is_left ? op.unit[x] : op.of[x]];
+                rm = &p.maps[op.unit_is_left ? op.of[x] : op.unit[x]];
+                if (op.unit_is_left) lr = 0, lk = 0, rk = t.m0;
+                else lk = t.n0, rr = 0, rk = 0;
+              }
+              ++q;
+            }
+            // (the coordinate along K is the second one of an operand that is not K-major)
+            if (elect_one()) {
+              copy_box<false>(dst, lm, left_mn ? lr : lk, left_mn ? lk : lr, full);
+              if (left_mn) copy_box<false>(dst + 8192, lm, lr + 64, lk, full);
+              copy_box<false>(dst + kOpM * 128, rm, right_mn ? rr : rk, right_mn ? rk : rr, full);
+            }
+            __syncwarp();
+            --in;
+            lk += kStep;
+            rk += kStep;
+          }
+          ++i;
+          if (++s == kOpStages) s = 0, phase ^= 1;
+        }
+      }
+    }
+    if (lane == 0) {
+      for (int s = 0; s < kOpStages; ++s) {
+        const uint32_t n = (i + kOpStages - 1 - s) / kOpStages;
+        if (n > 0) mbar_drain(&bars->empty[s], (n - 1) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t base = (1u << 4) | ((uint32_t)(kOpN >> 3) << 17) | ((uint32_t)(kOpM >> 4) << 24);   // fp16
+    const uint32_t stages = smem_u32(smem);
+    uint32_t c = 0, s = 0, phase = 0;
+    bool ok = true;
+    Item t;
+    for (int o = 0; o < p.count && ok; ++o) {
+      const Op& op = ops[o];
+      const uint32_t idesc = base | (op.left_mn ? kAMajorM : 0u) | (op.right_mn ? kBMajorN : 0u);
+      const uint32_t da = op.left_mn ? 128 : 2, db = op.right_mn ? 128 : 2;
+      const uint64_t ad0 = op.left_mn ? sw128_mnmajor_desc(stages, 8192) : sw128_kmajor_desc(stages);
+      const uint64_t bd0 = op.right_mn ? sw128_mnmajor_desc(stages + kOpM * 128, 8192) : sw128_kmajor_desc(stages + kOpM * 128);
+      for (int n = 0; ok && item_of(op, unit, units, n, t); ++n) {
+        const int all = steps_of(op, t);
+        for (int k = 0; k < all && ok; ++c) {
+          const int buf = c & 1, kend = min(k + kChunk, all);
+          ok = warp_wait(&bars->acc_empty[buf], ((c >> 1) & 1) ^ 1, abort, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          for (int kf = k; k < kend;) {
+            const int group = min(all - k, kOpGroup);
+            ok = warp_wait(&bars->full[s], phase, abort, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              uint64_t ad = ad0 + s * (kOpStageBytes / 16), bd = bd0 + s * (kOpStageBytes / 16);
+              for (int g = 0; g < group; ++g, ad += kOpStepBytes / 16, bd += kOpStepBytes / 16) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  umma_bf16(tmem + buf * kOpN, ad + kk * da, bd + kk * db, idesc, k + g != kf || kk != 0);
+              }
+              umma_commit(&bars->empty[s]);
+            }
+            __syncwarp();
+            k += group;
+            if (++s == kOpStages) s = 0, phase ^= 1;
+          }
+          if (ok && elect_one()) umma_commit(&bars->acc_full[buf]);
+          __syncwarp();
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3, h = (warp - 2) >> 2;
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + h * kOpCols;
+    uint32_t c = 0;
+    bool ok = true;
+    Item t;
+    for (int o = 0; o < p.count; ++o) {
+      const Op& op = ops[o];
+      for (int n = 0; item_of(op, unit, units, n, t); ++n) {
+        const int all = steps_of(op, t), chunks = div_up(all, kChunk);
+        float v[kOpCols];
+#pragma unroll
+        for (int j = 0; j < kOpCols; ++j) v[j] = 0.f;
+        for (int j = 0; j < chunks && ok; ++j, ++c) {
+          const int buf = c & 1;
+          ok = warp_wait(&bars->acc_full[buf], (c >> 1) & 1, abort, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          float x[kOpCols];
+          tmem_load_cols<kOpCols>(lanes + buf * kOpN, x);
+#pragma unroll
+          for (int e = 0; e < kOpCols; ++e) v[e] += x[e];
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->acc_empty[buf]);
+        }
+        // (a warp whose wait gave up goes on through the barriers)
+        const int row = t.m0 + q * 32 + lane, col = t.n0 + h * kOpCols;
+        if (op.parts > 1) {
+          const size_t at = (size_t)row * op.ld_part + col, plane = (size_t)op.rows * op.ld_part;
+          if (row < op.rows) {
+#pragma unroll
+            for (int j = 0; j < kOpCols; j += 4)
+              if (col + j < op.ld_part)
+                *reinterpret_cast<float4*>(op.part + t.part * plane + at + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+          }
+          // (a barrier, then one thread's fence: what the others wrote before is ordered by it too)
+          named_bar_sync(1, kEpiWarps * 32);
+          if (threadIdx.x == 64) {
+            __threadfence();
+            last_part = atomicAdd(p.split_counters + op.split_counter + t.tile, 1) == op.parts - 1;
+            __threadfence();
+          }
+          named_bar_sync(1, kEpiWarps * 32);
+          if (!last_part) continue;
+#pragma unroll
+          for (int j = 0; j < kOpCols; ++j) v[j] = 0.f;
+          if (row < op.rows) {
+#pragma unroll 4
+            for (int i = 0; i < op.parts; ++i) {
+#pragma unroll
+              for (int j = 0; j < kOpCols; j += 4) {
+                if (col + j >= op.ld_part) continue;
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(op.part + i * plane + at + j));
+                v[j] += x.x; v[j + 1] += x.y; v[j + 2] += x.z; v[j + 3] += x.w;
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kOpCols; ++j) {
+          v[j] *= op.scale;
+          if (op.diag != 0.f && col + j == row) v[j] += op.diag;
+        }
+        uint32_t w[kOpCols / 2];
+        unsigned char* mine = rows_s + q * 4096;
+        // this warp's 16 columns of 32 rows beside those of the other three, then
+        // whole rows of 128 bytes: a store of a row a thread takes 32 turns, of 4 rows
+        // a warp 4
+        auto store_rows = [&](void* to, long long ld) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            *reinterpret_cast<uint4*>(mine + lane * 128 + (((h * 2 + j) ^ (lane & 7)) << 4)) =
+                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          named_bar_sync(2 + q, 128);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int r = h * 8 + j * 4 + lane / 8, x = lane % 8, gr = t.m0 + q * 32 + r, gc = t.n0 + x * 8;
+            const uint4 y = *reinterpret_cast<const uint4*>(mine + r * 128 + ((x ^ (r & 7)) << 4));
+            if (gr < op.rows && gc < op.cols)
+              *reinterpret_cast<uint4*>(static_cast<unsigned short*>(to) + (size_t)gr * ld + gc) = y;
+          }
+          named_bar_sync(2 + q, 128);
+        };
+        if (op.out != nullptr) {
+#pragma unroll
+          for (int j = 0; j < kOpCols; j += 2) w[j / 2] = pack_bf16(v[j], v[j + 1]);
+          if (op.vec) {
+            store_rows(op.out, op.ld_out);
+          } else if (row < op.rows) {
+            unsigned short* dst = reinterpret_cast<unsigned short*>(op.out) + (size_t)row * op.ld_out + col;
+#pragma unroll
+            for (int j = 0; j < kOpCols; ++j)
+              if (col + j < op.cols) dst[j] = (unsigned short)(j % 2 ? w[j / 2] >> 16 : w[j / 2]);
+          }
+          continue;
+        }
+        const bool mirror = op.symmetric && t.n0 + kOpN <= t.m0;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          __half* to = half == 0 ? op.to0 : op.to1;
+          if (to == nullptr) break;
+#pragma unroll
+          for (int j = 0; j < kOpCols; j += 2) {
+            if (half == 1) {
+              const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&w[j / 2]));
+              w[j / 2] = pack_half(v[j] - back.x, v[j + 1] - back.y);
+            } else {
+              w[j / 2] = pack_half(v[j], v[j + 1]);
+            }
+          }
+          store_rows(to, op.ld);
+          if (mirror && row < op.rows) {
+#pragma unroll
+            for (int j = 0; j < kOpCols; ++j)
+              if (col + j < op.cols)
+                reinterpret_cast<unsigned short*>(to)[(size_t)(col + j) * op.ld + row] =
+                    (unsigned short)(j % 2 ? w[j / 2] >> 16 : w[j / 2]);
+          }
+        }
+        // the tile is done: its stores are seen by who sees the counter (and, behind
+        // the fence there, by copies, the async proxy)
+        named_bar_sync(1, kEpiWarps * 32);
+        if (threadIdx.x == 64) {
+          asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p.counter) : "memory");
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 2 * kOpN);
+}
+
+// ---------------------------------------------------------------------------
 // workspace and launches
 // ---------------------------------------------------------------------------
 constexpr long long kPartBytes = 64ll << 20;
@@ -414,7 +813,7 @@ struct Layout {
   long long ld, lda, ldp;   // of X, of A and B, of the parts
   int small;                // the shorter side
   int parts;                // of the Gram matrix's K at most
-  size_t partial, units, x[2][2], A[2], B[2], part, total;
+  size_t partial, counters, units, x[2][2], A[2], B[2], more[4][2], part, total;
   bool halves;
 };
 
@@ -432,6 +831,7 @@ Layout layout(int rows, int cols) {
     return a;
   };
   l.partial = take(8ull * kNormBlocks);
+  l.counters = take(4ull * (kPrograms + kCounters));
   l.units = take(3 * 2ull * kUnit * kUnit);
   for (auto& half : l.x)
     for (auto& x : half) x = take(2ull * rows * l.ld);
@@ -439,6 +839,8 @@ Layout layout(int rows, int cols) {
   for (int i = 0; i <= (int)l.halves; ++i) {
     l.A[i] = take(2ull * l.small * l.lda);
     l.B[i] = take(2ull * l.small * l.lda);
+    if (l.halves)
+      for (auto& m : l.more) m[i] = take(2ull * l.small * l.lda);
   }
   l.parts = (int)std::min<long long>(76, kPartBytes / (4ll * l.small * l.ldp));
   if (l.parts > 1) l.part = take(4ull * l.parts * l.small * l.ldp);
@@ -548,6 +950,112 @@ cudaError_t choose_product(const Product& q, int sms, cudaStream_t stream) {
   return launch_product<false, 64, kKind>(q, stream);
 }
 
+// A matrix in fp16 halves (low: may be null).
+struct Halves {
+  __half *hi, *lo;
+  long long rows, cols, ld;
+};
+
+// Builds programs and launches them when they are full or done.
+struct Builder {
+  Program p{};
+  int tiles = 0, items = 0, programs = 0, splits = 0;
+  int* counters;
+  int* status;
+  int sms;
+  cudaStream_t stream;
+  cudaError_t error = cudaSuccess;
+
+  Builder(int* counters, int* status, int sms, cudaStream_t stream)
+      : counters(counters), status(status), sms(sms), stream(stream) {}
+
+  void start() {
+    p.map_count = p.count = 0;
+    tiles = items = 0;
+  }
+  short map(const __half* base, long long rows, long long cols, long long ld, int box) {
+    for (int i = 0; i < p.map_count; ++i)
+      if (base_[i] == base && box_[i] == box) return (short)i;
+    if (p.map_count == kMaxMaps) {
+      error = cudaErrorInvalidValue;
+      return 0;
+    }
+    const cudaError_t e = map_16bit(base, false, rows, cols, ld, box, &p.maps[p.map_count]);
+    if (e != cudaSuccess) error = e;
+    base_[p.map_count] = base;
+    box_[p.map_count] = box;
+    return (short)p.map_count++;
+  }
+  short left(const __half* base, const Halves& m, bool mn) { return map(base, m.rows, m.cols, m.ld, mn ? kStep : kOpM); }
+  short right(const __half* base, const Halves& m, bool) { return map(base, m.rows, m.cols, m.ld, kOpN); }
+
+  // The product of two matrices (three products where both have low halves).
+  Op& add(const Halves& l, bool l_mn, const Halves& r, bool r_mn, int rows, int cols, int K, bool symmetric) {
+    Op& op = p.ops[p.count++];
+    op = Op{};
+    op.products = l.lo && r.lo ? 3 : 1;
+    op.left[0] = op.left[1] = left(l.hi, l, l_mn);
+    op.right[0] = op.right[2] = right(r.hi, r, r_mn);
+    if (op.products == 3) {
+      op.left[2] = left(l.lo, l, l_mn);
+      op.right[1] = right(r.lo, r, r_mn);
+    }
+    op.left_mn = l_mn;
+    op.right_mn = r_mn;
+    op.rows = rows;
+    op.cols = cols;
+    op.steps = (short)div_up(K, kStep);
+    op.mt = div_up(rows, kOpM);
+    op.nt = div_up(cols, kOpN);
+    // (the tiles above the diagonal where there are SMs for them: mirroring takes longer)
+    op.symmetric = symmetric && op.mt * op.nt > sms;
+    op.tiles = op.symmetric ? op.mt * (op.mt + 1) : op.mt * op.nt;
+    op.parts = 1;
+    op.base = tiles;
+    op.scale = kInvScale;
+    return op;
+  }
+  // After everything about the op but its place is known.
+  void place(Op& op) {
+    tiles += op.tiles;
+    items = std::max(items, op.tiles * op.parts);
+  }
+  void into(Op& op, const Halves& to) {
+    op.to0 = to.hi;
+    op.to1 = to.lo;
+    op.ld = to.ld;
+    place(op);
+  }
+  bool room(int ops) const { return p.count + ops <= kMaxOps; }
+
+  cudaError_t launch() {
+    if (error != cudaSuccess || p.count == 0) return error;
+    if (programs == kPrograms) return cudaErrorInvalidValue;
+    p.counter = counters + programs++;
+    p.split_counters = counters + kPrograms;
+    p.status = status;
+    cudaError_t e = cudaFuncSetAttribute(ns_program, cudaFuncAttributeMaxDynamicSharedMemorySize, kOpSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)std::min(sms, items));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kOpSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;   // its CTAs wait for one another
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, ns_program, p);
+    start();
+    return e;
+  }
+
+ private:
+  const __half* base_[kMaxMaps];
+  int box_[kMaxMaps];
+};
+
 template <int kType>
 cudaError_t launch_input(const InputParams& p, cudaStream_t stream) {
   ns_norm<kType><<<p.blocks, kNormThreads, 0, stream>>>(p);
@@ -586,6 +1094,7 @@ cudaError_t launch_newton_schulz(const NewtonSchulzArgs& a, cudaStream_t stream)
   in.hi = x[0][0];
   in.lo = x[0][1];
   in.ld = l.ld;
+  in.counters = reinterpret_cast<int*>(ws + l.counters);
   in.units = reinterpret_cast<__half*>(ws + l.units);
   // the linear terms are products with a diagonal tile as long as all its
   // values and B / a stay well within fp16, else an epilogue adds them
@@ -599,6 +1108,72 @@ cudaError_t launch_newton_schulz(const NewtonSchulzArgs& a, cudaStream_t stream)
 
   const bool tall = a.rows > a.cols;
   const int small = l.small, large = std::max(a.rows, a.cols);
+  const Halves mA{A[0], A[1], small, small, l.lda}, mB{B[0], B[1], small, small, l.lda};
+  auto X = [&](int i, bool low) { return Halves{x[i & 1][0], low ? x[i & 1][1] : nullptr, a.rows, a.cols, l.ld}; };
+  const Halves one{in.units, nullptr, kUnit, kUnit, kUnit}, ratio{in.units + kUnit * kUnit, in.units + 2 * kUnit * kUnit, kUnit, kUnit, kUnit};
+  Builder build(in.counters, a.status, sms, stream);
+  // b A + c A A + diag: b / c A by the diagonal tile
+  auto square = [&](const Halves& from, const Halves& to, float c, float diag) {
+    Op& op = build.add(from, false, from, false, small, small, small, true);
+    op.extra = l.halves ? 3 : 2;
+    op.unit_steps = kOpN / kStep;
+    op.of[0] = op.of[1] = op.left[0];
+    op.unit[0] = op.unit[2] = build.right(ratio.hi, ratio, false);
+    op.unit[1] = build.right(ratio.lo, ratio, false);
+    op.of[2] = op.left[2];
+    op.scale = c * kInvScale;
+    op.diag = diag * kScale;
+    build.into(op, to);
+  };
+  const long long x_tiles = (long long)div_up(a.rows, kOpM) * div_up(a.cols, kOpN);
+  const bool in_order = fold && x_tiles <= (small <= 256 ? 4 : 2) * sms;
+
+  if (in_order) {
+    // everything in one launch (of 8 steps each)
+    for (int i = 0; i < a.steps; ++i) {
+      if (!build.room(3)) NS_TRY(build.launch());
+      // A
+      Op& gram = build.add(X(i, l.halves), tall, X(i, l.halves), tall, small, small, large, true);
+      // K in parts: a part's steps against the reading of the parts
+      // (the parts cost about 24 steps' time, their reading one step each)
+      const int all = gram.products * gram.steps;
+      const int parts = std::min({l.parts, sms / gram.tiles, (int)(std::sqrt((double)all) + 0.5), gram.steps / 2});
+      if (parts > 1 && all / parts + parts + 24 < all && build.splits + gram.tiles <= kCounters) {
+        gram.parts = parts;
+        gram.part = reinterpret_cast<float*>(ws + l.part);
+        gram.ld_part = l.ldp;
+        gram.split_counter = build.splits;
+        build.splits += gram.tiles;
+      }
+      build.into(gram, mA);
+      // B: with a on its diagonal, or divided by a
+      square(mA, mB, l.halves ? a.c : a.c / a.a, l.halves ? a.a : 0.f);
+      // X
+      Op& op = tall ? build.add(X(i, l.halves), false, mB, false, a.rows, a.cols, small, false)
+                    : build.add(mB, false, X(i, l.halves), true, a.rows, a.cols, small, false);
+      if (!l.halves) {
+        const Halves from = X(i, true);
+        op.extra = 2;
+        op.unit_is_left = !tall;
+        op.unit_steps = (tall ? kOpN : kOpM) / kStep;
+        op.unit[0] = op.unit[1] = tall ? build.right(one.hi, one, false) : build.left(one.hi, one, false);
+        op.of[0] = tall ? build.left(from.hi, from, false) : build.right(from.hi, from, true);
+        op.of[1] = tall ? build.left(from.lo, from, false) : build.right(from.lo, from, true);
+        op.scale *= a.a;
+      }
+      if (i + 1 < a.steps) {
+        build.into(op, X(i + 1, true));
+      } else {
+        op.out = static_cast<__nv_bfloat16*>(a.out);
+        op.ld_out = a.cols;
+        op.vec = a.cols % 8 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
+        op.scale *= kInvScale;
+        build.place(op);
+      }
+    }
+    return build.launch();
+  }
+
   Product q{};
   q.status = a.status;
   for (int i = 0; i < a.steps; ++i) {
