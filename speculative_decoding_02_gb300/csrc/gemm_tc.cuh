@@ -20,7 +20,9 @@
 // epilogue adds it, rounded, to its sums while the next one fills (two of them).
 //
 // A policy P (a kernel parameter, so its tensor maps are too) has
-//   kPair, kN, kBoxBytes (shared memory of an epilogue warp, a multiple of
+//   kPair, kN, kSelf (a product of one matrix with itself, from halves: a() and
+//     b() are its high and low half, the sum is that of a a^T, a b^T and b a^T),
+//     kBoxBytes (shared memory of an epilogue warp, a multiple of
 //     1024), kExtraBytes (of the CTA); status, bf16, chunk;
 //   Counts counts()                     read once a thread, behind pdl_wait
 //   bool tile(counts, unit, units, i, Tile&)  the i-th tile of a unit, same
@@ -85,6 +87,7 @@ struct Shape {
   static constexpr uint32_t kTmemCols = 2 * P::kN;
   static_assert(kStages >= 3 && kSmem <= kMaxSmem, "shared memory");
   static_assert(P::kN == 64 || P::kN == 128 || P::kN == 256, "columns of a tile");
+  static_assert(!P::kSelf || kBRows == kRows, "the halves' tiles are alike");
   static_assert(!P::kPair || P::kN >= 128, "a CTA's share of B is 64 columns or more");
   static_assert(P::kBoxBytes % 1024 == 0, "128-byte swizzled boxes");
 };
@@ -255,8 +258,15 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             const uint64_t ad = ad0 + s * (S::kStageBytes / 16), bd = bd0 + s * (S::kStageBytes / 16);
             if (elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma<kPair>(tmem + buf * P::kN, ad + kk * da, bd + kk * db, idesc, k != kf || kk != 0);
+              for (int kk = 0; kk < 4; ++kk) {
+                if constexpr (P::kSelf) {
+                  mma<kPair>(tmem + buf * P::kN, ad + kk * da, ad + kk * da, idesc, k != kf || kk != 0);
+                  mma<kPair>(tmem + buf * P::kN, ad + kk * da, bd + kk * db, idesc, 1);
+                  mma<kPair>(tmem + buf * P::kN, bd + kk * db, ad + kk * da, idesc, 1);
+                } else {
+                  mma<kPair>(tmem + buf * P::kN, ad + kk * da, bd + kk * db, idesc, k != kf || kk != 0);
+                }
+              }
               commit<kPair>(&bars->empty[s]);
             }
             __syncwarp();

@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(128) ce_gather(const GatherParams p) {
 // sum of 2^(z log2 e - maximum) of its 256 columns.
 struct LossTiles {
   CUtensorMap h, w;
-  static constexpr bool kPair = true;
+  static constexpr bool kPair = true, kSelf = false;
   static constexpr int kN = 256, kBoxBytes = 0, kExtraBytes = 2 * 4 * kRows * 8;
   using Counts = int;
   int* status;
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(256) ce_combine(const CombineParams p) {
 // is kept apart and added to dh).
 struct SlopeTiles {
   CUtensorMap h, w, out;
-  static constexpr bool kPair = true;
+  static constexpr bool kPair = true, kSelf = false;
   static constexpr int kN = 256, kBoxBytes = kStoreBox, kExtraBytes = 0;
   using Counts = int;
   int* status;
@@ -428,7 +428,7 @@ struct SlopeTiles {
 // same time.
 struct GradTiles {
   CUtensorMap s_k, s_mn, w, h, dh, dW;
-  static constexpr bool kPair = true;
+  static constexpr bool kPair = true, kSelf = false;
   static constexpr int kN = 256, kBoxBytes = kStoreBox, kExtraBytes = 0;
   struct Counts {
     int mt, splits, kw, tx, tw, shared;

@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kNormThreads) ns_split(const InputParams p) {
 // ---------------------------------------------------------------------------
 // the products
 // ---------------------------------------------------------------------------
-enum Kind { kGram, kGramPart, kSquare, kStepX, kLastX };
+enum Kind { kGram, kGramPart, kGramSelf, kSquare, kStepX, kLastX };
 
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
   const __half2 v = __floats2half2_rn(a, b);
@@ -199,15 +199,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 
 // kGram    A = X X^T (or X^T X), lower tiles and their mirrors
-// kGramPart  the same over a part of K, fp32
+// kGramPart  the same over a part of K, fp32;  kGramSelf  of one tile, from halves
 // kSquare  B = b A + c A A, lower tiles and their mirrors
 // kStepX   X' = a X + B X (or X B) in halves;  kLastX  in bf16
 template <bool kPairs, int kTileN, Kind kKind>
 struct NsTiles {
-  static constexpr bool kPair = kPairs;
+  static constexpr bool kPair = kPairs, kSelf = kKind == kGramSelf;
   static constexpr int kN = kTileN, kM = kPairs ? 256 : 128, kCols = kTileN / 4;
   static constexpr int kBoxBytes = kStoreBox, kExtraBytes = 0;
-  static constexpr bool kSymmetric = kKind == kGram || kKind == kGramPart || kKind == kSquare;
+  static constexpr bool kSymmetric = kKind == kGram || kKind == kGramPart || kKind == kGramSelf || kKind == kSquare;
   using Counts = int;
 
   CUtensorMap left, left_low, right, right_low;
@@ -274,6 +274,7 @@ struct NsTiles {
     return Src{(kKind == kSquare ? u == 2 : u == 1) ? &left_low : &left, t.m0, t.n0 + j};
   }
   __device__ Src b(const Tile& t, int k) const {
+    if (kSelf) return Src{&left_low, t.n0, (t.k0 + k) * kStep};
     const int q = k / t.kind;
     if (q < products) return Src{q == 1 ? &right_low : &right, t.n0, (t.k0 + k - q * t.kind) * kStep};
     k -= products * t.kind;
@@ -349,7 +350,7 @@ struct NsTiles {
   __device__ void epilogue(const Epi& e, const Tile& t, float (&v)[kCols]) const {
     const int row = t.m0 + e.row, col = t.n0 + e.col;
     uint32_t w[kCols / 2];
-    if constexpr (kKind == kGramPart) {
+    if constexpr (kKind == kGramPart || kKind == kGramSelf) {
       static_assert(kCols == 64, "parts go out by boxes");
       store_fp32(e, &out0, v, col, cols, t.m0 + e.row0, rows, t.part, false);
       return;
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(256) ns_join(const JoinParams p) {
   const int r = blockIdx.y * 16 + threadIdx.x / 16, c = blockIdx.x * 16 + threadIdx.x % 16;
   if (r >= p.n || c >= p.n || c / 256 > r / 256) return;
   float s = 0.f;
-#pragma unroll 8
+#pragma unroll 19
   for (int i = 0; i < p.parts; ++i) s += p.part[((size_t)i * p.n + r) * p.cols + c];
   s *= kInvScale;
   const __half h = __float2half_rn(s), l = __float2half_rn(s - __half2float(h));
@@ -866,7 +867,7 @@ struct Product {
   float* part;
   long long ld_part;
   int parts;
-  float a, b, c;
+  float a, b, c, diag;
   int* status;
 };
 
@@ -885,14 +886,14 @@ cudaError_t launch_product(const Product& q, cudaStream_t stream) {
   p.left_low = p.left;
   p.right_low = p.right;
   p.products = 1;
-  if (q.left_low && q.right_low) p.products = 3;
+  if (q.left_low && q.right_low && kKind != kGramSelf) p.products = 3;
   if (q.left_low)
     NS_TRY(map_16bit(q.left_low, false, q.left_rows, q.left_cols, q.left_ld, q.left_mn ? kStep : kRows, &p.left_low));
   if (q.right_low)
     NS_TRY(map_16bit(q.right_low, false, q.right_rows, q.right_cols, q.right_ld, q.right_mn ? kStep : Shape<P>::kBRows,
                      &p.right_low));
   p.unit = p.unit_low = p.left;
-  p.extra = kKind == kGramPart || !q.unit ? 0 : q.extra;
+  p.extra = q.unit ? q.extra : 0;
   p.unit_is_left = q.unit_is_left;
   if (p.extra) {
     const int box = q.unit_is_left ? kRows : Shape<P>::kBRows;
@@ -901,7 +902,7 @@ cudaError_t launch_product(const Product& q, cudaStream_t stream) {
   }
   p.status = q.status;
   p.bf16 = false;
-  p.chunk = 8;
+  p.chunk = kKind == kGramSelf ? 4 : 8;
   p.left_mn = q.left_mn;
   p.right_mn = q.right_mn;
   p.rows = q.rows;
@@ -909,7 +910,8 @@ cudaError_t launch_product(const Product& q, cudaStream_t stream) {
   p.mt = div_up(q.rows, P::kM);
   p.nt = div_up(q.cols, P::kN);
   p.steps = div_up(q.K, kStep);
-  p.parts = kKind == kGramPart ? q.parts : 1;
+  constexpr bool kParts = kKind == kGramPart || kKind == kGramSelf;
+  p.parts = kParts ? q.parts : 1;
   p.in0 = q.in0; p.in1 = q.in1;
   p.to0 = q.to0; p.to1 = q.to1;
   p.out = q.out;
@@ -917,9 +919,10 @@ cudaError_t launch_product(const Product& q, cudaStream_t stream) {
   p.ld_out = q.ld_out;
   p.vec = kKind == kLastX && q.ld_out % 8 == 0 && q.cols % 8 == 0 && reinterpret_cast<uintptr_t>(q.out) % 16 == 0;
   p.ca = q.a; p.cb = q.b; p.cc = q.c;
+  p.diag = q.diag;
   p.out0 = p.out1 = p.left;
   if (P::kCols == 64) {
-    if (kKind == kGramPart) {
+    if (kParts) {
       NS_TRY(map_fp32(q.part, q.parts, q.rows, q.ld_part, &p.out0));
     } else if (kKind == kLastX) {
       if (p.vec) NS_TRY(map_16bit(q.out, true, q.rows, q.cols, q.ld_out, kBoxRows, &p.out0));
@@ -1176,13 +1179,17 @@ cudaError_t launch_newton_schulz(const NewtonSchulzArgs& a, cudaStream_t stream)
 
   Product q{};
   q.status = a.status;
-  for (int i = 0; i < a.steps; ++i) {
-    __half *hi = x[i & 1][0], *lo = x[i & 1][1];
-    // A
+  // A by parts of K, where the tiles of 256 leave most pairs idle and each part is still 16 steps or more
+  auto gram_parts = [&] {
+    const int mt = div_up(small, 256), tiles = mt * (mt + 1) / 2;
+    return std::min({l.parts, sms / 2 / tiles, div_up(large, kStep) / 16});
+  };
+  auto gram = [&](const Halves& from) {
     q.unit = q.unit_low = q.in0 = q.in1 = nullptr;
+    q.diag = 0.f;
     q.c = 1.f;
-    q.left = q.right = hi;
-    q.left_low = q.right_low = l.halves ? lo : nullptr;
+    q.left = q.right = from.hi;
+    q.left_low = q.right_low = from.lo;
     q.left_rows = q.right_rows = a.rows;
     q.left_cols = q.right_cols = a.cols;
     q.left_ld = q.right_ld = l.ld;
@@ -1192,21 +1199,108 @@ cudaError_t launch_newton_schulz(const NewtonSchulzArgs& a, cudaStream_t stream)
     q.to0 = A[0];
     q.to1 = A[1];
     q.ld = l.lda;
-    // K in parts where the tiles of 256 leave most pairs idle and each part is
-    // still 16 steps or more
-    const int mt = div_up(small, 256), tiles = mt * (mt + 1) / 2;
-    const int parts = std::min({l.parts, sms / 2 / tiles, div_up(large, kStep) / 16});
-    if (parts > 1) {
-      q.part = reinterpret_cast<float*>(ws + l.part);
-      q.ld_part = l.ldp;
-      q.parts = parts;
-      NS_TRY((launch_product<true, 256, kGramPart>(q, stream)));
-      JoinParams j{q.part, parts, small, l.ldp, l.lda, A[0], A[1]};
-      NS_TRY(launch_pdl(ns_join, dim3((unsigned)div_up(small, 16), (unsigned)div_up(small, 16)), dim3(256), 0, stream, j));
+    q.parts = gram_parts();
+    if (q.parts <= 1) return choose_product<kGram>(q, sms, stream);
+    q.part = reinterpret_cast<float*>(ws + l.part);
+    q.ld_part = l.ldp;
+    // (of one tile's halves each is read once, not three times)
+    if (from.lo && small <= 256) NS_TRY((launch_product<true, 256, kGramSelf>(q, stream)));
+    else NS_TRY((launch_product<true, 256, kGramPart>(q, stream)));
+    JoinParams j{q.part, q.parts, small, l.ldp, l.lda, A[0], A[1]};
+    return launch_pdl(ns_join, dim3((unsigned)div_up(small, 16), (unsigned)div_up(small, 16)), dim3(256), 0, stream, j);
+  };
+  // X' = X P or P X
+  auto times = [&](const Halves& from, const Halves& P, int i, bool last) {
+    Product s = q;
+    if (tall) {
+      s.left = from.hi; s.left_low = from.lo; s.left_rows = a.rows; s.left_cols = a.cols; s.left_ld = l.ld;
+      s.right = P.hi; s.right_low = P.lo; s.right_rows = s.right_cols = small; s.right_ld = l.lda;
+      s.right_mn = false;
     } else {
-      NS_TRY(choose_product<kGram>(q, sms, stream));
+      s.left = P.hi; s.left_low = P.lo; s.left_rows = s.left_cols = small; s.left_ld = l.lda;
+      s.right = from.hi; s.right_low = from.lo; s.right_rows = a.rows; s.right_cols = a.cols; s.right_ld = l.ld;
+      s.right_mn = true;
     }
-    // B
+    s.left_mn = false;
+    s.unit = s.unit_low = s.in0 = s.in1 = nullptr;
+    s.rows = a.rows;
+    s.cols = a.cols;
+    s.K = small;
+    s.a = a.a;
+    if (l.halves) {
+      s.a = 1.f;
+    } else if (fold) {
+      s.unit = in.units;
+      s.extra = 2;
+      s.unit_is_left = !tall;
+    }
+    if (!fold) {
+      s.a = a.a;
+      s.in0 = from.hi;
+      s.in1 = from.lo;
+    }
+    s.ld = l.ld;
+    s.to0 = x[1 - (i & 1)][0];
+    s.to1 = x[1 - (i & 1)][1];
+    if (!last) return choose_product<kStepX>(s, sms, stream);
+    s.out = static_cast<__nv_bfloat16*>(a.out);
+    s.ld_out = a.cols;
+    return choose_product<kLastX>(s, sms, stream);
+  };
+
+  // A long X is read and written once for several steps: X_k = X_0 P with P a
+  // polynomial in A alone, whose products are small.  By two and three steps at a
+  // time A's error stays far below what matters (2e-5 of nearly singular
+  // updates; by five at a time they diverge), so every group of steps starts
+  // from the Gram matrix of its own X.
+  const bool in_groups = fold && l.halves && std::fabs(a.a) < 3.9f;   // (P's values, up to a^3, stay within fp16)
+  if (in_groups) {
+    const Halves T{reinterpret_cast<__half*>(ws + l.more[0][0]), reinterpret_cast<__half*>(ws + l.more[0][1]), small, small, l.lda};
+    const Halves A2{reinterpret_cast<__half*>(ws + l.more[1][0]), reinterpret_cast<__half*>(ws + l.more[1][1]), small, small, l.lda};
+    const Halves P[2] = {{reinterpret_cast<__half*>(ws + l.more[2][0]), reinterpret_cast<__half*>(ws + l.more[2][1]), small, small, l.lda},
+                         {reinterpret_cast<__half*>(ws + l.more[3][0]), reinterpret_cast<__half*>(ws + l.more[3][1]), small, small, l.lda}};
+    auto small_product = [&](const Halves& left, const Halves& right, const Halves& to) -> Op& {
+      Op& op = build.add(left, false, right, false, small, small, small, true);
+      build.into(op, to);
+      return op;
+    };
+    const int groups = (a.steps + 2) / 3;
+    for (int g = 0, left = a.steps; g < groups; ++g) {
+      const int n = left / (groups - g);   // (the earlier ones, where X is worst conditioned, are the shorter ones)
+      left -= n;
+      NS_TRY(gram(X(g, true)));
+      const Halves* from = &mA;
+      int at = 0;                          // P's buffer
+      for (int k = 0; k < n; ++k) {
+        const Halves& Q = k == 0 ? P[0] : mB;
+        square(*from, Q, a.c, a.a);
+        if (k + 1 < n) {
+          const Halves* to = from == &mA ? &A2 : &mA;
+          Op& t = small_product(*from, Q, T);
+          if (k > 0) {
+            // beside it, by the CTAs that it leaves idle
+            Op& p = small_product(P[at], Q, P[1 - at]);
+            build.items = std::max(build.items, 2 * t.tiles);
+            p.base = t.base;
+            p.first = t.tiles % std::min(sms, build.items);
+            at = 1 - at;
+          }
+          small_product(T, Q, *to);
+          from = to;
+        } else if (k > 0) {
+          small_product(P[at], Q, P[1 - at]);
+          at = 1 - at;
+        }
+      }
+      NS_TRY(build.launch());
+      NS_TRY(times(X(g, true), P[at], g, g + 1 == groups));
+    }
+    return cudaSuccess;
+  }
+
+  for (int i = 0; i < a.steps; ++i) {
+    NS_TRY(gram(X(i, l.halves)));
+    // B: with a on its diagonal, or divided by a
     q.left = q.right = A[0];
     q.left_low = q.right_low = A[1];
     q.left_rows = q.right_rows = q.left_cols = q.right_cols = small;
@@ -1214,11 +1308,12 @@ cudaError_t launch_newton_schulz(const NewtonSchulzArgs& a, cudaStream_t stream)
     q.left_mn = q.right_mn = false;
     q.K = small;
     if (fold) {
-      q.unit = in.units + kUnit * kUnit;
-      q.unit_low = in.units + 2 * kUnit * kUnit;
+      q.unit = ratio.hi;
+      q.unit_low = ratio.lo;
       q.extra = l.halves ? 3 : 2;
       q.unit_is_left = false;
-      q.c = a.c / a.a;
+      q.c = l.halves ? a.c : a.c / a.a;
+      q.diag = l.halves ? a.a * kScale : 0.f;
     } else {
       q.in0 = A[0];
       q.in1 = A[1];
@@ -1228,38 +1323,7 @@ cudaError_t launch_newton_schulz(const NewtonSchulzArgs& a, cudaStream_t stream)
     q.to0 = B[0];
     q.to1 = B[1];
     NS_TRY(choose_product<kSquare>(q, sms, stream));
-    // X
-    Product s = q;
-    if (tall) {
-      s.left = hi; s.left_low = lo; s.left_rows = a.rows; s.left_cols = a.cols; s.left_ld = l.ld;
-      s.right = B[0]; s.right_low = B[1];
-    } else {
-      s.left = B[0]; s.left_low = B[1];
-      s.right = hi; s.right_low = lo; s.right_rows = a.rows; s.right_cols = a.cols; s.right_ld = l.ld;
-      s.right_mn = true;
-    }
-    s.rows = a.rows;
-    s.cols = a.cols;
-    s.a = a.a;
-    if (fold) {
-      s.unit = in.units;
-      s.unit_low = nullptr;
-      s.extra = 2;
-      s.unit_is_left = !tall;
-    } else {
-      s.in0 = hi;
-      s.in1 = lo;
-    }
-    s.ld = l.ld;
-    s.to0 = x[1 - (i & 1)][0];
-    s.to1 = x[1 - (i & 1)][1];
-    if (i + 1 < a.steps) {
-      NS_TRY(choose_product<kStepX>(s, sms, stream));
-    } else {
-      s.out = static_cast<__nv_bfloat16*>(a.out);
-      s.ld_out = a.cols;
-      NS_TRY(choose_product<kLastX>(s, sms, stream));
-    }
+    NS_TRY(times(X(i, true), mB, i, i + 1 == a.steps));
   }
   return cudaSuccess;
 }

@@ -91,7 +91,7 @@ def _one_step_bound(M, coefficients, eps):
 
 SHAPES = [(1, 1), (1, 40), (40, 1), (2, 3), (16, 16), (64, 300), (300, 64), (128, 128), (129, 257), (257, 129), (256, 512),
           (100, 5000), (5000, 100), (513, 513), (777, 1000), (1000, 777), (1280, 1536), (20011, 256), (256, 20011),
-          (30000, 72)]
+          (30000, 72), (33000, 200), (300, 17001), (20000, 500)]
 
 
 @pytest.mark.parametrize("m,n", SHAPES)
@@ -133,7 +133,7 @@ def test_singular_values():
 
 @pytest.mark.parametrize("steps,coefficients", [(1, (1.5, -0.5, 0.0)), (12, (1.5, -0.5, 0.0)), (3, (1.875, -1.25, 0.375)),
                                                 (10, MUON), (7, (2.0, -1.5, 0.5))])
-@pytest.mark.parametrize("m,n", [(96, 200), (400, 136)])
+@pytest.mark.parametrize("m,n", [(96, 200), (400, 136), (90001, 64), (400, 20000), (600, 530)])
 def test_other_coefficients(steps, coefficients, m, n):
     M = _update(m, n, torch.float32, 3)
     got = ds.newton_schulz(M, steps=steps, coefficients=coefficients).to(F64)
