@@ -27,7 +27,7 @@
 //   Counts counts()                     read once a thread, behind pdl_wait
 //   bool tile(counts, unit, units, i, Tile&)  the i-th tile of a unit, same
 //     for all its threads; false when there is none
-//   Src a(tile, k), b(tile, k)          map and coordinates of step k
+//   int segments(tile), Segment segment(tile, i)  where the operands' steps of K are
 //   void epilogue(Epi&, tile, acc)      every epilogue thread, converged
 //   void prefetch()                     of the tensor maps
 #pragma once
@@ -57,9 +57,12 @@ struct Tile {
   int kind, part, k0;  // the policy's own
 };
 
-struct Src {
-  const CUtensorMap* map;
-  int mn, k;           // coordinates of the tile's first row (column) and of the step's first k
+// Steps of K that follow one another in both operands: of either the map and the
+// coordinates of the tile's first row (column) and of the first k.
+struct Segment {
+  const CUtensorMap *a, *b;
+  int am, ak, bn, bk;
+  int steps;
 };
 
 struct Epi {
@@ -194,31 +197,35 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     bool ok = true;
     Tile t;
     for (int n = 0; ok && p.tile(counts, unit, units, n, t); ++n) {
-      for (int k = 0; k < t.steps; ++k, ++i) {
-        ok = warp_wait(&bars->empty[s], phase, abort, p.status);
-        if (!ok) break;
-        const Src a = p.a(t, k), b = p.b(t, k);
-        if (elect_one()) {
-          uint32_t dst = stages + s * S::kStageBytes;
-          const uint32_t full = kPair ? in_cta(&bars->full[s], 0) : smem_u32(&bars->full[s]);
-          if (rank == 0) mbar_arrive_expect_tx(&bars->full[s], (kPair ? 2 : 1) * S::kStageBytes);
-          const int am = a.mn + rank * kRows, bn = b.mn + rank * S::kBRows;
-          if (t.a_mn) {
+      const int segments = p.segments(t);
+      for (int q = 0; q < segments && ok; ++q) {
+        Segment g = p.segment(t, q);
+        g.am += rank * kRows;
+        g.bn += rank * S::kBRows;
+        for (int k = 0; k < g.steps; ++k, ++i, g.ak += kStep, g.bk += kStep) {
+          ok = warp_wait(&bars->empty[s], phase, abort, p.status);
+          if (!ok) break;
+          if (elect_one()) {
+            uint32_t dst = stages + s * S::kStageBytes;
+            const uint32_t full = kPair ? in_cta(&bars->full[s], 0) : smem_u32(&bars->full[s]);
+            if (rank == 0) mbar_arrive_expect_tx(&bars->full[s], (kPair ? 2 : 1) * S::kStageBytes);
+            if (t.a_mn) {
 #pragma unroll
-            for (int j = 0; j < kRows / 64; ++j) copy_box<kPair>(dst + j * 8192, a.map, am + j * 64, a.k, full);
-          } else {
-            copy_box<kPair>(dst, a.map, a.k, am, full);
-          }
-          dst += S::kABytes;
-          if (t.b_mn) {
+              for (int j = 0; j < kRows / 64; ++j) copy_box<kPair>(dst + j * 8192, g.a, g.am + j * 64, g.ak, full);
+            } else {
+              copy_box<kPair>(dst, g.a, g.ak, g.am, full);
+            }
+            dst += S::kABytes;
+            if (t.b_mn) {
 #pragma unroll
-            for (int j = 0; j < S::kBRows / 64; ++j) copy_box<kPair>(dst + j * 8192, b.map, bn + j * 64, b.k, full);
-          } else {
-            copy_box<kPair>(dst, b.map, b.k, bn, full);
+              for (int j = 0; j < S::kBRows / 64; ++j) copy_box<kPair>(dst + j * 8192, g.b, g.bn + j * 64, g.bk, full);
+            } else {
+              copy_box<kPair>(dst, g.b, g.bk, g.bn, full);
+            }
           }
+          __syncwarp();
+          if (++s == S::kStages) s = 0, phase ^= 1;
         }
-        __syncwarp();
-        if (++s == S::kStages) s = 0, phase ^= 1;
       }
     }
     // every stage is consumed before the CTA leaves (on a timeout: as far as

@@ -275,8 +275,8 @@ struct LossTiles {
     t.a_mn = t.b_mn = false;
     return true;
   }
-  __device__ Src a(const Tile& t, int k) const { return Src{&h, t.m0, k * kStep}; }
-  __device__ Src b(const Tile& t, int k) const { return Src{&w, t.n0, k * kStep}; }
+  __device__ int segments(const Tile&) const { return 1; }
+  __device__ Segment segment(const Tile& t, int) const { return Segment{&h, &w, t.m0, 0, t.n0, 0, t.steps}; }
 
   __device__ void epilogue(const Epi& e, const Tile& t, float (&z)[64]) const {
     const int left = V - (t.n0 + e.col);
@@ -391,8 +391,8 @@ struct SlopeTiles {
     t.a_mn = t.b_mn = false;
     return true;
   }
-  __device__ Src a(const Tile& t, int k) const { return Src{&h, t.m0, k * kStep}; }
-  __device__ Src b(const Tile& t, int k) const { return Src{&w, v0 + t.n0, k * kStep}; }
+  __device__ int segments(const Tile&) const { return 1; }
+  __device__ Segment segment(const Tile& t, int) const { return Segment{&h, &w, t.m0, 0, v0 + t.n0, 0, t.steps}; }
 
   __device__ void epilogue(const Epi& e, const Tile& t, float (&z)[64]) const {
     const RowInfo r = info[t.m0 + e.row];
@@ -497,13 +497,10 @@ struct GradTiles {
     t.a_mn = t.b_mn = true;
     return true;
   }
-  __device__ Src a(const Tile& t, int k) const {
-    if (t.kind == 1) return Src{&s_mn, t.m0, k * kStep};
-    return Src{&s_k, t.m0, (t.k0 + k) * kStep};
-  }
-  __device__ Src b(const Tile& t, int k) const {
-    if (t.kind == 1) return Src{&h, t.n0, k * kStep};
-    return Src{&w, t.n0, v0 + (t.k0 + k) * kStep};
+  __device__ int segments(const Tile&) const { return 1; }
+  __device__ Segment segment(const Tile& t, int) const {
+    if (t.kind == 1) return Segment{&s_mn, &h, t.m0, 0, t.n0, 0, t.steps};
+    return Segment{&s_k, &w, t.m0, t.k0 * kStep, t.n0, v0 + t.k0 * kStep, t.steps};
   }
 
   __device__ void epilogue(const Epi& e, const Tile& t, float (&v)[64]) const {

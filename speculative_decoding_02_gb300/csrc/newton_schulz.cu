@@ -256,31 +256,24 @@ struct NsTiles {
     t.n0 = n * kN;
     const int each = div_up(steps, parts);
     t.part = part;
-    t.kind = max(1, min(each, steps - part * each));   // steps of one product
+    t.kind = max(0, min(each, steps - part * each));   // steps of one product
     t.k0 = part * each;
-    t.steps = max(0, min(each, steps - t.k0)) * products + extra * unit_steps();
+    t.steps = t.kind * products + extra * unit_steps();
     t.a_mn = left_mn;
     t.b_mn = right_mn;
     return true;
   }
   __device__ int unit_steps() const { return (unit_is_left ? kM : kN) / kStep; }
-  __device__ Src a(const Tile& t, int k) const {
-    const int q = k / t.kind;
-    if (q < products) return Src{q == 2 ? &left_low : &left, t.m0, (t.k0 + k - q * t.kind) * kStep};
-    k -= products * t.kind;
-    const int u = k / unit_steps(), j = (k - u * unit_steps()) * kStep;
-    if (unit_is_left) return Src{&unit, 0, j};
-    // A with b / c, its low half, A's low half with b / c; X's halves
-    return Src{(kKind == kSquare ? u == 2 : u == 1) ? &left_low : &left, t.m0, t.n0 + j};
-  }
-  __device__ Src b(const Tile& t, int k) const {
-    if (kSelf) return Src{&left_low, t.n0, (t.k0 + k) * kStep};
-    const int q = k / t.kind;
-    if (q < products) return Src{q == 1 ? &right_low : &right, t.n0, (t.k0 + k - q * t.kind) * kStep};
-    k -= products * t.kind;
-    const int u = k / unit_steps(), j = (k - u * unit_steps()) * kStep;
-    if (unit_is_left) return Src{u == 1 ? &right_low : &right, t.n0, t.m0 + j};
-    return Src{kKind == kSquare && u == 1 ? &unit_low : &unit, 0, j};
+  __device__ int segments(const Tile&) const { return products + extra; }
+  __device__ Segment segment(const Tile& t, int i) const {
+    const int k = t.k0 * kStep;
+    if (kSelf) return Segment{&left, &left_low, t.m0, k, t.n0, k, t.kind};
+    if (i < products) return Segment{i == 2 ? &left_low : &left, i == 1 ? &right_low : &right, t.m0, k, t.n0, k, t.kind};
+    const int u = i - products;
+    if (unit_is_left) return Segment{&unit, u == 1 ? &right_low : &right, 0, 0, t.n0, t.m0, unit_steps()};
+    // A with b / c, with its low half, A's low half with b / c; X's halves
+    return Segment{(kKind == kSquare ? u == 2 : u == 1) ? &left_low : &left, kKind == kSquare && u == 1 ? &unit_low : &unit,
+                   t.m0, t.n0, 0, 0, unit_steps()};
   }
 
   // 8 values of a row, zeros outside the matrix (whose rows are padded to 8)
@@ -407,22 +400,47 @@ struct JoinParams {
   long long cols, ld;
   __half *A, *low;       // halves (low: may be null)
 };
+// A row a block: 64 threads take 4 columns each, four groups of them every fourth part.
 __global__ void __launch_bounds__(256) ns_join(const JoinParams p) {
+  __shared__ float4 sums[3][64];
   pdl_trigger();
   pdl_wait();
-  const int r = blockIdx.y * 16 + threadIdx.x / 16, c = blockIdx.x * 16 + threadIdx.x % 16;
-  if (r >= p.n || c >= p.n || c / 256 > r / 256) return;
-  float s = 0.f;
-#pragma unroll 19
-  for (int i = 0; i < p.parts; ++i) s += p.part[((size_t)i * p.n + r) * p.cols + c];
-  s *= kInvScale;
-  const __half h = __float2half_rn(s), l = __float2half_rn(s - __half2float(h));
-  const size_t at = (size_t)r * p.ld + c, mirror = (size_t)c * p.ld + r;
-  p.A[at] = h;
-  if (p.low != nullptr) p.low[at] = l;
-  if (c / 256 < r / 256) {
-    p.A[mirror] = h;
-    if (p.low != nullptr) p.low[mirror] = l;
+  const int r = blockIdx.x, g = threadIdx.x / 64, x = threadIdx.x % 64;
+  const size_t plane = (size_t)p.n * p.cols;
+  for (int c0 = 0; c0 < p.n && c0 / 256 <= r / 256; c0 += 256) {
+    const int c = c0 + 4 * x;
+    const bool on = c < p.n;   // (rows of the parts are padded to 8)
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float* from = p.part + (size_t)r * p.cols + c;
+    if (on) {
+#pragma unroll 10
+      for (int i = g; i < p.parts; i += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(from + i * plane);
+        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+      }
+    }
+    __syncthreads();   // (the sums before have been read)
+    if (g > 0) sums[g - 1][x] = s;
+    __syncthreads();
+    if (g > 0 || !on) continue;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const float4 v = sums[i][x];
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+    const float v[4] = {s.x * kInvScale, s.y * kInvScale, s.z * kInvScale, s.w * kInvScale};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (c + j >= p.n) break;
+      const __half h = __float2half_rn(v[j]), l = __float2half_rn(v[j] - __half2float(h));
+      const size_t at = (size_t)r * p.ld + c + j, mirror = (size_t)(c + j) * p.ld + r;
+      p.A[at] = h;
+      if (p.low != nullptr) p.low[at] = l;
+      if ((c + j) / 256 < r / 256) {
+        p.A[mirror] = h;
+        if (p.low != nullptr) p.low[mirror] = l;
+      }
+    }
   }
 }
 
@@ -818,13 +836,14 @@ struct Layout {
   bool halves;
 };
 
-long long pad8(long long x) { return (x + 7) / 8 * 8; }
+// Rows start on 128 bytes: copies of rows that straddle such lines take half as long again.
+long long pad_row(long long x) { return (x + 63) / 64 * 64; }
 
 Layout layout(int rows, int cols) {
   Layout l{};
   l.small = std::min(rows, cols);
-  l.ld = pad8(cols);
-  l.lda = l.ldp = pad8(l.small);
+  l.ld = pad_row(cols);
+  l.lda = l.ldp = pad_row(l.small);
   size_t at = 256;
   auto take = [&](size_t bytes) {
     const size_t a = at;
@@ -939,15 +958,18 @@ cudaError_t launch_product(const Product& q, cudaStream_t stream) {
 
 template <Kind kKind>
 cudaError_t choose_product(const Product& q, int sms, cudaStream_t stream) {
-  // time of a product by tiles of a shape: waves of a tile's steps and epilogue (us)
+  // Time of a product by tiles of a shape (us): the waves' steps of K, and the
+  // launch, its first copies and last epilogue.  Measured, fp16: the Gram matrix of
+  // 4096 x 4096 by tiles of 256 x 256, 128 x 128, 128 x 64: 56, 77 and 118; of
+  // 1024 x 1024: 16, 11 and 9.
   constexpr bool sym = kKind == kGram || kKind == kSquare;
   auto cost = [&](int tm, int tn, int units, double step, double more) {
     const double mt = div_up(q.rows, tm), nt = div_up(q.cols, tn);
     const double tiles = sym ? (double)tm / tn * mt * (mt + 1) / 2 : mt * nt;
-    return std::max(1.0, std::ceil(tiles / units)) * (div_up(q.K, kStep) * (q.left_low && q.right_low ? 3 : 1) * step + more);
+    return std::max(1.0, std::ceil(tiles / units)) * div_up(q.K, kStep) * (q.left_low && q.right_low ? 3 : 1) * step + more;
   };
-  const double big = cost(256, 256, sms / 2, 0.34, 2.0), mid = cost(128, 128, sms, 0.17, 1.4),
-               low = cost(128, 64, sms, 0.12, 1.0);
+  const double big = cost(256, 256, sms / 2, 0.36, 9.0), mid = cost(128, 128, sms, 0.28, 6.5),
+               low = cost(128, 64, sms, 0.25, 5.0);
   if (big <= mid && big <= low) return launch_product<true, 256, kKind>(q, stream);
   if (mid <= low) return launch_product<false, 128, kKind>(q, stream);
   return launch_product<false, 64, kKind>(q, stream);
@@ -1207,7 +1229,7 @@ cudaError_t launch_newton_schulz(const NewtonSchulzArgs& a, cudaStream_t stream)
     if (from.lo && small <= 256) NS_TRY((launch_product<true, 256, kGramSelf>(q, stream)));
     else NS_TRY((launch_product<true, 256, kGramPart>(q, stream)));
     JoinParams j{q.part, q.parts, small, l.ldp, l.lda, A[0], A[1]};
-    return launch_pdl(ns_join, dim3((unsigned)div_up(small, 16), (unsigned)div_up(small, 16)), dim3(256), 0, stream, j);
+    return launch_pdl(ns_join, dim3((unsigned)small), dim3(256), 0, stream, j);
   };
   // X' = X P or P X
   auto times = [&](const Halves& from, const Halves& P, int i, bool last) {
