@@ -19,6 +19,7 @@ forms):
 head_status is the word in which the last five record errors without a workspace.
 """
 import ctypes
+import functools
 import math
 import os
 
@@ -721,24 +722,36 @@ def _hidden_args(h, W, tokens, rows):
         raise TypeError(f"W must be {h.dtype}, got {W.dtype}")
     if W.dim() != 2 or W.shape[0] < 1 or W.shape[1] != D:
         raise ValueError(f"W must be [V, {D}] with V >= 1, got {list(W.shape)}")
-    _, _, V, _, _, W_stride, _ = _row_args(W, None, "W")
+    V, (W_stride, step) = W.shape[0], W.stride()
+    if V > _INT_MAX:
+        raise DSparkError(ERR_UNSUPPORTED, f"W of {list(W.shape)}")
+    if D > 1 and step != 1:
+        raise ValueError("W must have entries of a row next to each other")
+    if V == 1:
+        W_stride = D
+    elif W_stride < D:
+        raise ValueError(f"W must not have overlapping rows (strides {W.stride()})")
     _row_vector(_need(tokens, "tokens"), "tokens", lead, dev, torch.int32)
     return dev, lead, N, R, V, D, h_stride, W_stride, dt
+
+
+@functools.lru_cache(maxsize=1024)
+def _hidden_workspace_size(N, V, D, what):
+    return max(int(_load().dspark_linear_ce_workspace_size(N, V, D, what)), 256)
 
 
 def _hidden_workspace(ws, N, V, D, what, dev):
     """A workspace, and the word that errors are recorded in when it is not the caller's."""
     if ws is not None:
         return _need(ws, "ws", torch.uint8, dev), None
-    n = int(_load().dspark_linear_ce_workspace_size(N, V, D, what))
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=dev), _status_without_ws(dev)
+    return torch.empty(_hidden_workspace_size(N, V, D, what), dtype=torch.uint8, device=dev), _status_without_ws(dev)
 
 
 def linear_ce_workspace(N, V, D, device, dh=False, dW=False):
     """A workspace of linear_cross_entropy for N rows (dh and dW False), or of
     linear_cross_entropy_backward for these gradients."""
-    n = int(_load().dspark_linear_ce_workspace_size(N, V, D, int(bool(dh)) + 2 * int(bool(dW))))
-    ws = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+    n = _hidden_workspace_size(N, V, D, int(bool(dh)) + 2 * int(bool(dW)))
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
     ws[:256].zero_()
     return ws
 

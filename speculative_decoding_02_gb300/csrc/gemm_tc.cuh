@@ -30,6 +30,7 @@
 //   int segments(tile), Segment segment(tile, i)  where the operands' steps of K are
 //   void epilogue(Epi&, tile, acc)      every epilogue thread, converged
 //   void prefetch()                     of the tensor maps
+//   void early(unit, rank)              a warp, before pdl_wait
 #pragma once
 
 #include <algorithm>
@@ -120,6 +121,13 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, i
   }
 }
 
+// A box of a matrix into L2; nothing waits for it.
+__device__ __forceinline__ void prefetch_box(const CUtensorMap* map, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1)
+               : "memory");
+}
+
 // One lane of a converged warp, always the same.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -187,6 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   pdl_trigger();
+  if (warp == 0) p.early(unit, rank);
   pdl_wait();
   const typename P::Counts counts = p.counts();
 

@@ -73,6 +73,38 @@ __device__ int choose_splits(int mt, int dt, int kx, int wt, int n, int units, i
   return best;
 }
 
+__device__ int splits_of(const ScanParams& p, int n) {
+  return p.dt > 0 ? choose_splits(div_up(n, 256), p.dt, p.kx, p.wt, n, p.units, p.max_splits) : 1;
+}
+// The slopes' scale, 2 to this, when g is the largest |g_loss| or |g_loss + g_lse|.
+// fp16 holds 2^-24 to 65504: the slopes, at most 2 g, go up to 2^15, so that a
+// probability of 2^-29 keeps its digits (bf16 has fp32's range).
+__device__ int slope_exponent(const ScanParams& p, float g) {
+  int e = 0;
+  if (!p.half || !(g > 0.f && g < INFINITY)) return 0;
+  frexpf(g, &e);   // g < 2^e
+  return max(-100, min(100, 14 - e));
+}
+__device__ __forceinline__ bool in_group(const ScanParams& p, int n) {
+  return p.lens == nullptr || n % p.R < p.lens[n / p.R];
+}
+// Of a row that counts, what the slopes are scaled by.
+__device__ __forceinline__ float upstream(const ScanParams& p, long long n) {
+  if (p.g_loss == nullptr) return 0.f;
+  const float a = p.g_loss[n], b = p.g_lse ? a + p.g_lse[n] : a;
+  return fmaxf(fabsf(a), fabsf(b));
+}
+// The outputs of a row that does not count.
+__device__ __forceinline__ void leave_out(const ScanParams& p, long long n, bool in, int token) {
+  const bool bad = in && token != -1;
+  if (bad) record_status(p.status, DSPARK_ERR_INVALID);
+  if (p.loss) {
+    p.loss[n] = bad ? __int_as_float(0x7fc00000) : 0.f;
+    p.lse[n] = 0.f;
+  }
+  if (p.slot) p.slot[n] = bad ? -2 : -1;
+}
+
 constexpr int kScanThreads = 1024, kScanEach = 8;
 
 // One block: the rows that count, in order.
@@ -92,21 +124,12 @@ __global__ void __launch_bounds__(kScanThreads) ce_scan(const ScanParams p) {
       const long long n = first + j;
       if (n >= p.N) break;
       const int t = p.tokens[n];
-      const bool in = p.lens == nullptr || (int)(n % p.R) < p.lens[n / p.R];
+      const bool in = in_group(p, (int)n);
       if (in && t >= 0 && t < p.V) {
         on |= 1u << j;
-        if (p.g_loss) {
-          const float a = p.g_loss[n], b = p.g_lse ? a + p.g_lse[n] : a;
-          g = fmaxf(g, fmaxf(fabsf(a), fabsf(b)));
-        }
+        g = fmaxf(g, upstream(p, n));
       } else {
-        const bool bad = in && t != -1;
-        if (bad) record_status(p.status, DSPARK_ERR_INVALID);
-        if (p.loss) {
-          p.loss[n] = bad ? __int_as_float(0x7fc00000) : 0.f;
-          p.lse[n] = 0.f;
-        }
-        if (p.slot) p.slot[n] = bad ? -2 : -1;
+        leave_out(p, n, in, t);
       }
     }
     const int mine = __popc(on);
@@ -142,19 +165,8 @@ __global__ void __launch_bounds__(kScanThreads) ce_scan(const ScanParams p) {
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int w = 1; w < 32; ++w) g = fmaxf(g, most[w]);
-    Counts c;
-    c.n = base;
-    c.splits = p.dt > 0 ? choose_splits(div_up(base, 256), p.dt, p.kx, p.wt, base, p.units, p.max_splits) : 1;
-    // fp16 holds 2^-24 to 65504: the slopes, at most twice the largest |g|, go
-    // up to 2^15, so that a probability of 2^-29 keeps its digits (bf16 has fp32's range)
-    int e = 0;
-    if (p.half && g > 0.f && g < INFINITY) {
-      frexpf(g, &e);   // g < 2^e
-      e = max(-100, min(100, 14 - e));
-    }
-    c.scale = ldexpf(1.f, e);
-    c.inv_scale = ldexpf(1.f, -e);
-    *p.counts = c;
+    const int e = slope_exponent(p, g);
+    *p.counts = Counts{base, splits_of(p, base), ldexpf(1.f, e), ldexpf(1.f, -e)};
   }
 }
 
@@ -193,24 +205,19 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b, float s) {
   return s;
 }
 
-// A block per gathered row: the row, dense, and its token's logit (in fp32 from
-// the row itself: a loss is the difference of two logits that may be near each
-// other) or what its slopes need.  Rows up to the next multiple of 256 are zeros.
+// Gathered row j, a block of 128 threads: `row` of h, dense, and its token's logit
+// (in fp32 from the row itself: a loss is the difference of two logits that may be
+// near each other) or what its slopes need; zeros without a row.
 template <bool kBf16>
-__global__ void __launch_bounds__(128) ce_gather(const GatherParams p) {
-  __shared__ float sums[4];
-  pdl_trigger();
-  pdl_wait();
-  const int j = blockIdx.x, n = p.counts->n;
-  if (j >= ceil_to(n, 256)) return;
+__device__ __forceinline__ void gather_row(const GatherParams& p, int j, int row, float scale, float* sums) {
   uint4* out = reinterpret_cast<uint4*>(p.rows + (size_t)j * p.D);
   const int chunks = p.D / 8;
-  if (j >= n) {
+  if (row < 0) {
     for (int c = threadIdx.x; c < chunks; c += 128) out[c] = make_uint4(0, 0, 0, 0);
     if (p.info && threadIdx.x == 0) p.info[j] = RowInfo{0.f, 0.f, 0.f, -1};
     return;
   }
-  const int row = p.list[j], t = p.tokens[row];
+  const int t = p.tokens[row];
   const unsigned short* src = p.h + (size_t)row * p.h_stride;
   const uint4* w = reinterpret_cast<const uint4*>(p.W + (size_t)t * p.W_stride);
   float s = 0.f;
@@ -234,9 +241,73 @@ __global__ void __launch_bounds__(128) ce_gather(const GatherParams p) {
     __syncthreads();
     if (threadIdx.x == 0) p.logit[j] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
   } else if (threadIdx.x == 0) {
-    const float g = p.g_loss[row], scale = p.counts->scale;
+    const float g = p.g_loss[row];
     p.info[j] = RowInfo{p.lse[row] * kLog2e, scale * (p.g_lse ? g + p.g_lse[row] : g), scale * g, t};
   }
+}
+
+// A block per gathered row; the rows up to the next multiple of 256 are zeros.
+template <bool kBf16>
+__global__ void __launch_bounds__(128) ce_gather(const GatherParams p) {
+  __shared__ float sums[4];
+  pdl_trigger();
+  pdl_wait();
+  const int j = blockIdx.x, n = p.counts->n;
+  if (j >= ceil_to(n, 256)) return;
+  gather_row<kBf16>(p, j, j < n ? p.list[j] : -1, p.counts->scale, sums);
+}
+
+// Both for few rows, without a kernel in between: every block counts the rows
+// before its own and all of them (2048 blocks read 16 MB of tokens from L2), then
+// copies its row to its place and, beyond the last place, clears one.
+constexpr int kFewRows = 2048;
+
+template <bool kBf16>
+__global__ void __launch_bounds__(128) ce_scan_gather(const ScanParams p, const GatherParams q) {
+  __shared__ int counted[2][4];
+  __shared__ float most[4], sums[4];
+  pdl_trigger();
+  pdl_wait();
+  const int b = blockIdx.x;
+  int before = 0, all = 0;
+  float g = 0.f;
+  for (int n = threadIdx.x; n < p.N; n += 128) {
+    const int t = p.tokens[n];
+    if (t < 0 || t >= p.V || !in_group(p, n)) continue;
+    ++all;
+    if (n < b) ++before;
+    if (p.half) g = fmaxf(g, upstream(p, n));
+  }
+  all = __reduce_add_sync(0xffffffffu, all);
+  before = __reduce_add_sync(0xffffffffu, before);
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, d));
+  const int warp = threadIdx.x >> 5;
+  if ((threadIdx.x & 31) == 0) {
+    counted[0][warp] = before;
+    counted[1][warp] = all;
+    most[warp] = g;
+  }
+  __syncthreads();
+  before = counted[0][0] + counted[0][1] + counted[0][2] + counted[0][3];
+  all = counted[1][0] + counted[1][1] + counted[1][2] + counted[1][3];
+  g = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+  const int e = slope_exponent(p, g);
+  if (b == 0 && threadIdx.x == 0) *p.counts = Counts{all, splits_of(p, all), ldexpf(1.f, e), ldexpf(1.f, -e)};
+  if (b < p.N) {
+    const int t = p.tokens[b];
+    const bool in = in_group(p, b);
+    if (in && t >= 0 && t < p.V) {
+      if (threadIdx.x == 0) {
+        p.list[before] = b;
+        if (p.slot) p.slot[b] = before;
+      }
+      gather_row<kBf16>(q, before, b, ldexpf(1.f, e), sums);
+    } else if (threadIdx.x == 0) {
+      leave_out(p, b, in, t);
+    }
+  }
+  if (b >= all && b < ceil_to(all, 256)) gather_row<kBf16>(q, b, -1, 0.f, sums);
 }
 
 // ---------------------------------------------------------------------------
@@ -254,6 +325,7 @@ struct LossTiles {
   bool bf16;
   int chunk;
   const dspark::Counts* live;
+  bool one_row_tile;     // N <= 256
   float2* part;          // [vocabulary tiles][ld]
   long long ld;
   int V, steps, vtiles;
@@ -261,6 +333,13 @@ struct LossTiles {
   __device__ void prefetch() const {
     prefetch_tensormap(&h);
     prefetch_tensormap(&w);
+  }
+  // W, which no kernel of this call writes, on its way into L2 while the rows are
+  // gathered: the unit's first tile, known when there is one row tile (behind the
+  // kernel before, which began when all earlier work was done)
+  __device__ void early(int unit, int rank) const {
+    if (!one_row_tile) return;
+    for (int k = threadIdx.x; k < steps; k += 32) prefetch_box(&w, k * kStep, unit * 256 + rank * 128);
   }
   __device__ int counts() const { return live->n; }
   __device__ bool tile(int n, int unit, int units, int i, Tile& t) const {
@@ -380,6 +459,7 @@ struct SlopeTiles {
     prefetch_tensormap(&w);
     prefetch_tensormap(&out);
   }
+  __device__ void early(int, int) const {}
   __device__ int counts() const { return live->n; }
   __device__ bool tile(int n, int unit, int units, int i, Tile& t) const {
     const int mt = div_up(n, 256);
@@ -446,6 +526,7 @@ struct GradTiles {
   __device__ void prefetch() const {
     for (const CUtensorMap* m : {&s_k, &s_mn, &w, &h, &dh, &dW}) prefetch_tensormap(m);
   }
+  __device__ void early(int, int) const {}
   __device__ Counts counts() const {
     const dspark::Counts l = *live;
     Counts c;
@@ -654,8 +735,6 @@ cudaError_t small(K kern, long long grid, int block, cudaStream_t stream, const 
 
 cudaError_t scan_and_gather(const LinearCeArgs& a, const Layout& l, char* ws, const ScanParams& s, GatherParams& g,
                             cudaStream_t stream) {
-  ce_scan<<<1, kScanThreads, 0, stream>>>(s);
-  CE_TRY(cudaGetLastError());
   g.h = static_cast<const unsigned short*>(a.h);
   g.W = static_cast<const unsigned short*>(a.W);
   g.h_stride = a.h_stride;
@@ -666,7 +745,15 @@ cudaError_t scan_and_gather(const LinearCeArgs& a, const Layout& l, char* ws, co
   g.D = a.D;
   g.vec = reinterpret_cast<uintptr_t>(a.h) % 16 == 0 && (a.N == 1 || a.h_stride % 8 == 0);
   g.rows = reinterpret_cast<unsigned short*>(ws + l.h);
-  return small(a.dtype == DSPARK_BF16 ? ce_gather<true> : ce_gather<false>, l.rows, 128, stream, g);
+  const bool bf16 = a.dtype == DSPARK_BF16;
+  if (a.N <= kFewRows) {
+    auto kern = bf16 ? ce_scan_gather<true> : ce_scan_gather<false>;
+    kern<<<(unsigned)l.rows, 128, 0, stream>>>(s, g);
+    return cudaGetLastError();
+  }
+  ce_scan<<<1, kScanThreads, 0, stream>>>(s);
+  CE_TRY(cudaGetLastError());
+  return small(bf16 ? ce_gather<true> : ce_gather<false>, l.rows, 128, stream, g);
 }
 
 ScanParams scan_params(const LinearCeArgs& a, const Layout& l, char* ws) {
@@ -701,6 +788,7 @@ cudaError_t launch_linear_ce(const LinearCeArgs& a, cudaStream_t stream) {
   t.bf16 = bf16;
   t.chunk = 8;
   t.live = s.counts;
+  t.one_row_tile = l.rows == 256;
   t.part = reinterpret_cast<float2*>(ws + l.part);
   t.ld = l.rows;
   t.V = a.V;

@@ -88,7 +88,7 @@ struct InputParams {
 };
 
 constexpr int kNormThreads = 256;
-constexpr int kPrograms = 64, kCounters = 2048;   // counters of programs, and of tiles whose K is split
+constexpr int kPrograms = 64;   // counters of programs
 constexpr int kUnit = 256;   // side of a diagonal tile
 
 // Sums of squares of values of any size: fp32 sums of three ranges, each scaled
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kNormThreads) ns_norm(const InputParams p) {
   __shared__ float3 table[kNormThreads / 32];
   pdl_trigger();
   pdl_wait();
-  for (int i = blockIdx.x * kNormThreads + threadIdx.x; i < kPrograms + kCounters; i += gridDim.x * kNormThreads)
+  for (int i = blockIdx.x * kNormThreads + threadIdx.x; i < kPrograms; i += gridDim.x * kNormThreads)
     p.counters[i] = 0;
   const int chunks = (p.cols + 3) / 4;
   const long long all = (long long)p.rows * chunks;
@@ -233,6 +233,7 @@ struct NsTiles {
   __device__ void prefetch() const {
     for (const CUtensorMap* m : {&left, &left_low, &right, &right_low, &unit, &unit_low, &out0, &out1}) prefetch_tensormap(m);
   }
+  __device__ void early(int, int) const {}
   __device__ int counts() const { return 0; }
   __device__ bool tile(int, int unit, int units, int i, Tile& t) const {
     const int u = i * units + unit;
@@ -453,8 +454,7 @@ __global__ void __launch_bounds__(256) ns_join(const JoinParams p) {
 // launch) go from product to product: a tile's stores are followed by an increment
 // of a counter in global memory, and a product's copies wait until the counter
 // shows all tiles that it reads (bounded, as every wait).  Tiles are 128 x 64, a
-// CTA each; K may be split, the last CTA to finish a tile's part adds the parts
-// up in their order.
+// CTA each.
 // ---------------------------------------------------------------------------
 constexpr int kMaxOps = 24, kMaxMaps = 32;   // of a launch
 constexpr int kOpM = 128, kOpN = 64, kOpCols = kOpN / 4;
@@ -474,15 +474,13 @@ struct Op {
   short products, extra, steps, unit_steps;   // steps: of a product's K
   bool left_mn, right_mn, unit_is_left, symmetric, vec;
   int rows, cols, mt, nt;
-  int tiles, parts;            // work items: tiles * parts
+  int tiles;
   int base;                    // what the counter has to show first
   int first;                   // the CTA that takes its first item
-  int split_counter;           // of its first tile
   float scale, diag;           // result = scale sum + diag on the diagonal
-  long long ld, ld_part, ld_out;
+  long long ld, ld_out;
   __half *to0, *to1;           // halves (low: may be null)
   __nv_bfloat16* out;          // or the last X
-  float* part;
 };
 
 struct Program {
@@ -490,40 +488,32 @@ struct Program {
   Op ops[kMaxOps];
   int map_count, count;
   int* counter;                // tiles done
-  int* split_counters;
   int* status;
 };
 
 struct Item {
-  int m0, n0, part, tile, k0, steps;
+  int m0, n0;
 };
 
 __device__ __forceinline__ bool item_of(const Op& op, int unit, int units, int i, Item& t) {
   const int u = (unit >= op.first ? unit - op.first : unit + units - op.first) + i * units;
-  if (u >= op.tiles * op.parts) return false;
-  t.part = u / op.tiles;
-  t.tile = u - t.part * op.tiles;
+  if (u >= op.tiles) return false;
   int m, n;
   if (op.symmetric) {   // tiles on or below the diagonal: two more for each row tile
-    const int w = t.tile / 2;
+    const int w = u / 2;
     m = (int)((sqrtf(8.f * w + 1.f) - 1.f) * 0.5f);
     while (m * (m + 1) / 2 > w) --m;
     while ((m + 1) * (m + 2) / 2 <= w) ++m;
-    n = t.tile - m * (m + 1);
+    n = u - m * (m + 1);
   } else {
-    n = t.tile / op.mt;
-    m = t.tile - n * op.mt;
+    n = u / op.mt;
+    m = u - n * op.mt;
   }
   t.m0 = m * kOpM;
   t.n0 = n * kOpN;
-  const int each = div_up(op.steps, op.parts);
-  t.k0 = t.part * each;
-  t.steps = max(0, min(each, op.steps - t.k0));
   return true;
 }
-__device__ __forceinline__ int steps_of(const Op& op, const Item& t) {
-  return t.steps * op.products + op.extra * op.unit_steps;
-}
+__device__ __forceinline__ int steps_of(const Op& op) { return op.steps * op.products + op.extra * op.unit_steps; }
 
 // Until `counter` shows `least`; a converged warp.  What other CTAs stored before
 // they counted is seen by this warp's loads and its copies (the async proxy).
@@ -553,7 +543,6 @@ __global__ void __launch_bounds__(kThreads, 1) ns_program(const __grid_constant_
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   unsigned char* rows_s = smem + kOpStages * kOpStageBytes;   // a tile's rows on their way out
   Bars* bars = reinterpret_cast<Bars*>(rows_s + kOpRowsBytes);
-  __shared__ int last_part;
   // (in shared memory: a read of the parameters that misses their small cache takes 200 cycles)
   __shared__ Op ops[kMaxOps];
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -588,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_program(const __grid_constant_
       const bool left_mn = op.left_mn, right_mn = op.right_mn;
       for (int n = 0; ok && item_of(op, unit, units, n, t); ++n) {
         if (n == 0 && op.base > 0 && !(ok = wait_count(p.counter, op.base, abort, p.status))) break;
-        int left = steps_of(op, t), q = 0, in = 0;    // steps to go; segment, its steps to go
+        int left = steps_of(op), q = 0, in = 0;    // steps to go; segment, its steps to go
         const CUtensorMap *lm = nullptr, *rm = nullptr;
         int lr = 0, lk = 0, rr = 0, rk = 0;
         while (left > 0) {
@@ -604,9 +593,9 @@ __global__ void __launch_bounds__(kThreads, 1) ns_program(const __grid_constant_
             if (in == 0) {   // the next segment
               lr = t.m0;
               rr = t.n0;
-              lk = rk = t.k0 * kStep;
+              lk = rk = 0;
               if (q < op.products) {
-                in = t.steps;
+                in = op.steps;
                 lm = &p.maps[op.left[q]];
                 rm = &p.maps[op.right[q]];
               } else {
@@ -656,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_program(const __grid_constant_
       const uint64_t ad0 = op.left_mn ? sw128_mnmajor_desc(stages, 8192) : sw128_kmajor_desc(stages);
       const uint64_t bd0 = op.right_mn ? sw128_mnmajor_desc(stages + kOpM * 128, 8192) : sw128_kmajor_desc(stages + kOpM * 128);
       for (int n = 0; ok && item_of(op, unit, units, n, t); ++n) {
-        const int all = steps_of(op, t);
+        const int all = steps_of(op);
         for (int k = 0; k < all && ok; ++c) {
           const int buf = c & 1, kend = min(k + kChunk, all);
           ok = warp_wait(&bars->acc_empty[buf], ((c >> 1) & 1) ^ 1, abort, p.status);
@@ -696,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_program(const __grid_constant_
     for (int o = 0; o < p.count; ++o) {
       const Op& op = ops[o];
       for (int n = 0; item_of(op, unit, units, n, t); ++n) {
-        const int all = steps_of(op, t), chunks = div_up(all, kChunk);
+        const int all = steps_of(op), chunks = div_up(all, kChunk);
         float v[kOpCols];
 #pragma unroll
         for (int j = 0; j < kOpCols; ++j) v[j] = 0.f;
@@ -715,37 +704,6 @@ __global__ void __launch_bounds__(kThreads, 1) ns_program(const __grid_constant_
         }
         // (a warp whose wait gave up goes on through the barriers)
         const int row = t.m0 + q * 32 + lane, col = t.n0 + h * kOpCols;
-        if (op.parts > 1) {
-          const size_t at = (size_t)row * op.ld_part + col, plane = (size_t)op.rows * op.ld_part;
-          if (row < op.rows) {
-#pragma unroll
-            for (int j = 0; j < kOpCols; j += 4)
-              if (col + j < op.ld_part)
-                *reinterpret_cast<float4*>(op.part + t.part * plane + at + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-          }
-          // (a barrier, then one thread's fence: what the others wrote before is ordered by it too)
-          named_bar_sync(1, kEpiWarps * 32);
-          if (threadIdx.x == 64) {
-            __threadfence();
-            last_part = atomicAdd(p.split_counters + op.split_counter + t.tile, 1) == op.parts - 1;
-            __threadfence();
-          }
-          named_bar_sync(1, kEpiWarps * 32);
-          if (!last_part) continue;
-#pragma unroll
-          for (int j = 0; j < kOpCols; ++j) v[j] = 0.f;
-          if (row < op.rows) {
-#pragma unroll 4
-            for (int i = 0; i < op.parts; ++i) {
-#pragma unroll
-              for (int j = 0; j < kOpCols; j += 4) {
-                if (col + j >= op.ld_part) continue;
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(op.part + i * plane + at + j));
-                v[j] += x.x; v[j + 1] += x.y; v[j + 2] += x.z; v[j + 3] += x.w;
-              }
-            }
-          }
-        }
 #pragma unroll
         for (int j = 0; j < kOpCols; ++j) {
           v[j] *= op.scale;
@@ -851,7 +809,7 @@ Layout layout(int rows, int cols) {
     return a;
   };
   l.partial = take(8ull * kNormBlocks);
-  l.counters = take(4ull * (kPrograms + kCounters));
+  l.counters = take(4ull * (kPrograms));
   l.units = take(3 * 2ull * kUnit * kUnit);
   for (auto& half : l.x)
     for (auto& x : half) x = take(2ull * rows * l.ld);
@@ -984,7 +942,7 @@ struct Halves {
 // Builds programs and launches them when they are full or done.
 struct Builder {
   Program p{};
-  int tiles = 0, items = 0, programs = 0, splits = 0;
+  int tiles = 0, items = 0, programs = 0;
   int* counters;
   int* status;
   int sms;
@@ -1035,7 +993,6 @@ struct Builder {
     // (the tiles above the diagonal where there are SMs for them: mirroring takes longer)
     op.symmetric = symmetric && op.mt * op.nt > sms;
     op.tiles = op.symmetric ? op.mt * (op.mt + 1) : op.mt * op.nt;
-    op.parts = 1;
     op.base = tiles;
     op.scale = kInvScale;
     return op;
@@ -1043,7 +1000,7 @@ struct Builder {
   // After everything about the op but its place is known.
   void place(Op& op) {
     tiles += op.tiles;
-    items = std::max(items, op.tiles * op.parts);
+    items = std::max(items, op.tiles);
   }
   void into(Op& op, const Halves& to) {
     op.to0 = to.hi;
@@ -1057,7 +1014,6 @@ struct Builder {
     if (error != cudaSuccess || p.count == 0) return error;
     if (programs == kPrograms) return cudaErrorInvalidValue;
     p.counter = counters + programs++;
-    p.split_counters = counters + kPrograms;
     p.status = status;
     cudaError_t e = cudaFuncSetAttribute(ns_program, cudaFuncAttributeMaxDynamicSharedMemorySize, kOpSmem);
     if (e != cudaSuccess) return e;
@@ -1150,8 +1106,13 @@ cudaError_t launch_newton_schulz(const NewtonSchulzArgs& a, cudaStream_t stream)
     op.diag = diag * kScale;
     build.into(op, to);
   };
+  // Everything in one launch, or by groups of steps, or product by product.
+  // Measured (us), in that order: 256 x 256: 92, 114, 123; 256 x 512: 103, 119,
+  // 137; 512 x 1000: 195, 167, 197; 64 x 4000: 175, 119, 164; 16000 x 256: 466,
+  // 169, 240; without halves 1000 x 777: 109, -, 129; 2048 x 2048: 359, -, 411;
+  // 1536 x 1536: 234, -, 222; 3000 x 3000 product by product 603.
   const long long x_tiles = (long long)div_up(a.rows, kOpM) * div_up(a.cols, kOpN);
-  const bool in_order = fold && x_tiles <= (small <= 256 ? 4 : 2) * sms;
+  const bool in_order = fold && (l.halves ? large <= 2 * small && x_tiles < 64 : x_tiles <= 4 * sms);
 
   if (in_order) {
     // everything in one launch (of 8 steps each)
@@ -1159,17 +1120,6 @@ cudaError_t launch_newton_schulz(const NewtonSchulzArgs& a, cudaStream_t stream)
       if (!build.room(3)) NS_TRY(build.launch());
       // A
       Op& gram = build.add(X(i, l.halves), tall, X(i, l.halves), tall, small, small, large, true);
-      // K in parts: a part's steps against the reading of the parts
-      // (the parts cost about 24 steps' time, their reading one step each)
-      const int all = gram.products * gram.steps;
-      const int parts = std::min({l.parts, sms / gram.tiles, (int)(std::sqrt((double)all) + 0.5), gram.steps / 2});
-      if (parts > 1 && all / parts + parts + 24 < all && build.splits + gram.tiles <= kCounters) {
-        gram.parts = parts;
-        gram.part = reinterpret_cast<float*>(ws + l.part);
-        gram.ld_part = l.ldp;
-        gram.split_counter = build.splits;
-        build.splits += gram.tiles;
-      }
       build.into(gram, mA);
       // B: with a on its diagonal, or divided by a
       square(mA, mB, l.halves ? a.c : a.c / a.a, l.halves ? a.a : 0.f);
