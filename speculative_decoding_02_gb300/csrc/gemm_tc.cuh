@@ -16,15 +16,17 @@
 //
 // Either operand is K-major ([128 or fewer rows][64 of K] boxes) or not (boxes of
 // [64 of K][64 rows]), tile by tile.  The tensor cores truncate when they add
-// to an accumulator, so an accumulator takes p.chunk steps of K only and the
+// to an accumulator, so an accumulator takes p.chunk() steps of K only and the
 // epilogue adds it, rounded, to its sums while the next one fills (two of them).
 //
 // A policy P (a kernel parameter, so its tensor maps are too) has
 //   kPair, kN, kSelf (a product of one matrix with itself, from halves: a() and
 //     b() are its high and low half, the sum is that of a a^T, a b^T and b a^T),
 //     kBoxBytes (shared memory of an epilogue warp, a multiple of
-//     1024), kExtraBytes (of the CTA); status, bf16, chunk;
+//     1024), kExtraBytes (of the CTA); status, bf16;
 //   Counts counts()                     read once a thread, behind pdl_wait
+//   int chunk(counts)                   steps of K that an accumulator takes
+//   bool used(counts, tile, row)        whether any of the 32 rows from `row` (of the tile) is
 //   bool tile(counts, unit, units, i, Tile&)  the i-th tile of a unit, same
 //     for all its threads; false when there is none
 //   int segments(tile), Segment segment(tile, i)  where the operands' steps of K are
@@ -70,6 +72,7 @@ struct Epi {
   int row;             // of the tile
   int row0;            // the row of this warp's lane 0
   int col;             // of the tile: the thread's columns are col .. col + kN / 4 - 1
+  bool used;           // else the sums are zeros
   int q, h, lane;      // the warp's quarter of the CTA's rows and of the columns
   int n;               // tiles before this one
   unsigned char* box;    // this warp's
@@ -135,9 +138,26 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// mbar_wait of a converged warp.
+// mbar_wait of a converged warp.  The clock is read now and then only: a read takes
+// about a microsecond, and a tile's accumulators change hands several times.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
+  bool ok = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  uint64_t t0 = 0;
+  while (!ok) {
+#pragma unroll 1
+    for (int i = 0; i < 1024 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+    if (ok || *abort) break;
+    const uint64_t now = globaltimer();
+    if (t0 == 0) {
+      t0 = now;
+    } else if (now - t0 > kWaitLimitNs) {
+      *abort = 1;
+      record_status(status, DSPARK_ERR_TIMEOUT);
+      break;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 
 template <bool kPair>
@@ -198,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
   if (warp == 0) p.early(unit, rank);
   pdl_wait();
   const typename P::Counts counts = p.counts();
+  const int chunk = p.chunk(counts);
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -262,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         const uint64_t ad0 = t.a_mn ? sw128_mnmajor_desc(stages, 8192) : sw128_kmajor_desc(stages);
         const uint64_t bd0 = t.b_mn ? sw128_mnmajor_desc(stages + S::kABytes, 8192) : sw128_kmajor_desc(stages + S::kABytes);
         for (int k = 0; k < t.steps && ok; ++c) {
-          const int buf = c & 1, kend = min(k + p.chunk, t.steps);
+          const int buf = c & 1, kend = min(k + chunk, t.steps);
           ok = warp_wait(&bars->acc_empty[buf], ((c >> 1) & 1) ^ 1, abort, p.status);
           if (!ok) break;
           tc_fence_after();
@@ -312,26 +333,33 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     Tile t;
     for (int n = 0; p.tile(counts, unit, units, n, t); ++n) {
       float acc[S::kCols];
+      e.used = p.used(counts, t, e.row0);
 #pragma unroll
       for (int j = 0; j < S::kCols; ++j) acc[j] = 0.f;
-      const int chunks = (t.steps + p.chunk - 1) / p.chunk;
+      const int chunks = (t.steps + chunk - 1) / chunk;
       for (int j = 0; j < chunks && ok; ++j, ++c) {
         const int buf = c & 1;
         ok = warp_wait(&bars->acc_full[buf], (c >> 1) & 1, abort, p.status);
         if (!ok) break;
         tc_fence_after();
+        if (e.used) {
 #pragma unroll
-        for (int g = 0; g < S::kCols / 16; ++g) {
-          float v[16];
-          tmem_load_cols<16>(lanes + buf * P::kN + g * 16, v);
+          for (int g = 0; g < S::kCols / 16; ++g) {
+            float v[16];
+            tmem_load_cols<16>(lanes + buf * P::kN + g * 16, v);
 #pragma unroll
-          for (int x = 0; x < 16; ++x) acc[g * 16 + x] += v[x];
+            for (int x = 0; x < 16; ++x) acc[g * 16 + x] += v[x];
+          }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if constexpr (kPair) arrive_in_cluster(in_cta(&bars->acc_empty[buf], 0));
-          else mbar_arrive(&bars->acc_empty[buf]);
+          // (an arrival of CTA scope, for no memory but the tensor core's goes with it:
+          // a release to the cluster waits 2000 cycles for this thread's stores)
+          if constexpr (kPair)
+            asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(in_cta(&bars->acc_empty[buf], 0)) : "memory");
+          else
+            mbar_arrive(&bars->acc_empty[buf]);
         }
       }
       // (a policy's epilogue may hold barriers of the epilogue warps: a warp

@@ -24,7 +24,8 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Counts {
   int n;            // rows that count
-  int splits;       // parts of dh
+  int full;         // tiles of dh taken whole, the first ones
+  int splits;       // parts of K of the others
   float scale;      // of the slopes, a power of two
   float inv_scale;
 };
@@ -50,17 +51,16 @@ struct ScanParams {
   const float* g_loss;      // backward
   const float* g_lse;
   bool half;                // fp16: the slopes are scaled
-  int dt, kx, wt, units, max_splits;
+  int D, dt, kx, wt, units, max_splits;   // dt: column tiles of dh, wt: row tiles of a piece of dW (0: not wanted)
   Counts* counts;
   int32_t* list;            // [N]: the rows that count, in order
   int32_t* slot;            // [N]: a row's place there; -1 none, -2 none and its token is out of range
   int* status;
 };
 
-// The parts of K that give dh's tiles and dW's the earliest end: a tile takes
+// The parts of K that give tx tiles of dh and dW's the earliest end: a tile takes
 // its steps of K and about 4 steps' time for its epilogue.
-__device__ int choose_splits(int mt, int dt, int kx, int wt, int n, int units, int most) {
-  const int tx = mt * dt, tw = wt * dt, kw = div_up(n, kStep);
+__device__ int choose_splits(int tx, int tw, int kx, int kw, int units, int most) {
   int best = 1;
   long long best_cost = -1;
   for (int s = 1; s <= most; ++s) {
@@ -73,8 +73,19 @@ __device__ int choose_splits(int mt, int dt, int kx, int wt, int n, int units, i
   return best;
 }
 
-__device__ int splits_of(const ScanParams& p, int n) {
-  return p.dt > 0 ? choose_splits(div_up(n, 256), p.dt, p.kx, p.wt, n, p.units, p.max_splits) : 1;
+// With dh alone, as many tiles as fill all units go whole and the others in
+// parts: 80 tiles of 792 steps on 76 pairs by 76 whole and 4 in 19 parts end
+// after 838 steps (all 80 in 14 parts: 915, and 14 times the sums to keep).
+// Beside dW, whose tiles fill what is left, by parts only.
+__device__ Counts counts_of(const ScanParams& p, int n, int exponent) {
+  Counts c{n, 0, 1, ldexpf(1.f, exponent), ldexpf(1.f, -exponent)};
+  if (p.dt > 0) {
+    const int tiles = div_up(n, 256) * p.dt;
+    c.full = p.wt == 0 ? tiles / p.units * p.units : 0;
+    if (c.full < tiles)
+      c.splits = choose_splits(tiles - c.full, p.wt * div_up(p.D, 256), p.kx, div_up(n, kStep), p.units, p.max_splits);
+  }
+  return c;
 }
 // The slopes' scale, 2 to this, when g is the largest |g_loss| or |g_loss + g_lse|.
 // fp16 holds 2^-24 to 65504: the slopes, at most 2 g, go up to 2^15, so that a
@@ -166,7 +177,7 @@ __global__ void __launch_bounds__(kScanThreads) ce_scan(const ScanParams p) {
   if (threadIdx.x == 0) {
     for (int w = 1; w < 32; ++w) g = fmaxf(g, most[w]);
     const int e = slope_exponent(p, g);
-    *p.counts = Counts{base, splits_of(p, base), ldexpf(1.f, e), ldexpf(1.f, -e)};
+    *p.counts = counts_of(p, base, e);
   }
 }
 
@@ -293,7 +304,7 @@ __global__ void __launch_bounds__(128) ce_scan_gather(const ScanParams p, const 
   all = counted[1][0] + counted[1][1] + counted[1][2] + counted[1][3];
   g = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
   const int e = slope_exponent(p, g);
-  if (b == 0 && threadIdx.x == 0) *p.counts = Counts{all, splits_of(p, all), ldexpf(1.f, e), ldexpf(1.f, -e)};
+  if (b == 0 && threadIdx.x == 0) *p.counts = counts_of(p, all, e);
   if (b < p.N) {
     const int t = p.tokens[b];
     const bool in = in_group(p, b);
@@ -323,7 +334,6 @@ struct LossTiles {
   using Counts = int;
   int* status;
   bool bf16;
-  int chunk;
   const dspark::Counts* live;
   bool one_row_tile;     // N <= 256
   float2* part;          // [vocabulary tiles][ld]
@@ -342,6 +352,13 @@ struct LossTiles {
     for (int k = threadIdx.x; k < steps; k += 32) prefetch_box(&w, k * kStep, unit * 256 + rank * 128);
   }
   __device__ int counts() const { return live->n; }
+  // An accumulator loses about half a step an addition, always towards zero: by
+  // 16 steps of K an lse of 14 is off by -3.4e-6 (1.3e-6 at random besides; plain
+  // fp32 products: up to 9e-7 for the lse, 3e-6 to 5e-6 for the loss, at random), by 8
+  // -2e-6, by 4 -1e-6, by 2 -6e-7.  N = 2048, V = 151936, D = 2560: 800, 805, 837 and
+  // 899 us; one row: 135, 135, 135 and 139.
+  __device__ int chunk(int n) const { return n <= 256 ? 4 : 8; }
+  __device__ bool used(int n, const Tile& t, int row) const { return t.m0 + row < n; }
   __device__ bool tile(int n, int unit, int units, int i, Tile& t) const {
     // neighbouring units take the row tiles of the same columns, so that W
     // comes once from HBM
@@ -358,6 +375,7 @@ struct LossTiles {
   __device__ Segment segment(const Tile& t, int) const { return Segment{&h, &w, t.m0, 0, t.n0, 0, t.steps}; }
 
   __device__ void epilogue(const Epi& e, const Tile& t, float (&z)[64]) const {
+    if (!e.used) return;   // (nor are the other warps of these rows)
     const int left = V - (t.n0 + e.col);
     float m = -INFINITY;
 #pragma unroll
@@ -447,7 +465,6 @@ struct SlopeTiles {
   using Counts = int;
   int* status;
   bool bf16;
-  int chunk;
   const dspark::Counts* live;
   const RowInfo* info;
   float* corr;           // what the rounding of the token's slope took
@@ -461,6 +478,8 @@ struct SlopeTiles {
   }
   __device__ void early(int, int) const {}
   __device__ int counts() const { return live->n; }
+  __device__ int chunk(int) const { return 64; }   // (far below the slopes' rounding)
+  __device__ bool used(int n, const Tile& t, int row) const { return t.m0 + row < n; }
   __device__ bool tile(int n, int unit, int units, int i, Tile& t) const {
     const int mt = div_up(n, 256);
     const long long u = (long long)i * units + unit;
@@ -511,12 +530,11 @@ struct GradTiles {
   static constexpr bool kPair = true, kSelf = false;
   static constexpr int kN = 256, kBoxBytes = kStoreBox, kExtraBytes = 0;
   struct Counts {
-    int mt, splits, kw, tx, tw, shared;
+    int n, mt, full, splits, kw, tx, tw, shared;   // tx: work items of dh
     float inv_scale;
   };
   int* status;
   bool bf16;
-  int chunk;
   const dspark::Counts* live;
   int rows;              // of the slopes' matrix
   int v0, V, kx, wt;     // the piece: first column, of V; steps of K and (for dW) tiles of 256
@@ -530,10 +548,12 @@ struct GradTiles {
   __device__ Counts counts() const {
     const dspark::Counts l = *live;
     Counts c;
+    c.n = l.n;
     c.mt = div_up(l.n, 256);
+    c.full = l.full;
     c.splits = l.splits;
     c.kw = div_up(l.n, kStep);
-    c.tx = want_dh ? c.mt * dt * c.splits : 0;
+    c.tx = want_dh ? c.full + (c.mt * dt - c.full) * c.splits : 0;
     c.tw = wt * dt;
     c.inv_scale = l.inv_scale;
     // dW tiles that every unit takes: those with one more of dh's take no
@@ -545,16 +565,21 @@ struct GradTiles {
     c.shared = min(max((int)((all - most * cx) / cw + 0.5f), 0), c.tw / units);
     return c;
   }
+  __device__ int chunk(const Counts&) const { return 64; }
+  __device__ bool used(const Counts& c, const Tile& t, int row) const {
+    return t.kind == 0 ? t.m0 + row < c.n : v0 + t.m0 + row < V;
+  }
   __device__ bool tile(const Counts& c, int unit, int units, int i, Tile& t) const {
     const int more = c.tx % units;                      // the first `more` units take one more of dh's
     const int own = c.tx / units + (unit < more ? 1 : 0);
     if (i < own) {
-      const int u = i * units + unit, tiles = c.mt * dt;
+      const int u = i * units + unit, rest = c.mt * dt - c.full;
       t.kind = 0;
-      t.part = u / tiles;
-      const int each = div_up(kx, c.splits);
-      t.m0 = (u % tiles) % c.mt * 256;
-      t.n0 = (u % tiles) / c.mt * 256;
+      t.part = u < c.full ? 0 : (u - c.full) / rest;
+      const int v = u < c.full ? u : c.full + (u - c.full) % rest;
+      const int each = u < c.full ? kx : div_up(kx, c.splits);
+      t.m0 = v % c.mt * 256;
+      t.n0 = v / c.mt * 256;
       t.k0 = t.part * each;
       t.steps = max(0, min(each, kx - t.k0));
       t.a_mn = false;
@@ -585,6 +610,7 @@ struct GradTiles {
   }
 
   __device__ void epilogue(const Epi& e, const Tile& t, float (&v)[64]) const {
+    if (!e.used) return;
     if (t.kind == 0) {
       store_fp32(e, &dh, v, t.n0 + e.col, D, t.m0 + e.row0, rows, t.part, add);
       return;
@@ -633,6 +659,7 @@ __global__ void __launch_bounds__(128) ce_finish(const FinishParams p) {
   }
   const Counts counts = *p.counts;
   const float corr = p.corr[j];
+  const int mt = div_up(counts.n, 256);
   const uint4* w = reinterpret_cast<const uint4*>(p.W + (size_t)p.info[j].token * p.W_stride);
   for (int c = threadIdx.x; c < chunks; c += 128) {
     float a[8];
@@ -644,7 +671,8 @@ __global__ void __launch_bounds__(128) ce_finish(const FinishParams p) {
       a[2 * e] = corr * u.x;
       a[2 * e + 1] = corr * u.y;
     }
-    for (int s = 0; s < counts.splits; ++s) {
+    const int parts = (c * 8 / 256) * mt + j / 256 < counts.full ? 1 : counts.splits;
+    for (int s = 0; s < parts; ++s) {
       const float4* q = reinterpret_cast<const float4*>(p.part + ((size_t)s * p.rows + j) * p.D + 8 * c);
       const float4 u = q[0], v = q[1];
       a[0] += u.x; a[1] += u.y; a[2] += u.z; a[3] += u.w;
@@ -671,7 +699,7 @@ __global__ void __launch_bounds__(128) ce_finish(const FinishParams p) {
 // ---------------------------------------------------------------------------
 constexpr long long kPieceBytes = 256ll << 20;   // of the slopes
 constexpr long long kPartBytes = 256ll << 20;    // of dh's parts
-constexpr int kMaxSplits = 16;
+constexpr int kMaxSplits = 32;
 
 struct Layout {
   long long rows;                  // N, in whole row tiles
@@ -786,7 +814,6 @@ cudaError_t launch_linear_ce(const LinearCeArgs& a, cudaStream_t stream) {
   CE_TRY(map_16bit(a.W, bf16, a.V, a.D, a.W_stride, kRows, &t.w));
   t.status = a.status;
   t.bf16 = bf16;
-  t.chunk = 8;
   t.live = s.counts;
   t.one_row_tile = l.rows == 256;
   t.part = reinterpret_cast<float2*>(ws + l.part);
@@ -812,6 +839,7 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs& a, cudaStream_t stream
   s.slot = reinterpret_cast<int32_t*>(ws + l.slot);
   s.g_loss = a.g_loss;
   s.g_lse = a.g_lse;
+  s.D = a.D;
   s.dt = want_dh ? div_up(a.D, 256) : 0;
   s.kx = l.piece / kStep;
   s.wt = want_dW ? l.piece / 256 : 0;
@@ -831,7 +859,6 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs& a, cudaStream_t stream
   CE_TRY(map_16bit(slopes, bf16, l.rows, l.piece, l.piece, kBoxRows, &t.out));
   t.status = a.status;
   t.bf16 = bf16;
-  t.chunk = 64;
   t.live = s.counts;
   t.info = g.info;
   t.corr = reinterpret_cast<float*>(ws + l.corr);
@@ -849,7 +876,6 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs& a, cudaStream_t stream
   if (want_dW) CE_TRY(map_16bit(a.dW, bf16, a.V, a.D, a.D, kBoxRows, &d.dW));
   d.status = a.status;
   d.bf16 = bf16;
-  d.chunk = 64;
   d.live = s.counts;
   d.rows = (int)l.rows;
   d.V = a.V;

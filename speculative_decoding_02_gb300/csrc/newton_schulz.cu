@@ -215,7 +215,6 @@ struct NsTiles {
   CUtensorMap out0, out1;   // stores of 64 columns a warp
   int* status;
   bool bf16;             // false: fp16 operands
-  int chunk;
   bool left_mn, right_mn;
   int rows, cols;        // of the product
   int mt, nt, steps, parts;
@@ -235,6 +234,8 @@ struct NsTiles {
   }
   __device__ void early(int, int) const {}
   __device__ int counts() const { return 0; }
+  __device__ int chunk(int) const { return kSelf ? 4 : 8; }
+  __device__ bool used(int, const Tile&, int) const { return true; }
   __device__ bool tile(int, int unit, int units, int i, Tile& t) const {
     const int u = i * units + unit;
     constexpr int r = kM / kN > 0 ? kM / kN : 1;   // tiles of a row tile on the diagonal
@@ -519,14 +520,17 @@ __device__ __forceinline__ int steps_of(const Op& op) { return op.steps * op.pro
 // they counted is seen by this warp's loads and its copies (the async proxy).
 __device__ __forceinline__ bool wait_count(const int* counter, int least, volatile int* abort, int* status) {
   bool ok = true;
-  const uint64_t t0 = globaltimer();
+  uint64_t t0 = 0;
   for (unsigned polls = 0;; ++polls) {
     int v;
     asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
     if (v >= least) break;
-    if (polls % 16 != 15) continue;
+    if (polls % 256 != 255) continue;
     if (*abort) { ok = false; break; }
-    if (globaltimer() - t0 > kWaitLimitNs) {
+    const uint64_t now = globaltimer();
+    if (t0 == 0) {
+      t0 = now;
+    } else if (now - t0 > kWaitLimitNs) {
       *abort = 1;
       record_status(status, DSPARK_ERR_TIMEOUT);
       ok = false;
@@ -879,7 +883,6 @@ cudaError_t launch_product(const Product& q, cudaStream_t stream) {
   }
   p.status = q.status;
   p.bf16 = false;
-  p.chunk = kKind == kGramSelf ? 4 : 8;
   p.left_mn = q.left_mn;
   p.right_mn = q.right_mn;
   p.rows = q.rows;
