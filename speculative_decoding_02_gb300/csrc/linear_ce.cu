@@ -22,6 +22,8 @@ using namespace gemm;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+constexpr int kMaxSplits = 32;   // parts of dh
+
 struct Counts {
   int n;            // rows that count
   int full;         // tiles of dh taken whole, the first ones
@@ -59,24 +61,27 @@ struct ScanParams {
 };
 
 // The parts of K that give tx tiles of dh and dW's the earliest end: a tile takes
-// its steps of K and about 4 steps' time for its epilogue.
+// its steps of K and about 4 steps' time for its epilogue.  A warp, a choice a lane.
 __device__ int choose_splits(int tx, int tw, int kx, int kw, int units, int most) {
-  int best = 1;
-  long long best_cost = -1;
-  for (int s = 1; s <= most; ++s) {
-    const long long cx = div_up(kx, s) + 4;
-    const long long waves = div_up(tx * s, units) * cx;
-    const long long all = ((long long)tx * s * cx + (long long)tw * (kw + 4) + units - 1) / units;
-    const long long cost = waves > all ? waves : all;
-    if (best_cost < 0 || cost < best_cost) best = s, best_cost = cost;
+  static_assert(kMaxSplits <= 32, "a lane each");
+  const int s = (threadIdx.x & 31) + 1;
+  const long long cx = div_up(kx, s) + 4;
+  const long long waves = div_up(tx * s, units) * cx;
+  const long long all = ((long long)tx * s * cx + (long long)tw * (kw + 4)) / units;
+  long long cost = s <= most ? (waves > all ? waves : all) : 1ll << 56;
+  cost = cost << 6 | s;   // (of equal ones the fewest parts)
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) {
+    const long long other = __shfl_xor_sync(0xffffffffu, cost, d);
+    cost = other < cost ? other : cost;
   }
-  return best;
+  return (int)(cost & 63);
 }
 
 // With dh alone, as many tiles as fill all units go whole and the others in
 // parts: 80 tiles of 792 steps on 76 pairs by 76 whole and 4 in 19 parts end
 // after 838 steps (all 80 in 14 parts: 915, and 14 times the sums to keep).
-// Beside dW, whose tiles fill what is left, by parts only.
+// Beside dW, whose tiles fill what is left, by parts only.  A whole warp.
 __device__ Counts counts_of(const ScanParams& p, int n, int exponent) {
   Counts c{n, 0, 1, ldexpf(1.f, exponent), ldexpf(1.f, -exponent)};
   if (p.dt > 0) {
@@ -174,10 +179,10 @@ __global__ void __launch_bounds__(kScanThreads) ce_scan(const ScanParams p) {
   for (int d = 16; d > 0; d /= 2) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, d));
   if (lane == 0) most[warp] = g;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < 32; ++w) g = fmaxf(g, most[w]);
-    const int e = slope_exponent(p, g);
-    *p.counts = counts_of(p, base, e);
+  if (warp == 0) {
+    for (int w = 0; w < 32; ++w) g = fmaxf(g, most[w]);
+    const Counts c = counts_of(p, base, slope_exponent(p, g));
+    if (lane == 0) *p.counts = c;
   }
 }
 
@@ -304,7 +309,10 @@ __global__ void __launch_bounds__(128) ce_scan_gather(const ScanParams p, const 
   all = counted[1][0] + counted[1][1] + counted[1][2] + counted[1][3];
   g = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
   const int e = slope_exponent(p, g);
-  if (b == 0 && threadIdx.x == 0) *p.counts = counts_of(p, all, e);
+  if (b == 0 && warp == 0) {
+    const Counts c = counts_of(p, all, e);
+    if (threadIdx.x == 0) *p.counts = c;
+  }
   if (b < p.N) {
     const int t = p.tokens[b];
     const bool in = in_group(p, b);
@@ -336,8 +344,7 @@ struct LossTiles {
   bool bf16;
   const dspark::Counts* live;
   bool one_row_tile;     // N <= 256
-  float2* part;          // [vocabulary tiles][ld]
-  long long ld;
+  float2* part;          // [rows][vocabulary tiles]
   int V, steps, vtiles;
 
   __device__ void prefetch() const {
@@ -405,14 +412,13 @@ struct LossTiles {
       const float top = M == -INFINITY ? 0.f : M;
 #pragma unroll
       for (int i = 0; i < 4; ++i) S += v[i].y * ex2_approx(v[i].x - top);
-      part[(size_t)(t.n0 / 256) * ld + t.m0 + e.row] = make_float2(M, S);
+      part[(size_t)(t.m0 + e.row) * vtiles + t.n0 / 256] = make_float2(M, S);
     }
   }
 };
 
 struct CombineParams {
   const float2* part;
-  long long ld;
   int vtiles;
   const Counts* counts;
   const float* logit;
@@ -421,31 +427,39 @@ struct CombineParams {
   float* lse;
 };
 
-// 8 rows a block, 32 threads' tiles each.
-__global__ void __launch_bounds__(256) ce_combine(const CombineParams p) {
-  __shared__ float2 sums[32][8];
+// A warp a row.
+__global__ void __launch_bounds__(128) ce_combine(const CombineParams p) {
   pdl_trigger();
   pdl_wait();
-  const int r = threadIdx.x & 7, g = threadIdx.x >> 3, n = p.counts->n;
-  const int j = blockIdx.x * 8 + r;
-  if (blockIdx.x * 8 >= n) return;
+  const int j = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (j >= p.counts->n) return;
+  const float2* part = p.part + (size_t)j * p.vtiles;
   float m = -INFINITY, s = 0.f;
-#pragma unroll 4
-  for (int v = g; v < p.vtiles; v += 32) {
-    const float2 x = p.part[(size_t)v * p.ld + j];
-    const float M = fmaxf(m, x.x), top = M == -INFINITY ? 0.f : M;
-    s = s * exp2f(m - top) + x.y * exp2f(x.x - top);
+  for (int v0 = 0; v0 < p.vtiles; v0 += 32 * 8) {
+    float2 x[8];
+    float M = m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int v = v0 + i * 32 + lane;
+      x[i] = v < p.vtiles ? part[v] : make_float2(-INFINITY, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) M = fmaxf(M, x[i].x);
+    const float top = M == -INFINITY ? 0.f : M;
+    s *= exp2f(m - top);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fmaf(x[i].y, exp2f(x[i].x - top), s);
     m = M;
   }
-  sums[g][r] = make_float2(m, s);
-  __syncthreads();
-  if (threadIdx.x >= 8 || j >= n) return;
-  float M = -INFINITY, S = 0.f;
-  for (int i = 0; i < 32; ++i) M = fmaxf(M, sums[i][r].x);
-  const float top = M == -INFINITY ? 0.f : M;
-  for (int i = 0; i < 32; ++i) S += sums[i][r].y * exp2f(sums[i][r].x - top);
+  float M = m;
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  s *= exp2f(m - (M == -INFINITY ? 0.f : M));
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
+  if (lane != 0) return;
   const int row = p.list[j];
-  const float l = log2f(S);
+  const float l = log2f(s);
   p.lse[row] = (M + l) * kLn2;
   p.loss[row] = (fmaf(-p.logit[j], kLog2e, M) + l) * kLn2;
 }
@@ -699,7 +713,6 @@ __global__ void __launch_bounds__(128) ce_finish(const FinishParams p) {
 // ---------------------------------------------------------------------------
 constexpr long long kPieceBytes = 256ll << 20;   // of the slopes
 constexpr long long kPartBytes = 256ll << 20;    // of dh's parts
-constexpr int kMaxSplits = 32;
 
 struct Layout {
   long long rows;                  // N, in whole row tiles
@@ -817,15 +830,14 @@ cudaError_t launch_linear_ce(const LinearCeArgs& a, cudaStream_t stream) {
   t.live = s.counts;
   t.one_row_tile = l.rows == 256;
   t.part = reinterpret_cast<float2*>(ws + l.part);
-  t.ld = l.rows;
   t.V = a.V;
   t.steps = div_up(a.D, kStep);
   t.vtiles = l.vtiles;
   const int units = max_units<LossTiles>();
   if (units <= 0) return cudaErrorUnknown;
   CE_TRY(launch(t, (int)std::min<long long>(units, l.rows / 256 * l.vtiles), stream));
-  CombineParams c{t.part, t.ld, l.vtiles, s.counts, g.logit, s.list, a.loss, a.lse_out};
-  return small(ce_combine, div_up(a.N, 8), 256, stream, c);
+  CombineParams c{t.part, l.vtiles, s.counts, g.logit, s.list, a.loss, a.lse_out};
+  return small(ce_combine, div_up(a.N, 4), 128, stream, c);
 }
 
 cudaError_t launch_linear_ce_backward(const LinearCeArgs& a, cudaStream_t stream) {

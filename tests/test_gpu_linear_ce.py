@@ -152,7 +152,7 @@ def test_backward_against_64_bits(B, G, V, D, dtype, what):
 
 @pytest.mark.parametrize("masked", [0.0, 0.4, 1.0])
 @pytest.mark.parametrize("ragged", [False, True])
-@pytest.mark.parametrize("B,G,V,D", [(1, 1, 40, 16), (90, 7, 1000, 72), (600, 3, 300, 264)])
+@pytest.mark.parametrize("B,G,V,D", [(1, 1, 40, 16), (90, 7, 1000, 72), (600, 3, 300, 264), (1100, 3, 300, 136)])
 def test_rows_that_do_not_count(B, G, V, D, masked, ragged):
     h, W, t, rows, g_loss, g_lse = _inputs(B, G, V, D, BF16, 2, masked, ragged)
     off = ~_live(t, rows, V)
