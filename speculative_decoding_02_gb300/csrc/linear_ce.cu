@@ -26,18 +26,27 @@ constexpr int kMaxSplits = 32;   // parts of dh
 
 struct Counts {
   int n;            // rows that count
+  int all;          // and, of few rows with dW wanted, as many that hold what a rounding takes
   int full;         // tiles of dh taken whole, the first ones
   int splits;       // parts of K of the others
   float scale;      // of the slopes, a power of two
   float inv_scale;
 };
 
-// A row that counts, for its slopes.
+// A row, for its slopes.
 struct __align__(16) RowInfo {
   float lse2;       // lse log2 e
   float up, down;   // scale (g_loss + g_lse), scale g_loss
-  int token;
+  int token;        // or -2 - token: the row holds what the rounding of that slope took; -1: zeros
 };
+
+// With few rows what the rounding of a token's slope takes shows in dW (up to 2^-9
+// of the token's row, as much as dW's own rounding; with more rows it averages
+// out).  So up to kRestRows rows are repeated, from the next multiple of 32 on, with
+// those remainders alone as slopes: they fill the step of 64 rows that one row
+// takes anyway, and cost up to two steps more.
+constexpr int kRestRows = 128;
+__host__ __device__ constexpr int rest_at(int n) { return (n + 31) / 32 * 32; }
 
 __host__ __device__ constexpr long long ceil_to(long long x, long long m) { return (x + m - 1) / m * m; }
 
@@ -83,12 +92,13 @@ __device__ int choose_splits(int tx, int tw, int kx, int kw, int units, int most
 // after 838 steps (all 80 in 14 parts: 915, and 14 times the sums to keep).
 // Beside dW, whose tiles fill what is left, by parts only.  A whole warp.
 __device__ Counts counts_of(const ScanParams& p, int n, int exponent) {
-  Counts c{n, 0, 1, ldexpf(1.f, exponent), ldexpf(1.f, -exponent)};
+  Counts c{n, p.wt > 0 && n <= kRestRows ? rest_at(n) + n : n, 0, 1, ldexpf(1.f, exponent), ldexpf(1.f, -exponent)};
   if (p.dt > 0) {
     const int tiles = div_up(n, 256) * p.dt;
     c.full = p.wt == 0 ? tiles / p.units * p.units : 0;
     if (c.full < tiles)
-      c.splits = choose_splits(tiles - c.full, p.wt * div_up(p.D, 256), p.kx, div_up(n, kStep), p.units, p.max_splits);
+      c.splits = choose_splits(tiles - c.full, p.wt * div_up(p.D, 256), p.kx, div_up(c.all, kStep), p.units,
+                               p.max_splits);
   }
   return c;
 }
@@ -225,7 +235,8 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b, float s) {
 // (in fp32 from the row itself: a loss is the difference of two logits that may be
 // near each other) or what its slopes need; zeros without a row.
 template <bool kBf16>
-__device__ __forceinline__ void gather_row(const GatherParams& p, int j, int row, float scale, float* sums) {
+__device__ __forceinline__ void gather_row(const GatherParams& p, int j, int row, float scale, float* sums,
+                                           bool rest = false) {
   uint4* out = reinterpret_cast<uint4*>(p.rows + (size_t)j * p.D);
   const int chunks = p.D / 8;
   if (row < 0) {
@@ -258,7 +269,8 @@ __device__ __forceinline__ void gather_row(const GatherParams& p, int j, int row
     if (threadIdx.x == 0) p.logit[j] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
   } else if (threadIdx.x == 0) {
     const float g = p.g_loss[row];
-    p.info[j] = RowInfo{p.lse[row] * kLog2e, scale * (p.g_lse ? g + p.g_lse[row] : g), scale * g, t};
+    p.info[j] = RowInfo{p.lse[row] * kLog2e, scale * (p.g_lse ? g + p.g_lse[row] : g), scale * g,
+                        rest ? -2 - t : t};
   }
 }
 
@@ -268,9 +280,10 @@ __global__ void __launch_bounds__(128) ce_gather(const GatherParams p) {
   __shared__ float sums[4];
   pdl_trigger();
   pdl_wait();
-  const int j = blockIdx.x, n = p.counts->n;
+  const int j = blockIdx.x, n = p.counts->n, rest = rest_at(n);
   if (j >= ceil_to(n, 256)) return;
-  gather_row<kBf16>(p, j, j < n ? p.list[j] : -1, p.counts->scale, sums);
+  const bool again = p.counts->all > n && j >= rest && j < rest + n;
+  gather_row<kBf16>(p, j, again ? p.list[j - rest] : j < n ? p.list[j] : -1, p.counts->scale, sums, again);
 }
 
 // Both for few rows, without a kernel in between: every block counts the rows
@@ -308,7 +321,8 @@ __global__ void __launch_bounds__(128) ce_scan_gather(const ScanParams p, const 
   before = counted[0][0] + counted[0][1] + counted[0][2] + counted[0][3];
   all = counted[1][0] + counted[1][1] + counted[1][2] + counted[1][3];
   g = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-  const int e = slope_exponent(p, g);
+  const int e = slope_exponent(p, g), rest = rest_at(all);
+  const bool again = p.wt > 0 && all <= kRestRows;
   if (b == 0 && warp == 0) {
     const Counts c = counts_of(p, all, e);
     if (threadIdx.x == 0) *p.counts = c;
@@ -322,11 +336,12 @@ __global__ void __launch_bounds__(128) ce_scan_gather(const ScanParams p, const 
         if (p.slot) p.slot[b] = before;
       }
       gather_row<kBf16>(q, before, b, ldexpf(1.f, e), sums);
+      if (again) gather_row<kBf16>(q, rest + before, b, ldexpf(1.f, e), sums, true);
     } else if (threadIdx.x == 0) {
       leave_out(p, b, in, t);
     }
   }
-  if (b >= all && b < ceil_to(all, 256)) gather_row<kBf16>(q, b, -1, 0.f, sums);
+  if (b >= all && b < ceil_to(all, 256) && !(again && b >= rest && b < rest + all)) gather_row<kBf16>(q, b, -1, 0.f, sums);
 }
 
 // ---------------------------------------------------------------------------
@@ -364,7 +379,7 @@ struct LossTiles {
   // fp32 products: up to 9e-7 for the lse, 3e-6 to 5e-6 for the loss, at random), by 8
   // -2e-6, by 4 -1e-6, by 2 -6e-7.  N = 2048, V = 151936, D = 2560: 800, 805, 837 and
   // 899 us; one row: 135, 135, 135 and 139.
-  __device__ int chunk(int n) const { return n <= 256 ? 4 : 8; }
+  __device__ int chunk(int n) const { return n > 256 ? 8 : steps > 8 ? 4 : 2; }
   __device__ bool used(int n, const Tile& t, int row) const { return t.m0 + row < n; }
   __device__ bool tile(int n, int unit, int units, int i, Tile& t) const {
     // neighbouring units take the row tiles of the same columns, so that W
@@ -491,7 +506,7 @@ struct SlopeTiles {
     prefetch_tensormap(&out);
   }
   __device__ void early(int, int) const {}
-  __device__ int counts() const { return live->n; }
+  __device__ int counts() const { return live->all; }
   __device__ int chunk(int) const { return 64; }   // (far below the slopes' rounding)
   __device__ bool used(int n, const Tile& t, int row) const { return t.m0 + row < n; }
   __device__ bool tile(int n, int unit, int units, int i, Tile& t) const {
@@ -507,17 +522,24 @@ struct SlopeTiles {
   __device__ int segments(const Tile&) const { return 1; }
   __device__ Segment segment(const Tile& t, int) const { return Segment{&h, &w, t.m0, 0, v0 + t.n0, 0, t.steps}; }
 
+  __device__ float rounded(float x) const {
+    return bf16 ? __bfloat162float(__float2bfloat16_rn(x)) : __half2float(__float2half_rn(x));
+  }
   __device__ void epilogue(const Epi& e, const Tile& t, float (&z)[64]) const {
     const RowInfo r = info[t.m0 + e.row];
-    const int first = v0 + t.n0 + e.col, left = V - first, at = r.token - first;
+    const bool rest = r.token < -1;
+    const int first = v0 + t.n0 + e.col, left = rest ? 0 : V - first, at = (rest ? -2 - r.token : r.token) - first;
     uint32_t w[32];
 #pragma unroll
     for (int j = 0; j < 64; j += 2) {
       float x[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        x[i] = j + i < left ? ex2_approx(fmaf(z[j + i], kLog2e, -r.lse2)) * r.up : 0.f;
-        if (j + i == at) x[i] -= r.down;
+        x[i] = j + i < left || j + i == at ? ex2_approx(fmaf(z[j + i], kLog2e, -r.lse2)) * r.up : 0.f;
+        if (j + i == at) {
+          x[i] -= r.down;
+          if (rest) x[i] -= rounded(x[i]);
+        }
       }
       float2 back;
       if (bf16) {
@@ -566,7 +588,7 @@ struct GradTiles {
     c.mt = div_up(l.n, 256);
     c.full = l.full;
     c.splits = l.splits;
-    c.kw = div_up(l.n, kStep);
+    c.kw = div_up(l.all, kStep);
     c.tx = want_dh ? c.full + (c.mt * dt - c.full) * c.splits : 0;
     c.tw = wt * dt;
     c.inv_scale = l.inv_scale;
