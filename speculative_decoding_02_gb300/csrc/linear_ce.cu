@@ -205,7 +205,8 @@ struct GatherParams {
   const Counts* counts;
   int D;
   bool vec;                 // rows of h start on 16 bytes
-  unsigned short* rows;     // [..][D]
+  unsigned short* rows;     // [..][ld]
+  int ld;
   float* logit;             // forward: the token's logit
   const float* lse;         // backward
   const float* g_loss;
@@ -237,7 +238,7 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b, float s) {
 template <bool kBf16>
 __device__ __forceinline__ void gather_row(const GatherParams& p, int j, int row, float scale, float* sums,
                                            bool rest = false) {
-  uint4* out = reinterpret_cast<uint4*>(p.rows + (size_t)j * p.D);
+  uint4* out = reinterpret_cast<uint4*>(p.rows + (size_t)j * p.ld);
   const int chunks = p.D / 8;
   if (row < 0) {
     for (int c = threadIdx.x; c < chunks; c += 128) out[c] = make_uint4(0, 0, 0, 0);
@@ -738,6 +739,7 @@ constexpr long long kPartBytes = 256ll << 20;    // of dh's parts
 
 struct Layout {
   long long rows;                  // N, in whole row tiles
+  int ld;                          // of the gathered rows: on 128 bytes (copies of rows that straddle such lines take longer)
   size_t counts, list, slot, info, logit, corr, h, part, slopes, dh, total;
   int vtiles;                      // of the vocabulary
   int piece;                       // columns of a piece (a multiple of 256)
@@ -747,6 +749,7 @@ struct Layout {
 Layout layout(int N, int V, int D, bool backward, bool want_dh) {
   Layout l{};
   l.rows = ceil_to(N, 256);
+  l.ld = (int)ceil_to(D, 64);
   l.vtiles = div_up(V, 256);
   size_t at = 256;                 // the status word
   auto take = [&](size_t bytes) {
@@ -756,7 +759,7 @@ Layout layout(int N, int V, int D, bool backward, bool want_dh) {
   };
   l.counts = take(sizeof(Counts));
   l.list = take(4ull * N);
-  l.h = take(2ull * l.rows * D);
+  l.h = take(2ull * l.rows * l.ld);
   if (!backward) {
     l.logit = take(4ull * N);
     l.part = take(8ull * l.rows * l.vtiles);
@@ -807,6 +810,7 @@ cudaError_t scan_and_gather(const LinearCeArgs& a, const Layout& l, char* ws, co
   g.counts = s.counts;
   g.D = a.D;
   g.vec = reinterpret_cast<uintptr_t>(a.h) % 16 == 0 && (a.N == 1 || a.h_stride % 8 == 0);
+  g.ld = l.ld;
   g.rows = reinterpret_cast<unsigned short*>(ws + l.h);
   const bool bf16 = a.dtype == DSPARK_BF16;
   if (a.N <= kFewRows) {
@@ -845,7 +849,7 @@ cudaError_t launch_linear_ce(const LinearCeArgs& a, cudaStream_t stream) {
   CE_TRY(scan_and_gather(a, l, ws, s, g, stream));
 
   LossTiles t{};
-  CE_TRY(map_16bit(g.rows, bf16, l.rows, a.D, a.D, kRows, &t.h));
+  CE_TRY(map_16bit(g.rows, bf16, l.rows, a.D, l.ld, kRows, &t.h));
   CE_TRY(map_16bit(a.W, bf16, a.V, a.D, a.W_stride, kRows, &t.w));
   t.status = a.status;
   t.bf16 = bf16;
@@ -888,7 +892,7 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs& a, cudaStream_t stream
 
   unsigned short* slopes = reinterpret_cast<unsigned short*>(ws + l.slopes);
   SlopeTiles t{};
-  CE_TRY(map_16bit(g.rows, bf16, l.rows, a.D, a.D, kRows, &t.h));
+  CE_TRY(map_16bit(g.rows, bf16, l.rows, a.D, l.ld, kRows, &t.h));
   CE_TRY(map_16bit(a.W, bf16, a.V, a.D, a.W_stride, kRows, &t.w));
   CE_TRY(map_16bit(slopes, bf16, l.rows, l.piece, l.piece, kBoxRows, &t.out));
   t.status = a.status;
@@ -904,7 +908,7 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs& a, cudaStream_t stream
   CE_TRY(map_16bit(slopes, bf16, l.rows, l.piece, l.piece, kRows, &d.s_k));
   CE_TRY(map_16bit(slopes, bf16, l.rows, l.piece, l.piece, kStep, &d.s_mn));
   CE_TRY(map_16bit(a.W, bf16, a.V, a.D, a.W_stride, kStep, &d.w));
-  CE_TRY(map_16bit(g.rows, bf16, l.rows, a.D, a.D, kStep, &d.h));
+  CE_TRY(map_16bit(g.rows, bf16, l.rows, a.D, l.ld, kStep, &d.h));
   d.dh = d.dW = d.w;
   if (want_dh) CE_TRY(map_fp32(reinterpret_cast<float*>(ws + l.dh), l.splits, l.rows, a.D, &d.dh));
   if (want_dW) CE_TRY(map_16bit(a.dW, bf16, a.V, a.D, a.D, kBoxRows, &d.dW));

@@ -77,6 +77,7 @@ struct InputParams {
   long long stride;
   int rows, cols;
   bool vec;             // rows of M start on 4 of its values
+  bool flat;            // and M and the halves are dense arrays of whole fours
   float eps;
   double* partial;      // [blocks] sums of squares
   int* counters;        // cleared for the kernels that follow
@@ -87,26 +88,75 @@ struct InputParams {
   float ratio;          // b / c
 };
 
+// Where the i-th four values of M and of the halves are.
+struct Place {
+  size_t row, to;       // of M's row and of the halves' four
+  int c;
+};
+__device__ __forceinline__ Place place_of(const InputParams& p, long long i, int chunks) {
+  if (p.flat) return Place{(size_t)i * 4, (size_t)i * 4, 0};   // (no division)
+  const long long r = i / chunks;
+  const int c = (int)(i - r * chunks) * 4;
+  return Place{(size_t)r * p.stride, (size_t)r * p.ld + c, c};
+}
+
 constexpr int kNormThreads = 256;
 constexpr int kPrograms = 64;   // counters of programs
 constexpr int kUnit = 256;   // side of a diagonal tile
 
-// Sums of squares of values of any size: fp32 sums of three ranges, each scaled
-// so that no square leaves fp32's range, joined in 64 bits.
+// Four times four values of a thread's, kNormThreads apart and all loads first.
+template <int kType, class F>
+__device__ __forceinline__ void each_four(const InputParams& p, F f) {
+  const int chunks = (p.cols + 3) / 4;
+  const long long all = (long long)p.rows * chunks, step = (long long)gridDim.x * kNormThreads;
+  long long i = (long long)blockIdx.x * kNormThreads + threadIdx.x;
+  for (; i + 3 * step < all; i += 4 * step) {
+    float4 v[4];
+    Place at[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      at[u] = place_of(p, i + u * step, chunks);
+      v[u] = load4<kType>(p.M, at[u].row, at[u].c, p.cols, p.vec);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) f(v[u], at[u]);
+  }
+  for (; i < all; i += step) {
+    const Place at = place_of(p, i, chunks);
+    f(load4<kType>(p.M, at.row, at.c, p.cols, p.vec), at);
+  }
+}
+
+__device__ __forceinline__ float block_sum(float s, float* table) {
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
+  __syncthreads();   // (the sums before have been read)
+  if ((threadIdx.x & 31) == 0) table[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = 0.f;
+  for (int w = 0; w < kNormThreads / 32; ++w) s += table[w];
+  return s;
+}
+
+// Sums of squares of values of any size.  A block whose plain sum lies in the middle
+// of fp32's range has lost nothing that counts; another (of huge or tiny values, or
+// of zeros) sums again in three ranges, each scaled so that no square leaves fp32's
+// range.  The blocks' sums are joined in 64 bits.
 template <int kType>
 __global__ void __launch_bounds__(kNormThreads) ns_norm(const InputParams p) {
-  __shared__ float3 table[kNormThreads / 32];
+  __shared__ float table[kNormThreads / 32];
   pdl_trigger();
   pdl_wait();
-  for (int i = blockIdx.x * kNormThreads + threadIdx.x; i < kPrograms; i += gridDim.x * kNormThreads)
-    p.counters[i] = 0;
-  const int chunks = (p.cols + 3) / 4;
-  const long long all = (long long)p.rows * chunks;
+  for (int i = blockIdx.x * kNormThreads + threadIdx.x; i < kPrograms; i += gridDim.x * kNormThreads) p.counters[i] = 0;
+  float s = 0.f;
+  each_four<kType>(p, [&](float4 v, const Place&) { s = fmaf(v.x, v.x, fmaf(v.y, v.y, fmaf(v.z, v.z, fmaf(v.w, v.w, s)))); });
+  s = block_sum(s, table);
+  if (s > 0x1p-60f && s < 0x1p100f) {
+    if (threadIdx.x == 0) p.partial[blockIdx.x] = (double)s;
+    return;
+  }
   float small = 0.f, middle = 0.f, large = 0.f;
-#pragma unroll 4
-  for (long long i = (long long)blockIdx.x * kNormThreads + threadIdx.x; i < all; i += (long long)gridDim.x * kNormThreads) {
-    const long long r = i / chunks;
-    const float4 v = load4<kType>(p.M, (size_t)r * p.stride, (int)(i - r * chunks) * 4, p.cols, p.vec);
+  each_four<kType>(p, [&](float4 v, const Place&) {
     const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -115,20 +165,12 @@ __global__ void __launch_bounds__(kNormThreads) ns_norm(const InputParams p) {
       else if (t < 0x1p-40f) small = fmaf(t * 0x1p88f, t * 0x1p88f, small);
       else middle = fmaf(t, t, middle);   // (and NaN)
     }
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d /= 2) {
-    small += __shfl_xor_sync(0xffffffffu, small, d);
-    middle += __shfl_xor_sync(0xffffffffu, middle, d);
-    large += __shfl_xor_sync(0xffffffffu, large, d);
-  }
-  if ((threadIdx.x & 31) == 0) table[threadIdx.x >> 5] = make_float3(small, middle, large);
-  __syncthreads();
-  if (threadIdx.x != 0) return;
+  });
+  small = block_sum(small, table);
+  middle = block_sum(middle, table);
+  large = block_sum(large, table);
   // (64-bit arithmetic is slow here: one thread's)
-  small = middle = large = 0.f;
-  for (int w = 0; w < kNormThreads / 32; ++w) small += table[w].x, middle += table[w].y, large += table[w].z;
-  p.partial[blockIdx.x] = (double)middle + (double)large * 0x1p176 + (double)small * 0x1p-176;
+  if (threadIdx.x == 0) p.partial[blockIdx.x] = (double)middle + (double)large * 0x1p176 + (double)small * 0x1p-176;
 }
 
 // X_0 in high and low halves, and the diagonal tiles.
@@ -164,13 +206,7 @@ __global__ void __launch_bounds__(kNormThreads) ns_split(const InputParams p) {
   }
   __syncthreads();
   const float f = factors[0], p0 = factors[1], p1 = factors[2];
-  const int chunks = (p.cols + 3) / 4;
-  const long long all = (long long)p.rows * chunks;
-#pragma unroll 4
-  for (long long i = (long long)blockIdx.x * kNormThreads + threadIdx.x; i < all; i += (long long)gridDim.x * kNormThreads) {
-    const long long r = i / chunks;
-    const int c = (int)(i - r * chunks) * 4;
-    const float4 v = load4<kType>(p.M, (size_t)r * p.stride, c, p.cols, p.vec);
+  each_four<kType>(p, [&](float4 v, const Place& at) {
     const float x[4] = {v.x * p0 * p1 * f, v.y * p0 * p1 * f, v.z * p0 * p1 * f, v.w * p0 * p1 * f};
     __half2 h[2], l[2];
 #pragma unroll
@@ -179,9 +215,9 @@ __global__ void __launch_bounds__(kNormThreads) ns_split(const InputParams p) {
       const float2 back = __half22float2(h[j]);
       l[j] = __floats2half2_rn(x[2 * j] - back.x, x[2 * j + 1] - back.y);
     }
-    *reinterpret_cast<uint2*>(p.hi + (size_t)r * p.ld + c) = *reinterpret_cast<uint2*>(h);
-    *reinterpret_cast<uint2*>(p.lo + (size_t)r * p.ld + c) = *reinterpret_cast<uint2*>(l);
-  }
+    *reinterpret_cast<uint2*>(p.hi + at.to) = *reinterpret_cast<uint2*>(h);
+    *reinterpret_cast<uint2*>(p.lo + at.to) = *reinterpret_cast<uint2*>(l);
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -662,10 +698,20 @@ __global__ void __launch_bounds__(kThreads, 1) ns_program(const __grid_constant_
             tc_fence_after();
             if (elect_one()) {
               uint64_t ad = ad0 + s * (kOpStageBytes / 16), bd = bd0 + s * (kOpStageBytes / 16);
-              for (int g = 0; g < group; ++g, ad += kOpStepBytes / 16, bd += kOpStepBytes / 16) {
+              if (group == kOpGroup) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  umma_bf16(tmem + buf * kOpN, ad + kk * da, bd + kk * db, idesc, k + g != kf || kk != 0);
+                for (int g = 0; g < kOpGroup; ++g) {
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk)
+                    umma_bf16(tmem + buf * kOpN, ad + g * (kOpStepBytes / 16) + kk * da, bd + g * (kOpStepBytes / 16) + kk * db,
+                              idesc, g > 0 || kk > 0 || k != kf);
+                }
+              } else {
+                for (int g = 0; g < group; ++g, ad += kOpStepBytes / 16, bd += kOpStepBytes / 16) {
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk)
+                    umma_bf16(tmem + buf * kOpN, ad + kk * da, bd + kk * db, idesc, k + g != kf || kk != 0);
+                }
               }
               umma_commit(&bars->empty[s]);
             }
@@ -1072,6 +1118,7 @@ cudaError_t launch_newton_schulz(const NewtonSchulzArgs& a, cudaStream_t stream)
   in.cols = a.cols;
   const int size = a.dtype == DSPARK_F32 ? 4 : 2;
   in.vec = reinterpret_cast<uintptr_t>(a.M) % (4 * size) == 0 && (a.rows == 1 || a.row_stride % 4 == 0);
+  in.flat = in.vec && a.cols % 4 == 0 && l.ld == a.cols && (a.rows == 1 || a.row_stride == a.cols);
   in.eps = a.eps;
   in.partial = reinterpret_cast<double*>(ws + l.partial);
   in.blocks = (int)std::min<long long>(kNormBlocks, ((long long)a.rows * ((a.cols + 3) / 4) + kNormThreads - 1) / kNormThreads);
