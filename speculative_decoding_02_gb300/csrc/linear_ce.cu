@@ -380,7 +380,7 @@ struct LossTiles {
   // fp32 products: up to 9e-7 for the lse, 3e-6 to 5e-6 for the loss, at random), by 8
   // -2e-6, by 4 -1e-6, by 2 -6e-7.  N = 2048, V = 151936, D = 2560: 800, 805, 837 and
   // 899 us; one row: 135, 135, 135 and 139.
-  __device__ int chunk(int n) const { return n > 256 ? 8 : steps > 8 ? 4 : 2; }
+  __device__ int chunk(int n) const { return n > 256 ? 8 : n > 32 && steps > 8 ? 4 : 2; }
   __device__ bool used(int n, const Tile& t, int row) const { return t.m0 + row < n; }
   __device__ bool tile(int n, int unit, int units, int i, Tile& t) const {
     // neighbouring units take the row tiles of the same columns, so that W
