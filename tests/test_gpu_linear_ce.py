@@ -306,6 +306,34 @@ def test_differences():
         assert abs(float((grad.double() * u).sum() - slope)) < float(bound)
 
 
+def test_offsets_past_32_bits():
+    V, D = 140001, 16384   # the head has 2.3e9 values
+    g = torch.Generator(device="cuda").manual_seed(17)
+    W = torch.empty((V, D), dtype=BF16, device="cuda").normal_(0, 2 / math.sqrt(D), generator=g)
+    t = torch.tensor([[V - 1, 7, 139264]], dtype=torch.int32, device="cuda")
+    h = torch.empty((1, 3, D), device="cuda").normal_(0, 1, generator=g).to(BF16)
+    loss, lse = ds.linear_cross_entropy(h, W, t)
+    weight = torch.ones((1, 3), device="cuda")
+    dh, dW = ds.linear_cross_entropy_backward(h, W, t, lse, weight)
+    x, parts = h[0].to(F64), W.split(8192)
+    z = torch.cat([x @ w.to(F64).T for w in parts], 1)
+    size = torch.cat([x.abs() @ w.to(F64).abs().T for w in parts], 1)
+    want = torch.logsumexp(z, -1)
+    tz = 2 * ref.U * (D / 16 + 20) * size.amax()
+    ref.assert_close(lse[0], want, tz + 2.0 ** -18, "lse")
+    ref.assert_close(loss[0], want - z.gather(1, t[0].long()[:, None]).squeeze(1), 2 * tz + 2.0 ** -18, "loss")
+    s = torch.softmax(z, -1)
+    s[torch.arange(3), t[0].long()] -= 1.0
+    want = torch.zeros((3, D), dtype=F64, device="cuda")
+    for k, w in enumerate(parts):
+        want += s[:, 8192 * k:8192 * k + w.shape[0]] @ w.to(F64)
+    assert float((dh[0].to(F64) - want).norm() / want.norm()) < 2 * ref.HALF[BF16]
+    for first in (0, 131072, V - 700):   # pieces below, across and past 2^31 values
+        rows = slice(first, first + 700)
+        want = s[:, rows].T @ x
+        assert float((dW[rows].to(F64) - want).norm() / want.norm()) < 2 * ref.HALF[BF16]
+
+
 def test_results_are_reproducible():
     h, W, t, rows, g_loss, g_lse = _inputs(300, 4, 5000, 264, BF16, 13, 0.3, True)
     call = lambda: (*ds.linear_cross_entropy(h, W, t, rows=rows),

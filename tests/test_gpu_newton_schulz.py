@@ -203,6 +203,18 @@ def test_reproducible_and_a_dirty_workspace(m, n):
         assert ds.read_status(ws) == ds.OK
 
 
+@pytest.mark.parametrize("n,r", [(1040, 1024), (250, 1024)])
+def test_offsets_past_32_bits(n, r):
+    # r copies of a block below one another have the block's singular values times
+    # sqrt(r), so the result is the block's result over sqrt(r), r times
+    B = _update(2048, n, torch.bfloat16, 10)
+    got = ds.newton_schulz(B.repeat(r, 1))   # 2.2e9 values (n = 1040)
+    same = got.view(r, 2048, n)
+    assert all(torch.equal(same[k], same[0]) for k in range(1, r, 89)) and torch.equal(same[-1], same[0])
+    want = _steps(B, 5, MUON, 0.0, False) / math.sqrt(r)
+    assert float((got[:2048].to(F64) - want).norm()) <= 2.0 ** -8 * float(want.norm())
+
+
 def test_refusals():
     M = _update(20, 30)
     for bad in (M.double(), M.int()):
