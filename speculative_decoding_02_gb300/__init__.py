@@ -450,7 +450,7 @@ def _row_args(logits, rows, what="logits"):
     if V > 1 and N > 0 and logits.stride(-1) != 1:
         raise ValueError(f"{what} must have entries of a row next to each other")
     stride = V
-    if N > 1:
+    if N > 1 and not logits.is_contiguous():
         try:
             stride = logits.view(N, V).stride(0)
         except RuntimeError:
@@ -767,7 +767,8 @@ def linear_cross_entropy(h, W, tokens, rows=None, ws=None):
     allocated for the call and errors are recorded in head_status."""
     L = _load()
     dev, lead, N, R, V, D, h_stride, W_stride, dt = _hidden_args(h, W, tokens, rows)
-    loss, lse = (torch.empty(lead, dtype=torch.float32, device=dev) for _ in range(2))
+    loss = torch.empty(lead, dtype=torch.float32, device=dev)
+    lse = torch.empty(lead, dtype=torch.float32, device=dev)
     ws, status = _hidden_workspace(ws, N, V, D, 0, dev)
     _launch(L.dspark_linear_cross_entropy, "linear_cross_entropy", dev, h.data_ptr(), h_stride, W.data_ptr(), W_stride, dt,
             tokens.data_ptr(), _address(rows), N, R, V, D, loss.data_ptr(), lse.data_ptr(), _address(status),
