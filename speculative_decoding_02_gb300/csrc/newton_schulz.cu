@@ -495,12 +495,24 @@ __global__ void __launch_bounds__(256) ns_join(const JoinParams p) {
 // ---------------------------------------------------------------------------
 constexpr int kMaxOps = 24, kMaxMaps = 32;   // of a launch
 constexpr int kOpM = 128, kOpN = 64, kOpCols = kOpN / 4;
-constexpr int kOpGroup = 4;           // steps of K in a stage, which the waits and commits of a step are shared by
-constexpr int kOpStages = 2;
-constexpr int kOpStepBytes = (kOpM + kOpN) * 128, kOpStageBytes = kOpGroup * kOpStepBytes;
-constexpr int kOpRowsBytes = kOpM * 128;
-constexpr int kOpSmem = 1024 + kOpStages * kOpStageBytes + kOpRowsBytes + kBarBytes;
-static_assert(kOpSmem + 1024 + 24 * 160 <= kMaxSmem, "shared memory (and the static part)");
+constexpr int kOpLeftBytes = kOpM * 128, kOpRightBytes = kOpN * 128, kOpStepBytes = kOpLeftBytes + kOpRightBytes;
+
+// A stage of the ring holds a bundle, whose wait and commit its steps share.  Of
+// halves: both operands' for one step of K, which three products use (or two steps
+// of a product with a diagonal tile); else four steps.  Times of 256 x 256 (halves)
+// and of 1000 x 777 by the first form 86 and 112 us, by the second 92 and 105.
+template <bool kHalves>
+struct OpShape {
+  static constexpr int kSlots = kHalves ? 2 : 4, kStages = kHalves ? 3 : 2;
+  static constexpr int kStageBytes = kSlots * kOpStepBytes;
+  // where the right operand's and the next slot's tiles are
+  static constexpr int kRight = kHalves ? 2 * kOpLeftBytes : kOpLeftBytes;
+  static constexpr int kLeftSlot = kHalves ? kOpLeftBytes : kOpStepBytes, kRightSlot = kHalves ? kOpRightBytes : kOpStepBytes;
+  static constexpr int kRowsBytes = (kHalves ? 2 : 1) * kOpM * 128;
+  static constexpr int kChunk = kHalves ? 3 : 2;   // bundles that an accumulator takes: 24 to 36 additions
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + kRowsBytes + kBarBytes;
+  static_assert(kSmem + 1024 + 24 * 160 <= kMaxSmem, "shared memory (and the static part)");
+};
 
 // One product of a program.  Its sum over K is that of segments, each a pair of
 // maps and a number of steps: up to three products of halves, then up to three with
@@ -550,7 +562,17 @@ __device__ __forceinline__ bool item_of(const Op& op, int unit, int units, int i
   t.n0 = n * kOpN;
   return true;
 }
-__device__ __forceinline__ int steps_of(const Op& op) { return op.steps * op.products + op.extra * op.unit_steps; }
+// Bundles of a tile: of the operands' products, and of those with a diagonal tile
+// (which follow the product's steps in its bundles when there are no halves).
+struct Bundles {
+  int main, more;
+};
+template <bool kHalves>
+__device__ __forceinline__ Bundles bundles_of(const Op& op) {
+  constexpr int kSlots = OpShape<kHalves>::kSlots;
+  const int more = op.extra * op.unit_steps;
+  return kHalves ? Bundles{op.steps, div_up(more, kSlots)} : Bundles{div_up(op.steps + more, kSlots), 0};
+}
 
 // Until `counter` shows `least`; a converged warp.  What other CTAs stored before
 // they counted is seen by this warp's loads and its copies (the async proxy).
@@ -578,22 +600,22 @@ __device__ __forceinline__ bool wait_count(const int* counter, int least, volati
   return ok;
 }
 
+template <bool kHalves>
 __global__ void __launch_bounds__(kThreads, 1) ns_program(const __grid_constant__ Program p) {
+  using S = OpShape<kHalves>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  unsigned char* rows_s = smem + kOpStages * kOpStageBytes;   // a tile's rows on their way out
-  Bars* bars = reinterpret_cast<Bars*>(rows_s + kOpRowsBytes);
+  unsigned char* rows_s = smem + S::kStages * S::kStageBytes;   // a tile's rows on their way out
+  Bars* bars = reinterpret_cast<Bars*>(rows_s + S::kRowsBytes);
   // (in shared memory: a read of the parameters that misses their small cache takes 200 cycles)
   __shared__ Op ops[kMaxOps];
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int unit = blockIdx.x, units = gridDim.x;
   volatile int* abort = &bars->abort;
-  constexpr int kChunk = 8;
-  static_assert(kChunk % kOpGroup == 0, "whole groups in a chunk");
   for (int i = threadIdx.x; i < p.count * (int)(sizeof(Op) / 4); i += kThreads)
     reinterpret_cast<int*>(ops)[i] = reinterpret_cast<const int*>(p.ops)[i];
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kOpStages; ++s) { mbar_init(&bars->full[s], 1); mbar_init(&bars->empty[s], 1); }
+    for (int s = 0; s < S::kStages; ++s) { mbar_init(&bars->full[s], 1); mbar_init(&bars->empty[s], 1); }
     for (int s = 0; s < 2; ++s) { mbar_init(&bars->acc_full[s], 1); mbar_init(&bars->acc_empty[s], kEpiWarps); }
     bars->abort = 0;
     fence_mbar_init();
@@ -615,58 +637,77 @@ __global__ void __launch_bounds__(kThreads, 1) ns_program(const __grid_constant_
     for (int o = 0; o < p.count && ok; ++o) {
       const Op& op = ops[o];
       const bool left_mn = op.left_mn, right_mn = op.right_mn;
+      const CUtensorMap *l0 = &p.maps[op.left[0]], *l1 = &p.maps[op.left[2]], *r0 = &p.maps[op.right[0]], *r1 = &p.maps[op.right[1]];
       for (int n = 0; ok && item_of(op, unit, units, n, t); ++n) {
         if (n == 0 && op.base > 0 && !(ok = wait_count(p.counter, op.base, abort, p.status))) break;
-        int left = steps_of(op), q = 0, in = 0;    // steps to go; segment, its steps to go
+        const Bundles all = bundles_of<kHalves>(op);
+        // steps one by one: those left; segment, its steps left, maps and coordinates
+        int left = (kHalves ? 0 : op.steps) + op.extra * op.unit_steps, q = kHalves ? 3 : 0, in = 0;
         const CUtensorMap *lm = nullptr, *rm = nullptr;
         int lr = 0, lk = 0, rr = 0, rk = 0;
-        while (left > 0) {
-          const int group = min(left, kOpGroup);
-          left -= group;
+        for (int k = 0; k < all.main + all.more; ++k, ++i) {
           ok = warp_wait(&bars->empty[s], phase, abort, p.status);
           if (!ok) break;
-          uint32_t dst = stages + s * kOpStageBytes;
+          uint32_t l = stages + s * S::kStageBytes, r = l + S::kRight;
           const uint32_t full = smem_u32(&bars->full[s]);
-          if (elect_one()) mbar_arrive_expect_tx(&bars->full[s], group * kOpStepBytes);
-          __syncwarp();
-          for (int g = 0; g < group; ++g, dst += kOpStepBytes) {
-            if (in == 0) {   // the next segment
-              lr = t.m0;
-              rr = t.n0;
-              lk = rk = 0;
-              if (q < op.products) {
-                in = op.steps;
-                lm = &p.maps[op.left[q]];
-                rm = &p.maps[op.right[q]];
-              } else {
-                const int x = q - op.products;
-                in = op.unit_steps;
-                lm = &p.maps[op.unit_is_left ? op.unit[x] : op.of[x]];
-                rm = &p.maps[op.unit_is_left ? op.of[x] : op.unit[x]];
-                if (op.unit_is_left) lr = 0, lk = 0, rk = t.m0;
-                else lk = t.n0, rr = 0, rk = 0;
-              }
-              ++q;
-            }
-            // (the coordinate along K is the second one of an operand that is not K-major)
+          // (one lane's are the copies alone, and a step needs no division: an issuing
+          // loop that is longer shows in every product)
+          if (kHalves && k < all.main) {
+            const int at = k * kStep;
             if (elect_one()) {
-              copy_box<false>(dst, lm, left_mn ? lr : lk, left_mn ? lk : lr, full);
-              if (left_mn) copy_box<false>(dst + 8192, lm, lr + 64, lk, full);
-              copy_box<false>(dst + kOpM * 128, rm, right_mn ? rr : rk, right_mn ? rk : rr, full);
+              mbar_arrive_expect_tx(&bars->full[s], 2 * kOpStepBytes);
+              const int lx = left_mn ? t.m0 : at, ly = left_mn ? at : t.m0, rx = right_mn ? t.n0 : at, ry = right_mn ? at : t.n0;
+              copy_box<false>(l, l0, lx, ly, full);
+              if (left_mn) copy_box<false>(l + 8192, l0, lx + 64, ly, full);
+              copy_box<false>(r, r0, rx, ry, full);
+              copy_box<false>(r + kOpRightBytes, r1, rx, ry, full);   // the low halves in the second slot
+              copy_box<false>(l + kOpLeftBytes, l1, lx, ly, full);
+              if (left_mn) copy_box<false>(l + kOpLeftBytes + 8192, l1, lx + 64, ly, full);
             }
             __syncwarp();
-            --in;
-            lk += kStep;
-            rk += kStep;
+          } else {
+            const int group = min(left, S::kSlots);
+            left -= group;
+            if (elect_one()) mbar_arrive_expect_tx(&bars->full[s], group * kOpStepBytes);
+            __syncwarp();
+            for (int g = 0; g < group; ++g, l += S::kLeftSlot, r += S::kRightSlot) {
+              if (in == 0) {   // the next segment
+                lr = t.m0;
+                rr = t.n0;
+                lk = rk = 0;
+                if (q < op.products) {
+                  in = op.steps;
+                  lm = l0;
+                  rm = r0;
+                } else {
+                  const int x = q - op.products;
+                  in = op.unit_steps;
+                  lm = &p.maps[op.unit_is_left ? op.unit[x] : op.of[x]];
+                  rm = &p.maps[op.unit_is_left ? op.of[x] : op.unit[x]];
+                  if (op.unit_is_left) lr = 0, lk = 0, rk = t.m0;
+                  else lk = t.n0, rr = 0, rk = 0;
+                }
+                ++q;
+              }
+              // (the coordinate along K is the second one of an operand that is not K-major)
+              if (elect_one()) {
+                copy_box<false>(l, lm, left_mn ? lr : lk, left_mn ? lk : lr, full);
+                if (left_mn) copy_box<false>(l + 8192, lm, lr + 64, lk, full);
+                copy_box<false>(r, rm, right_mn ? rr : rk, right_mn ? rk : rr, full);
+              }
+              __syncwarp();
+              --in;
+              lk += kStep;
+              rk += kStep;
+            }
           }
-          ++i;
-          if (++s == kOpStages) s = 0, phase ^= 1;
+          if (++s == S::kStages) s = 0, phase ^= 1;
         }
       }
     }
     if (lane == 0) {
-      for (int s = 0; s < kOpStages; ++s) {
-        const uint32_t n = (i + kOpStages - 1 - s) / kOpStages;
+      for (int s = 0; s < S::kStages; ++s) {
+        const uint32_t n = (i + S::kStages - 1 - s) / S::kStages;
         if (n > 0) mbar_drain(&bars->empty[s], (n - 1) & 1);
       }
     }
@@ -683,41 +724,55 @@ __global__ void __launch_bounds__(kThreads, 1) ns_program(const __grid_constant_
       const uint32_t idesc = base | (op.left_mn ? kAMajorM : 0u) | (op.right_mn ? kBMajorN : 0u);
       const uint32_t da = op.left_mn ? 128 : 2, db = op.right_mn ? 128 : 2;
       const uint64_t ad0 = op.left_mn ? sw128_mnmajor_desc(stages, 8192) : sw128_kmajor_desc(stages);
-      const uint64_t bd0 = op.right_mn ? sw128_mnmajor_desc(stages + kOpM * 128, 8192) : sw128_kmajor_desc(stages + kOpM * 128);
+      const uint64_t bd0 = op.right_mn ? sw128_mnmajor_desc(stages + S::kRight, 8192) : sw128_kmajor_desc(stages + S::kRight);
+      const Bundles bundles = bundles_of<kHalves>(op);
+      const int all = bundles.main + bundles.more;
       for (int n = 0; ok && item_of(op, unit, units, n, t); ++n) {
-        const int all = steps_of(op);
         for (int k = 0; k < all && ok; ++c) {
-          const int buf = c & 1, kend = min(k + kChunk, all);
+          const int buf = c & 1, kend = min(k + S::kChunk, all);
           ok = warp_wait(&bars->acc_empty[buf], ((c >> 1) & 1) ^ 1, abort, p.status);
           if (!ok) break;
           tc_fence_after();
-          for (int kf = k; k < kend;) {
-            const int group = min(all - k, kOpGroup);
+          for (int kf = k; k < kend; ++k) {
             ok = warp_wait(&bars->full[s], phase, abort, p.status);
             if (!ok) break;
             tc_fence_after();
+            uint64_t ad = ad0 + s * (S::kStageBytes / 16), bd = bd0 + s * (S::kStageBytes / 16);
+            constexpr uint64_t a1 = S::kLeftSlot / 16, b1 = S::kRightSlot / 16;
+            const uint32_t d = tmem + buf * kOpN;
+            const int n = (kHalves ? S::kSlots * bundles.main : op.steps) + op.extra * op.unit_steps - S::kSlots * k;   // (of halves: behind the products)
             if (elect_one()) {
-              uint64_t ad = ad0 + s * (kOpStageBytes / 16), bd = bd0 + s * (kOpStageBytes / 16);
-              if (group == kOpGroup) {
+              if (kHalves) {
+                const bool three = k < bundles.main;
 #pragma unroll
-                for (int g = 0; g < kOpGroup; ++g) {
+                for (int kk = 0; kk < 4; ++kk) umma_bf16(d, ad + kk * da, bd + kk * db, idesc, k != kf || kk != 0);
+                if (three) {
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk) {
+                    umma_bf16(d, ad + kk * da, bd + b1 + kk * db, idesc, 1);
+                    umma_bf16(d, ad + a1 + kk * da, bd + kk * db, idesc, 1);
+                  }
+                } else if (n > 1) {
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk) umma_bf16(d, ad + a1 + kk * da, bd + b1 + kk * db, idesc, 1);
+                }
+              } else if (n >= S::kSlots) {
+#pragma unroll
+                for (int g = 0; g < S::kSlots; ++g) {
 #pragma unroll
                   for (int kk = 0; kk < 4; ++kk)
-                    umma_bf16(tmem + buf * kOpN, ad + g * (kOpStepBytes / 16) + kk * da, bd + g * (kOpStepBytes / 16) + kk * db,
-                              idesc, g > 0 || kk > 0 || k != kf);
+                    umma_bf16(d, ad + g * a1 + kk * da, bd + g * b1 + kk * db, idesc, g > 0 || kk > 0 || k != kf);
                 }
               } else {
-                for (int g = 0; g < group; ++g, ad += kOpStepBytes / 16, bd += kOpStepBytes / 16) {
+                for (int g = 0; g < n; ++g, ad += a1, bd += b1) {
 #pragma unroll
-                  for (int kk = 0; kk < 4; ++kk)
-                    umma_bf16(tmem + buf * kOpN, ad + kk * da, bd + kk * db, idesc, k + g != kf || kk != 0);
+                  for (int kk = 0; kk < 4; ++kk) umma_bf16(d, ad + kk * da, bd + kk * db, idesc, k != kf || g != 0 || kk != 0);
                 }
               }
               umma_commit(&bars->empty[s]);
             }
             __syncwarp();
-            k += group;
-            if (++s == kOpStages) s = 0, phase ^= 1;
+            if (++s == S::kStages) s = 0, phase ^= 1;
           }
           if (ok && elect_one()) umma_commit(&bars->acc_full[buf]);
           __syncwarp();
@@ -735,7 +790,8 @@ __global__ void __launch_bounds__(kThreads, 1) ns_program(const __grid_constant_
     for (int o = 0; o < p.count; ++o) {
       const Op& op = ops[o];
       for (int n = 0; item_of(op, unit, units, n, t); ++n) {
-        const int all = steps_of(op), chunks = div_up(all, kChunk);
+        const Bundles bundles = bundles_of<kHalves>(op);
+        const int chunks = div_up(bundles.main + bundles.more, S::kChunk);
         float v[kOpCols];
 #pragma unroll
         for (int j = 0; j < kOpCols; ++j) v[j] = 0.f;
@@ -760,30 +816,33 @@ __global__ void __launch_bounds__(kThreads, 1) ns_program(const __grid_constant_
           if (op.diag != 0.f && col + j == row) v[j] += op.diag;
         }
         uint32_t w[kOpCols / 2];
-        unsigned char* mine = rows_s + q * 4096;
+        unsigned char* mine = rows_s + q * 4096;   // (and 16 KB on for low halves)
         // this warp's 16 columns of 32 rows beside those of the other three, then
         // whole rows of 128 bytes: a store of a row a thread takes 32 turns, of 4 rows
         // a warp 4
-        auto store_rows = [&](void* to, long long ld) {
+        auto place = [&](unsigned char* at) {
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            *reinterpret_cast<uint4*>(mine + lane * 128 + (((h * 2 + j) ^ (lane & 7)) << 4)) =
+            *reinterpret_cast<uint4*>(at + lane * 128 + (((h * 2 + j) ^ (lane & 7)) << 4)) =
                 make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-          named_bar_sync(2 + q, 128);
+        };
+        auto store_rows = [&](const unsigned char* at, void* to, long long ld) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const int r = h * 8 + j * 4 + lane / 8, x = lane % 8, gr = t.m0 + q * 32 + r, gc = t.n0 + x * 8;
-            const uint4 y = *reinterpret_cast<const uint4*>(mine + r * 128 + ((x ^ (r & 7)) << 4));
+            const uint4 y = *reinterpret_cast<const uint4*>(at + r * 128 + ((x ^ (r & 7)) << 4));
             if (gr < op.rows && gc < op.cols)
               *reinterpret_cast<uint4*>(static_cast<unsigned short*>(to) + (size_t)gr * ld + gc) = y;
           }
-          named_bar_sync(2 + q, 128);
         };
         if (op.out != nullptr) {
 #pragma unroll
           for (int j = 0; j < kOpCols; j += 2) w[j / 2] = pack_bf16(v[j], v[j + 1]);
           if (op.vec) {
-            store_rows(op.out, op.ld_out);
+            place(mine);
+            named_bar_sync(2 + q, 128);
+            store_rows(mine, op.out, op.ld_out);
+            named_bar_sync(2 + q, 128);   // (the next tile's rows take their place)
           } else if (row < op.rows) {
             unsigned short* dst = reinterpret_cast<unsigned short*>(op.out) + (size_t)row * op.ld_out + col;
 #pragma unroll
@@ -792,28 +851,41 @@ __global__ void __launch_bounds__(kThreads, 1) ns_program(const __grid_constant_
           }
           continue;
         }
-        const bool mirror = op.symmetric && t.n0 + kOpN <= t.m0;
+        const bool mirror = op.symmetric && t.n0 + kOpN <= t.m0 && row < op.rows;
+        auto store_mirror = [&](__half* to) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          __half* to = half == 0 ? op.to0 : op.to1;
-          if (to == nullptr) break;
+          for (int j = 0; j < kOpCols; ++j)
+            if (col + j < op.cols)
+              reinterpret_cast<unsigned short*>(to)[(size_t)(col + j) * op.ld + row] =
+                  (unsigned short)(j % 2 ? w[j / 2] >> 16 : w[j / 2]);
+        };
+        auto make_low = [&] {
 #pragma unroll
           for (int j = 0; j < kOpCols; j += 2) {
-            if (half == 1) {
-              const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&w[j / 2]));
-              w[j / 2] = pack_half(v[j] - back.x, v[j + 1] - back.y);
-            } else {
-              w[j / 2] = pack_half(v[j], v[j + 1]);
-            }
+            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&w[j / 2]));
+            w[j / 2] = pack_half(v[j] - back.x, v[j + 1] - back.y);
           }
-          store_rows(to, op.ld);
-          if (mirror && row < op.rows) {
+        };
 #pragma unroll
-            for (int j = 0; j < kOpCols; ++j)
-              if (col + j < op.cols)
-                reinterpret_cast<unsigned short*>(to)[(size_t)(col + j) * op.ld + row] =
-                    (unsigned short)(j % 2 ? w[j / 2] >> 16 : w[j / 2]);
-          }
+        for (int j = 0; j < kOpCols; j += 2) w[j / 2] = pack_half(v[j], v[j + 1]);
+        place(mine);
+        if (mirror) store_mirror(op.to0);
+        if (kHalves && op.to1 != nullptr) {
+          make_low();
+          place(mine + kOpM * 128);
+          if (mirror) store_mirror(op.to1);
+        }
+        named_bar_sync(2 + q, 128);
+        store_rows(mine, op.to0, op.ld);
+        if (kHalves) {
+          if (op.to1 != nullptr) store_rows(mine + kOpM * 128, op.to1, op.ld);
+        } else if (op.to1 != nullptr) {   // (X's, in the place of the high ones)
+          make_low();
+          named_bar_sync(2 + q, 128);
+          place(mine);
+          if (mirror) store_mirror(op.to1);
+          named_bar_sync(2 + q, 128);
+          store_rows(mine, op.to1, op.ld);
         }
         // the tile is done: its stores are seen by who sees the counter (and, behind
         // the fence there, by copies, the async proxy)
@@ -998,8 +1070,10 @@ struct Builder {
   cudaStream_t stream;
   cudaError_t error = cudaSuccess;
 
-  Builder(int* counters, int* status, int sms, cudaStream_t stream)
-      : counters(counters), status(status), sms(sms), stream(stream) {}
+  bool halves;   // of every op's operands
+
+  Builder(bool halves, int* counters, int* status, int sms, cudaStream_t stream)
+      : counters(counters), status(status), sms(sms), stream(stream), halves(halves) {}
 
   void start() {
     p.map_count = p.count = 0;
@@ -1064,19 +1138,21 @@ struct Builder {
     if (programs == kPrograms) return cudaErrorInvalidValue;
     p.counter = counters + programs++;
     p.status = status;
-    cudaError_t e = cudaFuncSetAttribute(ns_program, cudaFuncAttributeMaxDynamicSharedMemorySize, kOpSmem);
+    auto kern = halves ? ns_program<true> : ns_program<false>;
+    const int smem = halves ? OpShape<true>::kSmem : OpShape<false>::kSmem;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)std::min(sms, items));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kOpSmem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;   // its CTAs wait for one another
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, ns_program, p);
+    e = cudaLaunchKernelEx(&cfg, kern, p);
     start();
     return e;
   }
@@ -1142,7 +1218,7 @@ cudaError_t launch_newton_schulz(const NewtonSchulzArgs& a, cudaStream_t stream)
   const Halves mA{A[0], A[1], small, small, l.lda}, mB{B[0], B[1], small, small, l.lda};
   auto X = [&](int i, bool low) { return Halves{x[i & 1][0], low ? x[i & 1][1] : nullptr, a.rows, a.cols, l.ld}; };
   const Halves one{in.units, nullptr, kUnit, kUnit, kUnit}, ratio{in.units + kUnit * kUnit, in.units + 2 * kUnit * kUnit, kUnit, kUnit, kUnit};
-  Builder build(in.counters, a.status, sms, stream);
+  Builder build(l.halves, in.counters, a.status, sms, stream);
   // b A + c A A + diag: b / c A by the diagonal tile
   auto square = [&](const Halves& from, const Halves& to, float c, float diag) {
     Op& op = build.add(from, false, from, false, small, small, small, true);
