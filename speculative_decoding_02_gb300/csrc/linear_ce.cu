@@ -10,6 +10,10 @@
 // Four products of 2 N V D operations (the gradients form z again), bound by the
 // tensor cores as soon as there are a few hundred rows and by the read of W below.
 // The rows that count are gathered first, so the others cost nothing.
+//
+// Measured (GB300, bf16): 2048 rows under a head of 151936 x 2560, the loss 792 us
+// (2.01 PFLOP/s, tensor pipe 97 %; 911 us for seconds on end, under the power
+// cap), dh 1659 us (1.92 PFLOP/s; 1923); one row 137 us (5.7 TB/s of W).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

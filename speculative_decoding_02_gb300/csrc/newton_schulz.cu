@@ -21,7 +21,12 @@
 // The linear terms a X and b A are products too, with a diagonal tile as an operand
 // (of X's halves with ones, of A with b / c in halves), so that no epilogue
 // reads anything: its loads took 5 us of a tile for A, 10 for X, against 0.3 us for
-// each step of 64 of K.  B is kept as B / a.
+// each step of 64 of K.  B is kept as B / a (of halves with a on its diagonal, so that
+// X <- B X is all of the step).
+//
+// Measured (GB300, 5 steps): 4096 x 4096 1181 us (1.16 PFLOP/s of the symmetric
+// count), bound by whole waves of tiles and 15 launches; 1000 x 777 112 us, 256 x 256
+// 87 us, bound by latency; 151936 x 256 362 us, half of it at HBM's rate.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
