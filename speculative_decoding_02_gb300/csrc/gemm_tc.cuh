@@ -31,6 +31,7 @@
 //     for all its threads; false when there is none
 //   int segments(tile), Segment segment(tile, i)  where the operands' steps of K are
 //   void epilogue(Epi&, tile, acc)      every epilogue thread, converged
+//   void finish(counts, Epi)            every epilogue thread, behind its last tile
 //   void prefetch()                     of the tensor maps
 //   void early(unit, rank)              a warp, before pdl_wait
 #pragma once
@@ -368,6 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
       e.n = n;
       p.epilogue(e, t, acc);
     }
+    p.finish(counts, e);
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   tc_fence_before();

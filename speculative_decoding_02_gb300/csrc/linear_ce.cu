@@ -35,6 +35,7 @@ struct Counts {
   int splits;       // parts of K of the others
   float scale;      // of the slopes, a power of two
   float inv_scale;
+  int done;         // CTAs of the loss' tiles that are done
 };
 
 // A row, for its slopes.
@@ -96,7 +97,7 @@ __device__ int choose_splits(int tx, int tw, int kx, int kw, int units, int most
 // after 838 steps (all 80 in 14 parts: 915, and 14 times the sums to keep).
 // Beside dW, whose tiles fill what is left, by parts only.  A whole warp.
 __device__ Counts counts_of(const ScanParams& p, int n, int exponent) {
-  Counts c{n, p.wt > 0 && n <= kRestRows ? rest_at(n) + n : n, 0, 1, ldexpf(1.f, exponent), ldexpf(1.f, -exponent)};
+  Counts c{n, p.wt > 0 && n <= kRestRows ? rest_at(n) + n : n, 0, 1, ldexpf(1.f, exponent), ldexpf(1.f, -exponent), 0};
   if (p.dt > 0) {
     const int tiles = div_up(n, 256) * p.dt;
     c.full = p.wt == 0 ? tiles / p.units * p.units : 0;
@@ -353,17 +354,63 @@ __global__ void __launch_bounds__(128) ce_scan_gather(const ScanParams p, const 
 // forward
 // ---------------------------------------------------------------------------
 
+struct CombineParams {
+  const float2* part;      // [rows][vocabulary tiles]
+  int vtiles;
+  Counts* counts;
+  const float* logit;
+  const int32_t* list;
+  float* loss;
+  float* lse;
+};
+
+// Row j from its tiles' maxima and sums; a warp.
+__device__ __forceinline__ void combine_row(const CombineParams& p, int j) {
+  const int lane = threadIdx.x & 31;
+  const float2* part = p.part + (size_t)j * p.vtiles;
+  float m = -INFINITY, s = 0.f;
+  for (int v0 = 0; v0 < p.vtiles; v0 += 32 * 8) {
+    float2 x[8];
+    float M = m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int v = v0 + i * 32 + lane;
+      x[i] = v < p.vtiles ? __ldcg(part + v) : make_float2(-INFINITY, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) M = fmaxf(M, x[i].x);
+    const float top = M == -INFINITY ? 0.f : M;
+    s *= exp2f(m - top);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fmaf(x[i].y, exp2f(x[i].x - top), s);
+    m = M;
+  }
+  float M = m;
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  s *= exp2f(m - (M == -INFINITY ? 0.f : M));
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
+  if (lane != 0) return;
+  const int row = p.list[j];
+  const float l = log2f(s);
+  p.lse[row] = (M + l) * kLn2;
+  p.loss[row] = (fmaf(-p.logit[j], kLog2e, M) + l) * kLn2;
+}
+
 // z = h W^T by tiles; of a tile's rows, the maximum (in units of log 2) and the
 // sum of 2^(z log2 e - maximum) of its 256 columns.
 struct LossTiles {
   CUtensorMap h, w;
   static constexpr bool kPair = true, kSelf = false;
-  static constexpr int kN = 256, kBoxBytes = 0, kExtraBytes = 2 * 4 * kRows * 8;
+  static constexpr int kN = 256, kBoxBytes = 0, kTables = 2 * 4 * kRows * 8, kExtraBytes = kTables + 128;
   using Counts = int;
   int* status;
   bool bf16;
   const dspark::Counts* live;
   bool one_row_tile;     // N <= 256
+  bool last_combines;    // the last CTA to end has the rows combined; else a kernel does
+  CombineParams rows;
   float2* part;          // [rows][vocabulary tiles]
   int V, steps, vtiles;
 
@@ -401,6 +448,21 @@ struct LossTiles {
   __device__ int segments(const Tile&) const { return 1; }
   __device__ Segment segment(const Tile& t, int) const { return Segment{&h, &w, t.m0, 0, t.n0, 0, t.steps}; }
 
+  // A few rows are combined here, which saves a launch (3 us).
+  __device__ void finish(int n, const Epi& e) const {
+    if (!last_combines || n == 0) return;
+    int* last = reinterpret_cast<int*>(e.extra + kTables);
+    named_bar_sync(5, kEpiWarps * 32);
+    if (threadIdx.x == 64) {
+      __threadfence();   // (all of this CTA's parts, through the barrier)
+      *last = atomicAdd(&rows.counts->done, 1) == (int)gridDim.x - 1;
+      __threadfence();
+    }
+    named_bar_sync(5, kEpiWarps * 32);
+    if (!*last) return;
+    for (int j = (threadIdx.x >> 5) - 2; j < n; j += kEpiWarps) combine_row(rows, j);
+  }
+
   __device__ void epilogue(const Epi& e, const Tile& t, float (&z)[64]) const {
     if (!e.used) return;   // (nor are the other warps of these rows)
     const int left = V - (t.n0 + e.col);
@@ -437,51 +499,12 @@ struct LossTiles {
   }
 };
 
-struct CombineParams {
-  const float2* part;
-  int vtiles;
-  const Counts* counts;
-  const float* logit;
-  const int32_t* list;
-  float* loss;
-  float* lse;
-};
-
 // A warp a row.
 __global__ void __launch_bounds__(128) ce_combine(const CombineParams p) {
   pdl_trigger();
   pdl_wait();
-  const int j = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (j >= p.counts->n) return;
-  const float2* part = p.part + (size_t)j * p.vtiles;
-  float m = -INFINITY, s = 0.f;
-  for (int v0 = 0; v0 < p.vtiles; v0 += 32 * 8) {
-    float2 x[8];
-    float M = m;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int v = v0 + i * 32 + lane;
-      x[i] = v < p.vtiles ? part[v] : make_float2(-INFINITY, 0.f);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) M = fmaxf(M, x[i].x);
-    const float top = M == -INFINITY ? 0.f : M;
-    s *= exp2f(m - top);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(x[i].y, exp2f(x[i].x - top), s);
-    m = M;
-  }
-  float M = m;
-#pragma unroll
-  for (int d = 16; d > 0; d /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  s *= exp2f(m - (M == -INFINITY ? 0.f : M));
-#pragma unroll
-  for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
-  if (lane != 0) return;
-  const int row = p.list[j];
-  const float l = log2f(s);
-  p.lse[row] = (M + l) * kLn2;
-  p.loss[row] = (fmaf(-p.logit[j], kLog2e, M) + l) * kLn2;
+  const int j = blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (j < p.counts->n) combine_row(p, j);
 }
 
 // ---------------------------------------------------------------------------
@@ -511,6 +534,8 @@ struct SlopeTiles {
     prefetch_tensormap(&out);
   }
   __device__ void early(int, int) const {}
+  template <class C>
+  __device__ void finish(const C&, const Epi&) const {}
   __device__ int counts() const { return live->all; }
   __device__ int chunk(int) const { return 64; }   // (far below the slopes' rounding)
   __device__ bool used(int n, const Tile& t, int row) const { return t.m0 + row < n; }
@@ -586,6 +611,8 @@ struct GradTiles {
     for (const CUtensorMap* m : {&s_k, &s_mn, &w, &h, &dh, &dW}) prefetch_tensormap(m);
   }
   __device__ void early(int, int) const {}
+  template <class C>
+  __device__ void finish(const C&, const Epi&) const {}
   __device__ Counts counts() const {
     const dspark::Counts l = *live;
     Counts c;
@@ -863,11 +890,13 @@ cudaError_t launch_linear_ce(const LinearCeArgs& a, cudaStream_t stream) {
   t.V = a.V;
   t.steps = div_up(a.D, kStep);
   t.vtiles = l.vtiles;
+  t.rows = CombineParams{t.part, l.vtiles, s.counts, g.logit, s.list, a.loss, a.lse_out};
+  // (16 warps, 256 tiles at a time: up to 5 turns of about 0.7 us)
+  t.last_combines = (long long)div_up(a.N, kEpiWarps) * div_up(l.vtiles, 256) <= 5;
   const int units = max_units<LossTiles>();
   if (units <= 0) return cudaErrorUnknown;
   CE_TRY(launch(t, (int)std::min<long long>(units, l.rows / 256 * l.vtiles), stream));
-  CombineParams c{t.part, l.vtiles, s.counts, g.logit, s.list, a.loss, a.lse_out};
-  return small(ce_combine, div_up(a.N, 4), 128, stream, c);
+  return t.last_combines ? cudaSuccess : small(ce_combine, div_up(a.N, 4), 128, stream, t.rows);
 }
 
 cudaError_t launch_linear_ce_backward(const LinearCeArgs& a, cudaStream_t stream) {

@@ -274,6 +274,7 @@ struct NsTiles {
     for (const CUtensorMap* m : {&left, &left_low, &right, &right_low, &unit, &unit_low, &out0, &out1}) prefetch_tensormap(m);
   }
   __device__ void early(int, int) const {}
+  __device__ void finish(int, const Epi&) const {}
   __device__ int counts() const { return 0; }
   __device__ int chunk(int) const { return kSelf ? 4 : 8; }
   __device__ bool used(int, const Tile&, int) const { return true; }
