@@ -13,7 +13,7 @@
 //
 // Measured (GB300, bf16): 2048 rows under a head of 151936 x 2560, the loss 792 us
 // (2.01 PFLOP/s, tensor pipe 97 %; 911 us for seconds on end, under the power
-// cap), dh 1659 us (1.92 PFLOP/s; 1923); one row 137 us (5.7 TB/s of W).
+// cap), dh 1659 us (1.92 PFLOP/s; 1923); one row 132 us (5.9 TB/s of W).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -400,10 +400,11 @@ __device__ __forceinline__ void combine_row(const CombineParams& p, int j) {
 
 // z = h W^T by tiles; of a tile's rows, the maximum (in units of log 2) and the
 // sum of 2^(z log2 e - maximum) of its 256 columns.
+template <bool kPairs>
 struct LossTiles {
   CUtensorMap h, w;
-  static constexpr bool kPair = true, kSelf = false;
-  static constexpr int kN = 256, kBoxBytes = 0, kTables = 2 * 4 * kRows * 8, kExtraBytes = kTables + 128;
+  static constexpr bool kPair = kPairs, kSelf = false;   // single CTAs: up to 128 rows, a tile each
+  static constexpr int kM = kPairs ? 256 : 128, kN = 256, kBoxBytes = 0, kTables = 2 * 4 * kRows * 8, kExtraBytes = kTables + 128;
   using Counts = int;
   int* status;
   bool bf16;
@@ -423,7 +424,7 @@ struct LossTiles {
   // kernel before, which began when all earlier work was done)
   __device__ void early(int unit, int rank) const {
     if (!one_row_tile) return;
-    for (int k = threadIdx.x; k < steps; k += 32) prefetch_box(&w, k * kStep, unit * 256 + rank * 128);
+    for (int k = threadIdx.x; k < steps; k += 32) prefetch_box(&w, k * kStep, unit * kN + rank * 128);
   }
   __device__ int counts() const { return live->n; }
   // An accumulator loses about half a step an addition, always towards zero: by
@@ -436,11 +437,11 @@ struct LossTiles {
   __device__ bool tile(int n, int unit, int units, int i, Tile& t) const {
     // neighbouring units take the row tiles of the same columns, so that W
     // comes once from HBM
-    const int mt = div_up(n, 256);
+    const int mt = div_up(n, kM);
     const long long u = (long long)i * units + unit;
     if (u >= (long long)mt * vtiles) return false;
-    t.m0 = (int)(u % mt) * 256;
-    t.n0 = (int)(u / mt) * 256;
+    t.m0 = (int)(u % mt) * kM;
+    t.n0 = (int)(u / mt) * kN;
     t.steps = steps;
     t.a_mn = t.b_mn = false;
     return true;
@@ -866,22 +867,14 @@ ScanParams scan_params(const LinearCeArgs& a, const Layout& l, char* ws) {
   return s;
 }
 
-}  // namespace
-
-cudaError_t launch_linear_ce(const LinearCeArgs& a, cudaStream_t stream) {
-  const Layout l = layout(a.N, a.V, a.D, false, false);
-  char* ws = static_cast<char*>(a.ws);
+// The tiles and, unless the last of them does it, the rows combined.
+template <bool kPairs>
+cudaError_t launch_loss(const LinearCeArgs& a, const Layout& l, char* ws, const ScanParams& s, const GatherParams& g,
+                        cudaStream_t stream) {
   const bool bf16 = a.dtype == DSPARK_BF16;
-  ScanParams s = scan_params(a, l, ws);
-  s.loss = a.loss;
-  s.lse = a.lse_out;
-  GatherParams g{};
-  g.logit = reinterpret_cast<float*>(ws + l.logit);
-  CE_TRY(scan_and_gather(a, l, ws, s, g, stream));
-
-  LossTiles t{};
+  LossTiles<kPairs> t{};
   CE_TRY(map_16bit(g.rows, bf16, l.rows, a.D, l.ld, kRows, &t.h));
-  CE_TRY(map_16bit(a.W, bf16, a.V, a.D, a.W_stride, kRows, &t.w));
+  CE_TRY(map_16bit(a.W, bf16, a.V, a.D, a.W_stride, Shape<LossTiles<kPairs>>::kBRows, &t.w));
   t.status = a.status;
   t.bf16 = bf16;
   t.live = s.counts;
@@ -893,10 +886,27 @@ cudaError_t launch_linear_ce(const LinearCeArgs& a, cudaStream_t stream) {
   t.rows = CombineParams{t.part, l.vtiles, s.counts, g.logit, s.list, a.loss, a.lse_out};
   // (16 warps, 256 tiles at a time: up to 5 turns of about 0.7 us)
   t.last_combines = (long long)div_up(a.N, kEpiWarps) * div_up(l.vtiles, 256) <= 5;
-  const int units = max_units<LossTiles>();
+  const int units = max_units<LossTiles<kPairs>>();
   if (units <= 0) return cudaErrorUnknown;
-  CE_TRY(launch(t, (int)std::min<long long>(units, l.rows / 256 * l.vtiles), stream));
+  CE_TRY(launch(t, (int)std::min<long long>(units, (long long)div_up(a.N, LossTiles<kPairs>::kM) * l.vtiles), stream));
   return t.last_combines ? cudaSuccess : small(ce_combine, div_up(a.N, 4), 128, stream, t.rows);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_ce(const LinearCeArgs& a, cudaStream_t stream) {
+  const Layout l = layout(a.N, a.V, a.D, false, false);
+  char* ws = static_cast<char*>(a.ws);
+  ScanParams s = scan_params(a, l, ws);
+  s.loss = a.loss;
+  s.lse = a.lse_out;
+  GatherParams g{};
+  g.logit = reinterpret_cast<float*>(ws + l.logit);
+  CE_TRY(scan_and_gather(a, l, ws, s, g, stream));
+
+  // (pairs would pad to 256 rows: one row under a head of 151936 x 2560 takes 132 us by
+  // single CTAs, 135 by pairs; 56 rows under 32000 x 1024, 21 and 25)
+  return a.N <= kRows ? launch_loss<false>(a, l, ws, s, g, stream) : launch_loss<true>(a, l, ws, s, g, stream);
 }
 
 cudaError_t launch_linear_ce_backward(const LinearCeArgs& a, cudaStream_t stream) {
