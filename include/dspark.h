@@ -65,7 +65,7 @@ extern "C" {
 /* storage types */
 #define DSPARK_F32 0
 #define DSPARK_BF16 1
-#define DSPARK_F16 2   /* logits and their gradients of the calls on rows of logits */
+#define DSPARK_F16 2   /* rows of logits, hidden states and their head, updates, and their gradients */
 
 /* scheduler modes */
 #define DSPARK_SCHED_FIXED 0   /* no truncation: l_r = gamma */
