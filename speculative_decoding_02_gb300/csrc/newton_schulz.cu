@@ -99,7 +99,7 @@ struct Place {
   int c;
 };
 __device__ __forceinline__ Place place_of(const InputParams& p, long long i, int chunks) {
-  if (p.flat) return Place{(size_t)i * 4, (size_t)i * 4, 0};   // (no division)
+  if (p.flat) return Place{(size_t)i * 4, (size_t)i * 4, 0};   // (no division: 360 against 364 us of 151936 x 256)
   const long long r = i / chunks;
   const int c = (int)(i - r * chunks) * 4;
   return Place{(size_t)r * p.stride, (size_t)r * p.ld + c, c};

@@ -257,6 +257,33 @@ def test_streams_and_graphs():
         assert torch.equal(out, w)
 
 
+def test_calls_at_once():
+    # launches whose CTAs wait for one another beside others that fill the GPU, from
+    # three threads on streams of their own
+    import threading
+    data = [_update(m, n, torch.float32, 11) for m, n in ((256, 256), (777, 1000), (4000, 64))]
+    g = torch.Generator(device="cuda").manual_seed(12)
+    W = torch.randn((30000, 512), device="cuda", generator=g).mul_(0.1).bfloat16()
+    h = torch.randn((2048, 512), device="cuda", generator=g).bfloat16()
+    t = torch.randint(0, 30000, (2048,), device="cuda", generator=g, dtype=torch.int32)
+    calls = [lambda k=k: (ds.newton_schulz(data[k % 3]),) for k in range(3)] + [lambda: ds.linear_cross_entropy(h, W, t)]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(first):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for i in range(24):
+                k = (first + i) % 4
+                if not all(torch.equal(a, b) for a, b in zip(calls[k](), want[k])):
+                    wrong.append(k)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(3)]
+    [x.start() for x in threads]
+    [x.join() for x in threads]
+    assert not wrong and ds.read_status(ds.head_status("cuda")) == ds.OK
+
+
 def test_a_training_step_of_draft_and_head():
     """The operators together, as a step uses them: the loss of a projection's
     hidden states under a head with the Markov head's rows beside it, the gradients,
