@@ -139,8 +139,8 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// mbar_wait of a converged warp.  The clock is read now and then only: a read takes
-// about a microsecond, and a tile's accumulators change hands several times.
+// mbar_wait of a converged warp, which reads the clock now and then only (a tile's
+// accumulators change hands several times).
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
   bool ok = mbar_try_wait(bar, parity);
   if (__all_sync(0xffffffffu, ok)) return true;
