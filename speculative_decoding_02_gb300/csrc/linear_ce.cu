@@ -75,13 +75,16 @@ struct ScanParams {
 };
 
 // The parts of K that give tx tiles of dh and dW's the earliest end: a tile takes
-// its steps of K and about 4 steps' time for its epilogue.  A warp, a choice a lane.
+// its steps of K and, where few follow one another in a unit, some 20 steps' time
+// for its first copies and its epilogue (64 rows under a head of 8192 x 512: 33.5 us,
+// with 4 steps' time and so twice the parts 35.9).  A warp, a choice a lane.
+constexpr int kTileSteps = 20;
 __device__ int choose_splits(int tx, int tw, int kx, int kw, int units, int most) {
   static_assert(kMaxSplits <= 32, "a lane each");
   const int s = (threadIdx.x & 31) + 1;
-  const long long cx = div_up(kx, s) + 4;
+  const long long cx = div_up(kx, s) + kTileSteps;
   const long long waves = div_up(tx * s, units) * cx;
-  const long long all = ((long long)tx * s * cx + (long long)tw * (kw + 4)) / units;
+  const long long all = ((long long)tx * s * cx + (long long)tw * (kw + kTileSteps)) / units;
   long long cost = s <= most ? (waves > all ? waves : all) : 1ll << 56;
   cost = cost << 6 | s;   // (of equal ones the fewest parts)
 #pragma unroll
@@ -94,7 +97,7 @@ __device__ int choose_splits(int tx, int tw, int kx, int kw, int units, int most
 
 // With dh alone, as many tiles as fill all units go whole and the others in
 // parts: 80 tiles of 792 steps on 76 pairs by 76 whole and 4 in 19 parts end
-// after 838 steps (all 80 in 14 parts: 915, and 14 times the sums to keep).
+// after 834 steps (all 80 in 14 parts: 855, and 14 times the sums to keep).
 // Beside dW, whose tiles fill what is left, by parts only.  A whole warp.
 __device__ Counts counts_of(const ScanParams& p, int n, int exponent) {
   Counts c{n, p.wt > 0 && n <= kRestRows ? rest_at(n) + n : n, 0, 1, ldexpf(1.f, exponent), ldexpf(1.f, -exponent), 0};
