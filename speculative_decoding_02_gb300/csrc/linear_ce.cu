@@ -468,7 +468,10 @@ struct LossTiles {
   }
 
   __device__ void epilogue(const Epi& e, const Tile& t, float (&z)[64]) const {
-    if (!e.used) return;   // (nor are the other warps of these rows)
+    if (!e.used) {   // (nor are the other warps of these rows)
+      named_bar_sync(1 + e.q, 128);
+      return;
+    }
     const int left = V - (t.n0 + e.col);
     float m = -INFINITY;
 #pragma unroll
@@ -482,7 +485,9 @@ struct LossTiles {
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < 64; ++j) s += ex2_approx(fmaf(z[j], kLog2e, -at));
-    // the four warps of these rows; two tables in turn, so that one barrier a tile is enough
+    // the four warps of these rows; two tables in turn, so that one barrier a tile is
+    // enough: behind tile n's reads its readers meet the others at tile n + 1's
+    // (whether that one is used or not) before any of these writes tile n + 2's
     float2* table = reinterpret_cast<float2*>(e.extra) + (e.n & 1) * 4 * kRows;
     const int r = e.q * 32 + e.lane;
     table[e.h * kRows + r] = make_float2(m, s);

@@ -442,3 +442,14 @@ def test_streams_and_graphs():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, w))
+
+
+@pytest.mark.parametrize("N,V,D,dtype", [(520, 50000, 64, BF16), (520, 50000, 512, BF16), (600, 50257, 136, F16), (1300, 33000, 256, BF16)])
+def test_tiles_without_rows_between_tiles_with_rows(N, V, D, dtype):
+    # a last row tile whose rows past N leave warps idle, and units that take the row tiles of several
+    # columns in turn, each in one accumulator
+    h, W, t, _, _, _ = _inputs(N, 1, V, D, dtype, 18)
+    loss, lse, _ = _check_loss(h, W, t, None)
+    for _ in range(40):
+        again = ds.linear_cross_entropy(h, W, t)
+        assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
