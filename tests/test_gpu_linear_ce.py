@@ -453,3 +453,32 @@ def test_tiles_without_rows_between_tiles_with_rows(N, V, D, dtype):
     for _ in range(40):
         again = ds.linear_cross_entropy(h, W, t)
         assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
+
+
+def test_many_rows_of_which_few_count():
+    # more rows than one kernel both counts and gathers, a hundred of them live
+    h, W, t, _, g_loss, g_lse = _inputs(3000, 1, 900, 136, BF16, 23)
+    keep = torch.zeros_like(t, dtype=torch.bool)
+    keep[torch.randperm(3000, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")[:100]] = True
+    t[~keep] = -1
+    for dh, dW in ((True, True), (False, True), (True, False)):
+        _check_backward(h, W, t, None, g_loss, g_lse, dh, dW)
+
+
+@pytest.mark.parametrize("N,V,D,dtype", [(2048, 3001, 2560, BF16), (1500, 2000, 4096, F16), (5000, 60001, 1032, BF16)])
+def test_dh_alone_of_more_tiles_than_pairs(N, V, D, dtype):
+    # some tiles of dh whole, the others in parts (77 to 100 for 76 pairs); the last case in several pieces of the vocabulary
+    h, W, t, rows, g_loss, g_lse = _inputs(N, 1, V, D, dtype, 24, 0.02)
+    _check_backward(h, W, t, rows, g_loss, g_lse, True, False)
+
+
+def test_a_dirty_workspace_of_dh_alone():
+    h, W, t, rows, g_loss, g_lse = _inputs(128, 16, 3001, 2568, BF16, 25)
+    _, lse = ds.linear_cross_entropy(h, W, t)
+    want, _ = ds.linear_cross_entropy_backward(h, W, t, lse, g_loss, g_lse, dW=False)
+    for byte in (0x00, 0x7f, 0xff):
+        ws = ds.linear_ce_workspace(2048, 3001, 2568, "cuda", dh=True)
+        ws.fill_(byte)
+        ws[:256].zero_()
+        got, _ = ds.linear_cross_entropy_backward(h, W, t, lse, g_loss, g_lse, dW=False, ws=ws)
+        assert torch.equal(got, want) and ds.read_status(ws) == ds.OK
