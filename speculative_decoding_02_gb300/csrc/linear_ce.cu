@@ -567,7 +567,8 @@ struct SlopeTiles {
   __device__ void epilogue(const Epi& e, const Tile& t, float (&z)[64]) const {
     const RowInfo r = info[t.m0 + e.row];
     const bool rest = r.token < -1;
-    const int first = v0 + t.n0 + e.col, left = rest ? 0 : V - first, at = (rest ? -2 - r.token : r.token) - first;
+    // (rows that only pad are zeros by choice, not by a factor of 0: the head may hold infinities)
+    const int first = v0 + t.n0 + e.col, left = r.token < 0 ? 0 : V - first, at = (rest ? -2 - r.token : r.token) - first;
     uint32_t w[32];
 #pragma unroll
     for (int j = 0; j < 64; j += 2) {

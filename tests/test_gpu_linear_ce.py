@@ -482,3 +482,22 @@ def test_a_dirty_workspace_of_dh_alone():
         ws[:256].zero_()
         got, _ = ds.linear_cross_entropy_backward(h, W, t, lse, g_loss, g_lse, dW=False, ws=ws)
         assert torch.equal(got, want) and ds.read_status(ws) == ds.OK
+
+
+@pytest.mark.parametrize("N", [1, 20, 45, 130, 2100])
+def test_an_infinite_entry_of_the_head_leaves_other_rows_of_dW(N):
+    # every row's logit at v is -inf: probability 0, so dW[v] is 0 (and dh, 0 times -inf, NaN there)
+    h, W, t, _, g_loss, g_lse = _inputs(N, 1, 700, 72, BF16, 19)
+    v = 333
+    t[t == v] = 1
+    h[..., 5] = h[..., 5].abs() + 0.5
+    W[v, 5] = -math.inf
+    loss, lse = ds.linear_cross_entropy(h, W, t)
+    assert torch.isfinite(loss).all() and torch.isfinite(lse).all()
+    dh, dW = ds.linear_cross_entropy_backward(h, W, t, lse, g_loss, g_lse)
+    assert (dW[v] == 0).all() and torch.isfinite(dW).all()
+    assert torch.isnan(dh[..., 5]).all()
+    dh[..., 5] = 0
+    assert torch.isfinite(dh).all()
+    _, alone = ds.linear_cross_entropy_backward(h, W, t, lse, g_loss, g_lse, dh=False)
+    assert torch.equal(alone, dW)
