@@ -722,6 +722,12 @@ struct FinishParams {
   unsigned short* dh;       // [N][D]
 };
 
+// What a remainder of a slope adds of x: nothing where x is infinite, for the slope's
+// own product is infinite there (and the remainder may be 0 or of the other sign).
+__device__ __forceinline__ float remainder_times(float corr, float x) {
+  return fabsf(x) < INFINITY ? corr * x : 0.f;
+}
+
 // dh of a row: the sum of its parts and what the rounding of its token's slope took.
 template <bool kBf16>
 __global__ void __launch_bounds__(128) ce_finish(const FinishParams p) {
@@ -746,8 +752,8 @@ __global__ void __launch_bounds__(128) ce_finish(const FinishParams p) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 u = unpack2<kBf16>(xs[e]);
-      a[2 * e] = corr * u.x;
-      a[2 * e + 1] = corr * u.y;
+      a[2 * e] = remainder_times(corr, u.x);
+      a[2 * e + 1] = remainder_times(corr, u.y);
     }
     const int parts = (c * 8 / 256) * mt + j / 256 < counts.full ? 1 : counts.splits;
     for (int s = 0; s < parts; ++s) {

@@ -501,3 +501,19 @@ def test_an_infinite_entry_of_the_head_leaves_other_rows_of_dW(N):
     assert torch.isfinite(dh).all()
     _, alone = ds.linear_cross_entropy_backward(h, W, t, lse, g_loss, g_lse, dh=False)
     assert torch.equal(alone, dW)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("g", [1.0, 1.00390625, -0.7])
+def test_the_remainder_of_a_slope_adds_no_infinity(dtype, g):
+    # one row whose token's own entry of the head is -inf: the loss is inf, its slope there is -g exactly
+    # (1.00390625 = 1 + 2^-8 leaves a remainder in bf16), and dh -g times -inf
+    h, W, t, _, _, _ = _inputs(1, 1, 300, 64, dtype, 20)
+    h[..., 5] = 1.0
+    W[t.long().flatten(), 5] = -math.inf
+    loss, lse = ds.linear_cross_entropy(h, W, t)
+    assert (loss == math.inf).all() and torch.isfinite(lse).all()
+    dh, dW = ds.linear_cross_entropy_backward(h, W, t, lse, torch.full((1, 1), g, device="cuda"))
+    assert (dh[..., 5] == math.copysign(math.inf, g)).all()
+    dh[..., 5] = 0
+    assert torch.isfinite(dh).all() and torch.isfinite(dW).all()
