@@ -594,9 +594,12 @@ int dspark_linear_cross_entropy(const void* h, int64_t h_stride, const void* W, 
  * Out: dh_out [N, D] and dW_out [V, D] dense, of h's type, 16-byte aligned and
  * wholly written; either may be NULL (a head that stays as it is), not both.
  * They overlap no input.  The logits are formed again, and the slopes s of a
- * piece of the vocabulary are rounded to h's type before the products (of fp16
- * after scaling by a power of two); sums are fp32, in an order that depends on
- * the sizes and on which rows count.  g_loss and g_lse of rows that do not count
+ * piece of the vocabulary are rounded to h's type before the products; sums are
+ * fp32, in an order that depends on the sizes and on which rows count.  fp16
+ * slopes are scaled by a power of two first, which keeps the digits of those down
+ * to 2^-27 of the largest |g_loss| or |g_loss + g_lse|: the row's own for dh
+ * alone, of all rows where dW is wanted (then a dh of a row whose upstream gradient
+ * is below 2^-10 of the largest loses the digits of its least probabilities).  g_loss and g_lse of rows that do not count
  * are not read.  N = 0 gives a dW of zeros.
  */
 int dspark_linear_cross_entropy_backward(const void* h, int64_t h_stride, const void* W, int64_t W_stride, int dtype,

@@ -66,7 +66,7 @@ struct ScanParams {
   float* lse;
   const float* g_loss;      // backward
   const float* g_lse;
-  bool half;                // fp16: the slopes are scaled
+  bool common;              // the slopes have one scale
   int D, dt, kx, wt, units, max_splits;   // dt: column tiles of dh, wt: row tiles of a piece of dW (0: not wanted)
   Counts* counts;
   int32_t* list;            // [N]: the rows that count, in order
@@ -110,22 +110,23 @@ __device__ Counts counts_of(const ScanParams& p, int n, int exponent) {
   }
   return c;
 }
-// The slopes' scale, 2 to this, when g is the largest |g_loss| or |g_loss + g_lse|.
-// fp16 holds 2^-24 to 65504: the slopes, at most 2 g, go up to 2^15, so that a
-// probability of 2^-29 keeps its digits (bf16 has fp32's range).
-__device__ int slope_exponent(const ScanParams& p, float g) {
+// The scale of fp16 slopes, 2 to this, when g is the largest |g_loss| or |g_loss +
+// g_lse|: of the row for dh alone, whose rows are sums of their own, of all rows when dW
+// sums over them.  fp16 has all its digits from 2^-14 to 65504 (and its last
+// one at 2^-24): the slopes, at most 2 g, go up to 2^15, so that g times a probability
+// of 2^-27 keeps its digits.  (bf16 has fp32's range.)
+__device__ int slope_exponent(float g) {
   int e = 0;
-  if (!p.half || !(g > 0.f && g < INFINITY)) return 0;
+  if (!(g > 0.f && g < INFINITY)) return 0;
   frexpf(g, &e);   // g < 2^e
   return max(-100, min(100, 14 - e));
 }
 __device__ __forceinline__ bool in_group(const ScanParams& p, int n) {
   return p.lens == nullptr || n % p.R < p.lens[n / p.R];
 }
-// Of a row that counts, what the slopes are scaled by.
-__device__ __forceinline__ float upstream(const ScanParams& p, long long n) {
-  if (p.g_loss == nullptr) return 0.f;
-  const float a = p.g_loss[n], b = p.g_lse ? a + p.g_lse[n] : a;
+// Of a row that counts, what its slopes are scaled by.
+__device__ __forceinline__ float upstream(const float* g_loss, const float* g_lse, long long n) {
+  const float a = g_loss[n], b = g_lse ? a + g_lse[n] : a;
   return fmaxf(fabsf(a), fabsf(b));
 }
 // The outputs of a row that does not count.
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kScanThreads) ce_scan(const ScanParams p) {
       const bool in = in_group(p, (int)n);
       if (in && t >= 0 && t < p.V) {
         on |= 1u << j;
-        g = fmaxf(g, upstream(p, n));
+        if (p.common) g = fmaxf(g, upstream(p.g_loss, p.g_lse, n));
       } else {
         leave_out(p, n, in, t);
       }
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kScanThreads) ce_scan(const ScanParams p) {
   __syncthreads();
   if (warp == 0) {
     for (int w = 0; w < 32; ++w) g = fmaxf(g, most[w]);
-    const Counts c = counts_of(p, base, slope_exponent(p, g));
+    const Counts c = counts_of(p, base, slope_exponent(g));
     if (lane == 0) *p.counts = c;
   }
 }
@@ -219,6 +220,7 @@ struct GatherParams {
   const float* lse;         // backward
   const float* g_loss;
   const float* g_lse;
+  bool own_scale;           // the row's slopes are scaled by itself
   RowInfo* info;
 };
 
@@ -278,6 +280,7 @@ __device__ __forceinline__ void gather_row(const GatherParams& p, int j, int row
     if (threadIdx.x == 0) p.logit[j] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
   } else if (threadIdx.x == 0) {
     const float g = p.g_loss[row];
+    if (p.own_scale) scale = ldexpf(1.f, slope_exponent(upstream(p.g_loss, p.g_lse, row)));
     p.info[j] = RowInfo{p.lse[row] * kLog2e, scale * (p.g_lse ? g + p.g_lse[row] : g), scale * g,
                         rest ? -2 - t : t};
   }
@@ -314,7 +317,7 @@ __global__ void __launch_bounds__(128) ce_scan_gather(const ScanParams p, const 
     if (t < 0 || t >= p.V || !in_group(p, n)) continue;
     ++all;
     if (n < b) ++before;
-    if (p.half) g = fmaxf(g, upstream(p, n));
+    if (p.common) g = fmaxf(g, upstream(p.g_loss, p.g_lse, n));
   }
   all = __reduce_add_sync(0xffffffffu, all);
   before = __reduce_add_sync(0xffffffffu, before);
@@ -330,7 +333,7 @@ __global__ void __launch_bounds__(128) ce_scan_gather(const ScanParams p, const 
   before = counted[0][0] + counted[0][1] + counted[0][2] + counted[0][3];
   all = counted[1][0] + counted[1][1] + counted[1][2] + counted[1][3];
   g = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-  const int e = slope_exponent(p, g), rest = rest_at(all);
+  const int e = slope_exponent(g), rest = rest_at(all);
   const bool again = p.wt > 0 && all <= kRestRows;
   if (b == 0 && warp == 0) {
     const Counts c = counts_of(p, all, e);
@@ -720,6 +723,8 @@ struct FinishParams {
   long long W_stride;
   int D;
   unsigned short* dh;       // [N][D]
+  const float* g_loss;      // where slopes were scaled by the row, else null
+  const float* g_lse;
 };
 
 // What a remainder of a slope adds of x: nothing where x is infinite, for the slope's
@@ -743,6 +748,7 @@ __global__ void __launch_bounds__(128) ce_finish(const FinishParams p) {
   }
   const Counts counts = *p.counts;
   const float corr = p.corr[j];
+  const float inv_scale = p.g_loss ? ldexpf(1.f, -slope_exponent(upstream(p.g_loss, p.g_lse, blockIdx.x))) : counts.inv_scale;
   const int mt = div_up(counts.n, 256);
   const uint4* w = reinterpret_cast<const uint4*>(p.W + (size_t)p.info[j].token * p.W_stride);
   for (int c = threadIdx.x; c < chunks; c += 128) {
@@ -765,7 +771,7 @@ __global__ void __launch_bounds__(128) ce_finish(const FinishParams p) {
     uint32_t o[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float lo = a[2 * e] * counts.inv_scale, hi = a[2 * e + 1] * counts.inv_scale;
+      const float lo = a[2 * e] * inv_scale, hi = a[2 * e + 1] * inv_scale;
       if constexpr (kBf16) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
         o[e] = *reinterpret_cast<const uint32_t*>(&v);
@@ -875,7 +881,6 @@ ScanParams scan_params(const LinearCeArgs& a, const Layout& l, char* ws) {
   s.tokens = a.tokens;
   s.lens = a.lens;
   s.N = a.N; s.R = a.R; s.V = a.V;
-  s.half = a.dtype == DSPARK_F16;
   s.counts = reinterpret_cast<Counts*>(ws + l.counts);
   s.list = reinterpret_cast<int32_t*>(ws + l.list);
   s.status = a.status;
@@ -935,6 +940,7 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs& a, cudaStream_t stream
   s.slot = reinterpret_cast<int32_t*>(ws + l.slot);
   s.g_loss = a.g_loss;
   s.g_lse = a.g_lse;
+  s.common = !bf16 && want_dW;
   s.D = a.D;
   s.dt = want_dh ? div_up(a.D, 256) : 0;
   s.kx = l.piece / kStep;
@@ -945,6 +951,7 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs& a, cudaStream_t stream
   g.lse = a.lse_in;
   g.g_loss = a.g_loss;
   g.g_lse = a.g_lse;
+  g.own_scale = !bf16 && !want_dW;
   g.info = reinterpret_cast<RowInfo*>(ws + l.info);
   CE_TRY(scan_and_gather(a, l, ws, s, g, stream));
 
@@ -992,7 +999,7 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs& a, cudaStream_t stream
   }
   if (!want_dh) return cudaSuccess;
   FinishParams f{reinterpret_cast<const float*>(ws + l.dh), l.rows, s.counts, s.slot, t.corr, g.info, g.W, a.W_stride, a.D,
-                 static_cast<unsigned short*>(a.dh)};
+                 static_cast<unsigned short*>(a.dh), g.own_scale ? a.g_loss : nullptr, a.g_lse};
   return small(bf16 ? ce_finish<true> : ce_finish<false>, a.N, 128, stream, f);
 }
 

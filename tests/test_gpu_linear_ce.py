@@ -517,3 +517,17 @@ def test_the_remainder_of_a_slope_adds_no_infinity(dtype, g):
     assert (dh[..., 5] == math.copysign(math.inf, g)).all()
     dh[..., 5] = 0
     assert torch.isfinite(dh).all() and torch.isfinite(dW).all()
+
+
+def test_fp16_rows_of_very_different_upstream_gradients():
+    # dh alone: a row's slopes keep their digits whatever the other rows' gradients are
+    h, W, t, _, g_loss, _ = _inputs(20, 4, 3001, 64, F16, 21)
+    W, g = W * 0.1, g_loss.abs() + 0.5
+    g[::2] *= 2.0 ** 13
+    g[1::2] *= 2.0 ** -9
+    _, lse = ds.linear_cross_entropy(h, W, t)
+    dh, _ = ds.linear_cross_entropy_backward(h, W, t, lse, g, dW=False)
+    for b in range(20):
+        parts = _plain(h[b:b + 1], W, t[b:b + 1], None)[4]
+        want, _, tol, _ = _gradients(h[b:b + 1], W, t[b:b + 1], lse[b:b + 1], g[b:b + 1], None, parts)
+        ref.assert_close(dh[b:b + 1], want, tol, "dh")
