@@ -280,7 +280,7 @@ __device__ __forceinline__ void gather_row(const GatherParams& p, int j, int row
     if (threadIdx.x == 0) p.logit[j] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
   } else if (threadIdx.x == 0) {
     const float g = p.g_loss[row];
-    if (p.own_scale) scale = ldexpf(1.f, slope_exponent(upstream(p.g_loss, p.g_lse, row)));
+    if (!kBf16 && p.own_scale) scale = ldexpf(1.f, slope_exponent(upstream(p.g_loss, p.g_lse, row)));
     p.info[j] = RowInfo{p.lse[row] * kLog2e, scale * (p.g_lse ? g + p.g_lse[row] : g), scale * g,
                         rest ? -2 - t : t};
   }
@@ -570,8 +570,7 @@ struct SlopeTiles {
   __device__ void epilogue(const Epi& e, const Tile& t, float (&z)[64]) const {
     const RowInfo r = info[t.m0 + e.row];
     const bool rest = r.token < -1;
-    // (rows that only pad are zeros by choice, not by a factor of 0: the head may hold infinities)
-    const int first = v0 + t.n0 + e.col, left = r.token < 0 ? 0 : V - first, at = (rest ? -2 - r.token : r.token) - first;
+    const int first = v0 + t.n0 + e.col, left = rest ? 0 : V - first, at = (rest ? -2 - r.token : r.token) - first;
     uint32_t w[32];
 #pragma unroll
     for (int j = 0; j < 64; j += 2) {
@@ -596,6 +595,10 @@ struct SlopeTiles {
       }
       if (j == at) corr[t.m0 + e.row] = x[0] - back.x;
       if (j + 1 == at) corr[t.m0 + e.row] = x[1] - back.y;
+    }
+    if (r.token == -1) {   // (zeros by choice, not by up = 0: the head may hold infinities)
+#pragma unroll
+      for (int j = 0; j < 32; ++j) w[j] = 0;
     }
     store_16bit(e, &out, w, t.n0 + e.col, vtiles * 256, t.m0 + e.row0, rows);
   }
@@ -748,7 +751,8 @@ __global__ void __launch_bounds__(128) ce_finish(const FinishParams p) {
   }
   const Counts counts = *p.counts;
   const float corr = p.corr[j];
-  const float inv_scale = p.g_loss ? ldexpf(1.f, -slope_exponent(upstream(p.g_loss, p.g_lse, blockIdx.x))) : counts.inv_scale;
+  float inv_scale = counts.inv_scale;
+  if (!kBf16 && p.g_loss) inv_scale = ldexpf(1.f, -slope_exponent(upstream(p.g_loss, p.g_lse, blockIdx.x)));
   const int mt = div_up(counts.n, 256);
   const uint4* w = reinterpret_cast<const uint4*>(p.W + (size_t)p.info[j].token * p.W_stride);
   for (int c = threadIdx.x; c < chunks; c += 128) {
