@@ -524,7 +524,7 @@ struct OpShape {
 // maps and a number of steps: up to three products of halves, then up to three with
 // a diagonal tile.
 struct Op {
-  short left[3], right[3];     // maps
+  short left, left_low, right, right_low;   // maps (low: of three products)
   short unit[3], of[3];        // maps of the diagonal tiles and of their other factors
   short products, extra, steps, unit_steps;   // steps: of a product's K
   bool left_mn, right_mn, unit_is_left, symmetric, vec;
@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_program(const __grid_constant_
     for (int o = 0; o < p.count && ok; ++o) {
       const Op& op = ops[o];
       const bool left_mn = op.left_mn, right_mn = op.right_mn;
-      const CUtensorMap *l0 = &p.maps[op.left[0]], *l1 = &p.maps[op.left[2]], *r0 = &p.maps[op.right[0]], *r1 = &p.maps[op.right[1]];
+      const CUtensorMap *l0 = &p.maps[op.left], *l1 = &p.maps[op.left_low], *r0 = &p.maps[op.right], *r1 = &p.maps[op.right_low];
       for (int n = 0; ok && item_of(op, unit, units, n, t); ++n) {
         if (n == 0 && op.base > 0 && !(ok = wait_count(p.counter, op.base, abort, p.status))) break;
         const Bundles all = bundles_of<kHalves>(op);
@@ -857,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_program(const __grid_constant_
           }
           continue;
         }
-        const bool mirror = op.symmetric && t.n0 + kOpN <= t.m0 && row < op.rows;
+        const bool mirror = !kHalves && op.symmetric && t.n0 + kOpN <= t.m0 && row < op.rows;
         auto store_mirror = [&](__half* to) {
 #pragma unroll
           for (int j = 0; j < kOpCols; ++j)
@@ -879,7 +879,6 @@ __global__ void __launch_bounds__(kThreads, 1) ns_program(const __grid_constant_
         if (kHalves && op.to1 != nullptr) {
           make_low();
           place(mine + kOpM * 128);
-          if (mirror) store_mirror(op.to1);
         }
         named_bar_sync(2 + q, 128);
         store_rows(mine, op.to0, op.ld);
@@ -1099,18 +1098,18 @@ struct Builder {
     return (short)p.map_count++;
   }
   short left(const __half* base, const Halves& m, bool mn) { return map(base, m.rows, m.cols, m.ld, mn ? kStep : kOpM); }
-  short right(const __half* base, const Halves& m, bool) { return map(base, m.rows, m.cols, m.ld, kOpN); }
+  short right(const __half* base, const Halves& m) { return map(base, m.rows, m.cols, m.ld, kOpN); }
 
   // The product of two matrices (three products where both have low halves).
   Op& add(const Halves& l, bool l_mn, const Halves& r, bool r_mn, int rows, int cols, int K, bool symmetric) {
     Op& op = p.ops[p.count++];
     op = Op{};
     op.products = l.lo && r.lo ? 3 : 1;
-    op.left[0] = op.left[1] = left(l.hi, l, l_mn);
-    op.right[0] = op.right[2] = right(r.hi, r, r_mn);
+    op.left = left(l.hi, l, l_mn);
+    op.right = right(r.hi, r);
     if (op.products == 3) {
-      op.left[2] = left(l.lo, l, l_mn);
-      op.right[1] = right(r.lo, r, r_mn);
+      op.left_low = left(l.lo, l, l_mn);
+      op.right_low = right(r.lo, r);
     }
     op.left_mn = l_mn;
     op.right_mn = r_mn;
@@ -1119,8 +1118,9 @@ struct Builder {
     op.steps = (short)div_up(K, kStep);
     op.mt = div_up(rows, kOpM);
     op.nt = div_up(cols, kOpN);
-    // (the tiles above the diagonal where there are SMs for them: mirroring takes longer)
-    op.symmetric = symmetric && op.mt * op.nt > sms;
+    // (the tiles above the diagonal where there are SMs for them, as for all operands in
+    // halves, at most 512 x 512: mirroring takes longer)
+    op.symmetric = symmetric && !halves && op.mt * op.nt > sms;
     op.tiles = op.symmetric ? op.mt * (op.mt + 1) : op.mt * op.nt;
     op.base = tiles;
     op.scale = kInvScale;
@@ -1230,10 +1230,10 @@ cudaError_t launch_newton_schulz(const NewtonSchulzArgs& a, cudaStream_t stream)
     Op& op = build.add(from, false, from, false, small, small, small, true);
     op.extra = l.halves ? 3 : 2;
     op.unit_steps = kOpN / kStep;
-    op.of[0] = op.of[1] = op.left[0];
-    op.unit[0] = op.unit[2] = build.right(ratio.hi, ratio, false);
-    op.unit[1] = build.right(ratio.lo, ratio, false);
-    op.of[2] = op.left[2];
+    op.of[0] = op.of[1] = op.left;
+    op.unit[0] = op.unit[2] = build.right(ratio.hi, ratio);
+    op.unit[1] = build.right(ratio.lo, ratio);
+    op.of[2] = op.left_low;
     op.scale = c * kInvScale;
     op.diag = diag * kScale;
     build.into(op, to);
@@ -1263,9 +1263,9 @@ cudaError_t launch_newton_schulz(const NewtonSchulzArgs& a, cudaStream_t stream)
         op.extra = 2;
         op.unit_is_left = !tall;
         op.unit_steps = (tall ? kOpN : kOpM) / kStep;
-        op.unit[0] = op.unit[1] = tall ? build.right(one.hi, one, false) : build.left(one.hi, one, false);
-        op.of[0] = tall ? build.left(from.hi, from, false) : build.right(from.hi, from, true);
-        op.of[1] = tall ? build.left(from.lo, from, false) : build.right(from.lo, from, true);
+        op.unit[0] = op.unit[1] = tall ? build.right(one.hi, one) : build.left(one.hi, one, false);
+        op.of[0] = tall ? build.left(from.hi, from, false) : build.right(from.hi, from);
+        op.of[1] = tall ? build.left(from.lo, from, false) : build.right(from.lo, from);
         op.scale *= a.a;
       }
       if (i + 1 < a.steps) {
