@@ -570,7 +570,8 @@ int dspark_markov_head_backward_ex(const void* dlogits, const void* W1, const vo
  * count either.  Rows that do not count are gathered out before the products
  * and cost next to nothing; their outputs are zeros.  A token outside [-1, V)
  * records DSPARK_ERR_INVALID, its loss is NaN (its lse 0), its dh NaN, and it
- * takes no part in dW.  A NaN or infinite h or W gives what the formulas give.
+ * takes no part in dW.  A NaN or +inf logit makes its row's loss, lse and dh
+ * NaN, and dW; one of -inf has probability 0 (its token's loss is inf).
  * status: the device word for errors (4-byte aligned, zero at first; NULL: the
  * workspace's, its first word).  Workspace: dspark_linear_ce_workspace_size
  * bytes, 256-byte aligned; `what` is 0 for the loss, else the gradients wanted.
@@ -599,8 +600,11 @@ int dspark_linear_cross_entropy(const void* h, int64_t h_stride, const void* W, 
  * slopes are scaled by a power of two first, which keeps the digits of those down
  * to 2^-27 of the largest |g_loss| or |g_loss + g_lse|: the row's own for dh
  * alone, of all rows where dW is wanted (then a dh of a row whose upstream gradient
- * is below 2^-10 of the largest loses the digits of its least probabilities).  g_loss and g_lse of rows that do not count
- * are not read.  N = 0 gives a dW of zeros.
+ * is below 2^-10 of the largest loses the digits of its least probabilities).  What the
+ * rounding takes of the token's own slope (up to 2^-8 of it in bf16, 2^-11 in fp16)
+ * is added to dh, and up to 128 rows that count to dW; with more, a bf16 dW is off
+ * by about 2.2e-3 of its 2-norm, where its own rounding takes 1.7e-3.  g_loss and
+ * g_lse of rows that do not count are not read.  N = 0 gives a dW of zeros.
  */
 int dspark_linear_cross_entropy_backward(const void* h, int64_t h_stride, const void* W, int64_t W_stride, int dtype,
                                          const int32_t* tokens, const int32_t* lens, const float* lse,
@@ -616,9 +620,13 @@ int dspark_linear_cross_entropy_backward(const void* h, int64_t h_stride, const 
  * `steps` (1..64) times
  *   A = X X^T (X^T X where rows > cols),  X <- a X + (b A + c A A) X
  *                                         (a X + X (b A + c A A)).
- * Out: X [rows, cols], dense bf16, the rounded result of steps held to about
- * 1e-3 of its 2-norm (fp16 operands, fp32 sums, X itself in 22 bits); it may not
- * overlap M.  The shorter side is at most 16384, the longer 2^21 (rows or cols 0:
+ * Out: X [rows, cols], dense bf16, the rounded result of steps with fp32 sums and X
+ * itself in 22 bits.  Up to a shorter side of 512 every operand has 22 bits, and the
+ * result is off by about 1e-6 of its 2-norm before its rounding; beyond, operands
+ * have fp16's 11, and it is off by 2e-4 (M nearly of low rank) to 1.5e-3 (random M).
+ * It may not overlap M.  Small updates take a cooperative launch of up to one CTA
+ * an SM: DSPARK_ERR_CUDA where the context has fewer SMs than the device reports.
+ * The shorter side is at most 16384, the longer 2^21 (rows or cols 0:
  * nothing is done); a, b, c and eps >= 0 are finite.  Values of X, A or b A + c A A
  * beyond 60 overflow to infinities: the coefficients have to keep the
  * singular values, at most 1 at first, near 1.  A NaN or infinite value in M

@@ -11,9 +11,9 @@
 // tensor cores as soon as there are a few hundred rows and by the read of W below.
 // The rows that count are gathered first, so the others cost nothing.
 //
-// Measured (GB300, bf16): 2048 rows under a head of 151936 x 2560, the loss 792 us
-// (2.01 PFLOP/s, tensor pipe 97 %; 911 us for seconds on end, under the power
-// cap), dh 1659 us (1.92 PFLOP/s; 1923); one row 132 us (5.9 TB/s of W).
+// Measured (GB300, bf16): 2048 rows under a head of 151936 x 2560, the loss 803 us
+// (1.98 PFLOP/s, tensor pipe 97 %; 921 us for seconds on end, under the power
+// cap), dh 1678 us (1.90 PFLOP/s; 1949); one row 131 us (5.9 TB/s of W).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -45,11 +45,18 @@ struct __align__(16) RowInfo {
   int token;        // or -2 - token: the row holds what the rounding of that slope took; -1: zeros
 };
 
-// With few rows what the rounding of a token's slope takes shows in dW (up to 2^-9
-// of the token's row, as much as dW's own rounding; with more rows it averages
-// out).  So up to kRestRows rows are repeated, from the next multiple of 32 on, with
-// those remainders alone as slopes: they fill the step of 64 rows that one row
-// takes anyway, and cost up to two steps more.
+// What the rounding of a token's slope takes shows in dW, where a token that comes
+// once has that slope alone, and the slopes of a token that comes often are near one
+// another (-g, where g_loss is a mean's) and so are their remainders: up to 2^-8 of
+// the token's row in bf16 and 2^-11 in fp16, as much as dW's own rounding.  Up to
+// kRestRows rows are repeated, from the next multiple of 32 on, with those
+// remainders alone as slopes: they fill the step of 64 rows that one row takes
+// anyway, and cost up to two steps more.  With more rows, which would be formed and
+// multiplied twice, the remainders stay out: dW of 1340 rows under 129280 x 4096
+// (bf16) is off by 2.2e-3 of its 2-norm, where its own rounding takes 1.6e-3.  (Added
+// in dW's epilogue, with the rows in order of tokens, they cost 1 % where a token
+// comes once or twice, but 36 -> 150 us of 2048 rows under 1000 x 512 with frequent
+// tokens, and 256 -> 610 of 2048 rows of one token under 32000 x 1024.)
 constexpr int kRestRows = 128;
 __host__ __device__ constexpr int rest_at(int n) { return (n + 31) / 32 * 32; }
 
@@ -142,7 +149,7 @@ __device__ __forceinline__ void leave_out(const ScanParams& p, long long n, bool
 
 constexpr int kScanThreads = 1024, kScanEach = 8;
 
-// One block: the rows that count, in order.
+// One block: the rows that count, in order (27 us of 32768 rows, 770 of 2^20).
 __global__ void __launch_bounds__(kScanThreads) ce_scan(const ScanParams p) {
   __shared__ int sums[32], before[32];
   __shared__ float most[32];
@@ -524,9 +531,9 @@ __global__ void __launch_bounds__(128) ce_combine(const CombineParams p) {
 // ---------------------------------------------------------------------------
 
 // The slopes of a piece of the vocabulary, rounded to the operands' type for the
-// products that follow (a relative 2^-9 of each in bf16, 2^-12 in fp16, which
-// averages out over a sum; of the token's own, which is most of dh, the rounding
-// is kept apart and added to dh).
+// products that follow: by up to 2^-8 of each in bf16 and 2^-11 in fp16.  The many small
+// ones' roundings average out over a sum.  That of the token's own, which is most
+// of a row's dh, is kept apart and added to dh; for dW see kRestRows.
 struct SlopeTiles {
   CUtensorMap h, w, out;
   static constexpr bool kPair = true, kSelf = false;

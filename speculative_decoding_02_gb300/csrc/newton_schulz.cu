@@ -25,8 +25,8 @@
 // X <- B X is all of the step).
 //
 // Measured (GB300, 5 steps): 4096 x 4096 1181 us (1.16 PFLOP/s of the symmetric
-// count), bound by whole waves of tiles and 15 launches; 1000 x 777 112 us, 256 x 256
-// 87 us, bound by latency; 151936 x 256 362 us, half of it at HBM's rate.
+// count), bound by whole waves of tiles and 15 launches; 1000 x 777 115 us, 256 x 256
+// 86 us, bound by latency; 151936 x 256 362 us, half of it at HBM's rate.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -505,8 +505,9 @@ constexpr int kOpLeftBytes = kOpM * 128, kOpRightBytes = kOpN * 128, kOpStepByte
 
 // A stage of the ring holds a bundle, whose wait and commit its steps share.  Of
 // halves: both operands' for one step of K, which three products use (or two steps
-// of a product with a diagonal tile); else four steps.  Times of 256 x 256 (halves)
-// and of 1000 x 777 by the first form 86 and 112 us, by the second 92 and 105.
+// of a product with a diagonal tile); else four steps.  Taken side by side, 256 x 256
+// (halves) had 86 us by the first form and 92 by the second, 1000 x 777 112 and 105
+// (on rows and tiles before the present ones, with which it has 115).
 template <bool kHalves>
 struct OpShape {
   static constexpr int kSlots = kHalves ? 2 : 4, kStages = kHalves ? 3 : 2;
@@ -1239,8 +1240,8 @@ cudaError_t launch_newton_schulz(const NewtonSchulzArgs& a, cudaStream_t stream)
     build.into(op, to);
   };
   // Everything in one launch, or by groups of steps, or product by product.
-  // Measured (us), in that order: 256 x 256: 92, 114, 123; 256 x 512: 103, 119,
-  // 137; 512 x 1000: 195, 167, 197; 64 x 4000: 175, 119, 164; 16000 x 256: 466,
+  // Measured side by side (us; the first form before its bundles), in that order:
+  // 256 x 256: 92, 114, 123; 256 x 512: 103, 119, 137; 512 x 1000: 195, 167, 197; 64 x 4000: 175, 119, 164; 16000 x 256: 466,
   // 169, 240; without halves 1000 x 777: 109, -, 129; 2048 x 2048: 359, -, 411;
   // 1536 x 1536: 234, -, 222; 3000 x 3000 product by product 603.
   const long long x_tiles = (long long)div_up(a.rows, kOpM) * div_up(a.cols, kOpN);

@@ -531,3 +531,20 @@ def test_fp16_rows_of_very_different_upstream_gradients():
         parts = _plain(h[b:b + 1], W, t[b:b + 1], None)[4]
         want, _, tol, _ = _gradients(h[b:b + 1], W, t[b:b + 1], lse[b:b + 1], g[b:b + 1], None, parts)
         ref.assert_close(dh[b:b + 1], want, tol, "dh")
+
+
+def test_a_logit_of_plus_infinity():
+    # reported as NaN, as for rows of logits; other rows keep their loss
+    h, W, t, _, g_loss, _ = _inputs(6, 2, 300, 64, BF16, 26)
+    h[..., 5] = -1.0
+    want = ds.linear_cross_entropy(h, W, t)
+    h[2, 1, 5] = 1.0
+    t[t == 17] = 18
+    W[17, 5] = math.inf   # the logit of 17 is +inf in row (2, 1), -inf in the others
+    bad = torch.zeros((6, 2), dtype=torch.bool, device="cuda")
+    bad[2, 1] = True
+    loss, lse = ds.linear_cross_entropy(h, W, t)
+    assert torch.isnan(loss[bad]).all() and torch.isnan(lse[bad]).all()
+    assert torch.isfinite(loss[~bad]).all() and (lse[~bad] <= want[1][~bad]).all()
+    dh, dW = ds.linear_cross_entropy_backward(h, W, t, lse, g_loss)
+    assert torch.isnan(dh[bad]).all() and torch.isnan(dW).all()
