@@ -639,8 +639,9 @@ _head_status = {}
 def head_status(device):
     """The status word of the calls of markov_logits, markov_head_backward,
     linear_cross_entropy(_backward) and newton_schulz on this device that were given
-    no ws, for read_status.  (A call that is captured into a graph before the device has one takes a word of its own, which
-    nobody reads: call this first, or give it a ws.)"""
+    no ws, for read_status.  (A call that is captured into a graph before the device
+    has one takes a word of its own, which nobody reads: call this first, or give it
+    a ws.)"""
     dev = torch.device(device)
     if dev.index is None:
         dev = torch.device(dev.type, torch.cuda.current_device())
